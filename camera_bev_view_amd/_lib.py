@@ -19,15 +19,20 @@ FBEV_DTYPE_F32 = 0
 FBEV_DTYPE_BF16 = 1
 FBEV_MAX_CAMERAS = 64
 FBEV_MAX_LEVELS = 4
-ABI_VERSION = 8
+ABI_VERSION = 9
 FBEV_MAX_KEYPOINTS = 256
+FBEV_MAX_HEAD_DIM = 128
+FBEV_MAX_ROTARY_PAIRS = 2048
+FBEV_ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 FBEV_NOALLOC_SCRATCH_BYTES = 4 << 20
 
 EXPORTED = ("fbev_forward", "fbev_backward", "fbev_forward_levels", "fbev_backward_levels", "fbev_lss_forward",
             "fbev_lss_backward", "fbev_deform_forward", "fbev_deform_backward_workspace", "fbev_deform_backward",
             "fbev_backward_cameras_workspace",
             "fbev_backward_cameras", "fbev_backward_cameras_noalloc", "fbev_forward_temporal", "fbev_backward_temporal", "fbev_status_string",
-            "fbev_last_error", "fbev_abi_version")
+            "fbev_last_error", "fbev_abi_version", "fbev_group_norm_workspace", "fbev_group_norm_forward",
+            "fbev_group_norm_backward", "fbev_rotary", "fbev_attention_workspace", "fbev_attention_forward",
+            "fbev_attention_backward")
 
 
 class FeatDesc(ctypes.Structure):
@@ -38,6 +43,29 @@ class FeatDesc(ctypes.Structure):
 class BevRange(ctypes.Structure):
     _fields_ = [("x_min", ctypes.c_float), ("x_max", ctypes.c_float), ("y_min", ctypes.c_float),
                 ("y_max", ctypes.c_float), ("z_min", ctypes.c_float), ("z_max", ctypes.c_float)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("images", ctypes.c_int64), ("pixels", ctypes.c_int64), ("image_stride", ctypes.c_int64),
+                ("pixel_stride", ctypes.c_int64), ("C", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("D", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("pairs", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("inverse", ctypes.c_int32), ("q_stride", ctypes.c_int64 * 3),
+                ("k_stride", ctypes.c_int64 * 3), ("q_out_stride", ctypes.c_int64 * 3),
+                ("k_out_stride", ctypes.c_int64 * 3)]
+
+
+class AttentionDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("Tq", ctypes.c_int32), ("Tk", ctypes.c_int32), ("Hq", ctypes.c_int32),
+                ("Hk", ctypes.c_int32), ("D", ctypes.c_int32), ("q_stride", ctypes.c_int64 * 3),
+                ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3), ("scale", ctypes.c_float),
+                ("cap", ctypes.c_float), ("dims", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("pos_q", ctypes.c_void_p), ("pos_k", ctypes.c_void_p), ("slope", ctypes.c_void_p),
+                ("doc_q", ctypes.c_void_p), ("doc_k", ctypes.c_void_p), ("prefix", ctypes.c_void_p)]
 
 
 class FlashBevError(RuntimeError):
@@ -101,6 +129,18 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.fbev_backward_temporal.argtypes = [f32p, FeatDesc, f32p, f32p, f32p, BevRange, i32, i32, i32, i32, f32p,
                                                f32p, f32p, vp]
         lib.fbev_backward_temporal.restype = ctypes.c_int
+        szp, sz, i = ctypes.POINTER(ctypes.c_size_t), ctypes.c_size_t, ctypes.c_int
+        ndp, rdp, adp = ctypes.POINTER(NormDesc), ctypes.POINTER(RotaryDesc), ctypes.POINTER(AttentionDesc)
+        lib.fbev_group_norm_workspace.argtypes = [ndp, i, i32, szp]
+        lib.fbev_group_norm_forward.argtypes = [vp, i, ndp, f32p, f32p, vp, f32p, vp, sz, vp]
+        lib.fbev_group_norm_backward.argtypes = [vp, vp, i, ndp, f32p, f32p, f32p, vp, f32p, f32p, vp, sz, vp]
+        lib.fbev_rotary.argtypes = [vp, vp, i, rdp, f32p, f32p, vp, vp, vp]
+        lib.fbev_attention_workspace.argtypes = [adp, i32, szp]
+        lib.fbev_attention_forward.argtypes = [vp, vp, vp, i, adp, vp, f32p, vp, sz, vp]
+        lib.fbev_attention_backward.argtypes = [vp, vp, vp, vp, i, adp, vp, f32p, vp, vp, vp, f32p, vp, sz, vp]
+        for name in ("fbev_group_norm_workspace", "fbev_group_norm_forward", "fbev_group_norm_backward", "fbev_rotary",
+                     "fbev_attention_workspace", "fbev_attention_forward", "fbev_attention_backward"):
+            getattr(lib, name).restype = i
         lib.fbev_status_string.argtypes = [ctypes.c_int]
         lib.fbev_status_string.restype = ctypes.c_char_p
         lib.fbev_last_error.argtypes = []

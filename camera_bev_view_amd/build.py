@@ -18,7 +18,9 @@ LIB = os.path.join(PKG, "libflashbev.so")
 SOURCES = [os.path.join(CSRC, "flashbev_api.cpp"), os.path.join(CSRC, "sampling_vt.hip"),
            os.path.join(CSRC, "lift_splat.hip"), os.path.join(CSRC, "deform_agg.hip"),
            os.path.join(CSRC, "camera_grad.hip"), os.path.join(CSRC, "temporal.hip"),
-           os.path.join(CSRC, "sampling_vt_runs.hip")]
+           os.path.join(CSRC, "sampling_vt_runs.hip"), os.path.join(CSRC, "encoder_api.cpp"),
+           os.path.join(CSRC, "group_norm.hip"), os.path.join(CSRC, "rotary.hip"),
+           os.path.join(CSRC, "attention_fwd.hip"), os.path.join(CSRC, "attention_bwd.hip")]
 ARCH = "gfx950"
 
 # Packed-fp32 VALU forms are switched off for all device code.

@@ -11,6 +11,7 @@
 #include <string>
 
 #include "../../include/flashbev.h"
+#include "host_status.h"
 #include "kernels.h"
 #include "lift_splat.h"
 #include "deform_agg.h"
@@ -18,12 +19,10 @@
 static_assert(fbev::kCameraScratchBytes == FBEV_NOALLOC_SCRATCH_BYTES, "the header states the scratch size");
 
 namespace {
-
 thread_local std::string g_last_error;
+}  // namespace
 
-fbev_status fail(fbev_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-
-fbev_status fail(fbev_status s, const char* fmt, ...) {
+fbev_status fbev::fail(fbev_status s, const char* fmt, ...) {
   char buf[512];
   va_list ap;
   va_start(ap, fmt);
@@ -32,6 +31,10 @@ fbev_status fail(fbev_status s, const char* fmt, ...) {
   g_last_error = buf;
   return s;
 }
+
+namespace {
+
+using fbev::fail;
 
 bool finite_range(float lo, float hi) { return std::isfinite(lo) && std::isfinite(hi) && hi > lo; }
 

@@ -463,3 +463,10 @@ def deform_backward(grad_out: torch.Tensor, features: torch.Tensor, K: torch.Ten
                                         _ptr(anchors), _ptr(offsets), _ptr(weights), Q, Kp, _ptr(gF), _ptr(gW),
                                         _ptr(gO), _ptr(gA), _ptr(workspace), workspace.numel(), _stream(dev)))
     return gF, gW, gO, gA
+
+
+# ---- encoder operators (group norm with an activation, rotary positions, attention)
+
+from .encoder import (GroupNormAct, QueryAttention, RotaryAxes, attention_backward,  # noqa: E402,F401
+                      attention_forward, group_norm_act, group_norm_backward, group_norm_forward,
+                      query_attention, rotary_axes, rotary_backward, rotary_forward, rotary_freqs)

@@ -46,11 +46,13 @@
 extern "C" {
 #endif
 
-#define FBEV_ABI_VERSION 8
+#define FBEV_ABI_VERSION 9
 #define FBEV_MAX_CAMERAS 64
 #define FBEV_MAX_GRID 65536
 #define FBEV_MAX_LEVELS 4
 #define FBEV_MAX_KEYPOINTS 256
+#define FBEV_MAX_HEAD_DIM 128
+#define FBEV_MAX_ROTARY_PAIRS 2048
 
 typedef enum {
   FBEV_OK = 0,
@@ -378,6 +380,132 @@ fbev_status fbev_deform_backward(const float* grad_out, const float* features, f
                                  const float* weights, int32_t Q, int32_t Kp, float* grad_features,
                                  float* grad_weights, float* grad_offsets, float* grad_anchors, void* workspace,
                                  size_t workspace_bytes, void* stream);
+
+/*
+ * Encoder operators: what stands before and after the view transforms in a
+ * camera-BEV model.  Tensors are fp32 or bf16 (`dtype`); sums, statistics and
+ * softmax are fp32 and results are rounded once to the tensor's type.  All
+ * three are deterministic, allocate nothing and write every element of their
+ * outputs.  The work runs on `stream`, whose device must be the current one.
+ *
+ * Group norm with an activation on channels-last maps: x holds `images`
+ * images of `pixels` pixels (image_stride and pixel_stride elements apart)
+ * with C contiguous channels in `groups` groups of neighbours.  Per image and
+ * group, over its pixels and channels:
+ *
+ *   xh = (x - mean) / sqrt(var + eps),  z = weight xh + bias,  y = act(z)
+ *
+ *   weight, bias : [C] fp32, device, or NULL (ones / zeros).
+ *   y            : [images, pixels, C] of dtype, contiguous.
+ *   stats        : [images, groups, 2] fp32: mean and 1 / sqrt(var + eps).
+ *   workspace    : device scratch of the size the workspace call reports
+ *                  (NULL when 0), 16-byte aligned; not needed before or after
+ *                  the call.  Calls that share it must not overlap.
+ *
+ * The backward takes grad_y and gives grad_x (both [images, pixels, C],
+ * contiguous, of dtype) and the fp32 sums grad_weight, grad_bias [C] (NULL
+ * skips one).  A ReLU's derivative at 0 is 0.
+ *
+ * C must be a multiple of groups, and a group may hold at most 1024 pieces of
+ * 16 bytes (1024 channels where C or the strides do not allow wide moves):
+ * FBEV_ERR_UNSUPPORTED beyond.  Zero images or pixels are allowed.
+ */
+typedef enum { FBEV_ACT_NONE = 0, FBEV_ACT_RELU = 1, FBEV_ACT_SILU = 2, FBEV_ACT_GELU = 3 } fbev_activation;
+
+typedef struct {
+  int64_t images, pixels;
+  int64_t image_stride, pixel_stride; /* of x, in elements */
+  int32_t C, groups;
+  int32_t activation; /* fbev_activation; GELU is the exact one (erf) */
+  float eps;
+} fbev_norm_desc;
+
+fbev_status fbev_group_norm_workspace(const fbev_norm_desc* nd, fbev_dtype dtype, int32_t backward, size_t* bytes);
+fbev_status fbev_group_norm_forward(const void* x, fbev_dtype dtype, const fbev_norm_desc* nd, const float* weight,
+                                    const float* bias, void* y, float* stats, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+fbev_status fbev_group_norm_backward(const void* grad_y, const void* x, fbev_dtype dtype, const fbev_norm_desc* nd,
+                                     const float* weight, const float* bias, const float* stats, void* grad_x,
+                                     float* grad_weight, float* grad_bias, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/*
+ * Rotary positions with several axes (time, height, width, metres ...): every
+ * token's queries and keys are turned, pair of channels by pair, by
+ *
+ *   theta[b,t,i] = sum_a pos[b,t,a] freqs[a,i]       (i < P; formed in double)
+ *   (x1, x2) -> (x1 cos theta - x2 sin theta, x2 cos theta + x1 sin theta)
+ *
+ * Pair i is channels (i, i + P), or (2i, 2i + 1) when `interleaved`; channels
+ * from 2P on are copied.  `inverse` turns by -theta: the backward of the
+ * operator, applied to the gradients.
+ *
+ *   q, k       : [B, T, heads, D] by element strides (batch, token, head), channels
+ *                contiguous; a tensor with 0 heads may be NULL.
+ *   q_out, k_out : the results, by their own strides; may be q and k themselves
+ *                (same strides), but must not overlap them otherwise.
+ *   pos        : [B, T, A] fp32;  freqs : [A, P] fp32, device; 1 <= A <= 8,
+ *                1 <= P <= min(D / 2, FBEV_MAX_ROTARY_PAIRS).
+ */
+typedef struct {
+  int32_t B, T, D, axes, pairs;
+  int32_t q_heads, k_heads;
+  int32_t interleaved, inverse;
+  int64_t q_stride[3], k_stride[3], q_out_stride[3], k_out_stride[3];
+} fbev_rotary_desc;
+
+fbev_status fbev_rotary(const void* q, const void* k, fbev_dtype dtype, const fbev_rotary_desc* rd, const float* pos,
+                        const float* freqs, void* q_out, void* k_out, void* stream);
+
+/*
+ * Attention between queries, BEV cells and tokens.  For query i, key j and
+ * query head n (key head n / (Hq / Hk)):
+ *
+ *   s = scale q_i . k_j,   s = cap tanh(s / cap)  when cap > 0,
+ *   s = s - slope[b,i,n] |pos_q[b,i] - pos_k[b,j]|_2  when dims > 0,
+ *   o_i = sum_j softmax_j(s) v_j  over the keys i sees.
+ *
+ * Key j is seen when doc_q[b,i] == doc_k[b,j] >= 0 (without documents:
+ * always) and, when `causal`, j <= i + Tk - Tq or j < prefix[b].  A query
+ * that sees no key gets zeros (and lse = -inf); what masked keys hold, NaN and
+ * infinities among it, reaches no query that does not see them.
+ *
+ *   q [B,Tq,Hq,D], k, v [B,Tk,Hk,D] : by element strides (batch, token, head), channels
+ *       contiguous; 16-byte aligned rows take the wide-load path.  Hq a
+ *       multiple of Hk, 1 <= D <= FBEV_MAX_HEAD_DIM.
+ *   pos_q [B,Tq,dims], pos_k [B,Tk,dims], slope [B,Tq,Hq] : fp32, contiguous,
+ *       dims 0 .. 3 (0: none of them is read).
+ *   doc_q [B,Tq], doc_k [B,Tk] : int32, both or neither; in any order, but
+ *       documents that lie together are skipped tile by tile.
+ *   prefix : [B] int32 or NULL; needs `causal`.
+ *   out [B,Tq,Hq,D] of dtype, lse [B,Hq,Tq] fp32 (log of the sum of exp(s)) : contiguous.
+ *   workspace : as for group norm.  Few rows over many keys are split along the
+ *       keys and joined from there.
+ *
+ * The backward takes grad_out, out [B,Tq,Hq,D] (contiguous, of dtype) and lse
+ * and gives grad_q, grad_k, grad_v (contiguous, of dtype; a key head's
+ * gradient is the sum over its query heads) and grad_slope [B,Tq,Hq] fp32
+ * (NULL skips it).  Positions are not differentiated.  Probabilities and score
+ * gradients of bf16 tensors are rounded to bf16 before the matrix products
+ * that use them.
+ */
+typedef struct {
+  int32_t B, Tq, Tk, Hq, Hk, D;
+  int64_t q_stride[3], k_stride[3], v_stride[3];
+  float scale, cap;
+  int32_t dims, causal;
+  const float *pos_q, *pos_k, *slope;
+  const int32_t *doc_q, *doc_k, *prefix;
+} fbev_attention_desc;
+
+fbev_status fbev_attention_workspace(const fbev_attention_desc* ad, int32_t backward, size_t* bytes);
+fbev_status fbev_attention_forward(const void* q, const void* k, const void* v, fbev_dtype dtype,
+                                   const fbev_attention_desc* ad, void* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+fbev_status fbev_attention_backward(const void* grad_out, const void* q, const void* k, const void* v,
+                                    fbev_dtype dtype, const fbev_attention_desc* ad, const void* out,
+                                    const float* lse, void* grad_q, void* grad_k, void* grad_v, float* grad_slope,
+                                    void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static text for a status code. */
 const char* fbev_status_string(fbev_status s);
