@@ -16,15 +16,21 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <typename T, int DP, int KW>
+// HB heads of a wave (two with a distance bias, whose distances they share), KW waves over the moving rows.
+template <typename T, int DP, int KW, int HB>
 struct Bwd {
   static constexpr int RW = 4 / KW;
   static constexpr int MT = KW == 1 ? 64 : 32 * KW;       // moving rows staged at a time
-  static constexpr int kPad = Mma<T, DP>::kPadRow;
-  static constexpr size_t kTiles = (size_t)2 * MT * kPad * sizeof(T);
+  static constexpr size_t kTile = (size_t)MT * Tile<T, DP>::kRowBytes;
+  static constexpr size_t kTiles = 2 * HB * kTile;
   static constexpr size_t kMerge = (size_t)4 * 32 * (DP + 4) * 4;
   static constexpr size_t kBytes = KW == 1 || kTiles > kMerge ? kTiles : kMerge;
 };
+
+template <typename T, int DP>
+constexpr int min_waves(int hb) {
+  return sizeof(T) == 4 || DP > 32 ? 1 : hb == 2 ? 2 : 3;
+}
 
 // Writes own rows' sums (scaled), or adds the four waves' sums over LDS first.  dst(n) is own row n's
 // address or NULL.
@@ -81,53 +87,58 @@ __device__ __forceinline__ void write_own(f32x16 (&acc)[DP / 32], float scale, f
 
 // ---- query rows: delta, gq, gslope
 
-template <typename T, int DP, int KW>
-__global__ __launch_bounds__(kThreads) void attn_bwd_rows(AttnArgs a, int tiles) {
-  using C = Bwd<T, DP, KW>;
+template <typename T, int DP, int KW, int HB, bool BIAS, bool CAP>
+__global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_rows(AttnArgs a, int tiles) {
+  using C = Bwd<T, DP, KW, HB>;
   using M = Mma<T, DP>;
   constexpr int NB = DP / 32, MT = C::MT, RW = C::RW;
   __shared__ alignas(16) char smem[C::kBytes];
-  __shared__ alignas(16) float pos[3][MT];
+  __shared__ alignas(16) float pos[BIAS ? 3 : 1][MT];
   __shared__ alignas(16) int docs[MT];
   __shared__ int doc_range[4][2];
-  __shared__ float slopes[4][3][32];
-  T* Ks = (T*)smem;
-  T* Vs = Ks + MT * C::kPad;
+  __shared__ float slopes[KW > 1 && BIAS ? 4 : 1][3][32];
+  char* Ks = smem;                                        // HB tiles each
+  char* Vs = smem + HB * C::kTile;
 
   const int bid = xcd_block(blockIdx.x, gridDim.x);
   const int tile = bid % tiles, bh = bid / tiles;
-  const int b = bh / a.Hk, hk = bh - b * a.Hk;
+  const int b = bh / (a.Hk / HB), hk = (bh - b * (a.Hk / HB)) * HB;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 31, h = lane >> 5;
   const int rw = wave / KW, kw = wave - rw * KW;
   const int first = tile * 32 * RW + rw * 32;
   const Row w = make_row(a, b, hk, min(first + n, a.R - 1));
-  const int64_t row_at = (((int64_t)b * a.Tq + w.t) * a.Hq + w.head) * a.D;
-  typename M::Frag q[M::kFrags], go[M::kFrags];
-  load_row<T, DP>((const T*)a.q + b * a.qs[0] + w.t * a.qs[1] + w.head * a.qs[2], true, a.vec, a.D, h, q);
-  load_row<T, DP>((const T*)a.gout + row_at, true, a.vec, a.D, h, go);
-  float delta = 0.0f;
-  {
+  const Unit un = make_unit(a);
+  typename M::Frag q[HB][M::kFrags], go[HB][M::kFrags];
+  float delta[HB], lse2[HB], slope[HB] = {};
+#pragma unroll
+  for (int i = 0; i < HB; ++i) {
+    const int64_t row_at = (((int64_t)b * a.Tq + w.t) * a.Hq + w.head + i) * a.D;
+    load_row<T, DP>((const T*)a.q + b * a.qs[0] + w.t * a.qs[1] + (w.head + i) * a.qs[2], a.vec, a.D, h, q[i]);
+    sign_row<T, DP>(a, q[i]);
+    load_row<T, DP>((const T*)a.gout + row_at, a.vec, a.D, h, go[i]);
     typename M::Frag o[M::kFrags];
-    load_row<T, DP>((const T*)a.out + row_at, true, a.vec, a.D, h, o);
+    load_row<T, DP>((const T*)a.out + row_at, a.vec, a.D, h, o);
+    float sum = 0.0f;
 #pragma unroll
     for (int f = 0; f < M::kFrags; ++f)
 #pragma unroll
-      for (int j = 0; j < M::kFragElems; ++j) delta = fmaf((float)go[f][j], (float)o[f][j], delta);
-    delta = pair_sum(delta);
+      for (int j = 0; j < M::kFragElems; ++j) sum = fmaf((float)go[i][f][j], (float)o[f][j], sum);
+    delta[i] = pair_sum(sum);
+    const int64_t stat_at = ((int64_t)b * a.Hq + w.head + i) * a.Tq + w.t;
+    if (kw == 0 && h == 0 && first + n < a.R) a.delta[stat_at] = delta[i];
+    lse2[i] = a.lse[stat_at] * kLog2e;
+    if (lse2[i] == kNegInf) lse2[i] = -kNegInf;           // a row without weights: all p are 0
+    if constexpr (BIAS) slope[i] = a.slope[((int64_t)b * a.Tq + w.t) * a.Hq + w.head + i] / un.raw;
   }
-  const int64_t stat_at = ((int64_t)b * a.Hq + w.head) * a.Tq + w.t;
-  if (kw == 0 && h == 0 && first + n < a.R) a.delta[stat_at] = delta;
-  float lse2 = a.lse[stat_at] * kLog2e;
-  if (lse2 == kNegInf) lse2 = -kNegInf;                   // a row without weights: all p are 0
-
-  float own[3] = {0.0f, 0.0f, 0.0f}, slope2 = 0.0f;
-  if (a.dims) {
-    for (int ax = 0; ax < a.dims; ++ax) own[ax] = a.pos_q[((int64_t)b * a.Tq + w.t) * a.dims + ax];
-    slope2 = a.slope[((int64_t)b * a.Tq + w.t) * a.Hq + w.head] * kLog2e;
+  float own[3] = {0.0f, 0.0f, 0.0f};
+  if constexpr (BIAS) {
+    own_point(a.pos_q + ((int64_t)b * a.Tq + w.t) * a.dims, a.dims, h, own);
+    for (int e = threadIdx.x; e < 3 * MT; e += kThreads) pos[0][e] = 0.0f;
   }
-  for (int e = threadIdx.x; e < MT; e += kThreads) pos[0][e] = pos[1][e] = pos[2][e] = 0.0f, docs[e] = 0;
+  for (int e = threadIdx.x; e < MT; e += kThreads) docs[e] = 0;
   const int lim_lo = row_limit(a, b, min(first, a.R - 1) / a.G);
   const int lim_hi = row_limit(a, b, min(first + 31, a.R - 1) / a.G);
+  const int blk_lo = row_limit(a, b, min(tile * 32 * RW, a.R - 1) / a.G);
   const int blk_hi = row_limit(a, b, min(tile * 32 * RW + 32 * RW - 1, a.R - 1) / a.G);
   int dmin = 0, dmax = 0, bmin = 0, bmax = 0;
   if (a.doc_q) {
@@ -140,9 +151,9 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_rows(AttnArgs a, int tiles)
   }
   const bool one_doc = dmin == dmax && wave_min(w.doc) == dmin;
 
-  f32x16 acc[NB] = {};
-  float sum_ds = 0.0f, sum_dsd = 0.0f, sum_pd = 0.0f;
-  const float c1 = a.scale * kLog2e, inv_cap = a.cap > 0.0f ? a.scale / a.cap : 0.0f, c0 = a.cap * kLog2e;
+  f32x16 acc[HB][NB] = {};
+  bool odd[HB] = {};                                      // the row sees a key with an infinite or NaN element
+  float sum_ds[HB] = {}, sum_dsd[HB] = {}, sum_pd[HB] = {};
   const int k_end = min(a.Tk, blk_hi + 1);
   for (int s0 = 0; s0 < k_end; s0 += MT) {
     const int nk = min(MT, a.Tk - s0);
@@ -153,19 +164,44 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_rows(AttnArgs a, int tiles)
     } else {
       __syncthreads();
     }
-    stage_rows<T, DP, MT, kThreads>(Ks, nk, a.vec, a.D, [&](int r) {
-      return (const T*)a.k + b * a.ks[0] + (int64_t)(s0 + r) * a.ks[1] + hk * a.ks[2];
-    });
-    stage_rows<T, DP, MT, kThreads>(Vs, nk, a.vec, a.D, [&](int r) {
-      return (const T*)a.v + b * a.vs[0] + (int64_t)(s0 + r) * a.vs[1] + hk * a.vs[2];
-    });
+    const bool mixed = a.doc_q != nullptr || (a.causal && s0 + MT - 1 > blk_lo);
+#pragma unroll
+    for (int i = 0; i < HB; ++i) {
+      stage_rows<T, DP, MT>(Ks + i * C::kTile, (const T*)a.k + b * a.ks[0] + s0 * a.ks[1] + (hk + i) * a.ks[2], a.ks[1],
+                            nk, a.vec, a.D);
+      stage_rows<T, DP, MT>(Vs + i * C::kTile, (const T*)a.v + b * a.vs[0] + s0 * a.vs[1] + (hk + i) * a.vs[2], a.vs[1],
+                            nk, a.vec, a.D);
+    }
     if ((int)threadIdx.x < MT) {
       if (a.doc_q) docs[threadIdx.x] = my_doc;
-      if (a.dims && (int)threadIdx.x < nk)
-        for (int ax = 0; ax < a.dims; ++ax)
-          pos[ax][threadIdx.x] = a.pos_k[((int64_t)b * a.Tk + s0 + threadIdx.x) * a.dims + ax];
+      if constexpr (BIAS) {
+        if ((int)threadIdx.x < nk)
+          for (int ax = 0; ax < a.dims; ++ax)
+            pos[ax][threadIdx.x] = a.pos_k[((int64_t)b * a.Tk + s0 + threadIdx.x) * a.dims + ax];
+      }
     }
+    auto visible = [&](int at) {
+      uint32_t vis = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int kr = at + acc_row(i, h);
+        vis |= (s0 + kr <= w.lim && docs[kr] == w.doc) ? 1u << i : 0u;
+      }
+      return vis;
+    };
+    wait_staged();
     __syncthreads();
+    if (mixed && __builtin_expect(__syncthreads_or(holds_odd<T, DP, HB * MT>(Ks)), 0)) {
+#pragma unroll 1
+      for (int at = 32 * kw; at < MT; at += 32 * KW) {
+        const uint32_t vis = visible(at);
+#pragma unroll
+        for (int hd = 0; hd < HB; ++hd) odd[hd] |= sees_odd<T, DP>(Ks + hd * C::kTile, at, vis, lane);
+      }
+      __syncthreads();
+      clean_rows<T, DP, HB * MT>(Ks);
+      __syncthreads();
+    }
 #pragma unroll 1
     for (int at = 32 * kw; at < MT; at += 32 * KW) {
       const int key0 = s0 + at;
@@ -176,125 +212,124 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_rows(AttnArgs a, int tiles)
         if (!__any(d >= dmin && d <= dmax)) continue;
         whole = whole && one_doc && __all(d == dmin);
       }
-      const T* kt = Ks + at * C::kPad;
-      const T* vt = Vs + at * C::kPad;
-      f32x16 s = {}, dp = {};
-#pragma unroll
-      for (int f = 0; f < M::kFrags; ++f) s = M::dot(tile_frag<T, DP>(kt, f, lane), q[f], s);
-#pragma unroll
-      for (int f = 0; f < M::kFrags; ++f) dp = M::dot(tile_frag<T, DP>(vt, f, lane), go[f], dp);
-      f32x16 th;
-      if (a.cap > 0.0f) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          th[i] = tanh_fast<sizeof(T) == 4>(s[i] * inv_cap);
-          s[i] = c0 * th[i];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] *= c1;
-      }
-      f32x16 seen;
-      if (!whole) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int kr = acc_row(i, h);
-          seen[i] = key0 + kr <= w.lim && docs[at + kr] == w.doc ? 1.0f : 0.0f;
-        }
-      }
+      const uint32_t vis = whole ? 0xFFFFu : visible(at);
       f32x16 d;
-      if (a.dims) {
-        distances<MT>(pos, at, a.dims, own, h, d);
+      if constexpr (BIAS) distances<MT>(pos, at, a.dims, own, lane, d);
+      if constexpr (BIAS) {
+        if (!whole) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = fmaf(-slope2, d[i], s[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float p = __builtin_amdgcn_exp2f(s[i] - lse2);
-        s[i] = p * (dp[i] - delta);
-        dp[i] = p;
-      }
-      if (!whole) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = seen[i] > 0.0f ? s[i] : 0.0f;
-      }
-      if (a.dims) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const bool vis = whole || seen[i] > 0.0f;
-          sum_ds += s[i];
-          sum_dsd = fmaf(s[i], vis ? d[i] : 0.0f, sum_dsd);
-          sum_pd += vis ? dp[i] * d[i] : 0.0f;
+          for (int i = 0; i < 16; ++i) d[i] = (vis >> i) & 1 ? d[i] : 0.0f;
         }
       }
-      if (a.cap > 0.0f) {
+#pragma unroll
+      for (int hd = 0; hd < HB; ++hd) {
+        __builtin_amdgcn_sched_barrier(0);                // one head's registers at a time
+        const char* kt = Ks + hd * C::kTile;
+        f32x16 s = tile_dot<T, DP>(kt, at, q[hd], lane);
+        // dp - delta: the sum starts from -delta
+        f32x16 dp = tile_dot<T, DP>(Vs + hd * C::kTile, at, go[hd], lane,
+                                    outer_sum(h == 0 ? 1.0f : 0.0f, h == 0 ? -delta[hd] : 0.0f));
+        f32x16 th;
+        if constexpr (CAP) {
+          cap_scores<T>(s, un.inv_cap);
+          th = s;
+        }
+        if constexpr (BIAS) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[i] = fmaf(-slope[hd], d[i], s[i]);
+        }
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            s[i] = (vis >> i) & 1 ? s[i] : kNegInf;
+            dp[i] = (vis >> i) & 1 ? dp[i] : 0.0f;
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float g = s[i] * fmaf(-th[i], th[i], 1.0f);
-          s[i] = whole || seen[i] > 0.0f ? g : 0.0f;
+          const float p = __builtin_amdgcn_exp2f(fmaf(s[i], un.unit, -lse2[hd]));
+          s[i] = p * dp[i];
+          if constexpr (BIAS) {
+            sum_ds[hd] += s[i];
+            sum_dsd[hd] = fmaf(s[i], d[i], sum_dsd[hd]);
+            sum_pd[hd] = fmaf(p, d[i], sum_pd[hd]);
+          }
         }
+        if constexpr (CAP) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[i] = whole || (vis >> i) & 1 ? s[i] * fmaf(-th[i], th[i], 1.0f) : 0.0f;
+        }
+        M::template accumulate<NB>(acc[hd], M::pack(s), kt, at, lane);
       }
-      if (whole)
-        M::template accumulate<NB>(acc, M::pack(s), kt, lane);
-      else
-        M::template accumulate_masked<NB>(acc, M::pack(s), M::pack(seen), kt, lane);
     }
   }
-  write_own<T, DP, KW>(acc, a.scale, (float*)smem, a.D, a.vec_out, kw, lane, [&](int r) -> T* {
-    if (first + r >= a.R) return nullptr;
-    const int t = (first + r) / a.G, head = hk * a.G + (first + r - t * a.G);
-    return (T*)a.gq + (((int64_t)b * a.Tq + t) * a.Hq + head) * a.D;
-  });
-  if (a.gslope) {
-    // delta came from the rounded output; ds sums to the error it made (sum_j p_ij = 1), which the distances'
-    // mean takes back out: the slope's gradient is fp32 whatever the tensors' type
-    sum_ds = pair_sum(sum_ds);
-    sum_dsd = pair_sum(sum_dsd);
-    sum_pd = pair_sum(sum_pd);
-    if constexpr (KW > 1) {
-      if (h == 0) slopes[kw][0][n] = sum_ds, slopes[kw][1][n] = sum_dsd, slopes[kw][2][n] = sum_pd;
-      __syncthreads();
-      sum_ds = (slopes[0][0][n] + slopes[1][0][n]) + (slopes[2][0][n] + slopes[3][0][n]);
-      sum_dsd = (slopes[0][1][n] + slopes[1][1][n]) + (slopes[2][1][n] + slopes[3][1][n]);
-      sum_pd = (slopes[0][2][n] + slopes[1][2][n]) + (slopes[2][2][n] + slopes[3][2][n]);
+#pragma unroll
+  for (int hd = 0; hd < HB; ++hd) {
+    make_nan<NB>(acc[hd], odd[hd]);
+    // the queries' sign is in s, not in k: a zero scale gives zeros
+    write_own<T, DP, KW>(acc[hd], a.scale, (float*)smem, a.D, a.vec_out, kw, lane, [&](int r) -> T* {
+      if (first + r >= a.R) return nullptr;
+      const int t = (first + r) / a.G, head = hk * a.G + (first + r - t * a.G) + hd;
+      return (T*)a.gq + (((int64_t)b * a.Tq + t) * a.Hq + head) * a.D;
+    });
+    if constexpr (BIAS) {
+      if (a.gslope == nullptr) continue;
+      // delta came from the rounded output; ds sums to the error it made (sum_j p_ij = 1), which the distances'
+      // mean takes back out: the slope's gradient is fp32 whatever the tensors' type
+      float sd = pair_sum(sum_ds[hd]), sdd = pair_sum(sum_dsd[hd]), pd = pair_sum(sum_pd[hd]);
+      bool bad = odd[hd];
+      if constexpr (KW > 1) {
+        __syncthreads();
+        if (h == 0) slopes[kw][0][n] = sd, slopes[kw][1][n] = bad ? __builtin_nanf("") : sdd, slopes[kw][2][n] = pd;
+        __syncthreads();
+        sd = (slopes[0][0][n] + slopes[1][0][n]) + (slopes[2][0][n] + slopes[3][0][n]);
+        sdd = (slopes[0][1][n] + slopes[1][1][n]) + (slopes[2][1][n] + slopes[3][1][n]);
+        pd = (slopes[0][2][n] + slopes[1][2][n]) + (slopes[2][2][n] + slopes[3][2][n]);
+        bad = false;
+      }
+      if (kw == 0 && h == 0 && first + n < a.R)
+        a.gslope[((int64_t)b * a.Tq + w.t) * a.Hq + w.head + hd] = bad ? __builtin_nanf("") : fmaf(sd, pd, -sdd);
     }
-    if (kw == 0 && h == 0 && first + n < a.R)
-      a.gslope[((int64_t)b * a.Tq + w.t) * a.Hq + w.head] = fmaf(sum_ds, sum_pd, -sum_dsd);
   }
 }
 
 // ---- keys: gk, gv
 
-template <typename T, int DP, int KW>
-__global__ __launch_bounds__(kThreads) void attn_bwd_keys(AttnArgs a, int tiles) {
-  using C = Bwd<T, DP, KW>;
+template <typename T, int DP, int KW, int HB, bool BIAS, bool CAP>
+__global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_keys(AttnArgs a, int tiles) {
+  using C = Bwd<T, DP, KW, HB>;
   using M = Mma<T, DP>;
   constexpr int NB = DP / 32, MT = C::MT, RW = C::RW;
   __shared__ alignas(16) char smem[C::kBytes];
-  __shared__ alignas(16) float pos[3][MT];
-  __shared__ alignas(16) float lse2s[MT], deltas[MT], slope2s[MT];
+  __shared__ alignas(16) float pos[BIAS ? 3 : 1][MT];
+  __shared__ alignas(16) float lse2s[HB][MT], deltas[HB][MT], slopes[HB][BIAS ? MT : 4];
   __shared__ alignas(16) int docs[MT], lims[MT];
   __shared__ int doc_range[4][2];
-  T* Qs = (T*)smem;
-  T* Gs = Qs + MT * C::kPad;
+  char* Qs = smem;                                        // HB tiles each
+  char* Gs = smem + HB * C::kTile;
 
   const int bid = xcd_block(blockIdx.x, gridDim.x);
   const int tile = bid % tiles, bh = bid / tiles;
-  const int b = bh / a.Hk, hk = bh - b * a.Hk;
+  const int b = bh / (a.Hk / HB), hk = (bh - b * (a.Hk / HB)) * HB;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 31, h = lane >> 5;
   const int rw = wave / KW, kw = wave - rw * KW;
   const int key0 = tile * 32 * RW + rw * 32;              // the wave's keys
   const int key = min(key0 + n, a.Tk - 1);
-  typename M::Frag k[M::kFrags], v[M::kFrags];
-  load_row<T, DP>((const T*)a.k + b * a.ks[0] + key * a.ks[1] + hk * a.ks[2], true, a.vec, a.D, h, k);
-  load_row<T, DP>((const T*)a.v + b * a.vs[0] + key * a.vs[1] + hk * a.vs[2], true, a.vec, a.D, h, v);
-  float own[3] = {0.0f, 0.0f, 0.0f};
-  for (int ax = 0; ax < a.dims; ++ax) own[ax] = a.pos_k[((int64_t)b * a.Tk + key) * a.dims + ax];
-  const int doc = a.doc_k ? a.doc_k[(int64_t)b * a.Tk + key] : 0;
-  for (int e = threadIdx.x; e < MT; e += kThreads) {
-    pos[0][e] = pos[1][e] = pos[2][e] = 0.0f;
-    slope2s[e] = 0.0f;
+  const Unit un = make_unit(a);
+  typename M::Frag k[HB][M::kFrags], v[HB][M::kFrags];
+#pragma unroll
+  for (int i = 0; i < HB; ++i) {
+    load_row<T, DP>((const T*)a.k + b * a.ks[0] + key * a.ks[1] + (hk + i) * a.ks[2], a.vec, a.D, h, k[i]);
+    sign_row<T, DP>(a, k[i]);                             // the sign of the scale, on the side that only scores read
+    load_row<T, DP>((const T*)a.v + b * a.vs[0] + key * a.vs[1] + (hk + i) * a.vs[2], a.vec, a.D, h, v[i]);
   }
+  float own[3] = {0.0f, 0.0f, 0.0f};
+  if constexpr (BIAS) {
+    own_point(a.pos_k + ((int64_t)b * a.Tk + key) * a.dims, a.dims, h, own);
+    for (int e = threadIdx.x; e < 3 * MT; e += kThreads) pos[0][e] = 0.0f;
+    for (int e = threadIdx.x; e < HB * MT; e += kThreads) slopes[0][e] = 0.0f;
+  }
+  const int doc = a.doc_k ? a.doc_k[(int64_t)b * a.Tk + key] : 0;
   int dmin = 0, dmax = 0, bmin = 0, bmax = 0;
   if (a.doc_q) {
     dmin = wave_min(doc < 0 ? INT32_MAX : doc);
@@ -306,8 +341,9 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_keys(AttnArgs a, int tiles)
   }
   const bool one_doc = dmin == dmax && wave_min(doc) == dmin;
 
-  f32x16 gk[NB] = {}, gv[NB] = {};
-  const float c1 = a.scale * kLog2e, inv_cap = a.cap > 0.0f ? a.scale / a.cap : 0.0f, c0 = a.cap * kLog2e;
+  f32x16 gk[HB][NB] = {}, gv[HB][NB] = {};
+  uint32_t odd[HB][NB] = {};                              // infinite or NaN output gradients the key is seen with
+  bool odd_key[HB] = {};                                  // seen by a query with an infinite or NaN element
   // rows from the first whose order lets it see the workgroup's first key
   const int blk_key = tile * 32 * RW;
   int r_begin = 0;
@@ -325,32 +361,73 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_keys(AttnArgs a, int tiles)
     } else {
       __syncthreads();
     }
-    stage_rows<T, DP, MT, kThreads>(Qs, nr, a.vec, a.D, [&](int r) {
-      const int t = (s0 + r) / a.G, head = hk * a.G + (s0 + r - t * a.G);
-      return (const T*)a.q + b * a.qs[0] + t * a.qs[1] + head * a.qs[2];
-    });
-    stage_rows<T, DP, MT, kThreads>(Gs, nr, a.vec, a.D, [&](int r) {
-      const int t = (s0 + r) / a.G, head = hk * a.G + (s0 + r - t * a.G);
-      return (const T*)a.gout + (((int64_t)b * a.Tq + t) * a.Hq + head) * a.D;
-    });
+    // some row of the tile may not see some key of the workgroup
+    const bool mixed = a.doc_q != nullptr ||
+                       (a.causal && row_limit(a, b, s0 / a.G) < min(blk_key + 32 * RW, a.Tk) - 1);
+#pragma unroll
+    for (int i = 0; i < HB; ++i) {
+      if (a.G == 1) {
+        stage_rows<T, DP, MT>(Qs + i * C::kTile, (const T*)a.q + b * a.qs[0] + s0 * a.qs[1] + (hk + i) * a.qs[2],
+                              a.qs[1], nr, a.vec, a.D);
+        stage_rows<T, DP, MT>(Gs + i * C::kTile, (const T*)a.gout + (((int64_t)b * a.Tq + s0) * a.Hq + hk + i) * a.D,
+                              (int64_t)a.Hq * a.D, nr, a.vec, a.D);
+      } else {
+        stage_group<T, DP, MT>(Qs, (const T*)a.q + b * a.qs[0] + hk * a.G * a.qs[2], a.qs[1], a.qs[2], s0, a.G, nr, a.vec,
+                               a.D);
+        stage_group<T, DP, MT>(Gs, (const T*)a.gout + ((int64_t)b * a.Tq * a.Hq + hk * a.G) * a.D, (int64_t)a.Hq * a.D,
+                               a.D, s0, a.G, nr, a.vec, a.D);
+      }
+    }
     if ((int)threadIdx.x < MT) {
       docs[threadIdx.x] = w.doc;
       lims[threadIdx.x] = w.lim;
-      float l2 = -kNegInf, dl = 0.0f;
-      if ((int)threadIdx.x < nr) {
-        const int64_t at = ((int64_t)b * a.Hq + w.head) * a.Tq + w.t;
-        const float x = a.lse[at] * kLog2e;
-        l2 = x == kNegInf ? -kNegInf : x;
-        dl = a.delta[at];
-        if (a.dims) {
+#pragma unroll
+      for (int i = 0; i < HB; ++i) {
+        float l2 = -kNegInf, dl = 0.0f;
+        if ((int)threadIdx.x < nr) {
+          const int64_t at = ((int64_t)b * a.Hq + w.head + i) * a.Tq + w.t;
+          const float x = CAP ? a.lse[at] * kLog2e : a.lse[at] / un.raw;
+          l2 = x == kNegInf ? -kNegInf : x;
+          dl = a.delta[at];
+          if constexpr (BIAS)
+            slopes[i][threadIdx.x] = a.slope[((int64_t)b * a.Tq + w.t) * a.Hq + w.head + i] / un.raw;
+        }
+        lse2s[i][threadIdx.x] = l2;
+        deltas[i][threadIdx.x] = dl;
+      }
+      if constexpr (BIAS) {
+        if ((int)threadIdx.x < nr)
           for (int ax = 0; ax < a.dims; ++ax) pos[ax][threadIdx.x] = a.pos_q[((int64_t)b * a.Tq + w.t) * a.dims + ax];
-          slope2s[threadIdx.x] = a.slope[((int64_t)b * a.Tq + w.t) * a.Hq + w.head] * kLog2e;
+      }
+    }
+    auto visible = [&](int at) {
+      uint32_t vis = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int r = at + acc_row(i, h);
+        vis |= (key0 + n <= lims[r] && docs[r] == doc) ? 1u << i : 0u;
+      }
+      return vis;
+    };
+    wait_staged();
+    __syncthreads();
+    if (mixed && __builtin_expect(__syncthreads_or(holds_odd<T, DP, 2 * HB * MT>(Qs)), 0)) {
+#pragma unroll 1
+      for (int at = 32 * kw; at < MT; at += 32 * KW) {
+        const uint32_t vis = visible(at);
+#pragma unroll
+        for (int hd = 0; hd < HB; ++hd) {
+          const char* gt = Gs + hd * C::kTile;
+          odd_key[hd] |= sees_odd<T, DP>(Qs + hd * C::kTile, at, vis, lane);
+          odd_key[hd] |= sees_odd<T, DP>(gt, at, vis, lane);
+#pragma unroll
+          for (int blk = 0; blk < NB; ++blk) odd[hd][blk] |= find_odd<T, DP>(gt, at, blk, vis, lane);
         }
       }
-      lse2s[threadIdx.x] = l2;
-      deltas[threadIdx.x] = dl;
+      __syncthreads();
+      clean_rows<T, DP, 2 * HB * MT>(Qs);
+      __syncthreads();
     }
-    __syncthreads();
 #pragma unroll 1
     for (int at = 32 * kw; at < MT; at += 32 * KW) {
       if (s0 + at >= a.R) continue;
@@ -362,99 +439,109 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_keys(AttnArgs a, int tiles)
         if (!__any(d >= dmin && d <= dmax)) continue;
         whole = whole && one_doc && __all(d == dmin);
       }
-      const T* qt = Qs + at * C::kPad;
-      const T* gt = Gs + at * C::kPad;
-      f32x16 s = {}, dp = {};
+      const uint32_t vis = whole ? 0xFFFFu : visible(at);
+      f32x16 d;
+      if constexpr (BIAS) distances<MT>(pos, at, a.dims, own, lane, d);
 #pragma unroll
-      for (int f = 0; f < M::kFrags; ++f) s = M::dot(tile_frag<T, DP>(qt, f, lane), k[f], s);
-#pragma unroll
-      for (int f = 0; f < M::kFrags; ++f) dp = M::dot(tile_frag<T, DP>(gt, f, lane), v[f], dp);
-      f32x16 th;
-      if (a.cap > 0.0f) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          th[i] = tanh_fast<sizeof(T) == 4>(s[i] * inv_cap);
-          s[i] = c0 * th[i];
+      for (int hd = 0; hd < HB; ++hd) {
+        __builtin_amdgcn_sched_barrier(0);                // one head's registers at a time
+        const char* qt = Qs + hd * C::kTile;
+        const char* gt = Gs + hd * C::kTile;
+        // the sums start from -lse (in score units; a cap comes between) and -delta of the moving row
+        const float one = h == 0 ? 1.0f : 0.0f;
+        const float l2 = CAP || h != 0 ? 0.0f : -lse2s[hd][at + n];
+        f32x16 s = CAP ? tile_dot<T, DP>(qt, at, k[hd], lane) : tile_dot<T, DP>(qt, at, k[hd], lane, outer_sum(l2, one));
+        f32x16 dp = tile_dot<T, DP>(gt, at, v[hd], lane, outer_sum(h == 0 ? -deltas[hd][at + n] : 0.0f, one));
+        f32x16 th;
+        if constexpr (CAP) {
+          cap_scores<T>(s, un.inv_cap);
+          th = s;
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] *= c1;
-      }
-      if (a.dims) {
-        f32x16 d;
-        distances<MT>(pos, at, a.dims, own, h, d);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const f32x4 sl = *(const f32x4*)&slope2s[at + 8 * u + 4 * h];
+          const int r = at + 8 * u + 4 * h;
+          f32x4 sl = {}, l2 = {};
+          if constexpr (CAP) l2 = *(const f32x4*)&lse2s[hd][r];
+          if constexpr (BIAS) sl = *(const f32x4*)&slopes[hd][r];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[4 * u + j] = fmaf(-sl[j], d[4 * u + j], s[4 * u + j]);
+          for (int j = 0; j < 4; ++j) {
+            const int i = 4 * u + j;
+            if constexpr (BIAS) s[i] = fmaf(-sl[j], d[i], s[i]);
+            s[i] = __builtin_amdgcn_exp2f(CAP ? fmaf(s[i], un.unit, -l2[j]) : s[i] * un.unit);
+            dp[i] *= s[i];
+            if constexpr (CAP) dp[i] *= fmaf(-th[i], th[i], 1.0f);
+          }
         }
-      }
-      f32x16 seen;
-      if (!whole) {
+        if (!whole) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int r = at + acc_row(i, h);
-          seen[i] = key0 + n <= lims[r] && docs[r] == doc ? 1.0f : 0.0f;
+          for (int i = 0; i < 16; ++i) {
+            s[i] = (vis >> i) & 1 ? s[i] : 0.0f;
+            dp[i] = (vis >> i) & 1 ? dp[i] : 0.0f;
+          }
         }
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const f32x4 l2 = *(const f32x4*)&lse2s[at + 8 * u + 4 * h];
-        const f32x4 dl = *(const f32x4*)&deltas[at + 8 * u + 4 * h];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int i = 4 * u + j;
-          s[i] = __builtin_amdgcn_exp2f(s[i] - l2[j]);
-          dp[i] = s[i] * (dp[i] - dl[j]);
-          if (a.cap > 0.0f) dp[i] *= fmaf(-th[i], th[i], 1.0f);
-        }
-      }
-      if (whole) {
-        M::template accumulate<NB>(gv, M::pack(s), gt, lane);
-        M::template accumulate<NB>(gk, M::pack(dp), qt, lane);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[i] = seen[i] > 0.0f ? s[i] : 0.0f;
-          dp[i] = seen[i] > 0.0f ? dp[i] : 0.0f;
-        }
-        const typename M::Values sv = M::pack(seen);
-        M::template accumulate_masked<NB>(gv, M::pack(s), sv, gt, lane);
-        M::template accumulate_masked<NB>(gk, M::pack(dp), sv, qt, lane);
+        __builtin_amdgcn_sched_barrier(0);
+        M::template accumulate<NB>(gv[hd], M::pack(s), gt, at, lane);
+        M::template accumulate<NB>(gk[hd], M::pack(dp), qt, at, lane);
       }
     }
   }
-  auto at_key = [&](void* base, int r) -> T* {
-    if (key0 + r >= a.Tk) return nullptr;
-    return (T*)base + (((int64_t)b * a.Tk + key0 + r) * a.Hk + hk) * a.D;
-  };
-  write_own<T, DP, KW>(gv, 1.0f, (float*)smem, a.D, a.vec_out, kw, lane, [&](int r) { return at_key(a.gv, r); });
-  write_own<T, DP, KW>(gk, a.scale, (float*)smem, a.D, a.vec_out, kw, lane, [&](int r) { return at_key(a.gk, r); });
+#pragma unroll
+  for (int hd = 0; hd < HB; ++hd) {
+    auto at_key = [&](void* base, int r) -> T* {
+      if (key0 + r >= a.Tk) return nullptr;
+      return (T*)base + (((int64_t)b * a.Tk + key0 + r) * a.Hk + hk + hd) * a.D;
+    };
+    add_odd<NB>(gv[hd], odd[hd]);
+    make_nan<NB>(gk[hd], odd_key[hd]);
+    write_own<T, DP, KW>(gv[hd], 1.0f, (float*)smem, a.D, a.vec_out, kw, lane, [&](int r) { return at_key(a.gv, r); });
+    write_own<T, DP, KW>(gk[hd], a.scale, (float*)smem, a.D, a.vec_out, kw, lane, [&](int r) { return at_key(a.gk, r); });
+  }
 }
 
-template <typename T, int DP>
-hipError_t run(const AttnArgs& a, hipStream_t stream) {
-  const int64_t bh = (int64_t)a.B * a.Hk;
+// Workgroups of 128 own rows that share staged tiles when there are enough to fill the card several times over,
+// of 32 rows whose four waves split the moving rows otherwise.
+bool wide_tiles(const AttnArgs& a, int64_t heads, int rows) {
+  return heads * ((rows + 127) / 128) >= (a.D <= 64 ? 2048 : 512);
+}
+
+template <typename T, int DP, int HB, bool BIAS, bool CAP>
+hipError_t launch(const AttnArgs& a, hipStream_t stream) {
+  const int64_t heads = (int64_t)a.B * a.Hk / HB;
   if (a.R > 0) {
-    const bool wide = bh * ((a.R + 127) / 128) >= 512;
+    const bool wide = wide_tiles(a, heads, a.R);
     const int tiles = (a.R + (wide ? 127 : 31)) / (wide ? 128 : 32);
+    const dim3 grid((unsigned)(heads * tiles));
     if (wide)
-      attn_bwd_rows<T, DP, 1><<<dim3((unsigned)(bh * tiles)), kThreads, 0, stream>>>(a, tiles);
+      attn_bwd_rows<T, DP, 1, HB, BIAS, CAP><<<grid, kThreads, 0, stream>>>(a, tiles);
     else
-      attn_bwd_rows<T, DP, 4><<<dim3((unsigned)(bh * tiles)), kThreads, 0, stream>>>(a, tiles);
+      attn_bwd_rows<T, DP, 4, HB, BIAS, CAP><<<grid, kThreads, 0, stream>>>(a, tiles);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (a.Tk > 0) {
-    const bool wide = bh * ((a.Tk + 127) / 128) >= 512;
+    const bool wide = wide_tiles(a, heads, a.Tk);
     const int tiles = (a.Tk + (wide ? 127 : 31)) / (wide ? 128 : 32);
+    const dim3 grid((unsigned)(heads * tiles));
     if (wide)
-      attn_bwd_keys<T, DP, 1><<<dim3((unsigned)(bh * tiles)), kThreads, 0, stream>>>(a, tiles);
+      attn_bwd_keys<T, DP, 1, HB, BIAS, CAP><<<grid, kThreads, 0, stream>>>(a, tiles);
     else
-      attn_bwd_keys<T, DP, 4><<<dim3((unsigned)(bh * tiles)), kThreads, 0, stream>>>(a, tiles);
+      attn_bwd_keys<T, DP, 4, HB, BIAS, CAP><<<grid, kThreads, 0, stream>>>(a, tiles);
   }
   return hipGetLastError();
+}
+
+template <typename T, int DP>
+hipError_t run(const AttnArgs& a, hipStream_t stream) {
+  if (a.cap > 0.0f)
+    return a.dims ? launch<T, DP, 1, true, true>(a, stream) : launch<T, DP, 1, false, true>(a, stream);
+  if (a.dims == 0) return launch<T, DP, 1, false, false>(a, stream);
+  // two heads a wave where they share the distances and there are enough of them to fill the card
+  if constexpr (DP == 32) {
+    const int64_t shorter = a.R < a.Tk ? a.R : a.Tk;
+    if (a.G == 1 && a.Hk % 2 == 0 && (int64_t)a.B * a.Hk * ((shorter + 31) / 32) >= 1024)
+      return launch<T, DP, 2, true, false>(a, stream);
+  }
+  return launch<T, DP, 1, true, false>(a, stream);
 }
 
 template <typename T>

@@ -40,6 +40,31 @@ __device__ __forceinline__ float pair_max(float x) {
 }
 __device__ __forceinline__ float pair_sum(float x) { return swap32_add(x, x); }
 
+// A staged tile of N rows: 16-byte pieces, P to a row, piece p of row r in slot r P + (p ^ turn(r)).  There is no padding,
+// so global memory moves straight into LDS (a wave's instruction fills 64 neighbouring slots, each lane fetching the piece
+// that belongs there); the turn spreads the rows over the banks, both for a row's pieces read by 32 lanes (all 16 bank
+// groups within 16 rows) and for the transposed reads (four rows by 64 bytes).
+template <typename T, int DP>
+struct Tile {
+  static constexpr int P = DP * (int)sizeof(T) / 16;      // pieces of a row
+  static constexpr int E = 16 / (int)sizeof(T);           // elements of a piece
+  static constexpr int kRowBytes = P * 16;
+
+  static __device__ __forceinline__ int turn(int r) {
+    if constexpr (P == 4) return (r >> 2) & 3;
+    if constexpr (P == 8) return ((r & 2) << 1) | ((r >> 2) & 3);
+    if constexpr (P == 16) return ((r & 3) << 2) | ((r >> 2) & 3);
+    return ((r & 3) << 2) | ((r >> 1) & 2);               // P == 32: a wave's chunks lie eight rows apart
+  }
+  static __device__ __forceinline__ int slot(int r, int p) { return r * P + (p ^ turn(r)); }
+  static __device__ __forceinline__ T* at(char* tile, int r, int c) {
+    return (T*)(tile + slot(r, c / E) * 16) + c % E;
+  }
+  static __device__ __forceinline__ const T* at(const char* tile, int r, int c) {
+    return (const T*)(tile + slot(r, c / E) * 16) + c % E;
+  }
+};
+
 template <typename T, int DP>
 struct Mma;
 
@@ -48,12 +73,9 @@ template <int DP>
 struct Mma<__bf16, DP> {
   using T = __bf16;
   using Frag = bf16x8;
+  using Tl = Tile<T, DP>;
   static constexpr int kFrags = DP / 16;                 // fragments of one row's DP channels
-  static constexpr int kPadRow = DP + (DP == 32 ? 8 : 8);  // LDS row stride in elements
-
-  // fragment f of a row: channels 16 f + 8 h ..
-  static __device__ __forceinline__ int frag_channel(int f, int h) { return 16 * f + 8 * h; }
-  static constexpr int kFragElems = 8;
+  static constexpr int kFragElems = 8;                   // fragment f of half-wave h: piece 2 f + h
 
   static __device__ __forceinline__ f32x16 dot(const Frag& a, const Frag& b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
@@ -74,76 +96,30 @@ struct Mma<__bf16, DP> {
 
   // The A operand: channels 32 blk + n of the rows above, read transposed (four rows by 16 channels for
   // every 16 lanes; lane i of the 16 addresses row i / 4, channels 4 (i mod 4)).
-  static __device__ __forceinline__ bf16x8 columns(const T* tile, int c, int blk, int lane) {
+  static __device__ __forceinline__ i16x4 transposed(const char* tile, int r, int c) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) i16x4*)(uint32_t)(uintptr_t)Tl::at(tile, r, c));
+  }
+  static __device__ __forceinline__ bf16x8 columns(const char* tile, int r0, int c, int blk, int lane) {
     const int h = lane >> 5, i = lane & 15;
-    const T* at = tile + (16 * c + 4 * h + (i >> 2)) * kPadRow + 32 * blk + (lane & 16) + 4 * (i & 3);
-    auto lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) i16x4*)(uint32_t)(uintptr_t)at);
-    auto hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) i16x4*)(uint32_t)(uintptr_t)(at + 8 * kPadRow));
+    const int r = r0 + 16 * c + 4 * h + (i >> 2), ch = 32 * blk + (lane & 16) + 4 * (i & 3);
     union {
       i16x4 s[2];
       bf16x8 v;
     } u;
-    u.s[0] = lo;
-    u.s[1] = hi;
+    u.s[0] = transposed(tile, r, ch);
+    u.s[1] = transposed(tile, r + 8, ch);
     return u.v;
   }
 
   template <int NB>
-  static __device__ __forceinline__ void accumulate(f32x16 (&acc)[NB], const Values& p, const T* tile, int lane) {
+  static __device__ __forceinline__ void accumulate(f32x16 (&acc)[NB], const Values& p, const char* tile, int r0,
+                                                    int lane) {
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
       for (int c = 0; c < 2; ++c)
-        acc[blk] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(columns(tile, c, blk, lane), p.v[c], acc[blk], 0, 0, 0);
-  }
-
-  // Infinities and NaN in a tile of which some (row, own row) pairs are masked: such an element must reach
-  // only the own rows that see it.  They are taken out of the product, and whether an own row sees a
-  // positive or a negative one (a NaN counts as both) comes from two products with the visibility.
-  static __device__ __forceinline__ bool odd(const bf16x8& a) {
-    const i32x4 w = __builtin_bit_cast(i32x4, a);
-    bool o = false;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      o |= ((w[j] & 0x7F80) == 0x7F80) | ((w[j] & 0x7F800000) == 0x7F800000);
-    return o;
-  }
-  template <int NB>
-  static __device__ __forceinline__ void accumulate_masked(f32x16 (&acc)[NB], const Values& p, const Values& seen,
-                                                           const T* tile, int lane) {
-#pragma unroll
-    for (int blk = 0; blk < NB; ++blk) {
-      bf16x8 a[2];
-      a[0] = columns(tile, 0, blk, lane);
-      a[1] = columns(tile, 1, blk, lane);
-      if (__builtin_expect(__any(odd(a[0]) || odd(a[1])), 0)) {
-        f32x16 up = {}, down = {};
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          bf16x8 u, d;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float x = (float)a[c][j];
-            const bool fin = fabsf(x) < __builtin_huge_valf();
-            u[j] = (__bf16)(!fin && !(x < 0.0f) ? 1.0f : 0.0f);
-            d[j] = (__bf16)(!fin && !(x > 0.0f) ? 1.0f : 0.0f);
-            if (!fin) a[c][j] = (__bf16)0.0f;
-          }
-          up = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u, seen.v[c], up, 0, 0, 0);
-          down = __builtin_amdgcn_mfma_f32_32x32x16_bf16(d, seen.v[c], down, 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          if (up[i] > 0.0f) acc[blk][i] += __builtin_huge_valf();
-          if (down[i] > 0.0f) acc[blk][i] += kNegInf;
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-        acc[blk] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[c], p.v[c], acc[blk], 0, 0, 0);
-    }
+        acc[blk] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(columns(tile, r0, c, blk, lane), p.v[c], acc[blk], 0, 0, 0);
   }
 };
 
@@ -152,9 +128,8 @@ template <int DP>
 struct Mma<float, DP> {
   using T = float;
   using Frag = f32x4;
+  using Tl = Tile<T, DP>;
   static constexpr int kFrags = DP / 8;
-  static constexpr int kPadRow = DP + 8;
-  static __device__ __forceinline__ int frag_channel(int f, int h) { return 8 * f + 4 * h; }
   static constexpr int kFragElems = 4;
 
   static __device__ __forceinline__ f32x16 dot(const Frag& a, const Frag& b, f32x16 c) {
@@ -168,99 +143,216 @@ struct Mma<float, DP> {
   };
   static __device__ __forceinline__ Values pack(const f32x16& p) { return Values{p}; }
 
-  static __device__ __forceinline__ float column(const T* tile, int i, int blk, int lane) {
-    return tile[acc_row(i, lane >> 5) * kPadRow + 32 * blk + (lane & 31)];
-  }
-
   template <int NB>
-  static __device__ __forceinline__ void accumulate(f32x16 (&acc)[NB], const Values& p, const T* tile, int lane) {
+  static __device__ __forceinline__ void accumulate(f32x16 (&acc)[NB], const Values& p, const char* tile, int r0,
+                                                    int lane) {
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        acc[blk] = __builtin_amdgcn_mfma_f32_32x32x2f32(column(tile, i, blk, lane), p.v[i], acc[blk], 0, 0, 0);
-  }
-
-  template <int NB>
-  static __device__ __forceinline__ void accumulate_masked(f32x16 (&acc)[NB], const Values& p, const Values& seen,
-                                                           const T* tile, int lane) {
-#pragma unroll
-    for (int blk = 0; blk < NB; ++blk) {
-      float a[16];
-      bool odd = false;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        a[i] = column(tile, i, blk, lane);
-        odd |= !(fabsf(a[i]) < __builtin_huge_valf());
-      }
-      if (__builtin_expect(__any(odd), 0)) {
-        f32x16 up = {}, down = {};
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const bool fin = fabsf(a[i]) < __builtin_huge_valf();
-          up = __builtin_amdgcn_mfma_f32_32x32x2f32(!fin && !(a[i] < 0.0f) ? 1.0f : 0.0f, seen.v[i], up, 0, 0, 0);
-          down = __builtin_amdgcn_mfma_f32_32x32x2f32(!fin && !(a[i] > 0.0f) ? 1.0f : 0.0f, seen.v[i], down, 0, 0, 0);
-          if (!fin) a[i] = 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          if (up[i] > 0.0f) acc[blk][i] += __builtin_huge_valf();
-          if (down[i] > 0.0f) acc[blk][i] += kNegInf;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        acc[blk] = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], p.v[i], acc[blk], 0, 0, 0);
-    }
+        acc[blk] = __builtin_amdgcn_mfma_f32_32x32x2f32(
+            *Tl::at(tile, r0 + acc_row(i, lane >> 5), 32 * blk + (lane & 31)), p.v[i], acc[blk], 0, 0, 0);
   }
 };
 
 // One row's fragments from global memory, zero beyond its D channels.
 template <typename T, int DP>
-__device__ __forceinline__ void load_row(const T* row, bool valid, bool vec, int D, int h,
+__device__ __forceinline__ void load_row(const T* row, bool vec, int D, int h,
                                          typename Mma<T, DP>::Frag (&f)[Mma<T, DP>::kFrags]) {
   using M = Mma<T, DP>;
+  constexpr int E = M::kFragElems;
+  if (vec) {
 #pragma unroll
-  for (int i = 0; i < M::kFrags; ++i) {
-    const int c = M::frag_channel(i, h);
-    if (valid && vec && c + M::kFragElems <= D) {
-      f[i] = *(const typename M::Frag*)(row + c);
-    } else {
+    for (int i = 0; i < M::kFrags; ++i) {
+      const int c = (2 * i + h) * E;
+      f[i] = typename M::Frag{};
+      if (c < D) f[i] = *(const typename M::Frag*)(row + c);
+    }
+  } else {
 #pragma unroll
-      for (int j = 0; j < M::kFragElems; ++j) f[i][j] = (valid && c + j < D) ? row[c + j] : (T)0.0f;
+    for (int i = 0; i < M::kFrags; ++i)
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const int c = (2 * i + h) * E + j;
+        f[i][j] = c < D ? row[c] : (T)0.0f;
+      }
+  }
+}
+
+// One wave instruction: 16 bytes a lane from the buffer's byte off + add to 64 neighbouring slots at `lds` (uniform).
+__device__ __forceinline__ void move_pieces(__amdgpu_buffer_rsrc_t rs, char* lds, int off, int add) {
+#ifdef __HIP_DEVICE_COMPILE__      // the host pass does not know the 16-byte form
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(uint32_t)(uintptr_t)lds, 16, off,
+                                           add, 0, 0);
+#endif
+}
+
+// Stages N rows of a tensor, `stride` elements apart from `base` (uniform), zero beyond `rows` and beyond D channels, by
+// the four waves of the workgroup.  The wide path (vec: 16-byte pieces, N rows within 2^31 bytes) only issues the moves:
+// wait_staged() before the barrier.
+constexpr int kFarOut = 0x7FFFFF00;      // an offset the buffer's bounds turn into zeros
+
+template <typename T, int DP, int N>
+__device__ __forceinline__ void stage_rows(char* tile, const T* base, int64_t stride, int rows, bool vec, int D) {
+  using Tl = Tile<T, DP>;
+  constexpr int CHUNKS = N * Tl::P / 64;                  // wave instructions
+  static_assert(CHUNKS % 4 == 0 && (Tl::P < 32 ? 256 / Tl::P % 16 == 0 : 256 / Tl::P % 8 == 0),
+                "a wave's chunks repeat the turn of their rows");
+  if (vec) {
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int s = 64 * wave + lane, r = s / Tl::P, p = (s % Tl::P) ^ Tl::turn(r);
+    const int bytes = (int)stride * (int)sizeof(T);
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<T*>(base), 0, (rows - 1) * bytes + D * (int)sizeof(T), 0x00020000);
+    const int off = p * Tl::E < D ? r * bytes + p * 16 : kFarOut;
+#pragma unroll
+    for (int k = 0; k < CHUNKS / 4; ++k)
+      move_pieces(rs, tile + (4 * k + wave) * 1024, off, k * (256 / Tl::P) * bytes);
+  } else {
+#pragma unroll 1
+    for (int e = threadIdx.x; e < N * DP; e += 256) {
+      const int r = e / DP, c = e - r * DP;
+      *Tl::at(tile, r, c) = r < rows && c < D ? base[r * stride + c] : (T)0.0f;
     }
   }
 }
 
-// Rows [r0, r0 + N) of a tensor into LDS rows of stride kPadRow, zero beyond `rows` and beyond D channels.
-// row_ptr(r) gives row r's address.  By the whole workgroup.
-template <typename T, int DP, int N, int THREADS, typename F>
-__device__ __forceinline__ void stage_rows(T* lds, int rows, bool vec, int D, F row_ptr) {
-  constexpr int E = 16 / sizeof(T), PIECES = DP / E;
-  typedef T Vec __attribute__((ext_vector_type(E)));
-#pragma unroll 2
-  for (int e = threadIdx.x; e < N * PIECES; e += THREADS) {
-    const int r = e / PIECES, c = (e - r * PIECES) * E;
-    Vec v;
-    if (r < rows && vec && c + E <= D) {
-      v = *(const Vec*)(row_ptr(r) + c);
-    } else {
+// The same for N rows r0 .. of a key head's group of G query heads: row r is token r / G, head r mod G.
+template <typename T, int DP, int N>
+__device__ __forceinline__ void stage_group(char* tile, const T* base, int64_t token, int64_t head, int r0, int G,
+                                            int rows, bool vec, int D) {
+  using Tl = Tile<T, DP>;
+  if (vec) {
+    // offsets from the tile's first token: at most N tokens, within 2^31 bytes
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), t0 = r0 / G;
+    const T* first = base + t0 * token;
+    const int tb = (int)token * (int)sizeof(T), hb = (int)head * (int)sizeof(T);
+    const __amdgpu_buffer_rsrc_t rs =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(first), 0, 0x7FFFFF00, 0x00020000);
 #pragma unroll
-      for (int j = 0; j < E; ++j) v[j] = (T)0.0f;
-      if (r < rows && c < D) {
-        const T* p = row_ptr(r) + c;
-        for (int j = 0; j < E && c + j < D; ++j) v[j] = p[j];
+    for (int k = 0; k < N * Tl::P / 256; ++k) {
+      const int s = 256 * k + 64 * wave + lane, r = s / Tl::P, p = (s % Tl::P) ^ Tl::turn(r);
+      const int t = (r0 + r) / G, g = r0 + r - t * G;
+      const int off = r < rows && p * Tl::E < D ? (t - t0) * tb + g * hb + p * 16 : kFarOut;
+      move_pieces(rs, tile + (4 * k + wave) * 1024, off, 0);
+    }
+  } else {
+#pragma unroll 1
+    for (int e = threadIdx.x; e < N * DP; e += 256) {
+      const int r = e / DP, c = e - r * DP, t = (r0 + r) / G, g = r0 + r - t * G;
+      *Tl::at(tile, r, c) = r < rows && c < D ? base[t * token + g * head + c] : (T)0.0f;
+    }
+  }
+}
+
+__device__ __forceinline__ void wait_staged() { __builtin_amdgcn_s_waitcnt(0x0F70); }      // vmcnt(0)
+
+// The row fragments of tile row r0 + n.
+template <typename T, int DP>
+__device__ __forceinline__ typename Mma<T, DP>::Frag tile_frag(const char* tile, int r0, int f, int lane) {
+  return *(const typename Mma<T, DP>::Frag*)(tile + Tile<T, DP>::slot(r0 + (lane & 31), 2 * f + (lane >> 5)) * 16);
+}
+
+// Products of tile rows r0 .. r0 + 31 with the own row, added to s.
+template <typename T, int DP>
+__device__ __forceinline__ f32x16 tile_dot(const char* tile, int r0,
+                                           const typename Mma<T, DP>::Frag (&own)[Mma<T, DP>::kFrags], int lane,
+                                           f32x16 s = f32x16{}) {
+  using M = Mma<T, DP>;
+#pragma unroll
+  for (int f = 0; f < M::kFrags; ++f) s = M::dot(tile_frag<T, DP>(tile, r0, f, lane), own[f], s);
+  return s;
+}
+
+// Infinities and NaN in masked places.  A transposed product multiplies every tile row with every own row, and
+// 0 x inf is NaN: a non-finite element must reach only the own rows that see its tile row.  Tiles with masks are
+// searched for one (holds_odd), and only when there is one the workgroup notes which sums it belongs to (find_odd),
+// takes it out of the tile (clean_rows), and puts it back at the end (add_odd).
+template <typename T, int DP, int N>
+__device__ __forceinline__ bool holds_odd(const char* tile) {
+  uint32_t odd = 0;
+#pragma unroll 2
+  for (int e = threadIdx.x; e < N * Tile<T, DP>::P; e += 256) {
+    const i32x4 w = *(const i32x4*)(tile + e * 16);
+    // the exponent's ones carry into the sign bit
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      odd |= sizeof(T) == 2 ? ((uint32_t)w[j] & 0x7F807F80u) + 0x00800080u : ((uint32_t)w[j] & 0x7F800000u) + 0x00800000u;
+  }
+  return (odd & (sizeof(T) == 2 ? 0x80008000u : 0x80000000u)) != 0;
+}
+
+template <typename T, int DP, int N>
+__device__ __forceinline__ void clean_rows(char* tile) {
+#pragma unroll 1
+  for (int e = threadIdx.x; e < N * DP; e += 256) {
+    T* x = (T*)tile + e;
+    if (!(fabsf((float)*x) < __builtin_huge_valf())) *x = (T)0.0f;
+  }
+}
+
+// Bit i of vis: the own row sees tile row r0 + acc_row(i, h).  The result's bit r: it sees tile row r0 + r.
+__device__ __forceinline__ uint32_t seen_rows(uint32_t vis, int h) {
+  const uint32_t other = __shfl_xor(vis, 32);
+  uint32_t seen = 0;
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    seen |= (((vis >> (4 * u)) & 15) << (8 * u + 4 * h)) | (((other >> (4 * u)) & 15) << (8 * u + 4 * (1 - h)));
+  return seen;
+}
+
+// Bit i: a positive infinite element (or a NaN) belongs to the lane's sum i of channels 32 blk ..; bit 16 + i: a
+// negative one (or a NaN).
+template <typename T, int DP>
+__device__ __forceinline__ uint32_t find_odd(const char* tile, int r0, int blk, uint32_t vis, int lane) {
+  const int h = lane >> 5;
+  const uint32_t seen = seen_rows(vis, h);
+  uint32_t odd = 0;
+#pragma unroll 1
+  for (int r = 0; r < 32; ++r) {
+    const bool sees = (seen >> r) & 1;
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {
+      const float x = (float)*Tile<T, DP>::at(tile, r0 + r, 32 * blk + acc_row(i, h));
+      if (sees && !(fabsf(x) < __builtin_huge_valf()))
+        odd |= (x < 0.0f ? 0u : 1u << i) | (x > 0.0f ? 0u : 1u << (16 + i));
+    }
+  }
+  return odd;
+}
+
+// Whether the own row sees a tile row that has a non-finite element.
+template <typename T, int DP>
+__device__ __forceinline__ bool sees_odd(const char* tile, int r0, uint32_t vis, int lane) {
+  const uint32_t seen = seen_rows(vis, lane >> 5);
+  bool odd = false;       // of tile row n
+#pragma unroll 1
+  for (int c = 0; c < DP; ++c)
+    odd |= !(fabsf((float)*Tile<T, DP>::at(tile, r0 + (lane & 31), c)) < __builtin_huge_valf());
+  return ((uint32_t)__ballot(odd) & seen) != 0;
+}
+
+template <int NB>
+__device__ __forceinline__ void add_odd(f32x16 (&acc)[NB], const uint32_t (&odd)[NB]) {
+#pragma unroll
+  for (int blk = 0; blk < NB; ++blk)
+    if (__builtin_expect(__any(odd[blk] != 0), 0)) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if ((odd[blk] >> i) & 1) acc[blk][i] += __builtin_huge_valf();
+        if ((odd[blk] >> (16 + i)) & 1) acc[blk][i] += kNegInf;
       }
     }
-    *(Vec*)(lds + r * Mma<T, DP>::kPadRow + c) = v;
-  }
 }
 
-// The row fragments of tile row n.
-template <typename T, int DP>
-__device__ __forceinline__ typename Mma<T, DP>::Frag tile_frag(const T* tile, int f, int lane) {
-  using M = Mma<T, DP>;
-  return *(const typename M::Frag*)(tile + (lane & 31) * M::kPadRow + M::frag_channel(f, lane >> 5));
+template <int NB>
+__device__ __forceinline__ void make_nan(f32x16 (&acc)[NB], bool odd) {
+  if (__builtin_expect(__any(odd), 0)) {
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[blk][i] = odd ? __builtin_nanf("") : acc[blk][i];
+  }
 }
 
 // tanh(u).  Through e = exp(-2 |u|) as (1 - e) / (1 + e); near zero, where 1 - e cancels, fp32 scores take the odd
@@ -316,32 +408,74 @@ __device__ __forceinline__ int wave_max(int x) {
   return __builtin_amdgcn_readfirstlane(x);
 }
 
-// Distances between the lane's own point and the 16 moving points of its accumulator registers
-// (pos[axis][tile row] in LDS).
+// The outer sum moving value x own factor + moving factor x own value as one fp32 matrix instruction (contraction of
+// two: the half-waves hold the two terms).  With factors of 1 it is a sum of the two values, rounded once.
+__device__ __forceinline__ f32x16 outer_sum(float moving, float own) {
+  return __builtin_amdgcn_mfma_f32_32x32x2f32(moving, own, f32x16{}, 0, 0, 0);
+}
+
+// Distances between the lane's own point and the 16 moving points of its accumulator registers (pos[axis][tile row] in
+// LDS).  own[axis] is 1 in the lower half-wave and minus the own coordinate in the upper one: the differences come from
+// the matrix cores, which the vector-bound loops leave idle, and a moving coordinate is read once a lane instead of
+// four times 16 bytes.
 template <int N>
-__device__ __forceinline__ void distances(const float (*pos)[N], int at, int dims, const float (&own)[3], int h,
+__device__ __forceinline__ void distances(const float (*pos)[N], int at, int dims, const float (&own)[3], int lane,
                                           f32x16& d) {
+  const bool low = lane < 32;
+  const int r = at + (lane & 31);
+  d = outer_sum(low ? pos[0][r] : 1.0f, own[0]);
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int r = at + 8 * u + 4 * h;
-    f32x4 x = *(const f32x4*)&pos[0][r];
-    f32x4 y = *(const f32x4*)&pos[1][r];
+  for (int i = 0; i < 16; ++i) d[i] *= d[i];
+  if (dims > 1) {
+    const f32x16 e = outer_sum(low ? pos[1][r] : 1.0f, own[1]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float dx = x[j] - own[0], dy = y[j] - own[1];
-      d[4 * u + j] = fmaf(dx, dx, dy * dy);
-    }
-    if (dims > 2) {
-      f32x4 z = *(const f32x4*)&pos[2][r];
+    for (int i = 0; i < 16; ++i) d[i] = fmaf(e[i], e[i], d[i]);
+  }
+  if (dims > 2) {
+    const f32x16 e = outer_sum(low ? pos[2][r] : 1.0f, own[2]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float dz = z[j] - own[2];
-        d[4 * u + j] = fmaf(dz, dz, d[4 * u + j]);
-      }
-    }
+    for (int i = 0; i < 16; ++i) d[i] = fmaf(e[i], e[i], d[i]);
   }
 #pragma unroll
   for (int i = 0; i < 16; ++i) d[i] = __builtin_amdgcn_sqrtf(d[i]);
+}
+
+// The own operand of distances(): a point's coordinates, negated, in the upper half-wave.
+__device__ __forceinline__ void own_point(const float* p, int dims, int h, float (&own)[3]) {
+#pragma unroll
+  for (int ax = 0; ax < 3; ++ax) own[ax] = h == 0 ? 1.0f : (ax < dims ? -p[ax] : 0.0f);
+}
+
+// Scores are kept in a unit that costs the loop no multiplication: the raw products (a negative scale turns
+// the queries' sign) or the cap's tanh.  `unit` takes them to base-2 exponents, a slope is divided by `raw`.
+struct Unit {
+  float unit, raw, inv_cap;
+};
+
+__device__ __forceinline__ Unit make_unit(const AttnArgs& a) {
+  Unit u;
+  const float sc = fabsf(a.scale);
+  u.raw = a.cap > 0.0f ? a.cap : (sc > 0.0f ? sc : 1.0f);
+  u.unit = u.raw * kLog2e;
+  u.inv_cap = a.cap > 0.0f ? sc / a.cap : 0.0f;
+  return u;
+}
+
+// Queries in that unit's sign: negated for a negative scale, zero for a zero one.
+template <typename T, int DP>
+__device__ __forceinline__ void sign_row(const AttnArgs& a, typename Mma<T, DP>::Frag (&f)[Mma<T, DP>::kFrags]) {
+  if (a.scale > 0.0f) return;
+#pragma unroll
+  for (int i = 0; i < Mma<T, DP>::kFrags; ++i)
+#pragma unroll
+    for (int j = 0; j < Mma<T, DP>::kFragElems; ++j)
+      f[i][j] = a.scale < 0.0f ? (T)(-(float)f[i][j]) : (T)0.0f;
+}
+
+template <typename T>
+__device__ __forceinline__ void cap_scores(f32x16& s, float inv_cap) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s[i] = tanh_fast<sizeof(T) == 4>(s[i] * inv_cap);
 }
 
 }  // namespace fbev

@@ -13,160 +13,35 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <typename T, int DP, int KW>
+// HB heads of a wave (two with a distance bias, whose distances they share), KW waves over the keys of a
+// row tile (their sums are joined at the end), 4 / KW row tiles.
+template <typename T, int DP, int KW, int HB>
 struct Fwd {
   static constexpr int RW = 4 / KW;                       // row tiles of a workgroup
   static constexpr int KT = KW == 1 ? 64 : 32 * KW;       // keys staged at a time
-  static constexpr int kPad = Mma<T, DP>::kPadRow;
-  static constexpr size_t kTiles = (size_t)2 * KT * kPad * sizeof(T);
+  static constexpr size_t kTile = (size_t)KT * Tile<T, DP>::kRowBytes;
+  static constexpr size_t kTiles = 2 * HB * kTile;
   static constexpr size_t kMerge = (size_t)4 * 32 * (DP + 4) * 4 + 4 * 32 * 8;
   static constexpr size_t kBytes = KW == 1 || kTiles > kMerge ? kTiles : kMerge;
 };
 
-template <typename T, int DP, int KW>
-__global__ __launch_bounds__(kThreads) void attn_fwd(AttnArgs a, int tiles) {
-  using C = Fwd<T, DP, KW>;
-  using M = Mma<T, DP>;
-  constexpr int NB = DP / 32, KT = C::KT, RW = C::RW;
-  __shared__ alignas(16) char smem[C::kBytes];
-  __shared__ alignas(16) float pos[3][KT];
-  __shared__ alignas(16) int docs[KT];
-  __shared__ int doc_range[4][2];
-  T* Ks = (T*)smem;
-  T* Vs = Ks + KT * C::kPad;
+template <typename T, int DP>
+constexpr int min_waves(int hb) {
+  return sizeof(T) == 4 || DP > 64 ? 1 : DP == 64 || hb == 2 ? 3 : 4;
+}
 
-  const int bid = xcd_block(blockIdx.x, gridDim.x);
-  const int split = bid % a.splits, tile = bid / a.splits % tiles, bh = bid / a.splits / tiles;
-  const int b = bh / a.Hk, hk = bh - b * a.Hk;
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 31, h = lane >> 5;
-  const int rw = wave / KW, kw = wave - rw * KW;
-  const int first = tile * 32 * RW + rw * 32;            // the wave's rows
-  const Row w = make_row(a, b, hk, min(first + n, a.R - 1));
-  typename M::Frag q[M::kFrags];
-  load_row<T, DP>((const T*)a.q + b * a.qs[0] + w.t * a.qs[1] + w.head * a.qs[2], true, a.vec, a.D, h, q);
-
-  float own[3] = {0.0f, 0.0f, 0.0f}, slope2 = 0.0f;
-  if (a.dims) {
-    for (int ax = 0; ax < a.dims; ++ax) own[ax] = a.pos_q[((int64_t)b * a.Tq + w.t) * a.dims + ax];
-    slope2 = a.slope[((int64_t)b * a.Tq + w.t) * a.Hq + w.head] * kLog2e;
-  }
-  for (int e = threadIdx.x; e < KT; e += kThreads) pos[0][e] = pos[1][e] = pos[2][e] = 0.0f, docs[e] = 0;
-  // the keys the workgroup's and the wave's rows can see by order
-  const int lim_lo = row_limit(a, b, min(first, a.R - 1) / a.G);
-  const int lim_hi = row_limit(a, b, min(first + 31, a.R - 1) / a.G);
-  const int blk_hi = row_limit(a, b, min(tile * 32 * RW + 32 * RW - 1, a.R - 1) / a.G);
-  int dmin = 0, dmax = 0, bmin = 0, bmax = 0;
-  if (a.doc_q) {
-    dmin = wave_min(w.doc < 0 ? INT32_MAX : w.doc);
-    dmax = wave_max(w.doc);
-    if (lane == 0) doc_range[wave][0] = dmin, doc_range[wave][1] = dmax;
-    __syncthreads();
-    bmin = min(min(doc_range[0][0], doc_range[1][0]), min(doc_range[2][0], doc_range[3][0]));
-    bmax = max(max(doc_range[0][1], doc_range[1][1]), max(doc_range[2][1], doc_range[3][1]));
-  }
-  const bool one_doc = dmin == dmax && wave_min(w.doc) == dmin;   // every row of the wave in one document
-
-  f32x16 acc[NB] = {};
-  float m = kNegInf, l = 0.0f;
-  const float c1 = a.scale * kLog2e, inv_cap = a.cap > 0.0f ? a.scale / a.cap : 0.0f, c0 = a.cap * kLog2e;
-  const int k_begin = split * a.split_keys;
-  const int k_end = min(min(a.Tk, blk_hi + 1), (split + 1) * a.split_keys);
-  for (int s0 = k_begin; s0 < k_end; s0 += KT) {
-    const int nk = min(KT, a.Tk - s0);
-    int my_doc = -1;
-    if (a.doc_q) {
-      if ((int)threadIdx.x < nk) my_doc = a.doc_k[(int64_t)b * a.Tk + s0 + threadIdx.x];
-      if (!__syncthreads_or(my_doc >= bmin && my_doc <= bmax)) continue;
-    } else {
-      __syncthreads();
-    }
-    stage_rows<T, DP, KT, kThreads>(Ks, nk, a.vec, a.D, [&](int r) {
-      return (const T*)a.k + b * a.ks[0] + (int64_t)(s0 + r) * a.ks[1] + hk * a.ks[2];
-    });
-    stage_rows<T, DP, KT, kThreads>(Vs, nk, a.vec, a.D, [&](int r) {
-      return (const T*)a.v + b * a.vs[0] + (int64_t)(s0 + r) * a.vs[1] + hk * a.vs[2];
-    });
-    if ((int)threadIdx.x < KT) {
-      if (a.doc_q) docs[threadIdx.x] = my_doc;
-      if (a.dims && (int)threadIdx.x < nk)
-        for (int ax = 0; ax < a.dims; ++ax)
-          pos[ax][threadIdx.x] = a.pos_k[((int64_t)b * a.Tk + s0 + threadIdx.x) * a.dims + ax];
-    }
-    __syncthreads();
-#pragma unroll 1
-    for (int at = 32 * kw; at < KT; at += 32 * KW) {
-      const int key0 = s0 + at;
-      if (key0 > lim_hi || key0 >= a.Tk) continue;
-      bool whole = key0 + 31 <= lim_lo;
-      if (a.doc_q) {
-        const int d = docs[at + n];
-        if (!__any(d >= dmin && d <= dmax)) continue;
-        whole = whole && one_doc && __all(d == dmin);
-      }
-      const T* kt = Ks + at * C::kPad;
-      const T* vt = Vs + at * C::kPad;
-      f32x16 s = {};
-#pragma unroll
-      for (int f = 0; f < M::kFrags; ++f) s = M::dot(tile_frag<T, DP>(kt, f, lane), q[f], s);
-      if (a.cap > 0.0f) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = c0 * tanh_fast<sizeof(T) == 4>(s[i] * inv_cap);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] *= c1;
-      }
-      if (a.dims) {
-        f32x16 d;
-        distances<KT>(pos, at, a.dims, own, h, d);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = fmaf(-slope2, d[i], s[i]);
-      }
-      f32x16 seen;
-      if (!whole) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int kr = acc_row(i, h);
-          const bool vis = key0 + kr <= w.lim && docs[at + kr] == w.doc;
-          seen[i] = vis ? 1.0f : 0.0f;
-          s[i] = vis ? s[i] : kNegInf;
-        }
-      }
-      float top = s[0];
-#pragma unroll
-      for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
-      top = pair_max(top);
-      // the maximum is only moved when some row's grew by more than 2^8: sums and products stay in range
-      if (__any(top > m + 8.0f)) {
-        const float m2 = fmaxf(m, top);
-        const float f = m2 == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - m2);
-        m = m2;
-        l *= f;
-#pragma unroll
-        for (int blk = 0; blk < NB; ++blk)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) acc[blk][i] *= f;
-      }
-      const float base = m == kNegInf ? 0.0f : m;
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[i] = __builtin_amdgcn_exp2f(s[i] - base);
-        sum += s[i];
-      }
-      l += sum;
-      if (whole)
-        M::template accumulate<NB>(acc, M::pack(s), vt, lane);
-      else
-        M::template accumulate_masked<NB>(acc, M::pack(s), M::pack(seen), vt, lane);
-    }
-  }
-  l = pair_sum(l);
-
+// Writes a head's rows (or their split's partial rows); the KW waves of a tile add up their parts first.
+template <typename T, int DP, int KW, int HB>
+__device__ __forceinline__ void finish(const AttnArgs& a, const Row& w, int first, int split, int64_t bh, int hd, int kw,
+                                       int lane, f32x16 (&acc)[DP / 32], float m, float l, char* smem) {
+  constexpr int NB = DP / 32;
+  const int n = lane & 31, h = lane >> 5, head = w.head + hd;
+  const int b = (int)(bh / a.Hk), hk = (int)(bh - (int64_t)b * a.Hk);
   const bool part = a.splits > 1;
   if constexpr (KW == 1) {
     if (first + n < a.R) {
       float* po = part ? a.part + (((int64_t)split * a.B * a.Hk + bh) * a.R + w.r) * (a.D + 2) : nullptr;
-      T* out = (T*)a.out + (((int64_t)b * a.Tq + w.t) * a.Hq + w.head) * a.D;
+      T* out = (T*)a.out + (((int64_t)b * a.Tq + w.t) * a.Hq + head) * a.D;
       const float inv = part ? 1.0f : (l > 0.0f || l != l ? 1.0f / l : 0.0f);
 #pragma unroll
       for (int blk = 0; blk < NB; ++blk)
@@ -194,7 +69,7 @@ __global__ __launch_bounds__(kThreads) void attn_fwd(AttnArgs a, int tiles) {
         if (part)
           po[a.D] = m, po[a.D + 1] = l;
         else
-          a.lse[((int64_t)b * a.Hq + w.head) * a.Tq + w.t] = l == 0.0f ? kNegInf : m * kLn2 + logf(l);
+          a.lse[((int64_t)b * a.Hq + head) * a.Tq + w.t] = l == 0.0f ? kNegInf : m * kLn2 + logf(l);
       }
     }
   } else {
@@ -228,7 +103,7 @@ __global__ __launch_bounds__(kThreads) void attn_fwd(AttnArgs a, int tiles) {
         float* po = a.part + (((int64_t)split * a.B * a.Hk + bh) * a.R + w.r) * (a.D + 2);
         po[a.D] = top, po[a.D + 1] = tot;
       } else {
-        a.lse[((int64_t)b * a.Hq + w.head) * a.Tq + w.t] = tot == 0.0f ? kNegInf : top * kLn2 + logf(tot);
+        a.lse[((int64_t)b * a.Hq + head) * a.Tq + w.t] = tot == 0.0f ? kNegInf : top * kLn2 + logf(tot);
       }
     }
     __syncthreads();
@@ -241,12 +116,186 @@ __global__ __launch_bounds__(kThreads) void attn_fwd(AttnArgs a, int tiles) {
       float o = 0.0f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) o += mo[(k * 32 + r) * (DP + 4) + c];
-      const int row = first + r, t = row / a.G, head = hk * a.G + (row - t * a.G);
+      const int row = first + r, t = row / a.G, hh = hk * a.G + (row - t * a.G);
       if (part)
         a.part[(((int64_t)split * a.B * a.Hk + bh) * a.R + row) * (a.D + 2) + c] = o;
       else
-        ((T*)a.out)[(((int64_t)b * a.Tq + t) * a.Hq + head) * a.D + c] = (T)(o * ml[r * 2]);
+        ((T*)a.out)[(((int64_t)b * a.Tq + t) * a.Hq + hh) * a.D + c] = (T)(o * ml[r * 2]);
     }
+  }
+}
+
+template <typename T, int DP, int KW, int HB, bool BIAS>
+__global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_fwd(AttnArgs a,
+                                                                                                   int tiles) {
+  using C = Fwd<T, DP, KW, HB>;
+  using M = Mma<T, DP>;
+  constexpr int NB = DP / 32, KT = C::KT, RW = C::RW;
+  __shared__ alignas(16) char smem[C::kBytes];
+  __shared__ alignas(16) float pos[BIAS ? 3 : 1][KT];
+  __shared__ alignas(16) int docs[KT];
+  __shared__ int doc_range[4][2];
+  char* Ks = smem;                                        // HB tiles each
+  char* Vs = smem + HB * C::kTile;
+
+  const int bid = xcd_block(blockIdx.x, gridDim.x);
+  const int split = bid % a.splits, tile = bid / a.splits % tiles, bh = bid / a.splits / tiles;
+  const int b = bh / (a.Hk / HB), hk = (bh - b * (a.Hk / HB)) * HB;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 31, h = lane >> 5;
+  const int rw = wave / KW, kw = wave - rw * KW;
+  const int first = tile * 32 * RW + rw * 32;            // the wave's rows
+  const Row w = make_row(a, b, hk, min(first + n, a.R - 1));
+  const Unit un = make_unit(a);
+  typename M::Frag q[HB][M::kFrags];
+#pragma unroll
+  for (int i = 0; i < HB; ++i) {
+    load_row<T, DP>((const T*)a.q + b * a.qs[0] + w.t * a.qs[1] + (w.head + i) * a.qs[2], a.vec, a.D, h, q[i]);
+    sign_row<T, DP>(a, q[i]);
+  }
+
+  float own[3] = {0.0f, 0.0f, 0.0f}, slope[HB] = {};
+  if constexpr (BIAS) {
+    own_point(a.pos_q + ((int64_t)b * a.Tq + w.t) * a.dims, a.dims, h, own);
+#pragma unroll
+    for (int i = 0; i < HB; ++i) slope[i] = a.slope[((int64_t)b * a.Tq + w.t) * a.Hq + w.head + i] / un.raw;
+    for (int e = threadIdx.x; e < 3 * KT; e += kThreads) pos[0][e] = 0.0f;
+  }
+  for (int e = threadIdx.x; e < KT; e += kThreads) docs[e] = 0;
+  // the keys the workgroup's and the wave's rows can see by order
+  const int lim_lo = row_limit(a, b, min(first, a.R - 1) / a.G);
+  const int lim_hi = row_limit(a, b, min(first + 31, a.R - 1) / a.G);
+  const int blk_lo = row_limit(a, b, min(tile * 32 * RW, a.R - 1) / a.G);
+  const int blk_hi = row_limit(a, b, min(tile * 32 * RW + 32 * RW - 1, a.R - 1) / a.G);
+  int dmin = 0, dmax = 0, bmin = 0, bmax = 0;
+  if (a.doc_q) {
+    dmin = wave_min(w.doc < 0 ? INT32_MAX : w.doc);
+    dmax = wave_max(w.doc);
+    if (lane == 0) doc_range[wave][0] = dmin, doc_range[wave][1] = dmax;
+    __syncthreads();
+    bmin = min(min(doc_range[0][0], doc_range[1][0]), min(doc_range[2][0], doc_range[3][0]));
+    bmax = max(max(doc_range[0][1], doc_range[1][1]), max(doc_range[2][1], doc_range[3][1]));
+  }
+  const bool one_doc = dmin == dmax && wave_min(w.doc) == dmin;   // every row of the wave in one document
+
+  f32x16 acc[HB][NB] = {};
+  uint32_t odd[HB][NB] = {};
+  float m[HB], l[HB];
+#pragma unroll
+  for (int i = 0; i < HB; ++i) m[i] = kNegInf, l[i] = 0.0f;
+  const int k_begin = split * a.split_keys;
+  const int k_end = min(min(a.Tk, blk_hi + 1), (split + 1) * a.split_keys);
+  for (int s0 = k_begin; s0 < k_end; s0 += KT) {
+    const int nk = min(KT, a.Tk - s0);
+    int my_doc = -1;
+    if (a.doc_q) {
+      if ((int)threadIdx.x < nk) my_doc = a.doc_k[(int64_t)b * a.Tk + s0 + threadIdx.x];
+      if (!__syncthreads_or(my_doc >= bmin && my_doc <= bmax)) continue;
+    } else {
+      __syncthreads();
+    }
+    // some row of the workgroup may not see some key
+    const bool mixed = a.doc_q != nullptr || (a.causal && s0 + KT - 1 > blk_lo);
+#pragma unroll
+    for (int i = 0; i < HB; ++i) {
+      stage_rows<T, DP, KT>(Ks + i * C::kTile, (const T*)a.k + b * a.ks[0] + s0 * a.ks[1] + (hk + i) * a.ks[2], a.ks[1],
+                            nk, a.vec, a.D);
+      stage_rows<T, DP, KT>(Vs + i * C::kTile, (const T*)a.v + b * a.vs[0] + s0 * a.vs[1] + (hk + i) * a.vs[2], a.vs[1],
+                            nk, a.vec, a.D);
+    }
+    if ((int)threadIdx.x < KT) {
+      if (a.doc_q) docs[threadIdx.x] = my_doc;
+      if constexpr (BIAS) {
+        if ((int)threadIdx.x < nk)
+          for (int ax = 0; ax < a.dims; ++ax)
+            pos[ax][threadIdx.x] = a.pos_k[((int64_t)b * a.Tk + s0 + threadIdx.x) * a.dims + ax];
+      }
+    }
+    // which of the tile's keys (16 of the lane's half) the lane's row sees
+    auto visible = [&](int at) {
+      uint32_t vis = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int kr = at + acc_row(i, h);
+        vis |= (s0 + kr <= w.lim && docs[kr] == w.doc) ? 1u << i : 0u;
+      }
+      return vis;
+    };
+    wait_staged();
+    __syncthreads();
+    if (mixed && __builtin_expect(__syncthreads_or(holds_odd<T, DP, HB * KT>(Vs)), 0)) {
+#pragma unroll 1
+      for (int at = 32 * kw; at < KT; at += 32 * KW) {
+        const uint32_t vis = visible(at);
+#pragma unroll
+        for (int hd = 0; hd < HB; ++hd)
+#pragma unroll
+          for (int blk = 0; blk < NB; ++blk) odd[hd][blk] |= find_odd<T, DP>(Vs + hd * C::kTile, at, blk, vis, lane);
+      }
+      __syncthreads();
+      clean_rows<T, DP, HB * KT>(Vs);
+      __syncthreads();
+    }
+#pragma unroll 1
+    for (int at = 32 * kw; at < KT; at += 32 * KW) {
+      const int key0 = s0 + at;
+      if (key0 > lim_hi || key0 >= a.Tk) continue;
+      bool whole = key0 + 31 <= lim_lo;
+      if (a.doc_q) {
+        const int d = docs[at + n];
+        if (!__any(d >= dmin && d <= dmax)) continue;
+        whole = whole && one_doc && __all(d == dmin);
+      }
+      const uint32_t vis = whole ? 0xFFFFu : visible(at);
+      f32x16 d;
+      if constexpr (BIAS) distances<KT>(pos, at, a.dims, own, lane, d);
+#pragma unroll
+      for (int hd = 0; hd < HB; ++hd) {
+        __builtin_amdgcn_sched_barrier(0);      // one head's registers at a time
+        f32x16 s = tile_dot<T, DP>(Ks + hd * C::kTile, at, q[hd], lane);
+        if (a.cap > 0.0f) cap_scores<T>(s, un.inv_cap);
+        if constexpr (BIAS) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[i] = fmaf(-slope[hd], d[i], s[i]);
+        }
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[i] = (vis >> i) & 1 ? s[i] : kNegInf;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        float top = fmaxf(s[0], s[1]);
+#pragma unroll
+        for (int i = 2; i < 16; i += 2) top = fmaxf(fmaxf(top, s[i]), s[i + 1]);
+        top = pair_max(top) * un.unit;
+        // the maximum is only moved when some row's grew by more than 2^8: sums and products stay in range
+        if (__any(top > m[hd] + 8.0f)) {
+          const float m2 = fmaxf(m[hd], top);
+          const float f = m2 == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[hd] - m2);
+          m[hd] = m2;
+          l[hd] *= f;
+#pragma unroll
+          for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[hd][blk][i] *= f;
+        }
+        const float base = m[hd] == kNegInf ? 0.0f : -m[hd];
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], un.unit, base));
+          sum += s[i];
+        }
+        l[hd] += sum;
+        __builtin_amdgcn_sched_barrier(0);
+        M::template accumulate<NB>(acc[hd], M::pack(s), Vs + hd * C::kTile, at, lane);
+      }
+    }
+  }
+
+#pragma unroll
+  for (int hd = 0; hd < HB; ++hd) {
+    add_odd<NB>(acc[hd], odd[hd]);
+    finish<T, DP, KW, HB>(a, w, first, split, (int64_t)b * a.Hk + hk + hd, hd, kw, lane, acc[hd], m[hd],
+                          pair_sum(l[hd]), smem);
   }
 }
 
@@ -281,17 +330,19 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
 }
 
 struct Plan {
-  int kw, tiles, splits, split_keys;
+  int kw, hb, tiles, splits, split_keys;
 };
 
 Plan make_plan(const AttnArgs& a) {
   Plan p;
   const int64_t bh = (int64_t)a.B * a.Hk;
-  // row tiles that share staged keys when they fill the card (two workgroups a CU), else keys over the waves
-  p.kw = bh * ((a.R + 127) / 128) >= 512 ? 1 : 4;
+  // two heads a wave where they share the distances and there are enough of them to fill the card
+  p.hb = a.dims > 0 && a.G == 1 && a.Hk % 2 == 0 && a.D <= 32 && bh * ((a.R + 31) / 32) >= 1024 ? 2 : 1;
+  // row tiles that share staged keys when they fill the card several times over, else keys over the waves
+  p.kw = bh / p.hb * ((a.R + 127) / 128) >= (a.D <= 64 ? 2048 : 512) ? 1 : 4;
   const int rows = 32 * (4 / p.kw), kt = p.kw == 1 ? 64 : 128;
   p.tiles = (a.R + rows - 1) / rows;
-  const int64_t blocks = bh * p.tiles;
+  const int64_t blocks = bh / p.hb * p.tiles;
   p.splits = 1;
   if (blocks < 256) {
     int64_t want = (1024 + blocks - 1) / blocks;
@@ -306,13 +357,24 @@ Plan make_plan(const AttnArgs& a) {
   return p;
 }
 
+template <typename T, int DP, int HB, bool BIAS>
+void launch(const AttnArgs& a, const Plan& p, hipStream_t stream) {
+  const dim3 grid((unsigned)((int64_t)a.B * a.Hk / HB * p.tiles * p.splits));
+  if (p.kw == 1)
+    attn_fwd<T, DP, 1, HB, BIAS><<<grid, kThreads, 0, stream>>>(a, p.tiles);
+  else
+    attn_fwd<T, DP, 4, HB, BIAS><<<grid, kThreads, 0, stream>>>(a, p.tiles);
+}
+
 template <typename T, int DP>
 hipError_t run(AttnArgs& a, const Plan& p, hipStream_t stream) {
-  const dim3 grid((unsigned)((int64_t)a.B * a.Hk * p.tiles * p.splits));
-  if (p.kw == 1)
-    attn_fwd<T, DP, 1><<<grid, kThreads, 0, stream>>>(a, p.tiles);
-  else
-    attn_fwd<T, DP, 4><<<grid, kThreads, 0, stream>>>(a, p.tiles);
+  if (a.dims == 0) {
+    launch<T, DP, 1, false>(a, p, stream);
+  } else if (p.hb == 1) {
+    launch<T, DP, 1, true>(a, p, stream);
+  } else {
+    if constexpr (DP == 32) launch<T, DP, 2, true>(a, p, stream);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   const int64_t rows = (int64_t)a.B * a.Hk * a.R;

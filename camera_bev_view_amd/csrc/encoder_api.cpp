@@ -210,8 +210,11 @@ fbev_status check_attention_data(fbev::AttnArgs& a, const void* q, const void* k
   a.v = v;
   a.elem_bytes = dtype == FBEV_DTYPE_F32 ? 4 : 2;
   const int e = 16 / a.elem_bytes;
-  a.vec = aligned(q, 16) && aligned(k, 16) && aligned(v, 16);
+  a.vec = a.D % e == 0 && aligned(q, 16) && aligned(k, 16) && aligned(v, 16);
   const int nq[3] = {a.B, a.Tq, a.Hq}, nk[3] = {a.B, a.Tk, a.Hk};
+  // a staged tile (128 tokens, all heads of a group) is addressed with 31 bits
+  const int64_t far = ((int64_t)1 << 30) / (128 * a.elem_bytes);
+  a.vec = a.vec && a.qs[1] < far && a.ks[1] < far && a.vs[1] < far && a.qs[2] < far / a.G * 64;
   for (int i = 0; i < 3; ++i) {
     a.vec = a.vec && (nq[i] <= 1 || a.qs[i] % e == 0);
     a.vec = a.vec && (nk[i] <= 1 || (a.ks[i] % e == 0 && a.vs[i] % e == 0));
@@ -363,7 +366,7 @@ fbev_status fbev_attention_backward(const void* grad_out, const void* q, const v
     return fail(FBEV_ERR_INVALID_ARGUMENT, "grad_slope without a distance bias (dims=0)");
   s = check_workspace(workspace, workspace_bytes, rows ? fbev::attention_backward_workspace_bytes(a) : 0);
   if (s != FBEV_OK) return s;
-  a.vec = a.vec && a.D % (16 / a.elem_bytes) == 0 && aligned(out, 16) && aligned(grad_out, 16);
+  a.vec = a.vec && (int64_t)a.Hq * a.D < ((int64_t)1 << 30) / (128 * a.elem_bytes) && aligned(out, 16) && aligned(grad_out, 16);
   a.vec_out = a.D % 4 == 0 && aligned(grad_q, 4 * a.elem_bytes) && aligned(grad_k, 4 * a.elem_bytes) &&
               aligned(grad_v, 4 * a.elem_bytes);
   a.gout = grad_out;
