@@ -81,6 +81,8 @@ _lib = None
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Open libflashbev.so once and declare its signatures."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

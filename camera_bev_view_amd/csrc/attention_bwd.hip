@@ -29,7 +29,7 @@ struct Bwd {
 
 template <typename T, int DP>
 constexpr int min_waves(int hb) {
-  return sizeof(T) == 4 || DP > 32 ? 1 : hb == 2 ? 2 : 3;
+  return sizeof(T) == 4 || DP > 32 ? 1 : hb == 2 ? 2 : 4;
 }
 
 // Writes own rows' sums (scaled), or adds the four waves' sums over LDS first.  dst(n) is own row n's
@@ -85,6 +85,19 @@ __device__ __forceinline__ void write_own(f32x16 (&acc)[DP / 32], float scale, f
   }
 }
 
+// A (sample, key head)'s rows in the workspace: delta and lse, with a bias slope and position (lse and slope in score
+// units).
+struct RowStats {
+  float *delta, *lse, *slope, *pos;
+};
+
+__host__ __device__ __forceinline__ int64_t stat_floats(const AttnArgs& a) { return a.dims ? 3 + a.dims : 2; }
+
+__device__ __forceinline__ RowStats row_stats(const AttnArgs& a, int64_t bh) {
+  float* p = a.delta + bh * a.R * stat_floats(a);
+  return RowStats{p, p + a.R, p + 2 * (int64_t)a.R, p + 3 * (int64_t)a.R};
+}
+
 // ---- query rows: delta, gq, gslope
 
 template <typename T, int DP, int KW, int HB, bool BIAS, bool CAP>
@@ -93,7 +106,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_row
   using M = Mma<T, DP>;
   constexpr int NB = DP / 32, MT = C::MT, RW = C::RW;
   __shared__ alignas(16) char smem[C::kBytes];
-  __shared__ alignas(16) float pos[BIAS ? 3 : 1][MT];
+  __shared__ alignas(16) float pos[BIAS ? 3 * MT : 1];   // [key][axis]
   __shared__ alignas(16) int docs[MT];
   __shared__ int doc_range[4][2];
   __shared__ float slopes[KW > 1 && BIAS ? 4 : 1][3][32];
@@ -124,16 +137,25 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_row
 #pragma unroll
       for (int j = 0; j < M::kFragElems; ++j) sum = fmaf((float)go[i][f][j], (float)o[f][j], sum);
     delta[i] = pair_sum(sum);
-    const int64_t stat_at = ((int64_t)b * a.Hq + w.head + i) * a.Tq + w.t;
-    if (kw == 0 && h == 0 && first + n < a.R) a.delta[stat_at] = delta[i];
-    lse2[i] = a.lse[stat_at] * kLog2e;
-    if (lse2[i] == kNegInf) lse2[i] = -kNegInf;           // a row without weights: all p are 0
+    float lse = a.lse[((int64_t)b * a.Hq + w.head + i) * a.Tq + w.t];
+    if (lse == kNegInf) lse = -kNegInf;                   // a row without weights: all p are 0
+    lse2[i] = lse * kLog2e;
     if constexpr (BIAS) slope[i] = a.slope[((int64_t)b * a.Tq + w.t) * a.Hq + w.head + i] / un.raw;
+    // what the keys' launch needs of its moving rows, in the order it walks them
+    if (kw == 0 && h == 0 && first + n < a.R) {
+      const RowStats st = row_stats(a, (int64_t)b * a.Hk + hk + i);
+      st.delta[w.r] = delta[i];
+      st.lse[w.r] = CAP ? lse2[i] : lse / un.raw;
+      if constexpr (BIAS) {
+        st.slope[w.r] = slope[i];
+        for (int ax = 0; ax < a.dims; ++ax)
+          st.pos[(int64_t)w.r * a.dims + ax] = a.pos_q[((int64_t)b * a.Tq + w.t) * a.dims + ax];
+      }
+    }
   }
   float own[3] = {0.0f, 0.0f, 0.0f};
   if constexpr (BIAS) {
     own_point(a.pos_q + ((int64_t)b * a.Tq + w.t) * a.dims, a.dims, h, own);
-    for (int e = threadIdx.x; e < 3 * MT; e += kThreads) pos[0][e] = 0.0f;
   }
   for (int e = threadIdx.x; e < MT; e += kThreads) docs[e] = 0;
   const int lim_lo = row_limit(a, b, min(first, a.R - 1) / a.G);
@@ -172,20 +194,15 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_row
       stage_rows<T, DP, MT>(Vs + i * C::kTile, (const T*)a.v + b * a.vs[0] + s0 * a.vs[1] + (hk + i) * a.vs[2], a.vs[1],
                             nk, a.vec, a.D);
     }
-    if ((int)threadIdx.x < MT) {
-      if (a.doc_q) docs[threadIdx.x] = my_doc;
-      if constexpr (BIAS) {
-        if ((int)threadIdx.x < nk)
-          for (int ax = 0; ax < a.dims; ++ax)
-            pos[ax][threadIdx.x] = a.pos_k[((int64_t)b * a.Tk + s0 + threadIdx.x) * a.dims + ax];
-      }
-    }
+    if (a.doc_q && (int)threadIdx.x < MT) docs[threadIdx.x] = my_doc;
+    if constexpr (BIAS) stage_floats(pos, a.pos_k + ((int64_t)b * a.Tk + s0) * a.dims, nk * a.dims, MT * a.dims);
     auto visible = [&](int at) {
       uint32_t vis = 0;
+      const int hh = (int)opaque(h);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int kr = at + acc_row(i, h);
-        vis |= (s0 + kr <= w.lim && docs[kr] == w.doc) ? 1u << i : 0u;
+      for (int i = 15; i >= 0; --i) {
+        const int kr = at + acc_row(i, hh);
+        vis = 2 * vis + (s0 + kr <= w.lim && docs[kr] == w.doc ? 1u : 0u);
       }
       return vis;
     };
@@ -212,11 +229,12 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_row
         if (!__any(d >= dmin && d <= dmax)) continue;
         whole = whole && one_doc && __all(d == dmin);
       }
-      const uint32_t vis = whole ? 0xFFFFu : visible(at);
+      const uint32_t seen = whole ? 0xFFFFu : visible(at);
       f32x16 d;
-      if constexpr (BIAS) distances<MT>(pos, at, a.dims, own, lane, d);
+      if constexpr (BIAS) distances(pos, at, a.dims, own, lane, d);
       if constexpr (BIAS) {
         if (!whole) {
+          const uint32_t vis = opaque(seen);
 #pragma unroll
           for (int i = 0; i < 16; ++i) d[i] = (vis >> i) & 1 ? d[i] : 0.0f;
         }
@@ -239,6 +257,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_row
           for (int i = 0; i < 16; ++i) s[i] = fmaf(-slope[hd], d[i], s[i]);
         }
         if (!whole) {
+          const uint32_t vis = opaque(seen);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             s[i] = (vis >> i) & 1 ? s[i] : kNegInf;
@@ -255,10 +274,16 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_row
             sum_pd[hd] = fmaf(p, d[i], sum_pd[hd]);
           }
         }
+        if constexpr (BIAS) {
+          pin(sum_ds[hd]);
+          pin(sum_dsd[hd]);
+          pin(sum_pd[hd]);
+        }
         if constexpr (CAP) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) s[i] = whole || (vis >> i) & 1 ? s[i] * fmaf(-th[i], th[i], 1.0f) : 0.0f;
+          for (int i = 0; i < 16; ++i) s[i] = whole || (seen >> i) & 1 ? s[i] * fmaf(-th[i], th[i], 1.0f) : 0.0f;
         }
+        __builtin_amdgcn_sched_barrier(0);
         M::template accumulate<NB>(acc[hd], M::pack(s), kt, at, lane);
       }
     }
@@ -301,7 +326,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_key
   using M = Mma<T, DP>;
   constexpr int NB = DP / 32, MT = C::MT, RW = C::RW;
   __shared__ alignas(16) char smem[C::kBytes];
-  __shared__ alignas(16) float pos[BIAS ? 3 : 1][MT];
+  __shared__ alignas(16) float pos[BIAS ? 3 * MT : 1];   // [row][axis]
   __shared__ alignas(16) float lse2s[HB][MT], deltas[HB][MT], slopes[HB][BIAS ? MT : 4];
   __shared__ alignas(16) int docs[MT], lims[MT];
   __shared__ int doc_range[4][2];
@@ -326,8 +351,6 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_key
   float own[3] = {0.0f, 0.0f, 0.0f};
   if constexpr (BIAS) {
     own_point(a.pos_k + ((int64_t)b * a.Tk + key) * a.dims, a.dims, h, own);
-    for (int e = threadIdx.x; e < 3 * MT; e += kThreads) pos[0][e] = 0.0f;
-    for (int e = threadIdx.x; e < HB * MT; e += kThreads) slopes[0][e] = 0.0f;
   }
   const int doc = a.doc_k ? a.doc_k[(int64_t)b * a.Tk + key] : 0;
   int dmin = 0, dmax = 0, bmin = 0, bmax = 0;
@@ -354,8 +377,10 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_key
   for (int s0 = r_begin; s0 < a.R; s0 += MT) {
     const int nr = min(MT, a.R - s0);
     Row w;
-    w.doc = -1, w.lim = -1, w.t = 0, w.head = 0;
-    if ((int)threadIdx.x < nr) w = make_row(a, b, hk, s0 + threadIdx.x);
+    w.doc = -1, w.lim = -1;
+    if (a.causal || a.doc_q) {
+      if ((int)threadIdx.x < nr) w = make_row(a, b, hk, s0 + threadIdx.x);
+    }
     if (a.doc_q) {
       if (!__syncthreads_or(w.doc >= bmin && w.doc <= bmax)) continue;
     } else {
@@ -378,34 +403,27 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_key
                                a.D, s0, a.G, nr, a.vec, a.D);
       }
     }
-    if ((int)threadIdx.x < MT) {
+    if ((a.causal || a.doc_q) && (int)threadIdx.x < MT) {
       docs[threadIdx.x] = w.doc;
       lims[threadIdx.x] = w.lim;
+    }
 #pragma unroll
-      for (int i = 0; i < HB; ++i) {
-        float l2 = -kNegInf, dl = 0.0f;
-        if ((int)threadIdx.x < nr) {
-          const int64_t at = ((int64_t)b * a.Hq + w.head + i) * a.Tq + w.t;
-          const float x = CAP ? a.lse[at] * kLog2e : a.lse[at] / un.raw;
-          l2 = x == kNegInf ? -kNegInf : x;
-          dl = a.delta[at];
-          if constexpr (BIAS)
-            slopes[i][threadIdx.x] = a.slope[((int64_t)b * a.Tq + w.t) * a.Hq + w.head + i] / un.raw;
-        }
-        lse2s[i][threadIdx.x] = l2;
-        deltas[i][threadIdx.x] = dl;
-      }
+    for (int i = 0; i < HB; ++i) {
+      const RowStats st = row_stats(a, (int64_t)b * a.Hk + hk + i);
+      stage_floats(lse2s[i], st.lse + s0, nr, MT);
+      stage_floats(deltas[i], st.delta + s0, nr, MT);
       if constexpr (BIAS) {
-        if ((int)threadIdx.x < nr)
-          for (int ax = 0; ax < a.dims; ++ax) pos[ax][threadIdx.x] = a.pos_q[((int64_t)b * a.Tq + w.t) * a.dims + ax];
+        stage_floats(slopes[i], st.slope + s0, nr, MT);
+        if (i == 0) stage_floats(pos, st.pos + (int64_t)s0 * a.dims, nr * a.dims, MT * a.dims);
       }
     }
     auto visible = [&](int at) {
       uint32_t vis = 0;
+      const int hh = (int)opaque(h);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int r = at + acc_row(i, h);
-        vis |= (key0 + n <= lims[r] && docs[r] == doc) ? 1u << i : 0u;
+      for (int i = 15; i >= 0; --i) {
+        const int r = at + acc_row(i, hh);
+        vis = 2 * vis + (key0 + n <= lims[r] && docs[r] == doc ? 1u : 0u);
       }
       return vis;
     };
@@ -431,17 +449,20 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_key
 #pragma unroll 1
     for (int at = 32 * kw; at < MT; at += 32 * KW) {
       if (s0 + at >= a.R) continue;
-      const int lim = s0 + at + n < a.R ? lims[at + n] : INT32_MAX;
-      if (!__any(lim != INT32_MAX && lim >= key0)) continue;
-      bool whole = __all(lim >= min(key0 + 31, a.Tk - 1));
+      bool whole = true;
+      if (a.causal || a.doc_q) {
+        const int lim = s0 + at + n < a.R ? lims[at + n] : INT32_MAX;
+        if (!__any(lim != INT32_MAX && lim >= key0)) continue;
+        whole = __all(lim >= min(key0 + 31, a.Tk - 1));
+      }
       if (a.doc_q) {
         const int d = docs[at + n];
         if (!__any(d >= dmin && d <= dmax)) continue;
         whole = whole && one_doc && __all(d == dmin);
       }
-      const uint32_t vis = whole ? 0xFFFFu : visible(at);
+      const uint32_t seen = whole ? 0xFFFFu : visible(at);
       f32x16 d;
-      if constexpr (BIAS) distances<MT>(pos, at, a.dims, own, lane, d);
+      if constexpr (BIAS) distances(pos, at, a.dims, own, lane, d);
 #pragma unroll
       for (int hd = 0; hd < HB; ++hd) {
         __builtin_amdgcn_sched_barrier(0);                // one head's registers at a time
@@ -473,6 +494,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_key
           }
         }
         if (!whole) {
+          const uint32_t vis = opaque(seen);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             s[i] = (vis >> i) & 1 ? s[i] : 0.0f;
@@ -553,7 +575,9 @@ hipError_t by_width(const AttnArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-size_t attention_backward_workspace_bytes(const AttnArgs& a) { return (size_t)a.B * a.Hq * a.Tq * sizeof(float); }
+size_t attention_backward_workspace_bytes(const AttnArgs& a) {
+  return (size_t)a.B * a.Hk * a.R * stat_floats(a) * sizeof(float);
+}
 
 hipError_t launch_attention_backward(AttnArgs a, hipStream_t stream) {
   return a.elem_bytes == 4 ? by_width<float>(a, stream) : by_width<__bf16>(a, stream);

@@ -31,6 +31,16 @@ constexpr float kNegInf = -__builtin_huge_valf();
 // The moving row of accumulator register i (0 .. 15) in half-wave h.
 __device__ __forceinline__ int acc_row(int i, int h) { return 8 * (i >> 2) + 4 * h + (i & 3); }
 
+// The same value, of which the compiler keeps no derived ones: what rare paths compute from it (or the 16 bit tests of a
+// mask) does not move out of the loops and hold registers there.
+__device__ __forceinline__ uint32_t opaque(uint32_t x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// Keeps a sum's additions where they are written: sunk behind the next head's work they would hold its terms' registers.
+__device__ __forceinline__ void pin(float& x) { asm volatile("" : "+v"(x)); }
+
 // Over the two lanes of an own row.
 __device__ __forceinline__ float pair_max(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x),
@@ -95,20 +105,21 @@ struct Mma<__bf16, DP> {
   }
 
   // The A operand: channels 32 blk + n of the rows above, read transposed (four rows by 16 channels for
-  // every 16 lanes; lane i of the 16 addresses row i / 4, channels 4 (i mod 4)).
-  static __device__ __forceinline__ i16x4 transposed(const char* tile, int r, int c) {
+  // every 16 lanes; lane i of the 16 addresses row i / 4, channels 4 (i mod 4)).  The turn repeats every 16 rows, so
+  // the lane's addresses differ by constants between the tile's halves.
+  static __device__ __forceinline__ i16x4 transposed(const char* tile, int r0, int u, int blk, int lane) {
+    const int x = 4 * (lane >> 5) + ((lane >> 2) & 3), ch = 32 * blk + (lane & 16) + 4 * (lane & 3);
+    const uint32_t at = (x * Tl::P + ((ch / 8) ^ Tl::turn(8 * (u & 1) + x))) * 16 + (ch & 4) * 2;
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) i16x4*)(uint32_t)(uintptr_t)Tl::at(tile, r, c));
+        (__attribute__((address_space(3))) i16x4*)((uint32_t)(uintptr_t)tile + at + (r0 + 8 * u) * Tl::kRowBytes));
   }
   static __device__ __forceinline__ bf16x8 columns(const char* tile, int r0, int c, int blk, int lane) {
-    const int h = lane >> 5, i = lane & 15;
-    const int r = r0 + 16 * c + 4 * h + (i >> 2), ch = 32 * blk + (lane & 16) + 4 * (i & 3);
     union {
       i16x4 s[2];
       bf16x8 v;
     } u;
-    u.s[0] = transposed(tile, r, ch);
-    u.s[1] = transposed(tile, r + 8, ch);
+    u.s[0] = transposed(tile, r0, 2 * c, blk, lane);
+    u.s[1] = transposed(tile, r0, 2 * c + 1, blk, lane);
     return u.v;
   }
 
@@ -151,7 +162,7 @@ struct Mma<float, DP> {
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         acc[blk] = __builtin_amdgcn_mfma_f32_32x32x2f32(
-            *Tl::at(tile, r0 + acc_row(i, lane >> 5), 32 * blk + (lane & 31)), p.v[i], acc[blk], 0, 0, 0);
+            *Tl::at(tile + r0 * Tl::kRowBytes, acc_row(i, lane >> 5), 32 * blk + (lane & 31)), p.v[i], acc[blk], 0, 0, 0);
   }
 };
 
@@ -187,6 +198,21 @@ __device__ __forceinline__ void move_pieces(__amdgpu_buffer_rsrc_t rs, char* lds
 #endif
 }
 
+// One wave instruction: 4 bytes a lane.
+__device__ __forceinline__ void move_words(__amdgpu_buffer_rsrc_t rs, void* lds, int off) {
+#ifdef __HIP_DEVICE_COMPILE__
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(uint32_t)(uintptr_t)lds, 4, off,
+                                           0, 0, 0);
+#endif
+}
+
+// `count` of the up to `room` (a multiple of 64) floats at `base` (uniform), zeros behind them, by the four waves.
+__device__ __forceinline__ void stage_floats(float* lds, const float* base, int count, int room) {
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(base), 0, count * 4, 0x00020000);
+  for (int at = 64 * wave; at < room; at += 256) move_words(rs, lds + at, (at + lane) * 4);
+}
+
 // Stages N rows of a tensor, `stride` elements apart from `base` (uniform), zero beyond `rows` and beyond D channels, by
 // the four waves of the workgroup.  The wide path (vec: 16-byte pieces, N rows within 2^31 bytes) only issues the moves:
 // wait_staged() before the barrier.
@@ -210,7 +236,7 @@ __device__ __forceinline__ void stage_rows(char* tile, const T* base, int64_t st
       move_pieces(rs, tile + (4 * k + wave) * 1024, off, k * (256 / Tl::P) * bytes);
   } else {
 #pragma unroll 1
-    for (int e = threadIdx.x; e < N * DP; e += 256) {
+    for (int e = (int)opaque(threadIdx.x); e < N * DP; e += 256) {
       const int r = e / DP, c = e - r * DP;
       *Tl::at(tile, r, c) = r < rows && c < D ? base[r * stride + c] : (T)0.0f;
     }
@@ -224,7 +250,7 @@ __device__ __forceinline__ void stage_group(char* tile, const T* base, int64_t t
   using Tl = Tile<T, DP>;
   if (vec) {
     // offsets from the tile's first token: at most N tokens, within 2^31 bytes
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), t0 = r0 / G;
+    const int lane = (int)opaque(threadIdx.x) & 63, wave = uniform(threadIdx.x >> 6), t0 = r0 / G;
     const T* first = base + t0 * token;
     const int tb = (int)token * (int)sizeof(T), hb = (int)head * (int)sizeof(T);
     const __amdgpu_buffer_rsrc_t rs =
@@ -238,7 +264,7 @@ __device__ __forceinline__ void stage_group(char* tile, const T* base, int64_t t
     }
   } else {
 #pragma unroll 1
-    for (int e = threadIdx.x; e < N * DP; e += 256) {
+    for (int e = (int)opaque(threadIdx.x); e < N * DP; e += 256) {
       const int r = e / DP, c = e - r * DP, t = (r0 + r) / G, g = r0 + r - t * G;
       *Tl::at(tile, r, c) = r < rows && c < D ? base[t * token + g * head + c] : (T)0.0f;
     }
@@ -250,7 +276,9 @@ __device__ __forceinline__ void wait_staged() { __builtin_amdgcn_s_waitcnt(0x0F7
 // The row fragments of tile row r0 + n.
 template <typename T, int DP>
 __device__ __forceinline__ typename Mma<T, DP>::Frag tile_frag(const char* tile, int r0, int f, int lane) {
-  return *(const typename Mma<T, DP>::Frag*)(tile + Tile<T, DP>::slot(r0 + (lane & 31), 2 * f + (lane >> 5)) * 16);
+  const int n = lane & 31;
+  return *(const typename Mma<T, DP>::Frag*)(tile + r0 * Tile<T, DP>::kRowBytes +
+                                             Tile<T, DP>::slot(n, 2 * f + (lane >> 5)) * 16);
 }
 
 // Products of tile rows r0 .. r0 + 31 with the own row, added to s.
@@ -271,8 +299,8 @@ __device__ __forceinline__ f32x16 tile_dot(const char* tile, int r0,
 template <typename T, int DP, int N>
 __device__ __forceinline__ bool holds_odd(const char* tile) {
   uint32_t odd = 0;
-#pragma unroll 2
-  for (int e = threadIdx.x; e < N * Tile<T, DP>::P; e += 256) {
+#pragma unroll 1
+  for (int e = (int)opaque(threadIdx.x); e < N * Tile<T, DP>::P; e += 256) {
     const i32x4 w = *(const i32x4*)(tile + e * 16);
     // the exponent's ones carry into the sign bit
 #pragma unroll
@@ -285,7 +313,7 @@ __device__ __forceinline__ bool holds_odd(const char* tile) {
 template <typename T, int DP, int N>
 __device__ __forceinline__ void clean_rows(char* tile) {
 #pragma unroll 1
-  for (int e = threadIdx.x; e < N * DP; e += 256) {
+  for (int e = (int)opaque(threadIdx.x); e < N * DP; e += 256) {
     T* x = (T*)tile + e;
     if (!(fabsf((float)*x) < __builtin_huge_valf())) *x = (T)0.0f;
   }
@@ -305,7 +333,7 @@ __device__ __forceinline__ uint32_t seen_rows(uint32_t vis, int h) {
 // negative one (or a NaN).
 template <typename T, int DP>
 __device__ __forceinline__ uint32_t find_odd(const char* tile, int r0, int blk, uint32_t vis, int lane) {
-  const int h = lane >> 5;
+  const int h = (int)opaque(lane) >> 5;
   const uint32_t seen = seen_rows(vis, h);
   uint32_t odd = 0;
 #pragma unroll 1
@@ -324,6 +352,7 @@ __device__ __forceinline__ uint32_t find_odd(const char* tile, int r0, int blk, 
 // Whether the own row sees a tile row that has a non-finite element.
 template <typename T, int DP>
 __device__ __forceinline__ bool sees_odd(const char* tile, int r0, uint32_t vis, int lane) {
+  lane = (int)opaque(lane);
   const uint32_t seen = seen_rows(vis, lane >> 5);
   bool odd = false;       // of tile row n
 #pragma unroll 1
@@ -414,25 +443,24 @@ __device__ __forceinline__ f32x16 outer_sum(float moving, float own) {
   return __builtin_amdgcn_mfma_f32_32x32x2f32(moving, own, f32x16{}, 0, 0, 0);
 }
 
-// Distances between the lane's own point and the 16 moving points of its accumulator registers (pos[axis][tile row] in
+// Distances between the lane's own point and the 16 moving points of its accumulator registers (pos[tile row][axis] in
 // LDS).  own[axis] is 1 in the lower half-wave and minus the own coordinate in the upper one: the differences come from
 // the matrix cores, which the vector-bound loops leave idle, and a moving coordinate is read once a lane instead of
 // four times 16 bytes.
-template <int N>
-__device__ __forceinline__ void distances(const float (*pos)[N], int at, int dims, const float (&own)[3], int lane,
+__device__ __forceinline__ void distances(const float* pos, int at, int dims, const float (&own)[3], int lane,
                                           f32x16& d) {
   const bool low = lane < 32;
-  const int r = at + (lane & 31);
-  d = outer_sum(low ? pos[0][r] : 1.0f, own[0]);
+  const float* p = pos + (at + (lane & 31)) * dims;
+  d = outer_sum(low ? p[0] : 1.0f, own[0]);
 #pragma unroll
   for (int i = 0; i < 16; ++i) d[i] *= d[i];
   if (dims > 1) {
-    const f32x16 e = outer_sum(low ? pos[1][r] : 1.0f, own[1]);
+    const f32x16 e = outer_sum(low ? p[1] : 1.0f, own[1]);
 #pragma unroll
     for (int i = 0; i < 16; ++i) d[i] = fmaf(e[i], e[i], d[i]);
   }
   if (dims > 2) {
-    const f32x16 e = outer_sum(low ? pos[2][r] : 1.0f, own[2]);
+    const f32x16 e = outer_sum(low ? p[2] : 1.0f, own[2]);
 #pragma unroll
     for (int i = 0; i < 16; ++i) d[i] = fmaf(e[i], e[i], d[i]);
   }

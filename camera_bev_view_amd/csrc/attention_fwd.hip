@@ -27,7 +27,7 @@ struct Fwd {
 
 template <typename T, int DP>
 constexpr int min_waves(int hb) {
-  return sizeof(T) == 4 || DP > 64 ? 1 : DP == 64 || hb == 2 ? 3 : 4;
+  return sizeof(T) == 4 || DP > 64 ? 1 : DP == 64 ? 3 : 4;
 }
 
 // Writes a head's rows (or their split's partial rows); the KW waves of a tile add up their parts first.
@@ -132,7 +132,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_fwd(Att
   using M = Mma<T, DP>;
   constexpr int NB = DP / 32, KT = C::KT, RW = C::RW;
   __shared__ alignas(16) char smem[C::kBytes];
-  __shared__ alignas(16) float pos[BIAS ? 3 : 1][KT];
+  __shared__ alignas(16) float pos[BIAS ? 3 * KT : 1];   // [key][axis]
   __shared__ alignas(16) int docs[KT];
   __shared__ int doc_range[4][2];
   char* Ks = smem;                                        // HB tiles each
@@ -158,7 +158,6 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_fwd(Att
     own_point(a.pos_q + ((int64_t)b * a.Tq + w.t) * a.dims, a.dims, h, own);
 #pragma unroll
     for (int i = 0; i < HB; ++i) slope[i] = a.slope[((int64_t)b * a.Tq + w.t) * a.Hq + w.head + i] / un.raw;
-    for (int e = threadIdx.x; e < 3 * KT; e += kThreads) pos[0][e] = 0.0f;
   }
   for (int e = threadIdx.x; e < KT; e += kThreads) docs[e] = 0;
   // the keys the workgroup's and the wave's rows can see by order
@@ -202,21 +201,16 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_fwd(Att
       stage_rows<T, DP, KT>(Vs + i * C::kTile, (const T*)a.v + b * a.vs[0] + s0 * a.vs[1] + (hk + i) * a.vs[2], a.vs[1],
                             nk, a.vec, a.D);
     }
-    if ((int)threadIdx.x < KT) {
-      if (a.doc_q) docs[threadIdx.x] = my_doc;
-      if constexpr (BIAS) {
-        if ((int)threadIdx.x < nk)
-          for (int ax = 0; ax < a.dims; ++ax)
-            pos[ax][threadIdx.x] = a.pos_k[((int64_t)b * a.Tk + s0 + threadIdx.x) * a.dims + ax];
-      }
-    }
+    if (a.doc_q && (int)threadIdx.x < KT) docs[threadIdx.x] = my_doc;
+    if constexpr (BIAS) stage_floats(pos, a.pos_k + ((int64_t)b * a.Tk + s0) * a.dims, nk * a.dims, KT * a.dims);
     // which of the tile's keys (16 of the lane's half) the lane's row sees
     auto visible = [&](int at) {
       uint32_t vis = 0;
+      const int hh = (int)opaque(h);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int kr = at + acc_row(i, h);
-        vis |= (s0 + kr <= w.lim && docs[kr] == w.doc) ? 1u << i : 0u;
+      for (int i = 15; i >= 0; --i) {
+        const int kr = at + acc_row(i, hh);
+        vis = 2 * vis + (s0 + kr <= w.lim && docs[kr] == w.doc ? 1u : 0u);
       }
       return vis;
     };
@@ -245,9 +239,9 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_fwd(Att
         if (!__any(d >= dmin && d <= dmax)) continue;
         whole = whole && one_doc && __all(d == dmin);
       }
-      const uint32_t vis = whole ? 0xFFFFu : visible(at);
+      const uint32_t seen = whole ? 0xFFFFu : visible(at);
       f32x16 d;
-      if constexpr (BIAS) distances<KT>(pos, at, a.dims, own, lane, d);
+      if constexpr (BIAS) distances(pos, at, a.dims, own, lane, d);
 #pragma unroll
       for (int hd = 0; hd < HB; ++hd) {
         __builtin_amdgcn_sched_barrier(0);      // one head's registers at a time
@@ -258,6 +252,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_fwd(Att
           for (int i = 0; i < 16; ++i) s[i] = fmaf(-slope[hd], d[i], s[i]);
         }
         if (!whole) {
+          const uint32_t vis = opaque(seen);
 #pragma unroll
           for (int i = 0; i < 16; ++i) s[i] = (vis >> i) & 1 ? s[i] : kNegInf;
         }
@@ -285,6 +280,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_fwd(Att
           sum += s[i];
         }
         l[hd] += sum;
+        pin(l[hd]);
         __builtin_amdgcn_sched_barrier(0);
         M::template accumulate<NB>(acc[hd], M::pack(s), Vs + hd * C::kTile, at, lane);
       }
@@ -299,34 +295,45 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_fwd(Att
   }
 }
 
-// Joins the splits of a row, in split order: one wave a row.
+// Joins the splits of a row, one workgroup a row: the maximum and the weights over all threads, then wave w adds up
+// splits w, w + 4, ... (their loads do not depend on each other) and the four sums are added in wave order.
 template <typename T>
-__global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
-  const int64_t rows = (int64_t)a.B * a.Hk * a.R, row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= rows) return;
-  const int lane = threadIdx.x & 63;
+__global__ __launch_bounds__(kThreads) void attn_join(AttnArgs a) {
+  __shared__ float red[4], sums[4], part[4][128];
+  const int64_t rows = (int64_t)a.B * a.Hk * a.R, row = blockIdx.x;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t stride = rows * (a.D + 2);
   const float* p = a.part + row * (a.D + 2);
   float top = kNegInf;
-  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, p[s * stride + a.D]);
+  for (int s = threadIdx.x; s < a.splits; s += kThreads) top = fmaxf(top, p[s * stride + a.D]);
+  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+  if (lane == 0) red[wave] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const float base = top == kNegInf ? 0.0f : top;
   float tot = 0.0f, o[2] = {0.0f, 0.0f};
-  for (int s = 0; s < a.splits; ++s) {
-    const float mk = p[s * stride + a.D];
-    const float f = mk == kNegInf ? (top == kNegInf ? 1.0f : 0.0f) : __builtin_amdgcn_exp2f(mk - top);
+#pragma unroll 4
+  for (int s = wave; s < a.splits; s += 4) {
+    const float f = __builtin_amdgcn_exp2f(p[s * stride + a.D] - base);
     tot = fmaf(p[s * stride + a.D + 1], f, tot);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
       if (lane + 64 * j < a.D) o[j] = fmaf(p[s * stride + lane + 64 * j], f, o[j]);
   }
+  if (lane == 0) sums[wave] = tot;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) part[wave][lane + 64 * j] = o[j];
+  __syncthreads();
+  tot = (sums[0] + sums[1]) + (sums[2] + sums[3]);
   const int64_t bh = row / a.R;
   const int r = (int)(row - bh * a.R), t = r / a.G, b = (int)(bh / a.Hk);
   const int head = (int)(bh - (int64_t)b * a.Hk) * a.G + (r - t * a.G);
   const float inv = tot > 0.0f || tot != tot ? 1.0f / tot : 0.0f;
-  T* out = (T*)a.out + (((int64_t)b * a.Tq + t) * a.Hq + head) * a.D;
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-    if (lane + 64 * j < a.D) out[lane + 64 * j] = (T)(o[j] * inv);
-  if (lane == 0) a.lse[((int64_t)b * a.Hq + head) * a.Tq + t] = tot == 0.0f ? kNegInf : top * kLn2 + logf(tot);
+  const int c = threadIdx.x;
+  if (c < a.D)
+    ((T*)a.out)[(((int64_t)b * a.Tq + t) * a.Hq + head) * a.D + c] =
+        (T)(((part[0][c] + part[1][c]) + (part[2][c] + part[3][c])) * inv);
+  if (c == 0) a.lse[((int64_t)b * a.Hq + head) * a.Tq + t] = tot == 0.0f ? kNegInf : top * kLn2 + logf(tot);
 }
 
 struct Plan {
@@ -378,7 +385,7 @@ hipError_t run(AttnArgs& a, const Plan& p, hipStream_t stream) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   const int64_t rows = (int64_t)a.B * a.Hk * a.R;
-  attn_join<T><<<dim3((unsigned)((rows + 3) / 4)), 256, 0, stream>>>(a);
+  attn_join<T><<<dim3((unsigned)rows), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 

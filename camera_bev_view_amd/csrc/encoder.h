@@ -71,7 +71,7 @@ struct AttnArgs {
   const void* gout;        // [B, Tq, Hq, D]
   void *gq, *gk, *gv;      // contiguous
   float* gslope;           // [B, Tq, Hq] or NULL
-  float* delta;            // workspace [B, Hq, Tq]
+  float* delta;            // workspace: per (sample, key head) what the keys' launch needs of the rows
 };
 size_t attention_forward_workspace_bytes(const AttnArgs& a);
 size_t attention_backward_workspace_bytes(const AttnArgs& a);

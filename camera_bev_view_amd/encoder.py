@@ -7,6 +7,7 @@ queries, BEV cells and tokens.  Each operator has a forward and a backward call 
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -22,13 +23,35 @@ def _data(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr() or None
 
 
-def _call(fn, dev: torch.device, *args) -> None:
-    """fn(*args, stream) on the current stream of ``dev``, with that device current."""
+def _call(name: str, dev: torch.device, *args) -> None:
+    """The library's ``name``(*args, stream) on the current stream of ``dev``, with that device current."""
+    fn = getattr(_lib.load(), name)
     if torch.cuda.current_device() == dev.index:
-        _lib.check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
     else:
         with torch.cuda.device(dev):
-            _lib.check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status:
+        _lib.check(status)
+
+
+# Workspace sizes depend on the sizes alone: asked once for each.
+
+@functools.lru_cache(maxsize=1024)
+def _norm_scratch(images: int, pixels: int, C: int, groups: int, dtype: int, backward: int) -> int:
+    lib, need = _lib.load(), ctypes.c_size_t()
+    nd = _lib.NormDesc(images, pixels, 0, 0, C, groups, 0, 0.0)
+    _lib.check(lib.fbev_group_norm_workspace(nd, dtype, backward, _byref(need)))
+    return need.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_scratch(B: int, Tq: int, Tk: int, Hq: int, Hk: int, D: int, dims: int, backward: int) -> int:
+    lib, need = _lib.load(), ctypes.c_size_t()
+    z = (0, 0, 0)
+    ad = _lib.AttentionDesc(B, Tq, Tk, Hq, Hk, D, z, z, z, 1.0, 0.0, dims, 0, None, None, None, None, None, None)
+    _lib.check(lib.fbev_attention_workspace(ad, backward, _byref(need)))
+    return need.value
 
 
 def _check_values(name: str, x: torch.Tensor, ndim: int, device=None, dtype=None) -> None:
@@ -118,11 +141,9 @@ def group_norm_forward(x: torch.Tensor, groups: int, weight: Optional[torch.Tens
     else:
         _check_plain("out", out, x.shape, x.dtype, dev)
     stats = torch.empty((nd.images, max(groups, 0), 2), dtype=torch.float32, device=dev)
-    lib, dt = _lib.load(), _DTYPES[x.dtype]
-    need = ctypes.c_size_t()
-    _lib.check(lib.fbev_group_norm_workspace(nd, dt, 0, _byref(need)))
-    workspace, have = _scratch(need.value, workspace, dev)
-    _call(lib.fbev_group_norm_forward, dev, _data(x), dt, nd, _data(weight), _data(bias), _data(out), _data(stats),
+    dt = _DTYPES[x.dtype]
+    workspace, have = _scratch(_norm_scratch(nd.images, nd.pixels, nd.C, groups, dt, 0), workspace, dev)
+    _call("fbev_group_norm_forward", dev, _data(x), dt, nd, _data(weight), _data(bias), _data(out), _data(stats),
           _data(workspace), have)
     return out, stats
 
@@ -145,11 +166,9 @@ def group_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, stats: torch.Tens
     if with_params:
         gw = torch.empty(nd.C, dtype=torch.float32, device=dev)
         gb = torch.empty(nd.C, dtype=torch.float32, device=dev)
-    lib, dt = _lib.load(), _DTYPES[x.dtype]
-    need = ctypes.c_size_t()
-    _lib.check(lib.fbev_group_norm_workspace(nd, dt, 1, _byref(need)))
-    workspace, have = _scratch(need.value, workspace, dev)
-    _call(lib.fbev_group_norm_backward, dev, _data(grad_y), _data(x), dt, nd, _data(weight), _data(bias), _data(stats),
+    dt = _DTYPES[x.dtype]
+    workspace, have = _scratch(_norm_scratch(nd.images, nd.pixels, nd.C, groups, dt, 1), workspace, dev)
+    _call("fbev_group_norm_backward", dev, _data(grad_y), _data(x), dt, nd, _data(weight), _data(bias), _data(stats),
           _data(gx), _data(gw), _data(gb), _data(workspace), have)
     return gx, gw, gb
 
@@ -243,8 +262,7 @@ def _rotary(q, k, pos, freqs, interleaved, inverse, q_out, k_out):
     rd = _lib.RotaryDesc(B, T, D, pos.shape[2], freqs.shape[1], 0 if q is None else q.shape[2],
                          0 if k is None else k.shape[2], bool(interleaved), bool(inverse), strides[0][:3],
                          strides[1][:3], strides[2][:3], strides[3][:3])
-    lib = _lib.load()
-    _call(lib.fbev_rotary, dev, _data(ins[0]), _data(ins[1]), _DTYPES[dtype], rd, _data(pos), _data(freqs),
+    _call("fbev_rotary", dev, _data(ins[0]), _data(ins[1]), _DTYPES[dtype], rd, _data(pos), _data(freqs),
           _data(outs[0]), _data(outs[1]))
     return outs[0], outs[1]
 
@@ -369,11 +387,8 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scal
     else:
         _check_plain("out", out, q.shape, q.dtype, dev)
     lse = torch.empty((ad.B, ad.Hq, ad.Tq), dtype=torch.float32, device=dev)
-    lib = _lib.load()
-    need = ctypes.c_size_t()
-    _lib.check(lib.fbev_attention_workspace(ad, 0, _byref(need)))
-    workspace, have = _scratch(need.value, workspace, dev)
-    _call(lib.fbev_attention_forward, dev, _data(q), _data(k), _data(v), _DTYPES[q.dtype], ad, _data(out), _data(lse),
+    workspace, have = _scratch(_attention_scratch(ad.B, ad.Tq, ad.Tk, ad.Hq, ad.Hk, ad.D, ad.dims, 0), workspace, dev)
+    _call("fbev_attention_forward", dev, _data(q), _data(k), _data(v), _DTYPES[q.dtype], ad, _data(out), _data(lse),
           _data(workspace), have)
     del keep
     return out, lse
@@ -398,11 +413,8 @@ def attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
     gk = torch.empty(k.shape, dtype=dtype, device=dev)
     gv = torch.empty(v.shape, dtype=dtype, device=dev)
     gslope = torch.empty((ad.B, ad.Tq, ad.Hq), dtype=torch.float32, device=dev) if ad.dims else None
-    lib = _lib.load()
-    need = ctypes.c_size_t()
-    _lib.check(lib.fbev_attention_workspace(ad, 1, _byref(need)))
-    workspace, have = _scratch(need.value, workspace, dev)
-    _call(lib.fbev_attention_backward, dev, _data(grad_out), _data(q), _data(k), _data(v), _DTYPES[dtype], ad,
+    workspace, have = _scratch(_attention_scratch(ad.B, ad.Tq, ad.Tk, ad.Hq, ad.Hk, ad.D, ad.dims, 1), workspace, dev)
+    _call("fbev_attention_backward", dev, _data(grad_out), _data(q), _data(k), _data(v), _DTYPES[dtype], ad,
           _data(out), _data(lse), _data(gq), _data(gk), _data(gv), _data(gslope), _data(workspace), have)
     del keep
     return gq, gk, gv, gslope

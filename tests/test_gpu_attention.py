@@ -116,6 +116,16 @@ def test_many_heads_share_staged_keys(D, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("form", ["dense", "causal", "documents"])
+def test_two_heads_share_their_distances(form, dtype):
+    """Enough heads with a distance bias that a wave takes two: dense, causal and packed, 1 to 3 axes."""
+    docs = [runs([40, 9, 20], 75)] * 4
+    kw = dict(dense={}, causal=dict(causal=True), documents=dict(docs=(docs, docs)))[form]
+    dims = dict(dense=2, causal=1, documents=3)[form]
+    check(*draw(4, 75, 75, 96, 96, 32, dtype, 52, dims=dims, **kw), f"shared distances {form}")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("Tq,G,D", [(1, 1, 64), (1, 8, 32), (3, 4, 128), (2, 40, 40)])
 def test_few_rows_over_many_keys(Tq, G, D, dtype):
     check(*draw(2, Tq, 5000, 2 * G, 2, D, dtype, 42, dims=2), f"split {Tq} x {G}", backward=False)
