@@ -32,7 +32,7 @@ struct alignas(sizeof(T) * V) Piece {
 template <int ACT>
 __device__ __forceinline__ float act_fwd(float z) {
   if constexpr (ACT == FBEV_ACT_RELU) return z < 0.0f ? 0.0f : z;
-  if constexpr (ACT == FBEV_ACT_SILU) return z / (1.0f + __expf(-z));
+  if constexpr (ACT == FBEV_ACT_SILU) return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
   if constexpr (ACT == FBEV_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
   return z;
 }
@@ -41,13 +41,17 @@ template <int ACT>
 __device__ __forceinline__ float act_grad(float z) {
   if constexpr (ACT == FBEV_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
   if constexpr (ACT == FBEV_ACT_SILU) {
-    const float s = 1.0f / (1.0f + __expf(-z));
+    const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-z));
     return s * (1.0f + z * (1.0f - s));
   }
   if constexpr (ACT == FBEV_ACT_GELU)
     return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z);
   return 1.0f;
 }
+
+// i / n for 0 <= i < 2^20, n >= 1 from 1 / n in fp32: (i + 1/2) / n is at least 1 / (2 n) away from a whole number, far
+// more than the product's rounding.
+__device__ __forceinline__ int small_div(int i, float inv) { return (int)(((float)i + 0.5f) * inv); }
 
 // A workgroup's share: channels [c0, c0 + nv V) (whole groups) of pixels [s0, s0 + ns).  Thread (ty, cv)
 // holds channel piece cv of pixels s0 + ty, s0 + ty + TY, ...
@@ -56,36 +60,14 @@ struct Share {
   bool active;
 };
 
-// Sums over the workgroup per group, for two values a channel: buf[(ty nv + cv) per + j] holds a thread's
-// value for channel c0 + cv V + j.  out[g] = sums of the share's groups, valid in all threads after the call.
-// `per` is 1 when a piece lies inside one group (its channels were summed first) and V otherwise.
-template <int BLOCK>
-__device__ __forceinline__ void group_sums(const float* buf, float* out, int TY, int cols, int gcols) {
-  const int ng = cols / gcols;
-  int gt = 64;
-  while (gt > 1 && gt * ng > BLOCK) gt >>= 1;
-  __syncthreads();
-  for (int g0 = 0; g0 < ng; g0 += BLOCK / gt) {
-    const int g = g0 + (int)threadIdx.x / gt, l = threadIdx.x & (gt - 1);
-    float s = 0.0f;
-    if (g < ng) {
-      const int n = TY * gcols;
-      for (int e = l; e < n; e += gt) {
-        const int ty = e / gcols, c = e - ty * gcols;
-        s += buf[ty * cols + g * gcols + c];
-      }
-    }
-    for (int o = gt >> 1; o > 0; o >>= 1) s += __shfl_xor(s, o);
-    if (g < ng && l == 0) out[g] = s;
-  }
-  __syncthreads();
-}
-
+// Per group or channel of the share, two results.
 template <int BLOCK, int V>
-struct Lds {
-  float buf[BLOCK * V];
-  float g1[BLOCK * V];     // per group of the share (at most one group a channel)
-  float g2[BLOCK * V];
+struct Groups {
+  float g1[BLOCK * V], g2[BLOCK * V];
+};
+template <int BLOCK, int V>
+struct Lds : Groups<BLOCK, V> {
+  float buf[BLOCK * V], buf2[BLOCK * V];
 };
 
 template <int BLOCK, int V>
@@ -97,7 +79,7 @@ __device__ __forceinline__ Share make_share(int img, int c0, int nch, int s0, in
   w.s0 = s0;
   w.ns = ns;
   w.TY = BLOCK / w.nv;
-  w.ty = threadIdx.x / w.nv;
+  w.ty = small_div(threadIdx.x, 1.0f / (float)w.nv);
   w.cv = threadIdx.x - w.ty * w.nv;
   w.active = w.ty < w.TY;
   return w;
@@ -124,55 +106,95 @@ __device__ __forceinline__ void load_rows(const void* src, const NormArgs& a, co
   }
 }
 
-// Writes a thread's per-channel values into the buffer (summed over the piece when per is 1).
-template <int V>
-__device__ __forceinline__ void put_sums(float* buf, const Share& w, int per, const float (&v)[V]) {
-  if (!w.active) return;
-  float* at = buf + (w.ty * w.nv + w.cv) * per;
-  if (per == 1) {
-    float s = v[0];
-#pragma unroll
-    for (int j = 1; j < V; ++j) s += v[j];
-    at[0] = s;
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) at[j] = v[j];
-  }
-}
-
-// Mean and sum of squares around it of every group of the share, into L.g1 and L.g2.
+// Mean and sum of squares around it of every group of the share, into L.g1 and L.g2.  A thread takes its own values'
+// mean and squares first (of a channel, or of the piece when it lies inside one group); a group's lanes then join them:
+//   mean = sum n_i m_i / n,  squares = sum (q_i + n_i (m_i - mean)^2).
 template <int BLOCK, typename T, int V, int R>
-__device__ __forceinline__ void share_moments(const NormArgs& a, const Share& w, const Piece<T, V> (&x)[R],
-                                              Lds<BLOCK, V>& L, int cg, int per) {
-  const int cols = w.nv * per, gcols = per == 1 ? cg / V : cg;
-  float v[V];
+__device__ __forceinline__ void share_moments(const Share& w, const Piece<T, V> (&x)[R], Lds<BLOCK, V>& L, int cg,
+                                              int per) {
+  const int base = w.ns / w.TY, rem = w.ns - base * w.TY;
+  const int rows = w.active ? base + (w.ty < rem ? 1 : 0) : 0;          // this thread's
+  if (w.active) {
+    float m[V], q[V];
+    const float inv = rows > 0 ? 1.0f / (float)rows : 0.0f;
 #pragma unroll
-  for (int j = 0; j < V; ++j) v[j] = 0.0f;
+    for (int j = 0; j < V; ++j) m[j] = q[j] = 0.0f;
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-    if (w.ty + r * w.TY < w.ns)
+    for (int r = 0; r < R; ++r)
+      if (r < rows)
 #pragma unroll
-      for (int j = 0; j < V; ++j) v[j] += to_f32(x[r].e[j]);
-  put_sums<V>(L.buf, w, per, v);
-  group_sums<BLOCK>(L.buf, L.g1, w.TY, cols, gcols);
-  const float inv = 1.0f / ((float)w.ns * (float)cg);
-  float m[V];
+        for (int j = 0; j < V; ++j) m[j] += to_f32(x[r].e[j]);
+    if (per == 1) {
+      float t = m[0];
 #pragma unroll
-  for (int j = 0; j < V; ++j) m[j] = w.active ? L.g1[(w.cv * V + j) / cg] * inv : 0.0f;
+      for (int j = 1; j < V; ++j) t += m[j];
+      t *= inv / (float)V;
 #pragma unroll
-  for (int j = 0; j < V; ++j) v[j] = 0.0f;
+      for (int j = 0; j < V; ++j) m[j] = t;
+    } else {
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-    if (w.ty + r * w.TY < w.ns)
+      for (int j = 0; j < V; ++j) m[j] *= inv;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (r < rows)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float d = to_f32(x[r].e[j]) - m[j];
+          q[j] = fmaf(d, d, q[j]);
+        }
+    const int at = (w.ty * w.nv + w.cv) * per;
+    if (per == 1) {
+      float t = q[0];
+#pragma unroll
+      for (int j = 1; j < V; ++j) t += q[j];
+      L.buf[at] = m[0];
+      L.buf2[at] = t;
+    } else {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float d = to_f32(x[r].e[j]) - m[j];
-        v[j] = fmaf(d, d, v[j]);
+        L.buf[at + j] = m[j];
+        L.buf2[at + j] = q[j];
       }
-  put_sums<V>(L.buf, w, per, v);
-  group_sums<BLOCK>(L.buf, L.g2, w.TY, cols, gcols);
-  const int ng = w.nv * V / cg;
-  for (int g = threadIdx.x; g < ng; g += BLOCK) L.g1[g] *= inv;
+    }
+  }
+  __syncthreads();
+  const int cols = w.nv * per, gcols = per == 1 ? cg / V : cg, ng = cols / gcols;
+  const int ty_n = min(w.TY, w.ns);
+  const float each = (float)base * (per == 1 ? (float)V : 1.0f);        // elements of an entry
+  const float more = (float)(base + 1) * (per == 1 ? (float)V : 1.0f);
+  int gt = 64;
+  while (gt > 1 && gt * ng > BLOCK) gt >>= 1;
+  const int dty = gt / gcols, dc = gt - dty * gcols;
+  for (int g0 = 0; g0 < ng; g0 += BLOCK / gt) {
+    const int g = g0 + (int)threadIdx.x / gt, l = threadIdx.x & (gt - 1);
+    float s = 0.0f, q = 0.0f;
+    // entries l, l + gt, ... of the group's gcols columns by ty_n rows; a row has base or base + 1 pixels
+    const int ty0 = l / gcols, c0 = l - ty0 * gcols;
+    if (g < ng)
+      for (int ty = ty0, c = c0; ty < ty_n;) {
+        s = fmaf(ty < rem ? more : each, L.buf[ty * cols + g * gcols + c], s);
+        ty += dty;
+        c += dc;
+        if (c >= gcols) c -= gcols, ++ty;
+      }
+    for (int o = gt >> 1; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    const float mean = s / ((float)w.ns * (float)cg);
+    if (g < ng)
+      for (int ty = ty0, c = c0; ty < ty_n;) {
+        const int at = ty * cols + g * gcols + c;
+        const float d = L.buf[at] - mean;
+        q += fmaf((ty < rem ? more : each) * d, d, L.buf2[at]);
+        ty += dty;
+        c += dc;
+        if (c >= gcols) c -= gcols, ++ty;
+      }
+    for (int o = gt >> 1; o > 0; o >>= 1) q += __shfl_xor(q, o);
+    if (g < ng && l == 0) {
+      L.g1[g] = mean;
+      L.g2[g] = q;
+    }
+  }
   __syncthreads();
 }
 
@@ -192,20 +214,30 @@ __device__ __forceinline__ void write_normed(const NormArgs& a, const Share& w, 
   }
 }
 
-// z = x mul + add for the thread's channels, from its groups' mean and rstd in L.g1, L.g2.
-template <int BLOCK, int V>
-__device__ __forceinline__ void affine(const NormArgs& a, const Share& w, const Lds<BLOCK, V>& L, int cg,
-                                       float (&mul)[V], float (&add)[V]) {
+// The thread's channels' weight and bias, and z = x mul + add from its groups' mean and rstd in L.g1, L.g2.
+template <int V>
+struct Affine {
+  float mul[V], add[V];
+
+  __device__ __forceinline__ void load(const NormArgs& a, const Share& w) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    mul[j] = add[j] = 0.0f;
-    if (w.active) {
-      const int c = w.cv * V + j, g = c / cg;
-      mul[j] = L.g2[g] * (a.weight ? a.weight[w.c0 + c] : 1.0f);
-      add[j] = (a.bias ? a.bias[w.c0 + c] : 0.0f) - L.g1[g] * mul[j];
+    for (int j = 0; j < V; ++j) {
+      const int c = w.c0 + w.cv * V + j;
+      mul[j] = w.active && a.weight ? a.weight[c] : 1.0f;
+      add[j] = w.active && a.bias ? a.bias[c] : 0.0f;
     }
   }
-}
+  template <int BLOCK>
+  __device__ __forceinline__ void finish(const Share& w, const Groups<BLOCK, V>& L, int cg) {
+    const float inv = 1.0f / (float)cg;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int g = w.active ? small_div(w.cv * V + j, inv) : 0;
+      mul[j] *= L.g2[g];
+      add[j] -= L.g1[g] * mul[j];
+    }
+  }
+};
 
 // One launch: block (slab, image) normalises all pixels of `nch` channels.
 template <int BLOCK, typename T, int V, int R, int ACT>
@@ -216,7 +248,9 @@ __global__ __launch_bounds__(BLOCK) void norm_whole(NormArgs a, int nch, int sla
   const int cg = a.C / a.groups, per = cg % V == 0 ? 1 : V;
   Piece<T, V> x[R];
   load_share<T, V, R>(a, w, x);
-  share_moments<BLOCK, T, V, R>(a, w, x, L, cg, per);
+  Affine<V> af;
+  af.load(a, w);
+  share_moments<BLOCK, T, V, R>(w, x, L, cg, per);
   const int ng = w.nv * V / cg;
   const float inv = 1.0f / ((float)w.ns * (float)cg);
   for (int g = threadIdx.x; g < ng; g += BLOCK) {
@@ -227,9 +261,8 @@ __global__ __launch_bounds__(BLOCK) void norm_whole(NormArgs a, int nch, int sla
     st[1] = rstd;
   }
   __syncthreads();
-  float mul[V], add[V];
-  affine<BLOCK, V>(a, w, L, cg, mul, add);
-  write_normed<T, V, R, ACT>(a, w, x, mul, add);
+  af.template finish<BLOCK>(w, L, cg);
+  write_normed<T, V, R, ACT>(a, w, x, af.mul, af.add);
 }
 
 // Two launches, the first: block (chunk, image, slab) leaves (mean, squares) of its groups.
@@ -242,7 +275,7 @@ __global__ __launch_bounds__(BLOCK) void norm_moments(NormArgs a, int nch, int s
   const int cg = a.C / a.groups, per = cg % V == 0 ? 1 : V;
   Piece<T, V> x[R];
   load_share<T, V, R>(a, w, x);
-  share_moments<BLOCK, T, V, R>(a, w, x, L, cg, per);
+  share_moments<BLOCK, T, V, R>(w, x, L, cg, per);
   const int ng = w.nv * V / cg;
   float* part = a.part + (((int64_t)img * chunks + ch) * a.groups + c0 / cg) * 2;
   for (int g = threadIdx.x; g < ng; g += BLOCK) {
@@ -251,43 +284,57 @@ __global__ __launch_bounds__(BLOCK) void norm_moments(NormArgs a, int nch, int s
   }
 }
 
+constexpr int kKeep = 12;
+
 // The second: merges the image's chunks and normalises.
 template <int BLOCK, typename T, int V, int R, int ACT>
-__global__ __launch_bounds__(BLOCK) void norm_apply(NormArgs a, int nch, int slabs, int chunk, int chunks) {
-  __shared__ Lds<BLOCK, V> L;
-  const int per_img = slabs * chunks, img = blockIdx.x / per_img, rest = blockIdx.x - img * per_img;
-  const int slab = rest / chunks, ch = rest - slab * chunks, c0 = slab * nch;
-  const Share w = make_share<BLOCK, V>(img, c0, min(nch, a.C - c0), ch * chunk, min(chunk, a.pixels - ch * chunk));
+__global__ __launch_bounds__(BLOCK) void norm_apply(NormArgs a, int nch, int slabs, int chunk, int chunks, int share,
+                                                   int shares) {
+  __shared__ Groups<BLOCK, V> L;
+  const int per_img = slabs * shares, img = blockIdx.x / per_img, rest = blockIdx.x - img * per_img;
+  const int slab = rest / shares, ch = rest - slab * shares, c0 = slab * nch;
+  const Share w = make_share<BLOCK, V>(img, c0, min(nch, a.C - c0), ch * share, min(share, a.pixels - ch * share));
   const int cg = a.C / a.groups;
   Piece<T, V> x[R];
   load_share<T, V, R>(a, w, x);
+  Affine<V> af;
+  af.load(a, w);
   const int ng = w.nv * V / cg;
-  // lanes of a group take every gt-th chunk and merge their (n, mean, squares) in a fixed tree
+  // the lanes of a group join its chunks as share_moments joins threads
   int gt = 64;
   while (gt > 1 && gt * ng > BLOCK) gt >>= 1;
+  const float n = (float)a.pixels * (float)cg;
   for (int g0 = 0; g0 < ng; g0 += BLOCK / gt) {
     const int g = g0 + (int)threadIdx.x / gt, l = threadIdx.x & (gt - 1);
-    float n = 0.0f, mean = 0.0f, m2 = 0.0f;
-    if (g < ng)
-      for (int k = l; k < chunks; k += gt) {
-        const float* p = a.part + (((int64_t)img * chunks + k) * a.groups + c0 / cg + g) * 2;
-        const float nk = (float)min(chunk, a.pixels - k * chunk) * (float)cg;
-        const float tot = n + nk, d = p[0] - mean;
-        mean += d * (nk / tot);
-        m2 += p[1] + d * d * (n * (nk / tot));
-        n = tot;
-      }
-    for (int o = 1; o < gt; o <<= 1) {
-      const float on = __shfl_xor(n, o), om = __shfl_xor(mean, o), o2 = __shfl_xor(m2, o);
-      const float tot = n + on;
-      const bool low = (l & o) == 0;          // both sides merge (lower, upper) in the same order
-      const float na = low ? n : on, ma = low ? mean : om, sa = low ? m2 : o2;
-      const float nb = low ? on : n, mb = low ? om : mean, sb = low ? o2 : m2;
-      const float f = tot > 0.0f ? nb / tot : 0.0f, d = mb - ma;
-      mean = nb > 0.0f ? ma + d * f : ma;
-      m2 = sa + sb + (nb > 0.0f ? d * d * (na * f) : 0.0f);
-      n = tot;
+    const float2* p = (const float2*)a.part + (int64_t)img * chunks * a.groups + c0 / cg + g;
+    float mean = 0.0f, m2 = 0.0f;
+    // the first kKeep of a lane's chunks stay in registers, all their loads in flight at once
+    float2 c[kKeep];
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+      const int k = l + i * gt;
+      c[i] = g < ng && k < chunks ? p[(int64_t)k * a.groups] : make_float2(0.0f, 0.0f);
     }
+    const float full = (float)chunk * (float)cg, rest = (float)(a.pixels - (chunks - 1) * chunk) * (float)cg;
+    auto size = [&](int k) { return k < chunks - 1 ? full : (k == chunks - 1 ? rest : 0.0f); };
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) mean = fmaf(size(l + i * gt), c[i].x, mean);
+    if (g < ng)
+      for (int k = l + kKeep * gt; k < chunks; k += gt) mean = fmaf(size(k), p[(int64_t)k * a.groups].x, mean);
+    for (int o = gt >> 1; o > 0; o >>= 1) mean += __shfl_xor(mean, o);
+    mean /= n;
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+      const float d = c[i].x - mean;
+      m2 += fmaf(size(l + i * gt) * d, d, c[i].y);
+    }
+    if (g < ng)
+      for (int k = l + kKeep * gt; k < chunks; k += gt) {
+        const float2 x = p[(int64_t)k * a.groups];
+        const float d = x.x - mean;
+        m2 += fmaf(size(k) * d, d, x.y);
+      }
+    for (int o = gt >> 1; o > 0; o >>= 1) m2 += __shfl_xor(m2, o);
     if (g < ng && l == 0) {
       const float rstd = 1.0f / sqrtf(m2 / n + a.eps);
       L.g1[g] = mean;
@@ -300,9 +347,8 @@ __global__ __launch_bounds__(BLOCK) void norm_apply(NormArgs a, int nch, int sla
     }
   }
   __syncthreads();
-  float mul[V], add[V];
-  affine<BLOCK, V>(a, w, L, cg, mul, add);
-  write_normed<T, V, R, ACT>(a, w, x, mul, add);
+  af.template finish<BLOCK>(w, L, cg);
+  write_normed<T, V, R, ACT>(a, w, x, af.mul, af.add);
 }
 
 // ---- backward
@@ -316,12 +362,13 @@ struct Channel {
 template <int V>
 __device__ __forceinline__ Channel<V> load_channel(const NormArgs& a, const Share& w, int cg) {
   Channel<V> p;
+  const float inv = 1.0f / (float)cg;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     p.mean[j] = p.rstd[j] = p.wt[j] = p.bs[j] = 0.0f;
     if (w.active) {
       const int c = w.c0 + w.cv * V + j;
-      const float* st = a.stats + ((int64_t)w.img * a.groups + c / cg) * 2;
+      const float* st = a.stats + ((int64_t)w.img * a.groups + w.c0 / cg + small_div(w.cv * V + j, inv)) * 2;
       p.mean[j] = st[0];
       p.rstd[j] = st[1];
       p.wt[j] = a.weight ? a.weight[c] : 1.0f;
@@ -348,10 +395,40 @@ __device__ __forceinline__ void channel_sums(const Share& w, const Piece<T, V> (
       }
 }
 
-// Column sums over ty of a [TY][cols] buffer into out[cols].
-template <int BLOCK>
-__device__ __forceinline__ void column_sums(const float* buf, float* out, int TY, int cols) {
-  group_sums<BLOCK>(buf, out, TY, cols, 1);
+// The workgroup's sums of two values a channel, into L.g1 and L.g2: gt lanes a channel, in a fixed order.
+template <int BLOCK, int V>
+__device__ __forceinline__ void channel_totals(const Share& w, const float (&a)[V], const float (&b)[V],
+                                               Lds<BLOCK, V>& L) {
+  const int cols = w.nv * V;
+  if (w.active) {
+    const int at = w.ty * cols + w.cv * V;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      L.buf[at + j] = a[j];
+      L.buf2[at + j] = b[j];
+    }
+  }
+  __syncthreads();
+  int gt = 64;
+  while (gt > 1 && gt * cols > BLOCK) gt >>= 1;
+  for (int c0 = 0; c0 < cols; c0 += BLOCK / gt) {
+    const int c = c0 + (int)threadIdx.x / gt, l = threadIdx.x & (gt - 1);
+    float s = 0.0f, t = 0.0f;
+    if (c < cols)
+      for (int ty = l; ty < w.TY; ty += gt) {
+        s += L.buf[ty * cols + c];
+        t += L.buf2[ty * cols + c];
+      }
+    for (int o = gt >> 1; o > 0; o >>= 1) {
+      s += __shfl_xor(s, o);
+      t += __shfl_xor(t, o);
+    }
+    if (c < cols && l == 0) {
+      L.g1[c] = s;
+      L.g2[c] = t;
+    }
+  }
+  __syncthreads();
 }
 
 template <typename T, int V, int R, int ACT>
@@ -378,16 +455,16 @@ __device__ __forceinline__ void write_gx(const NormArgs& a, const Share& w, cons
 // Group means of u and u xh for the thread's channels, from per-channel sums of dz (L.g1) and dz xh (L.g2)
 // over the image, which the threads of a group add up in channel order.
 template <int BLOCK, int V>
-__device__ __forceinline__ void group_means(const NormArgs& a, const Share& w, const Lds<BLOCK, V>& L, int cg,
+__device__ __forceinline__ void group_means(const NormArgs& a, const Share& w, const Groups<BLOCK, V>& L, int cg,
                                             float (&m1)[V], float (&m2)[V]) {
-  const float inv = 1.0f / ((float)a.pixels * (float)cg);
+  const float inv = 1.0f / ((float)a.pixels * (float)cg), inv_cg = 1.0f / (float)cg;
   int last = -1;
   float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     m1[j] = m2[j] = 0.0f;
     if (w.active) {
-      const int g = (w.cv * V + j) / cg;
+      const int g = small_div(w.cv * V + j, inv_cg);
       if (g != last) {
         s1 = s2 = 0.0f;
         for (int c = g * cg; c < (g + 1) * cg; ++c) {
@@ -416,10 +493,7 @@ __global__ __launch_bounds__(BLOCK) void norm_bwd_whole(NormArgs a, int nch, int
   const Channel<V> p = load_channel<V>(a, w, cg);
   float sb[V], sw[V];
   channel_sums<T, V, R, ACT>(w, x, gy, p, sb, sw);
-  put_sums<V>(L.buf, w, V, sb);
-  column_sums<BLOCK>(L.buf, L.g1, w.TY, cols);
-  put_sums<V>(L.buf, w, V, sw);
-  column_sums<BLOCK>(L.buf, L.g2, w.TY, cols);
+  channel_totals<BLOCK, V>(w, sb, sw, L);
   float* part = a.part + (int64_t)img * 2 * a.C + c0;
   for (int c = threadIdx.x; c < cols; c += BLOCK) {
     part[c] = L.g1[c];
@@ -444,10 +518,7 @@ __global__ __launch_bounds__(BLOCK) void norm_bwd_sums(NormArgs a, int nch, int 
   const Channel<V> p = load_channel<V>(a, w, cg);
   float sb[V], sw[V];
   channel_sums<T, V, R, ACT>(w, x, gy, p, sb, sw);
-  put_sums<V>(L.buf, w, V, sb);
-  column_sums<BLOCK>(L.buf, L.g1, w.TY, cols);
-  put_sums<V>(L.buf, w, V, sw);
-  column_sums<BLOCK>(L.buf, L.g2, w.TY, cols);
+  channel_totals<BLOCK, V>(w, sb, sw, L);
   float* part = a.part + ((int64_t)img * chunks + ch) * 2 * a.C + c0;
   for (int c = threadIdx.x; c < cols; c += BLOCK) {
     part[c] = L.g1[c];
@@ -458,6 +529,7 @@ __global__ __launch_bounds__(BLOCK) void norm_bwd_sums(NormArgs a, int nch, int 
 // Sums of one column of the [rows][2 C] partial sums, by a wave.
 __device__ __forceinline__ float wave_column(const float* part, int64_t rows, int stride, int col) {
   float s = 0.0f;
+#pragma unroll 8
   for (int64_t r = threadIdx.x & 63; r < rows; r += 64) s += part[r * stride + col];
   for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
   return s;
@@ -481,7 +553,7 @@ __global__ __launch_bounds__(BLOCK) void norm_param_grads(NormArgs a, int64_t ro
 // The second: gx from the image's sums; the blocks behind the last chunk add up the parameters' gradients.
 template <int BLOCK, typename T, int V, int R, int ACT>
 __global__ __launch_bounds__(BLOCK) void norm_bwd_apply(NormArgs a, int nch, int slabs, int chunk, int chunks) {
-  __shared__ Lds<BLOCK, V> L;
+  __shared__ Groups<BLOCK, V> L;
   const int per_img = slabs * chunks, img = blockIdx.x / per_img, rest = blockIdx.x - img * per_img;
   if (img >= a.images) {
     param_grads<BLOCK>(a, (int64_t)a.images * chunks, blockIdx.x - a.images * per_img);
@@ -497,6 +569,7 @@ __global__ __launch_bounds__(BLOCK) void norm_bwd_apply(NormArgs a, int nch, int
   for (int c = threadIdx.x; c < 2 * cols; c += BLOCK) {
     const int col = c < cols ? c : a.C + c - cols;
     float s = 0.0f;
+#pragma unroll 16
     for (int k = 0; k < chunks; ++k) s += a.part[((int64_t)img * chunks + k) * 2 * a.C + c0 + col];
     (c < cols ? L.g1 : L.g2)[c < cols ? c : c - cols] = s;
   }
@@ -508,9 +581,11 @@ __global__ __launch_bounds__(BLOCK) void norm_bwd_apply(NormArgs a, int nch, int
 
 // ---- launch plan
 
-constexpr int kR = 16;          // pieces a thread holds (forward)
-constexpr int kRB = 8;          // pieces of x and of gy a thread holds (backward)
 constexpr int kSmall = 256, kBig = 1024;
+constexpr int kWhole = 2;       // pieces a thread of a kBig workgroup holds of a whole slab (32 KB)
+constexpr int kR = 8;           // pieces a thread holds of a chunk (forward)
+constexpr int kRA = 8;          // pieces a thread normalises (forward, the second launch)
+constexpr int kRB = 4;          // pieces of x and of gy a thread holds of a chunk (backward)
 
 struct Plan {
   bool whole;
@@ -526,20 +601,18 @@ Plan make_plan(const NormArgs& a, int R) {
   Plan p{};
   const int cg = a.C / a.groups;
   const int unit = cg / gcd(cg, a.vec) * a.vec;
-  // whole images: slabs of at least 64 bytes a pixel that fit kBig threads' registers
-  int want = 64 / a.elem_bytes;
+  // whole images: slabs of at least 64 bytes a pixel, up to kWhole pieces for each of kBig threads
+  const int want = 64 / a.elem_bytes;
   int nch = unit;
   while (nch < want && nch < a.C) nch += unit;
   if (nch > a.C) nch = a.C;
-  const int64_t fit = (int64_t)R * (kBig / (nch / a.vec > kBig ? kBig : nch / a.vec));
-  if (nch / a.vec <= kBig && a.pixels <= fit) {
+  if (nch / a.vec <= kBig && a.pixels <= (int64_t)kWhole * (kBig / (nch / a.vec))) {
     p.whole = true;
     p.nch = nch;
     p.slabs = (a.C + nch - 1) / nch;
-    p.big = a.pixels > (int64_t)R * (kSmall / (nch / a.vec > kSmall ? kSmall + 1 : nch / a.vec));
     return p;
   }
-  // chunks: all channels, or as many whole units as kSmall pieces hold
+  // chunks: all channels, or as many whole units as kSmall pieces hold (as kBig pieces, for a wide unit)
   nch = a.C;
   if (nch / a.vec > kSmall) {
     nch = kSmall * a.vec / unit * unit;
@@ -555,39 +628,38 @@ Plan make_plan(const NormArgs& a, int R) {
 }
 
 template <int BLOCK, typename T, int V, int ACT>
-hipError_t forward(const NormArgs& a, const Plan& p, hipStream_t stream) {
-  if (p.whole) {
-    norm_whole<BLOCK, T, V, kR, ACT><<<dim3((unsigned)(a.images * p.slabs)), BLOCK, 0, stream>>>(a, p.nch, p.slabs);
-  } else {
-    const dim3 grid((unsigned)(a.images * p.slabs * p.chunks));
-    norm_moments<BLOCK, T, V, kR><<<grid, BLOCK, 0, stream>>>(a, p.nch, p.slabs, p.chunk, p.chunks);
-    norm_apply<BLOCK, T, V, kR, ACT><<<grid, BLOCK, 0, stream>>>(a, p.nch, p.slabs, p.chunk, p.chunks);
-  }
-  return hipGetLastError();
+void forward(const NormArgs& a, const Plan& p, hipStream_t stream) {
+  const int share = kRA * (BLOCK / (p.nch / V)), shares = (a.pixels + share - 1) / share;
+  norm_moments<BLOCK, T, V, kR><<<dim3((unsigned)(a.images * p.slabs * p.chunks)), BLOCK, 0, stream>>>(
+      a, p.nch, p.slabs, p.chunk, p.chunks);
+  norm_apply<BLOCK, T, V, kRA, ACT><<<dim3((unsigned)(a.images * p.slabs * shares)), BLOCK, 0, stream>>>(
+      a, p.nch, p.slabs, p.chunk, p.chunks, share, shares);
 }
 
 template <int BLOCK, typename T, int V, int ACT>
-hipError_t backward(const NormArgs& a, const Plan& p, hipStream_t stream) {
-  const unsigned extra = (unsigned)((2 * a.C + BLOCK / 64 - 1) / (BLOCK / 64));
-  if (p.whole) {
-    norm_bwd_whole<BLOCK, T, V, kRB, ACT><<<dim3((unsigned)(a.images * p.slabs)), BLOCK, 0, stream>>>(a, p.nch,
-                                                                                                      p.slabs);
-    if (a.gweight || a.gbias)
-      norm_param_grads<BLOCK><<<dim3(extra), BLOCK, 0, stream>>>(a, a.images);
-  } else {
-    const unsigned n = (unsigned)(a.images * p.slabs * p.chunks);
-    norm_bwd_sums<BLOCK, T, V, kRB, ACT><<<dim3(n), BLOCK, 0, stream>>>(a, p.nch, p.slabs, p.chunk, p.chunks);
-    norm_bwd_apply<BLOCK, T, V, kRB, ACT>
-        <<<dim3(n + (a.gweight || a.gbias ? extra : 0)), BLOCK, 0, stream>>>(a, p.nch, p.slabs, p.chunk, p.chunks);
-  }
-  return hipGetLastError();
+void backward(const NormArgs& a, const Plan& p, hipStream_t stream) {
+  const unsigned extra = a.gweight || a.gbias ? (unsigned)((2 * a.C + BLOCK / 64 - 1) / (BLOCK / 64)) : 0;
+  const unsigned n = (unsigned)(a.images * p.slabs * p.chunks);
+  norm_bwd_sums<BLOCK, T, V, kRB, ACT><<<dim3(n), BLOCK, 0, stream>>>(a, p.nch, p.slabs, p.chunk, p.chunks);
+  norm_bwd_apply<BLOCK, T, V, kRB, ACT><<<dim3(n + extra), BLOCK, 0, stream>>>(a, p.nch, p.slabs, p.chunk, p.chunks);
 }
 
 template <typename T, int V, int ACT>
 hipError_t run(const NormArgs& a, bool bwd, hipStream_t stream) {
   const Plan p = make_plan(a, bwd ? kRB : kR);
-  if (bwd) return p.big ? backward<kBig, T, V, ACT>(a, p, stream) : backward<kSmall, T, V, ACT>(a, p, stream);
-  return p.big ? forward<kBig, T, V, ACT>(a, p, stream) : forward<kSmall, T, V, ACT>(a, p, stream);
+  const dim3 whole((unsigned)(a.images * p.slabs));
+  if (p.whole && !bwd) {
+    norm_whole<kBig, T, V, kWhole, ACT><<<whole, kBig, 0, stream>>>(a, p.nch, p.slabs);
+  } else if (p.whole) {
+    norm_bwd_whole<kBig, T, V, kWhole, ACT><<<whole, kBig, 0, stream>>>(a, p.nch, p.slabs);
+    if (a.gweight || a.gbias)
+      norm_param_grads<kSmall><<<dim3((unsigned)((2 * a.C + 3) / 4)), kSmall, 0, stream>>>(a, a.images);
+  } else if (bwd) {
+    p.big ? backward<kBig, T, V, ACT>(a, p, stream) : backward<kSmall, T, V, ACT>(a, p, stream);
+  } else {
+    p.big ? forward<kBig, T, V, ACT>(a, p, stream) : forward<kSmall, T, V, ACT>(a, p, stream);
+  }
+  return hipGetLastError();
 }
 
 template <typename T, int V>

@@ -49,13 +49,83 @@ struct alignas(sizeof(T) * V) Piece {
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__bf16 x) { return (float)x; }
 
-// A workgroup takes `tokens` tokens of one sample; items are (token, head, piece of V channels' pairs).
+constexpr int kAhead = 4;             // items a thread loads before the angles are ready
+
+// One item: a piece of V channels (and its V partners, half-split) of a token's head.
+template <typename T, int V, bool IL>
+struct Item {
+  using P = Piece<T, V>;
+  T* y;
+  const float2* turn;                 // the piece's angles, or NULL: it is copied
+  P u, w;
+
+  __device__ __forceinline__ void load(const RotaryArgs& a, const float2* table, int b, int t0, int e, int per_token,
+                                       int pieces, int turned) {
+    const int t = e / per_token, rest = e - t * per_token;
+    int h = rest / pieces;
+    const int c = rest - h * pieces;
+    const int which = h >= a.heads[0];
+    if (which) h -= a.heads[0];
+    const T* x = (const T*)a.x[which] + b * a.xs[which][0] + (t0 + t) * a.xs[which][1] + h * a.xs[which][2];
+    y = (T*)a.y[which] + b * a.ys[which][0] + (t0 + t) * a.ys[which][1] + h * a.ys[which][2];
+    turn = nullptr;
+    int at = 2 * a.P + (c - turned) * V;
+    if (c < turned) {
+      turn = table + t * a.P + (IL ? (V > 1 ? c * (V / 2) : c) : c * V);
+      at = IL && V == 1 ? 2 * c : c * V;
+    }
+    u = *(const P*)(x + at);
+    if (c < turned) {
+      if constexpr (!IL) w = *(const P*)(x + at + a.P);
+      if constexpr (IL && V == 1) w = *(const P*)(x + at + 1);     // rows without alignment: a pair at a time
+    }
+    y += at;
+  }
+
+  __device__ __forceinline__ void store(int half) const {
+    P p = u, q = w;
+    if (turn != nullptr) {
+      if constexpr (IL && V > 1) {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+          const float2 sc = turn[j];
+          const float x1 = to_f32(u.e[2 * j]), x2 = to_f32(u.e[2 * j + 1]);
+          p.e[2 * j] = (T)fmaf(x1, sc.y, -x2 * sc.x);
+          p.e[2 * j + 1] = (T)fmaf(x2, sc.y, x1 * sc.x);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float2 sc = turn[j];
+          const float x1 = to_f32(u.e[j]), x2 = to_f32(w.e[j]);
+          p.e[j] = (T)fmaf(x1, sc.y, -x2 * sc.x);
+          q.e[j] = (T)fmaf(x2, sc.y, x1 * sc.x);
+        }
+        *(P*)(y + (IL ? 1 : half)) = q;
+      }
+    }
+    *(P*)y = p;
+  }
+};
+
+// A workgroup takes `tokens` tokens of one sample: its threads issue the loads of their first items, form the angles
+// and then turn.  In place an item's loads all come before its stores, and no other item touches its channels.
 template <typename T, int V, bool IL>
 __global__ __launch_bounds__(kBlock) void rotary_kernel(RotaryArgs a, int tokens, int blocks_per_sample) {
   __shared__ float2 table[kTableMax];
   const int b = blockIdx.x / blocks_per_sample;
   const int t0 = (blockIdx.x - b * blocks_per_sample) * tokens;
   const int nt = min(tokens, a.T - t0);
+  // pieces of a head's row: rotated ones first (a half-split piece is V channels and their V partners)
+  const int turned = (IL && V > 1) ? 2 * a.P / V : a.P / V;
+  const int pieces = turned + (a.D - 2 * a.P) / V;
+  const int per_token = (a.heads[0] + a.heads[1]) * pieces, items = nt * per_token;
+  Item<T, V, IL> it[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    const int e = threadIdx.x + i * kBlock;
+    if (e < items) it[i].load(a, table, b, t0, e, per_token, pieces, turned);
+  }
   for (int e = threadIdx.x; e < nt * a.P; e += kBlock) {
     const int t = e / a.P, i = e - t * a.P;
     const float* p = a.pos + ((int64_t)b * a.T + t0 + t) * a.A;
@@ -66,62 +136,30 @@ __global__ __launch_bounds__(kBlock) void rotary_kernel(RotaryArgs a, int tokens
     table[e] = sc;
   }
   __syncthreads();
-  const int heads = a.heads[0] + a.heads[1];
-  // pieces of a head's row: rotated ones first (a half-split piece is V channels and their V partners)
-  const int turned = (IL && V > 1) ? 2 * a.P / V : a.P / V;
-  const int pieces = turned + (a.D - 2 * a.P) / V;
-  const int per_token = heads * pieces;
-  for (int e = threadIdx.x; e < nt * per_token; e += kBlock) {
-    const int t = e / per_token, rest = e - t * per_token;
-    int h = rest / pieces;
-    const int c = rest - h * pieces;
-    const int which = h >= a.heads[0];
-    if (which) h -= a.heads[0];
-    const T* x = (const T*)a.x[which] + b * a.xs[which][0] + (t0 + t) * a.xs[which][1] + h * a.xs[which][2];
-    T* y = (T*)a.y[which] + b * a.ys[which][0] + (t0 + t) * a.ys[which][1] + h * a.ys[which][2];
-    using P = Piece<T, V>;
-    if (c >= turned) {
-      const int at = 2 * a.P + (c - turned) * V;
-      *(P*)(y + at) = *(const P*)(x + at);
-    } else if constexpr (IL && V == 1) {      // rows without alignment: a pair at a time
-      const float2 sc = table[t * a.P + c];
-      const float x1 = to_f32(x[2 * c]), x2 = to_f32(x[2 * c + 1]);
-      y[2 * c] = (T)fmaf(x1, sc.y, -x2 * sc.x);
-      y[2 * c + 1] = (T)fmaf(x2, sc.y, x1 * sc.x);
-    } else if constexpr (IL) {
-      P v = *(const P*)(x + c * V);
 #pragma unroll
-      for (int j = 0; j < V / 2; ++j) {
-        const float2 sc = table[t * a.P + c * (V / 2) + j];
-        const float x1 = to_f32(v.e[2 * j]), x2 = to_f32(v.e[2 * j + 1]);
-        v.e[2 * j] = (T)fmaf(x1, sc.y, -x2 * sc.x);
-        v.e[2 * j + 1] = (T)fmaf(x2, sc.y, x1 * sc.x);
-      }
-      *(P*)(y + c * V) = v;
-    } else {
-      P u = *(const P*)(x + c * V), w = *(const P*)(x + a.P + c * V);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float2 sc = table[t * a.P + c * V + j];
-        const float x1 = to_f32(u.e[j]), x2 = to_f32(w.e[j]);
-        u.e[j] = (T)fmaf(x1, sc.y, -x2 * sc.x);
-        w.e[j] = (T)fmaf(x2, sc.y, x1 * sc.x);
-      }
-      *(P*)(y + c * V) = u;
-      *(P*)(y + a.P + c * V) = w;
-    }
+  for (int i = 0; i < kAhead; ++i)
+    if ((int)threadIdx.x + i * kBlock < items) it[i].store(a.P);
+  for (int e = threadIdx.x + kAhead * kBlock; e < items; e += kBlock) {
+    it[0].load(a, table, b, t0, e, per_token, pieces, turned);
+    it[0].store(a.P);
   }
 }
 
 template <typename T, int V>
 hipError_t launch(const RotaryArgs& a, hipStream_t stream) {
-  const int tokens = max(1, min(kMaxTokens, kBlock / a.P));
-  const int per = (a.T + tokens - 1) / tokens;
+  // at most one angle a thread, and no more items than the threads load ahead; few tokens are spread over the CUs
+  const int turned = (a.interleaved && V > 1) ? 2 * a.P / V : a.P / V;
+  const int64_t per_token = (int64_t)(a.heads[0] + a.heads[1]) * (turned + (a.D - 2 * a.P) / V);
+  int64_t tokens = kBlock / a.P < kMaxTokens ? kBlock / a.P : kMaxTokens;
+  if (tokens > kAhead * kBlock / per_token) tokens = kAhead * kBlock / per_token;
+  if (tokens > (int64_t)a.B * a.T / 512) tokens = (int64_t)a.B * a.T / 512;
+  if (tokens < 1) tokens = 1;
+  const int per = (int)((a.T + tokens - 1) / tokens);
   const dim3 grid((unsigned)((int64_t)a.B * per));
   if (a.interleaved)
-    rotary_kernel<T, V, true><<<grid, kBlock, 0, stream>>>(a, tokens, per);
+    rotary_kernel<T, V, true><<<grid, kBlock, 0, stream>>>(a, (int)tokens, per);
   else
-    rotary_kernel<T, V, false><<<grid, kBlock, 0, stream>>>(a, tokens, per);
+    rotary_kernel<T, V, false><<<grid, kBlock, 0, stream>>>(a, (int)tokens, per);
   return hipGetLastError();
 }
 

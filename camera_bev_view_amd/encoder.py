@@ -19,18 +19,22 @@ _DTYPES = {torch.float32: _lib.FBEV_DTYPE_F32, torch.bfloat16: _lib.FBEV_DTYPE_B
 _byref = ctypes.byref
 
 
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream      # current_stream().cuda_stream without the Stream object
+
+
 def _data(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr() or None
+    return None if t is None else t.data_ptr()
 
 
 def _call(name: str, dev: torch.device, *args) -> None:
     """The library's ``name``(*args, stream) on the current stream of ``dev``, with that device current."""
     fn = getattr(_lib.load(), name)
-    if torch.cuda.current_device() == dev.index:
-        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if _device() == dev.index:
+        status = fn(*args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            status = fn(*args, _raw_stream(dev.index))
     if status:
         _lib.check(status)
 
