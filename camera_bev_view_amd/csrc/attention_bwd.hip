@@ -29,7 +29,8 @@ struct Bwd {
 
 template <typename T, int DP>
 constexpr int min_waves(int hb) {
-  return sizeof(T) == 4 || DP > 32 ? 1 : hb == 2 ? 2 : 4;
+  if (sizeof(T) == 4) return DP <= 64 && hb == 1 ? 2 : 1;
+  return DP == 128 ? 1 : DP == 64 || hb == 2 ? 2 : 4;
 }
 
 // Writes own rows' sums (scaled), or adds the four waves' sums over LDS first.  dst(n) is own row n's
@@ -109,12 +110,14 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_row
   __shared__ alignas(16) float pos[BIAS ? 3 * MT : 1];   // [key][axis]
   __shared__ alignas(16) int docs[MT];
   __shared__ int doc_range[4][2];
+  __shared__ uint32_t stage_bits;
   __shared__ float slopes[KW > 1 && BIAS ? 4 : 1][3][32];
   char* Ks = smem;                                        // HB tiles each
   char* Vs = smem + HB * C::kTile;
 
   const int bid = xcd_block(blockIdx.x, gridDim.x);
-  const int tile = bid % tiles, bh = bid / tiles;
+  const int bh = bid / tiles, order = bid - bh * tiles;
+  const int tile = a.causal ? tiles - 1 - order : order;  // causal rows: those with the most keys first
   const int b = bh / (a.Hk / HB), hk = (bh - b * (a.Hk / HB)) * HB;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 31, h = lane >> 5;
   const int rw = wave / KW, kw = wave - rw * KW;
@@ -177,15 +180,18 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_row
   bool odd[HB] = {};                                      // the row sees a key with an infinite or NaN element
   float sum_ds[HB] = {}, sum_dsd[HB] = {}, sum_pd[HB] = {};
   const int k_end = min(a.Tk, blk_hi + 1);
+  uint32_t stages = 0;
   for (int s0 = 0; s0 < k_end; s0 += MT) {
     const int nk = min(MT, a.Tk - s0);
     int my_doc = -1;
     if (a.doc_q) {
+      const int stage = s0 / MT & 31;
+      if (stage == 0)
+        stages = stages_with<MT>(&stage_bits, s0, k_end, bmin, bmax, [&](int j) { return a.doc_k[(int64_t)b * a.Tk + j]; });
+      if (!((stages >> stage) & 1)) continue;
       if ((int)threadIdx.x < nk) my_doc = a.doc_k[(int64_t)b * a.Tk + s0 + threadIdx.x];
-      if (!__syncthreads_or(my_doc >= bmin && my_doc <= bmax)) continue;
-    } else {
-      __syncthreads();
     }
+    __syncthreads();
     const bool mixed = a.doc_q != nullptr || (a.causal && s0 + MT - 1 > blk_lo);
 #pragma unroll
     for (int i = 0; i < HB; ++i) {
@@ -330,6 +336,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_key
   __shared__ alignas(16) float lse2s[HB][MT], deltas[HB][MT], slopes[HB][BIAS ? MT : 4];
   __shared__ alignas(16) int docs[MT], lims[MT];
   __shared__ int doc_range[4][2];
+  __shared__ uint32_t stage_bits;
   char* Qs = smem;                                        // HB tiles each
   char* Gs = smem + HB * C::kTile;
 
@@ -374,18 +381,22 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_key
     const int64_t t0 = (int64_t)blk_key - a.Tk + a.Tq;
     if (t0 > 0) r_begin = (int)((t0 < a.Tq ? t0 : a.Tq) * a.G) / MT * MT;
   }
+  uint32_t stages = 0;
   for (int s0 = r_begin; s0 < a.R; s0 += MT) {
     const int nr = min(MT, a.R - s0);
     Row w;
     w.doc = -1, w.lim = -1;
+    if (a.doc_q) {
+      const int stage = (s0 - r_begin) / MT & 31;
+      if (stage == 0)
+        stages = stages_with<MT>(&stage_bits, s0, a.R, bmin, bmax,
+                                 [&](int r) { return a.doc_q[(int64_t)b * a.Tq + r / a.G]; });
+      if (!((stages >> stage) & 1)) continue;
+    }
     if (a.causal || a.doc_q) {
       if ((int)threadIdx.x < nr) w = make_row(a, b, hk, s0 + threadIdx.x);
     }
-    if (a.doc_q) {
-      if (!__syncthreads_or(w.doc >= bmin && w.doc <= bmax)) continue;
-    } else {
-      __syncthreads();
-    }
+    __syncthreads();
     // some row of the tile may not see some key of the workgroup
     const bool mixed = a.doc_q != nullptr ||
                        (a.causal && row_limit(a, b, s0 / a.G) < min(blk_key + 32 * RW, a.Tk) - 1);

@@ -41,6 +41,25 @@ __device__ __forceinline__ uint32_t opaque(uint32_t x) {
 // Keeps a sum's additions where they are written: sunk behind the next head's work they would hold its terms' registers.
 __device__ __forceinline__ void pin(float& x) { asm volatile("" : "+v"(x)); }
 
+// Bit i: the i-th of the next 32 stages (N moving rows each, from s0 on) has a row of a document in [lo, hi].  One round of
+// loads by the whole workgroup instead of one in front of every stage.
+template <int N, typename F>
+__device__ __forceinline__ uint32_t stages_with(uint32_t* shared, int s0, int end, int lo, int hi, F doc_of) {
+  __syncthreads();
+  if (threadIdx.x == 0) *shared = 0;
+  __syncthreads();
+  uint32_t bits = 0;
+#pragma unroll 4
+  for (int j = 0; j < 32 * N / 256; ++j) {
+    const int r = s0 + 256 * j + (int)threadIdx.x;
+    const int d = r < end ? doc_of(r) : INT32_MIN;
+    if (__any(d >= lo && d <= hi)) bits |= 1u << ((256 * j + ((int)threadIdx.x & ~63)) / N);
+  }
+  if ((threadIdx.x & 63) == 0 && bits != 0) atomicOr(shared, bits);
+  __syncthreads();
+  return (uint32_t)uniform((int)*shared);
+}
+
 // Over the two lanes of an own row.
 __device__ __forceinline__ float pair_max(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x),

@@ -12,6 +12,7 @@ namespace fbev {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kFewSplits = 8;
 
 // HB heads of a wave (two with a distance bias, whose distances they share), KW waves over the keys of a
 // row tile (their sums are joined at the end), 4 / KW row tiles.
@@ -27,7 +28,8 @@ struct Fwd {
 
 template <typename T, int DP>
 constexpr int min_waves(int hb) {
-  return sizeof(T) == 4 || DP > 64 ? 1 : DP == 64 ? 3 : 4;
+  if (sizeof(T) == 4) return DP <= 64 && hb == 1 ? 2 : 1;
+  return DP == 128 ? 2 : DP == 64 ? 3 : 4;
 }
 
 // Writes a head's rows (or their split's partial rows); the KW waves of a tile add up their parts first.
@@ -135,11 +137,14 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_fwd(Att
   __shared__ alignas(16) float pos[BIAS ? 3 * KT : 1];   // [key][axis]
   __shared__ alignas(16) int docs[KT];
   __shared__ int doc_range[4][2];
+  __shared__ uint32_t stage_bits;
   char* Ks = smem;                                        // HB tiles each
   char* Vs = smem + HB * C::kTile;
 
   const int bid = xcd_block(blockIdx.x, gridDim.x);
-  const int split = bid % a.splits, tile = bid / a.splits % tiles, bh = bid / a.splits / tiles;
+  const int split = bid % a.splits, bh = bid / a.splits / tiles;
+  const int order = bid / a.splits - bh * tiles;
+  const int tile = a.causal ? tiles - 1 - order : order;  // causal rows: those with the most keys first
   const int b = bh / (a.Hk / HB), hk = (bh - b * (a.Hk / HB)) * HB;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 31, h = lane >> 5;
   const int rw = wave / KW, kw = wave - rw * KW;
@@ -183,15 +188,18 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_fwd(Att
   for (int i = 0; i < HB; ++i) m[i] = kNegInf, l[i] = 0.0f;
   const int k_begin = split * a.split_keys;
   const int k_end = min(min(a.Tk, blk_hi + 1), (split + 1) * a.split_keys);
+  uint32_t stages = 0;
   for (int s0 = k_begin; s0 < k_end; s0 += KT) {
     const int nk = min(KT, a.Tk - s0);
     int my_doc = -1;
     if (a.doc_q) {
+      const int stage = (s0 - k_begin) / KT & 31;
+      if (stage == 0)
+        stages = stages_with<KT>(&stage_bits, s0, k_end, bmin, bmax, [&](int k) { return a.doc_k[(int64_t)b * a.Tk + k]; });
+      if (!((stages >> stage) & 1)) continue;
       if ((int)threadIdx.x < nk) my_doc = a.doc_k[(int64_t)b * a.Tk + s0 + threadIdx.x];
-      if (!__syncthreads_or(my_doc >= bmin && my_doc <= bmax)) continue;
-    } else {
-      __syncthreads();
     }
+    __syncthreads();
     // some row of the workgroup may not see some key
     const bool mixed = a.doc_q != nullptr || (a.causal && s0 + KT - 1 > blk_lo);
 #pragma unroll
@@ -295,7 +303,43 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_fwd(Att
   }
 }
 
-// Joins the splits of a row, one workgroup a row: the maximum and the weights over all threads, then wave w adds up
+// Joins the splits of a row.  Few of them: a wave a row, in split order.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void attn_join_few(AttnArgs a) {
+  const int64_t rows = (int64_t)a.B * a.Hk * a.R, row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= rows) return;
+  const int lane = threadIdx.x & 63;
+  const int64_t stride = rows * (a.D + 2);
+  const float* p = a.part + row * (a.D + 2);
+  float m[kFewSplits], top = kNegInf;
+#pragma unroll
+  for (int s = 0; s < kFewSplits; ++s) {
+    m[s] = s < a.splits ? p[s * stride + a.D] : kNegInf;
+    top = fmaxf(top, m[s]);
+  }
+  const float base = top == kNegInf ? 0.0f : top;
+  float tot = 0.0f, o[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int s = 0; s < kFewSplits; ++s)
+    if (s < a.splits) {
+      const float f = __builtin_amdgcn_exp2f(m[s] - base);
+      tot = fmaf(p[s * stride + a.D + 1], f, tot);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (lane + 64 * j < a.D) o[j] = fmaf(p[s * stride + lane + 64 * j], f, o[j]);
+    }
+  const int64_t bh = row / a.R;
+  const int r = (int)(row - bh * a.R), t = r / a.G, b = (int)(bh / a.Hk);
+  const int head = (int)(bh - (int64_t)b * a.Hk) * a.G + (r - t * a.G);
+  const float inv = tot > 0.0f || tot != tot ? 1.0f / tot : 0.0f;
+  T* out = (T*)a.out + (((int64_t)b * a.Tq + t) * a.Hq + head) * a.D;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (lane + 64 * j < a.D) out[lane + 64 * j] = (T)(o[j] * inv);
+  if (lane == 0) a.lse[((int64_t)b * a.Hq + head) * a.Tq + t] = tot == 0.0f ? kNegInf : top * kLn2 + logf(tot);
+}
+
+// Many: one workgroup a row, the maximum and the weights over all threads, then wave w adds up
 // splits w, w + 4, ... (their loads do not depend on each other) and the four sums are added in wave order.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void attn_join(AttnArgs a) {
@@ -385,7 +429,10 @@ hipError_t run(AttnArgs& a, const Plan& p, hipStream_t stream) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   const int64_t rows = (int64_t)a.B * a.Hk * a.R;
-  attn_join<T><<<dim3((unsigned)rows), kThreads, 0, stream>>>(a);
+  if (p.splits <= kFewSplits)
+    attn_join_few<T><<<dim3((unsigned)((rows + 3) / 4)), kThreads, 0, stream>>>(a);
+  else
+    attn_join<T><<<dim3((unsigned)rows), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
