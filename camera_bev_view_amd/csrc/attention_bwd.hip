@@ -24,13 +24,16 @@ struct Bwd {
   static constexpr size_t kTile = (size_t)MT * Tile<T, DP>::kRowBytes;
   static constexpr size_t kTiles = 2 * HB * kTile;
   static constexpr size_t kMerge = (size_t)4 * 32 * (DP + 4) * 4;
+  // two heads a wave: their own rows' fragments are read from LDS, which leaves registers for a third wave a SIMD
+  static constexpr bool kOwnLds = HB == 2;
+  static constexpr int kOwn = Mma<T, DP>::kFrags * 64 * 16;        // bytes of a tensor's fragments
   static constexpr size_t kBytes = KW == 1 || kTiles > kMerge ? kTiles : kMerge;
 };
 
 template <typename T, int DP>
 constexpr int min_waves(int hb) {
   if (sizeof(T) == 4) return DP <= 64 && hb == 1 ? 2 : 1;
-  return DP == 128 ? 1 : DP == 64 || hb == 2 ? 2 : 4;
+  return DP == 128 ? 1 : DP == 64 ? 2 : 3;
 }
 
 // Writes own rows' sums (scaled), or adds the four waves' sums over LDS first.  dst(n) is own row n's
@@ -124,21 +127,34 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_row
   const int first = tile * 32 * RW + rw * 32;
   const Row w = make_row(a, b, hk, min(first + n, a.R - 1));
   const Unit un = make_unit(a);
-  typename M::Frag q[HB][M::kFrags], go[HB][M::kFrags];
+  const Stager st = make_stager<T, DP>(a.D);
+  __shared__ alignas(16) char own_frags[C::kOwnLds ? RW * HB * 2 * C::kOwn : 16];   // [row tile][head][q, go]
+  char* own_at = own_frags + rw * HB * 2 * C::kOwn;
+  typename M::Frag q[C::kOwnLds ? 1 : HB][M::kFrags], go[C::kOwnLds ? 1 : HB][M::kFrags];
   float delta[HB], lse2[HB], slope[HB] = {};
 #pragma unroll
   for (int i = 0; i < HB; ++i) {
     const int64_t row_at = (((int64_t)b * a.Tq + w.t) * a.Hq + w.head + i) * a.D;
-    load_row<T, DP>((const T*)a.q + b * a.qs[0] + w.t * a.qs[1] + (w.head + i) * a.qs[2], a.vec, a.D, h, q[i]);
-    sign_row<T, DP>(a, q[i]);
-    load_row<T, DP>((const T*)a.gout + row_at, a.vec, a.D, h, go[i]);
+    constexpr bool L = C::kOwnLds;
+    auto& qi = q[L ? 0 : i];
+    auto& gi = go[L ? 0 : i];
+    load_row<T, DP>((const T*)a.q + b * a.qs[0] + w.t * a.qs[1] + (w.head + i) * a.qs[2], a.vec, a.D, h, qi);
+    sign_row<T, DP>(a, qi);
+    load_row<T, DP>((const T*)a.gout + row_at, a.vec, a.D, h, gi);
     typename M::Frag o[M::kFrags];
     load_row<T, DP>((const T*)a.out + row_at, a.vec, a.D, h, o);
     float sum = 0.0f;
 #pragma unroll
     for (int f = 0; f < M::kFrags; ++f)
 #pragma unroll
-      for (int j = 0; j < M::kFragElems; ++j) sum = fmaf((float)go[i][f][j], (float)o[f][j], sum);
+      for (int j = 0; j < M::kFragElems; ++j) sum = fmaf((float)gi[f][j], (float)o[f][j], sum);
+    if (L && kw == 0) {
+#pragma unroll
+      for (int f = 0; f < M::kFrags; ++f) {
+        *(typename M::Frag*)(own_at + 2 * i * C::kOwn + (f * 64 + lane) * 16) = qi[f];
+        *(typename M::Frag*)(own_at + (2 * i + 1) * C::kOwn + (f * 64 + lane) * 16) = gi[f];
+      }
+    }
     delta[i] = pair_sum(sum);
     float lse = a.lse[((int64_t)b * a.Hq + w.head + i) * a.Tq + w.t];
     if (lse == kNegInf) lse = -kNegInf;                   // a row without weights: all p are 0
@@ -196,9 +212,9 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_row
 #pragma unroll
     for (int i = 0; i < HB; ++i) {
       stage_rows<T, DP, MT>(Ks + i * C::kTile, (const T*)a.k + b * a.ks[0] + s0 * a.ks[1] + (hk + i) * a.ks[2], a.ks[1],
-                            nk, a.vec, a.D);
+                            nk, a.vec, a.D, st);
       stage_rows<T, DP, MT>(Vs + i * C::kTile, (const T*)a.v + b * a.vs[0] + s0 * a.vs[1] + (hk + i) * a.vs[2], a.vs[1],
-                            nk, a.vec, a.D);
+                            nk, a.vec, a.D, st);
     }
     if (a.doc_q && (int)threadIdx.x < MT) docs[threadIdx.x] = my_doc;
     if constexpr (BIAS) stage_floats(pos, a.pos_k + ((int64_t)b * a.Tk + s0) * a.dims, nk * a.dims, MT * a.dims);
@@ -226,8 +242,8 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_row
       __syncthreads();
     }
 #pragma unroll 1
-    for (int at = 32 * kw; at < MT; at += 32 * KW) {
-      const int key0 = s0 + at;
+    for (int sub = 0; sub < MT / (32 * KW); ++sub) {
+      const int at = 32 * (sub * KW + kw), key0 = s0 + at;
       if (key0 > lim_hi || key0 >= a.Tk) continue;
       bool whole = key0 + 31 <= lim_lo;
       if (a.doc_q) {
@@ -249,10 +265,17 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_row
       for (int hd = 0; hd < HB; ++hd) {
         __builtin_amdgcn_sched_barrier(0);                // one head's registers at a time
         const char* kt = Ks + hd * C::kTile;
-        f32x16 s = tile_dot<T, DP>(kt, at, q[hd], lane);
+        f32x16 s;
+        if constexpr (C::kOwnLds)
+          s = tile_dot<T, DP>(kt, at, own_at + 2 * hd * C::kOwn, lane);
+        else
+          s = tile_dot<T, DP>(kt, at, q[hd], lane);
         // dp - delta: the sum starts from -delta
-        f32x16 dp = tile_dot<T, DP>(Vs + hd * C::kTile, at, go[hd], lane,
-                                    outer_sum(h == 0 ? 1.0f : 0.0f, h == 0 ? -delta[hd] : 0.0f));
+        f32x16 dp = outer_sum(h == 0 ? 1.0f : 0.0f, h == 0 ? -delta[hd] : 0.0f);
+        if constexpr (C::kOwnLds)
+          dp = tile_dot<T, DP>(Vs + hd * C::kTile, at, own_at + (2 * hd + 1) * C::kOwn, lane, dp);
+        else
+          dp = tile_dot<T, DP>(Vs + hd * C::kTile, at, go[hd], lane, dp);
         f32x16 th;
         if constexpr (CAP) {
           cap_scores<T>(s, un.inv_cap);
@@ -348,12 +371,25 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_key
   const int key0 = tile * 32 * RW + rw * 32;              // the wave's keys
   const int key = min(key0 + n, a.Tk - 1);
   const Unit un = make_unit(a);
-  typename M::Frag k[HB][M::kFrags], v[HB][M::kFrags];
+  const Stager st = make_stager<T, DP>(a.D);
+  __shared__ alignas(16) char own_frags[C::kOwnLds ? RW * HB * 2 * C::kOwn : 16];   // [key tile][head][k, v]
+  char* own_at = own_frags + rw * HB * 2 * C::kOwn;
+  typename M::Frag k[C::kOwnLds ? 1 : HB][M::kFrags], v[C::kOwnLds ? 1 : HB][M::kFrags];
 #pragma unroll
   for (int i = 0; i < HB; ++i) {
-    load_row<T, DP>((const T*)a.k + b * a.ks[0] + key * a.ks[1] + (hk + i) * a.ks[2], a.vec, a.D, h, k[i]);
-    sign_row<T, DP>(a, k[i]);                             // the sign of the scale, on the side that only scores read
-    load_row<T, DP>((const T*)a.v + b * a.vs[0] + key * a.vs[1] + (hk + i) * a.vs[2], a.vec, a.D, h, v[i]);
+    constexpr bool L = C::kOwnLds;
+    auto& ki = k[L ? 0 : i];
+    auto& vi = v[L ? 0 : i];
+    load_row<T, DP>((const T*)a.k + b * a.ks[0] + key * a.ks[1] + (hk + i) * a.ks[2], a.vec, a.D, h, ki);
+    sign_row<T, DP>(a, ki);                               // the sign of the scale, on the side that only scores read
+    load_row<T, DP>((const T*)a.v + b * a.vs[0] + key * a.vs[1] + (hk + i) * a.vs[2], a.vec, a.D, h, vi);
+    if (L && kw == 0) {
+#pragma unroll
+      for (int f = 0; f < M::kFrags; ++f) {
+        *(typename M::Frag*)(own_at + 2 * i * C::kOwn + (f * 64 + lane) * 16) = ki[f];
+        *(typename M::Frag*)(own_at + (2 * i + 1) * C::kOwn + (f * 64 + lane) * 16) = vi[f];
+      }
+    }
   }
   float own[3] = {0.0f, 0.0f, 0.0f};
   if constexpr (BIAS) {
@@ -404,9 +440,9 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_key
     for (int i = 0; i < HB; ++i) {
       if (a.G == 1) {
         stage_rows<T, DP, MT>(Qs + i * C::kTile, (const T*)a.q + b * a.qs[0] + s0 * a.qs[1] + (hk + i) * a.qs[2],
-                              a.qs[1], nr, a.vec, a.D);
+                              a.qs[1], nr, a.vec, a.D, st);
         stage_rows<T, DP, MT>(Gs + i * C::kTile, (const T*)a.gout + (((int64_t)b * a.Tq + s0) * a.Hq + hk + i) * a.D,
-                              (int64_t)a.Hq * a.D, nr, a.vec, a.D);
+                              (int64_t)a.Hq * a.D, nr, a.vec, a.D, st);
       } else {
         stage_group<T, DP, MT>(Qs, (const T*)a.q + b * a.qs[0] + hk * a.G * a.qs[2], a.qs[1], a.qs[2], s0, a.G, nr, a.vec,
                                a.D);
@@ -458,7 +494,8 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_key
       __syncthreads();
     }
 #pragma unroll 1
-    for (int at = 32 * kw; at < MT; at += 32 * KW) {
+    for (int sub = 0; sub < MT / (32 * KW); ++sub) {
+      const int at = 32 * (sub * KW + kw);
       if (s0 + at >= a.R) continue;
       bool whole = true;
       if (a.causal || a.doc_q) {
@@ -482,8 +519,15 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_key
         // the sums start from -lse (in score units; a cap comes between) and -delta of the moving row
         const float one = h == 0 ? 1.0f : 0.0f;
         const float l2 = CAP || h != 0 ? 0.0f : -lse2s[hd][at + n];
-        f32x16 s = CAP ? tile_dot<T, DP>(qt, at, k[hd], lane) : tile_dot<T, DP>(qt, at, k[hd], lane, outer_sum(l2, one));
-        f32x16 dp = tile_dot<T, DP>(gt, at, v[hd], lane, outer_sum(h == 0 ? -deltas[hd][at + n] : 0.0f, one));
+        f32x16 s = {}, dp = outer_sum(h == 0 ? -deltas[hd][at + n] : 0.0f, one);
+        if constexpr (!CAP) s = outer_sum(l2, one);
+        if constexpr (C::kOwnLds) {
+          s = tile_dot<T, DP>(qt, at, own_at + 2 * hd * C::kOwn, lane, s);
+          dp = tile_dot<T, DP>(gt, at, own_at + (2 * hd + 1) * C::kOwn, lane, dp);
+        } else {
+          s = tile_dot<T, DP>(qt, at, k[hd], lane, s);
+          dp = tile_dot<T, DP>(gt, at, v[hd], lane, dp);
+        }
         f32x16 th;
         if constexpr (CAP) {
           cap_scores<T>(s, un.inv_cap);

@@ -232,27 +232,44 @@ __device__ __forceinline__ void stage_floats(float* lds, const float* base, int 
   for (int at = 64 * wave; at < room; at += 256) move_words(rs, lds + at, (at + lane) * 4);
 }
 
-// Stages N rows of a tensor, `stride` elements apart from `base` (uniform), zero beyond `rows` and beyond D channels, by
-// the four waves of the workgroup.  The wide path (vec: 16-byte pieces, N rows within 2^31 bytes) only issues the moves:
-// wait_staged() before the barrier.
-constexpr int kFarOut = 0x7FFFFF00;      // an offset the buffer's bounds turn into zeros
+// A thread's part in staging: row and byte offset of its piece within the first 256 pieces of a tile (an offset out of every
+// buffer's bounds for channels beyond D: such pieces become zeros).
+constexpr uint32_t kFarOut = 0x7FFFFF00u;
 
+struct Stager {
+  uint32_t row, byte;
+};
+
+template <typename T, int DP>
+__device__ __forceinline__ Stager make_stager(int D) {
+  using Tl = Tile<T, DP>;
+  const uint32_t tid = threadIdx.x, p = (tid % Tl::P) ^ (uint32_t)Tl::turn((int)(tid / Tl::P));
+  Stager s;
+  s.row = tid / Tl::P;
+  s.byte = p * Tl::E < (uint32_t)D ? p * 16 : kFarOut;
+  asm volatile("" : "+v"(s.row), "+v"(s.byte));      // kept, not formed again for every tile
+  return s;
+}
+
+// Stages N rows of a tensor, `stride` elements apart from `base` (uniform), zero beyond `rows` and beyond D channels, by
+// the four waves of the workgroup.  The wide path (vec: 16-byte pieces, N rows within 2^30 bytes) only issues the moves:
+// wait_staged() before the barrier.
 template <typename T, int DP, int N>
-__device__ __forceinline__ void stage_rows(char* tile, const T* base, int64_t stride, int rows, bool vec, int D) {
+__device__ __forceinline__ void stage_rows(char* tile, const T* base, int64_t stride, int rows, bool vec, int D,
+                                           const Stager& st) {
   using Tl = Tile<T, DP>;
   constexpr int CHUNKS = N * Tl::P / 64;                  // wave instructions
   static_assert(CHUNKS % 4 == 0 && (Tl::P < 32 ? 256 / Tl::P % 16 == 0 : 256 / Tl::P % 8 == 0),
                 "a wave's chunks repeat the turn of their rows");
   if (vec) {
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int s = 64 * wave + lane, r = s / Tl::P, p = (s % Tl::P) ^ Tl::turn(r);
-    const int bytes = (int)stride * (int)sizeof(T);
+    const int wave = uniform(threadIdx.x >> 6);
+    const uint32_t bytes = (uint32_t)stride * (uint32_t)sizeof(T);
     const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<T*>(base), 0, (rows - 1) * bytes + D * (int)sizeof(T), 0x00020000);
-    const int off = p * Tl::E < D ? r * bytes + p * 16 : kFarOut;
+        const_cast<T*>(base), 0, (int)((uint32_t)(rows - 1) * bytes + (uint32_t)D * (uint32_t)sizeof(T)), 0x00020000);
+    const int off = (int)(st.row * bytes + st.byte);
 #pragma unroll
     for (int k = 0; k < CHUNKS / 4; ++k)
-      move_pieces(rs, tile + (4 * k + wave) * 1024, off, k * (256 / Tl::P) * bytes);
+      move_pieces(rs, tile + (4 * k + wave) * 1024, off, k * (256 / Tl::P) * (int)bytes);
   } else {
 #pragma unroll 1
     for (int e = (int)opaque(threadIdx.x); e < N * DP; e += 256) {
@@ -278,7 +295,7 @@ __device__ __forceinline__ void stage_group(char* tile, const T* base, int64_t t
     for (int k = 0; k < N * Tl::P / 256; ++k) {
       const int s = 256 * k + 64 * wave + lane, r = s / Tl::P, p = (s % Tl::P) ^ Tl::turn(r);
       const int t = (r0 + r) / G, g = r0 + r - t * G;
-      const int off = r < rows && p * Tl::E < D ? (t - t0) * tb + g * hb + p * 16 : kFarOut;
+      const int off = r < rows && p * Tl::E < D ? (t - t0) * tb + g * hb + p * 16 : (int)kFarOut;
       move_pieces(rs, tile + (4 * k + wave) * 1024, off, 0);
     }
   } else {
@@ -308,6 +325,16 @@ __device__ __forceinline__ f32x16 tile_dot(const char* tile, int r0,
   using M = Mma<T, DP>;
 #pragma unroll
   for (int f = 0; f < M::kFrags; ++f) s = M::dot(tile_frag<T, DP>(tile, r0, f, lane), own[f], s);
+  return s;
+}
+
+// The same with the own row's fragments in LDS ([fragment][lane], 16 bytes each) instead of registers.
+template <typename T, int DP>
+__device__ __forceinline__ f32x16 tile_dot(const char* tile, int r0, const char* own, int lane, f32x16 s = f32x16{}) {
+  using M = Mma<T, DP>;
+#pragma unroll
+  for (int f = 0; f < M::kFrags; ++f)
+    s = M::dot(tile_frag<T, DP>(tile, r0, f, lane), *(const typename M::Frag*)(own + (f * 64 + lane) * 16), s);
   return s;
 }
 

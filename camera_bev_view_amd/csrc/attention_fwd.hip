@@ -29,7 +29,7 @@ struct Fwd {
 template <typename T, int DP>
 constexpr int min_waves(int hb) {
   if (sizeof(T) == 4) return DP <= 64 && hb == 1 ? 2 : 1;
-  return DP == 128 ? 2 : DP == 64 ? 3 : 4;
+  return DP == 128 || hb == 2 ? 2 : DP == 64 ? 3 : 4;
 }
 
 // Writes a head's rows (or their split's partial rows); the KW waves of a tile add up their parts first.
@@ -151,6 +151,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_fwd(Att
   const int first = tile * 32 * RW + rw * 32;            // the wave's rows
   const Row w = make_row(a, b, hk, min(first + n, a.R - 1));
   const Unit un = make_unit(a);
+  const Stager st = make_stager<T, DP>(a.D);
   typename M::Frag q[HB][M::kFrags];
 #pragma unroll
   for (int i = 0; i < HB; ++i) {
@@ -205,9 +206,9 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_fwd(Att
 #pragma unroll
     for (int i = 0; i < HB; ++i) {
       stage_rows<T, DP, KT>(Ks + i * C::kTile, (const T*)a.k + b * a.ks[0] + s0 * a.ks[1] + (hk + i) * a.ks[2], a.ks[1],
-                            nk, a.vec, a.D);
+                            nk, a.vec, a.D, st);
       stage_rows<T, DP, KT>(Vs + i * C::kTile, (const T*)a.v + b * a.vs[0] + s0 * a.vs[1] + (hk + i) * a.vs[2], a.vs[1],
-                            nk, a.vec, a.D);
+                            nk, a.vec, a.D, st);
     }
     if (a.doc_q && (int)threadIdx.x < KT) docs[threadIdx.x] = my_doc;
     if constexpr (BIAS) stage_floats(pos, a.pos_k + ((int64_t)b * a.Tk + s0) * a.dims, nk * a.dims, KT * a.dims);
@@ -238,8 +239,8 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_fwd(Att
       __syncthreads();
     }
 #pragma unroll 1
-    for (int at = 32 * kw; at < KT; at += 32 * KW) {
-      const int key0 = s0 + at;
+    for (int sub = 0; sub < KT / (32 * KW); ++sub) {
+      const int at = 32 * (sub * KW + kw), key0 = s0 + at;
       if (key0 > lim_hi || key0 >= a.Tk) continue;
       bool whole = key0 + 31 <= lim_lo;
       if (a.doc_q) {
