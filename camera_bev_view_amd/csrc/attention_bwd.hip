@@ -19,11 +19,12 @@ constexpr int kThreads = 256;
 // HB heads of a wave (two with a distance bias, whose distances they share), KW waves over the moving rows.
 template <typename T, int DP, int KW, int HB>
 struct Bwd {
-  static constexpr int RW = 4 / KW;
+  static constexpr int kWaves = KW == 8 ? 8 : 4, kThreads = 64 * kWaves;
+  static constexpr int RW = kWaves / KW;
   static constexpr int MT = KW == 1 ? 64 : 32 * KW;       // moving rows staged at a time
   static constexpr size_t kTile = (size_t)MT * Tile<T, DP>::kRowBytes;
   static constexpr size_t kTiles = 2 * HB * kTile;
-  static constexpr size_t kMerge = (size_t)4 * 32 * (DP + 4) * 4;
+  static constexpr size_t kMerge = (size_t)KW * 32 * (DP + 4) * 4;
   // two heads a wave: their own rows' fragments are read from LDS, which leaves registers for a third wave a SIMD
   static constexpr bool kOwnLds = HB == 2;
   static constexpr int kOwn = Mma<T, DP>::kFrags * 64 * 16;        // bytes of a tensor's fragments
@@ -36,12 +37,12 @@ constexpr int min_waves(int hb) {
   return DP == 128 ? 1 : DP == 64 ? 2 : 3;
 }
 
-// Writes own rows' sums (scaled), or adds the four waves' sums over LDS first.  dst(n) is own row n's
+// Writes own rows' sums (scaled), or adds the waves' sums over LDS first.  dst(n) is own row n's
 // address or NULL.
 template <typename T, int DP, int KW, typename F>
 __device__ __forceinline__ void write_own(f32x16 (&acc)[DP / 32], float scale, float* mo, int D, bool vec_out, int kw,
                                           int lane, F dst) {
-  constexpr int NB = DP / 32;
+  constexpr int NB = DP / 32, kThreads = KW == 8 ? 512 : 256;
   const int n = lane & 31, h = lane >> 5;
   if constexpr (KW == 1) {
     T* out = dst(n);
@@ -83,7 +84,7 @@ __device__ __forceinline__ void write_own(f32x16 (&acc)[DP / 32], float scale, f
       if (c >= D || out == nullptr) continue;
       float o = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o += mo[(k * 32 + r) * (DP + 4) + c];
+      for (int k = 0; k < KW; ++k) o += mo[(k * 32 + r) * (DP + 4) + c];
       out[c] = (T)(o * scale);
     }
   }
@@ -105,16 +106,16 @@ __device__ __forceinline__ RowStats row_stats(const AttnArgs& a, int64_t bh) {
 // ---- query rows: delta, gq, gslope
 
 template <typename T, int DP, int KW, int HB, bool BIAS, bool CAP>
-__global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_rows(AttnArgs a, int tiles) {
+__global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(HB))) void attn_bwd_rows(AttnArgs a, int tiles) {
   using C = Bwd<T, DP, KW, HB>;
   using M = Mma<T, DP>;
   constexpr int NB = DP / 32, MT = C::MT, RW = C::RW;
   __shared__ alignas(16) char smem[C::kBytes];
   __shared__ alignas(16) float pos[BIAS ? 3 * MT : 1];   // [key][axis]
   __shared__ alignas(16) int docs[MT];
-  __shared__ int doc_range[4][2];
+  __shared__ int doc_range[C::kWaves][2];
   __shared__ uint32_t stage_bits;
-  __shared__ float slopes[KW > 1 && BIAS ? 4 : 1][3][32];
+  __shared__ float slopes[KW > 1 && BIAS ? KW : 1][3][32];
   char* Ks = smem;                                        // HB tiles each
   char* Vs = smem + HB * C::kTile;
 
@@ -176,7 +177,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_row
   if constexpr (BIAS) {
     own_point(a.pos_q + ((int64_t)b * a.Tq + w.t) * a.dims, a.dims, h, own);
   }
-  for (int e = threadIdx.x; e < MT; e += kThreads) docs[e] = 0;
+  for (int e = threadIdx.x; e < MT; e += C::kThreads) docs[e] = 0;
   const int lim_lo = row_limit(a, b, min(first, a.R - 1) / a.G);
   const int lim_hi = row_limit(a, b, min(first + 31, a.R - 1) / a.G);
   const int blk_lo = row_limit(a, b, min(tile * 32 * RW, a.R - 1) / a.G);
@@ -187,8 +188,9 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_row
     dmax = wave_max(w.doc);
     if (lane == 0) doc_range[wave][0] = dmin, doc_range[wave][1] = dmax;
     __syncthreads();
-    bmin = min(min(doc_range[0][0], doc_range[1][0]), min(doc_range[2][0], doc_range[3][0]));
-    bmax = max(max(doc_range[0][1], doc_range[1][1]), max(doc_range[2][1], doc_range[3][1]));
+    bmin = doc_range[0][0], bmax = doc_range[0][1];
+#pragma unroll
+    for (int i = 1; i < C::kWaves; ++i) bmin = min(bmin, doc_range[i][0]), bmax = max(bmax, doc_range[i][1]);
   }
   const bool one_doc = dmin == dmax && wave_min(w.doc) == dmin;
 
@@ -203,7 +205,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_row
     if (a.doc_q) {
       const int stage = s0 / MT & 31;
       if (stage == 0)
-        stages = stages_with<MT>(&stage_bits, s0, k_end, bmin, bmax, [&](int j) { return a.doc_k[(int64_t)b * a.Tk + j]; });
+        stages = stages_with<MT, C::kThreads>(&stage_bits, s0, k_end, bmin, bmax, [&](int j) { return a.doc_k[(int64_t)b * a.Tk + j]; });
       if (!((stages >> stage) & 1)) continue;
       if ((int)threadIdx.x < nk) my_doc = a.doc_k[(int64_t)b * a.Tk + s0 + threadIdx.x];
     }
@@ -211,13 +213,13 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_row
     const bool mixed = a.doc_q != nullptr || (a.causal && s0 + MT - 1 > blk_lo);
 #pragma unroll
     for (int i = 0; i < HB; ++i) {
-      stage_rows<T, DP, MT>(Ks + i * C::kTile, (const T*)a.k + b * a.ks[0] + s0 * a.ks[1] + (hk + i) * a.ks[2], a.ks[1],
+      stage_rows<T, DP, MT, C::kThreads>(Ks + i * C::kTile, (const T*)a.k + b * a.ks[0] + s0 * a.ks[1] + (hk + i) * a.ks[2], a.ks[1],
                             nk, a.vec, a.D, st);
-      stage_rows<T, DP, MT>(Vs + i * C::kTile, (const T*)a.v + b * a.vs[0] + s0 * a.vs[1] + (hk + i) * a.vs[2], a.vs[1],
+      stage_rows<T, DP, MT, C::kThreads>(Vs + i * C::kTile, (const T*)a.v + b * a.vs[0] + s0 * a.vs[1] + (hk + i) * a.vs[2], a.vs[1],
                             nk, a.vec, a.D, st);
     }
     if (a.doc_q && (int)threadIdx.x < MT) docs[threadIdx.x] = my_doc;
-    if constexpr (BIAS) stage_floats(pos, a.pos_k + ((int64_t)b * a.Tk + s0) * a.dims, nk * a.dims, MT * a.dims);
+    if constexpr (BIAS) stage_floats<C::kThreads>(pos, a.pos_k + ((int64_t)b * a.Tk + s0) * a.dims, nk * a.dims, MT * a.dims);
     auto visible = [&](int at) {
       uint32_t vis = 0;
       const int hh = (int)opaque(h);
@@ -230,7 +232,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_row
     };
     wait_staged();
     __syncthreads();
-    if (mixed && __builtin_expect(__syncthreads_or(holds_odd<T, DP, HB * MT>(Ks)), 0)) {
+    if (mixed && __builtin_expect(__syncthreads_or(holds_odd<T, DP, HB * MT, C::kThreads>(Ks)), 0)) {
 #pragma unroll 1
       for (int at = 32 * kw; at < MT; at += 32 * KW) {
         const uint32_t vis = visible(at);
@@ -238,7 +240,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_row
         for (int hd = 0; hd < HB; ++hd) odd[hd] |= sees_odd<T, DP>(Ks + hd * C::kTile, at, vis, lane);
       }
       __syncthreads();
-      clean_rows<T, DP, HB * MT>(Ks);
+      clean_rows<T, DP, HB * MT, C::kThreads>(Ks);
       __syncthreads();
     }
 #pragma unroll 1
@@ -336,9 +338,9 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_row
         __syncthreads();
         if (h == 0) slopes[kw][0][n] = sd, slopes[kw][1][n] = bad ? __builtin_nanf("") : sdd, slopes[kw][2][n] = pd;
         __syncthreads();
-        sd = (slopes[0][0][n] + slopes[1][0][n]) + (slopes[2][0][n] + slopes[3][0][n]);
-        sdd = (slopes[0][1][n] + slopes[1][1][n]) + (slopes[2][1][n] + slopes[3][1][n]);
-        pd = (slopes[0][2][n] + slopes[1][2][n]) + (slopes[2][2][n] + slopes[3][2][n]);
+        sd = sdd = pd = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KW; ++k) sd += slopes[k][0][n], sdd += slopes[k][1][n], pd += slopes[k][2][n];
         bad = false;
       }
       if (kw == 0 && h == 0 && first + n < a.R)
@@ -350,7 +352,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_row
 // ---- keys: gk, gv
 
 template <typename T, int DP, int KW, int HB, bool BIAS, bool CAP>
-__global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_keys(AttnArgs a, int tiles) {
+__global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(HB))) void attn_bwd_keys(AttnArgs a, int tiles) {
   using C = Bwd<T, DP, KW, HB>;
   using M = Mma<T, DP>;
   constexpr int NB = DP / 32, MT = C::MT, RW = C::RW;
@@ -358,7 +360,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_key
   __shared__ alignas(16) float pos[BIAS ? 3 * MT : 1];   // [row][axis]
   __shared__ alignas(16) float lse2s[HB][MT], deltas[HB][MT], slopes[HB][BIAS ? MT : 4];
   __shared__ alignas(16) int docs[MT], lims[MT];
-  __shared__ int doc_range[4][2];
+  __shared__ int doc_range[C::kWaves][2];
   __shared__ uint32_t stage_bits;
   char* Qs = smem;                                        // HB tiles each
   char* Gs = smem + HB * C::kTile;
@@ -402,8 +404,9 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_key
     dmax = wave_max(doc);
     if (lane == 0) doc_range[wave][0] = dmin, doc_range[wave][1] = dmax;
     __syncthreads();
-    bmin = min(min(doc_range[0][0], doc_range[1][0]), min(doc_range[2][0], doc_range[3][0]));
-    bmax = max(max(doc_range[0][1], doc_range[1][1]), max(doc_range[2][1], doc_range[3][1]));
+    bmin = doc_range[0][0], bmax = doc_range[0][1];
+#pragma unroll
+    for (int i = 1; i < C::kWaves; ++i) bmin = min(bmin, doc_range[i][0]), bmax = max(bmax, doc_range[i][1]);
   }
   const bool one_doc = dmin == dmax && wave_min(doc) == dmin;
 
@@ -425,7 +428,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_key
     if (a.doc_q) {
       const int stage = (s0 - r_begin) / MT & 31;
       if (stage == 0)
-        stages = stages_with<MT>(&stage_bits, s0, a.R, bmin, bmax,
+        stages = stages_with<MT, C::kThreads>(&stage_bits, s0, a.R, bmin, bmax,
                                  [&](int r) { return a.doc_q[(int64_t)b * a.Tq + r / a.G]; });
       if (!((stages >> stage) & 1)) continue;
     }
@@ -439,14 +442,14 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_key
 #pragma unroll
     for (int i = 0; i < HB; ++i) {
       if (a.G == 1) {
-        stage_rows<T, DP, MT>(Qs + i * C::kTile, (const T*)a.q + b * a.qs[0] + s0 * a.qs[1] + (hk + i) * a.qs[2],
+        stage_rows<T, DP, MT, C::kThreads>(Qs + i * C::kTile, (const T*)a.q + b * a.qs[0] + s0 * a.qs[1] + (hk + i) * a.qs[2],
                               a.qs[1], nr, a.vec, a.D, st);
-        stage_rows<T, DP, MT>(Gs + i * C::kTile, (const T*)a.gout + (((int64_t)b * a.Tq + s0) * a.Hq + hk + i) * a.D,
+        stage_rows<T, DP, MT, C::kThreads>(Gs + i * C::kTile, (const T*)a.gout + (((int64_t)b * a.Tq + s0) * a.Hq + hk + i) * a.D,
                               (int64_t)a.Hq * a.D, nr, a.vec, a.D, st);
       } else {
-        stage_group<T, DP, MT>(Qs, (const T*)a.q + b * a.qs[0] + hk * a.G * a.qs[2], a.qs[1], a.qs[2], s0, a.G, nr, a.vec,
+        stage_group<T, DP, MT, C::kThreads>(Qs, (const T*)a.q + b * a.qs[0] + hk * a.G * a.qs[2], a.qs[1], a.qs[2], s0, a.G, nr, a.vec,
                                a.D);
-        stage_group<T, DP, MT>(Gs, (const T*)a.gout + ((int64_t)b * a.Tq * a.Hq + hk * a.G) * a.D, (int64_t)a.Hq * a.D,
+        stage_group<T, DP, MT, C::kThreads>(Gs, (const T*)a.gout + ((int64_t)b * a.Tq * a.Hq + hk * a.G) * a.D, (int64_t)a.Hq * a.D,
                                a.D, s0, a.G, nr, a.vec, a.D);
       }
     }
@@ -457,11 +460,11 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_key
 #pragma unroll
     for (int i = 0; i < HB; ++i) {
       const RowStats st = row_stats(a, (int64_t)b * a.Hk + hk + i);
-      stage_floats(lse2s[i], st.lse + s0, nr, MT);
-      stage_floats(deltas[i], st.delta + s0, nr, MT);
+      stage_floats<C::kThreads>(lse2s[i], st.lse + s0, nr, MT);
+      stage_floats<C::kThreads>(deltas[i], st.delta + s0, nr, MT);
       if constexpr (BIAS) {
-        stage_floats(slopes[i], st.slope + s0, nr, MT);
-        if (i == 0) stage_floats(pos, st.pos + (int64_t)s0 * a.dims, nr * a.dims, MT * a.dims);
+        stage_floats<C::kThreads>(slopes[i], st.slope + s0, nr, MT);
+        if (i == 0) stage_floats<C::kThreads>(pos, st.pos + (int64_t)s0 * a.dims, nr * a.dims, MT * a.dims);
       }
     }
     auto visible = [&](int at) {
@@ -476,7 +479,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_key
     };
     wait_staged();
     __syncthreads();
-    if (mixed && __builtin_expect(__syncthreads_or(holds_odd<T, DP, 2 * HB * MT>(Qs)), 0)) {
+    if (mixed && __builtin_expect(__syncthreads_or(holds_odd<T, DP, 2 * HB * MT, C::kThreads>(Qs)), 0)) {
 #pragma unroll 1
       for (int at = 32 * kw; at < MT; at += 32 * KW) {
         const uint32_t vis = visible(at);
@@ -490,7 +493,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_key
         }
       }
       __syncthreads();
-      clean_rows<T, DP, 2 * HB * MT>(Qs);
+      clean_rows<T, DP, 2 * HB * MT, C::kThreads>(Qs);
       __syncthreads();
     }
 #pragma unroll 1
@@ -575,34 +578,43 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_bwd_key
   }
 }
 
-// Workgroups of 128 own rows that share staged tiles when there are enough to fill the card several times over,
-// of 32 rows whose four waves split the moving rows otherwise.
-bool wide_tiles(const AttnArgs& a, int64_t heads, int rows) {
-  return heads * ((rows + 127) / 128) >= (a.D <= 64 ? 2048 : 512);
+// Waves that split the moving rows of a tile of own rows.
+template <typename T, int DP, int HB>
+int pick_waves(const AttnArgs& a, int64_t heads, int rows) {
+  // 128 own rows a workgroup, which share staged tiles, when there are enough to fill the card several times over
+  if (heads * ((rows + 127) / 128) >= (a.D <= 64 ? 2048 : 512)) return 1;
+  // too few workgroups to keep every SIMD busy and to even out masked ones: eight (512 workgroups of packed fp32 keys:
+  // the pass takes 266 us against 299 us; with 1024 of them eight waves lose what they gain)
+  if (HB == 1 && eight_waves<T>(DP) && heads * ((rows + 31) / 32) < 768) return 8;
+  return 4;
 }
 
 template <typename T, int DP, int HB, bool BIAS, bool CAP>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
   const int64_t heads = (int64_t)a.B * a.Hk / HB;
   if (a.R > 0) {
-    const bool wide = wide_tiles(a, heads, a.R);
-    const int tiles = (a.R + (wide ? 127 : 31)) / (wide ? 128 : 32);
+    const int kw = pick_waves<T, DP, HB>(a, heads, a.R), rows = kw == 1 ? 128 : 32;
+    const int tiles = (a.R + rows - 1) / rows;
     const dim3 grid((unsigned)(heads * tiles));
-    if (wide)
-      attn_bwd_rows<T, DP, 1, HB, BIAS, CAP><<<grid, kThreads, 0, stream>>>(a, tiles);
-    else
-      attn_bwd_rows<T, DP, 4, HB, BIAS, CAP><<<grid, kThreads, 0, stream>>>(a, tiles);
+    if (kw == 1)
+      attn_bwd_rows<T, DP, 1, HB, BIAS, CAP><<<grid, 256, 0, stream>>>(a, tiles);
+    else if (kw == 4)
+      attn_bwd_rows<T, DP, 4, HB, BIAS, CAP><<<grid, 256, 0, stream>>>(a, tiles);
+    else if constexpr (HB == 1 && eight_waves<T>(DP))
+      attn_bwd_rows<T, DP, 8, HB, BIAS, CAP><<<grid, 512, 0, stream>>>(a, tiles);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (a.Tk > 0) {
-    const bool wide = wide_tiles(a, heads, a.Tk);
-    const int tiles = (a.Tk + (wide ? 127 : 31)) / (wide ? 128 : 32);
+    const int kw = pick_waves<T, DP, HB>(a, heads, a.Tk), rows = kw == 1 ? 128 : 32;
+    const int tiles = (a.Tk + rows - 1) / rows;
     const dim3 grid((unsigned)(heads * tiles));
-    if (wide)
-      attn_bwd_keys<T, DP, 1, HB, BIAS, CAP><<<grid, kThreads, 0, stream>>>(a, tiles);
-    else
-      attn_bwd_keys<T, DP, 4, HB, BIAS, CAP><<<grid, kThreads, 0, stream>>>(a, tiles);
+    if (kw == 1)
+      attn_bwd_keys<T, DP, 1, HB, BIAS, CAP><<<grid, 256, 0, stream>>>(a, tiles);
+    else if (kw == 4)
+      attn_bwd_keys<T, DP, 4, HB, BIAS, CAP><<<grid, 256, 0, stream>>>(a, tiles);
+    else if constexpr (HB == 1 && eight_waves<T>(DP))
+      attn_bwd_keys<T, DP, 8, HB, BIAS, CAP><<<grid, 512, 0, stream>>>(a, tiles);
   }
   return hipGetLastError();
 }
@@ -615,7 +627,7 @@ hipError_t run(const AttnArgs& a, hipStream_t stream) {
   // two heads a wave where they share the distances and there are enough of them to fill the card
   if constexpr (DP == 32) {
     const int64_t shorter = a.R < a.Tk ? a.R : a.Tk;
-    if (a.G == 1 && a.Hk % 2 == 0 && (int64_t)a.B * a.Hk * ((shorter + 31) / 32) >= 1024)
+    if (a.G == 1 && a.Hk % 2 == 0 && (int64_t)a.B * a.Hk * ((shorter + 31) / 32) >= 512)
       return launch<T, DP, 2, true, false>(a, stream);
   }
   return launch<T, DP, 1, true, false>(a, stream);

@@ -43,17 +43,17 @@ __device__ __forceinline__ void pin(float& x) { asm volatile("" : "+v"(x)); }
 
 // Bit i: the i-th of the next 32 stages (N moving rows each, from s0 on) has a row of a document in [lo, hi].  One round of
 // loads by the whole workgroup instead of one in front of every stage.
-template <int N, typename F>
+template <int N, int THREADS, typename F>
 __device__ __forceinline__ uint32_t stages_with(uint32_t* shared, int s0, int end, int lo, int hi, F doc_of) {
   __syncthreads();
   if (threadIdx.x == 0) *shared = 0;
   __syncthreads();
   uint32_t bits = 0;
 #pragma unroll 4
-  for (int j = 0; j < 32 * N / 256; ++j) {
-    const int r = s0 + 256 * j + (int)threadIdx.x;
+  for (int j = 0; j < 32 * N / THREADS; ++j) {
+    const int r = s0 + THREADS * j + (int)threadIdx.x;
     const int d = r < end ? doc_of(r) : INT32_MIN;
-    if (__any(d >= lo && d <= hi)) bits |= 1u << ((256 * j + ((int)threadIdx.x & ~63)) / N);
+    if (__any(d >= lo && d <= hi)) bits |= 1u << ((THREADS * j + ((int)threadIdx.x & ~63)) / N);
   }
   if ((threadIdx.x & 63) == 0 && bits != 0) atomicOr(shared, bits);
   __syncthreads();
@@ -68,6 +68,12 @@ __device__ __forceinline__ float pair_max(float x) {
   return fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
 }
 __device__ __forceinline__ float pair_sum(float x) { return swap32_add(x, x); }
+
+// Eight waves over a tile's moving rows stage 256 of them at a time, two tensors: up to 128 KB.
+template <typename T>
+constexpr bool eight_waves(int dp) {
+  return 2 * 256 * dp * sizeof(T) <= (128 << 10);
+}
 
 // A staged tile of N rows: 16-byte pieces, P to a row, piece p of row r in slot r P + (p ^ turn(r)).  There is no padding,
 // so global memory moves straight into LDS (a wave's instruction fills 64 neighbouring slots, each lane fetching the piece
@@ -225,14 +231,15 @@ __device__ __forceinline__ void move_words(__amdgpu_buffer_rsrc_t rs, void* lds,
 #endif
 }
 
-// `count` of the up to `room` (a multiple of 64) floats at `base` (uniform), zeros behind them, by the four waves.
+// `count` of the up to `room` (a multiple of 64) floats at `base` (uniform), zeros behind them, by the whole workgroup.
+template <int THREADS>
 __device__ __forceinline__ void stage_floats(float* lds, const float* base, int count, int room) {
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(base), 0, count * 4, 0x00020000);
-  for (int at = 64 * wave; at < room; at += 256) move_words(rs, lds + at, (at + lane) * 4);
+  for (int at = 64 * wave; at < room; at += THREADS) move_words(rs, lds + at, (at + lane) * 4);
 }
 
-// A thread's part in staging: row and byte offset of its piece within the first 256 pieces of a tile (an offset out of every
+// A thread's part in staging: row and byte offset of its piece within a tile's first pieces, one a thread (an offset out of every
 // buffer's bounds for channels beyond D: such pieces become zeros).
 constexpr uint32_t kFarOut = 0x7FFFFF00u;
 
@@ -252,14 +259,14 @@ __device__ __forceinline__ Stager make_stager(int D) {
 }
 
 // Stages N rows of a tensor, `stride` elements apart from `base` (uniform), zero beyond `rows` and beyond D channels, by
-// the four waves of the workgroup.  The wide path (vec: 16-byte pieces, N rows within 2^30 bytes) only issues the moves:
+// the whole workgroup.  The wide path (vec: 16-byte pieces, N rows within 2^30 bytes) only issues the moves:
 // wait_staged() before the barrier.
-template <typename T, int DP, int N>
+template <typename T, int DP, int N, int THREADS>
 __device__ __forceinline__ void stage_rows(char* tile, const T* base, int64_t stride, int rows, bool vec, int D,
                                            const Stager& st) {
   using Tl = Tile<T, DP>;
-  constexpr int CHUNKS = N * Tl::P / 64;                  // wave instructions
-  static_assert(CHUNKS % 4 == 0 && (Tl::P < 32 ? 256 / Tl::P % 16 == 0 : 256 / Tl::P % 8 == 0),
+  constexpr int WAVES = THREADS / 64, CHUNKS = N * Tl::P / 64;      // wave instructions
+  static_assert(CHUNKS % WAVES == 0 && THREADS / Tl::P % (Tl::P < 32 ? 16 : 8) == 0,
                 "a wave's chunks repeat the turn of their rows");
   if (vec) {
     const int wave = uniform(threadIdx.x >> 6);
@@ -268,11 +275,11 @@ __device__ __forceinline__ void stage_rows(char* tile, const T* base, int64_t st
         const_cast<T*>(base), 0, (int)((uint32_t)(rows - 1) * bytes + (uint32_t)D * (uint32_t)sizeof(T)), 0x00020000);
     const int off = (int)(st.row * bytes + st.byte);
 #pragma unroll
-    for (int k = 0; k < CHUNKS / 4; ++k)
-      move_pieces(rs, tile + (4 * k + wave) * 1024, off, k * (256 / Tl::P) * (int)bytes);
+    for (int k = 0; k < CHUNKS / WAVES; ++k)
+      move_pieces(rs, tile + (WAVES * k + wave) * 1024, off, k * (THREADS / Tl::P) * (int)bytes);
   } else {
 #pragma unroll 1
-    for (int e = (int)opaque(threadIdx.x); e < N * DP; e += 256) {
+    for (int e = (int)opaque(threadIdx.x); e < N * DP; e += THREADS) {
       const int r = e / DP, c = e - r * DP;
       *Tl::at(tile, r, c) = r < rows && c < D ? base[r * stride + c] : (T)0.0f;
     }
@@ -280,7 +287,7 @@ __device__ __forceinline__ void stage_rows(char* tile, const T* base, int64_t st
 }
 
 // The same for N rows r0 .. of a key head's group of G query heads: row r is token r / G, head r mod G.
-template <typename T, int DP, int N>
+template <typename T, int DP, int N, int THREADS>
 __device__ __forceinline__ void stage_group(char* tile, const T* base, int64_t token, int64_t head, int r0, int G,
                                             int rows, bool vec, int D) {
   using Tl = Tile<T, DP>;
@@ -292,15 +299,15 @@ __device__ __forceinline__ void stage_group(char* tile, const T* base, int64_t t
     const __amdgpu_buffer_rsrc_t rs =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(first), 0, 0x7FFFFF00, 0x00020000);
 #pragma unroll
-    for (int k = 0; k < N * Tl::P / 256; ++k) {
-      const int s = 256 * k + 64 * wave + lane, r = s / Tl::P, p = (s % Tl::P) ^ Tl::turn(r);
+    for (int k = 0; k < N * Tl::P / THREADS; ++k) {
+      const int s = THREADS * k + 64 * wave + lane, r = s / Tl::P, p = (s % Tl::P) ^ Tl::turn(r);
       const int t = (r0 + r) / G, g = r0 + r - t * G;
       const int off = r < rows && p * Tl::E < D ? (t - t0) * tb + g * hb + p * 16 : (int)kFarOut;
-      move_pieces(rs, tile + (4 * k + wave) * 1024, off, 0);
+      move_pieces(rs, tile + (THREADS / 64 * k + wave) * 1024, off, 0);
     }
   } else {
 #pragma unroll 1
-    for (int e = (int)opaque(threadIdx.x); e < N * DP; e += 256) {
+    for (int e = (int)opaque(threadIdx.x); e < N * DP; e += THREADS) {
       const int r = e / DP, c = e - r * DP, t = (r0 + r) / G, g = r0 + r - t * G;
       *Tl::at(tile, r, c) = r < rows && c < D ? base[t * token + g * head + c] : (T)0.0f;
     }
@@ -342,11 +349,11 @@ __device__ __forceinline__ f32x16 tile_dot(const char* tile, int r0, const char*
 // 0 x inf is NaN: a non-finite element must reach only the own rows that see its tile row.  Tiles with masks are
 // searched for one (holds_odd), and only when there is one the workgroup notes which sums it belongs to (find_odd),
 // takes it out of the tile (clean_rows), and puts it back at the end (add_odd).
-template <typename T, int DP, int N>
+template <typename T, int DP, int N, int THREADS>
 __device__ __forceinline__ bool holds_odd(const char* tile) {
   uint32_t odd = 0;
 #pragma unroll 1
-  for (int e = (int)opaque(threadIdx.x); e < N * Tile<T, DP>::P; e += 256) {
+  for (int e = (int)opaque(threadIdx.x); e < N * Tile<T, DP>::P; e += THREADS) {
     const i32x4 w = *(const i32x4*)(tile + e * 16);
     // the exponent's ones carry into the sign bit
 #pragma unroll
@@ -356,10 +363,10 @@ __device__ __forceinline__ bool holds_odd(const char* tile) {
   return (odd & (sizeof(T) == 2 ? 0x80008000u : 0x80000000u)) != 0;
 }
 
-template <typename T, int DP, int N>
+template <typename T, int DP, int N, int THREADS>
 __device__ __forceinline__ void clean_rows(char* tile) {
 #pragma unroll 1
-  for (int e = (int)opaque(threadIdx.x); e < N * DP; e += 256) {
+  for (int e = (int)opaque(threadIdx.x); e < N * DP; e += THREADS) {
     T* x = (T*)tile + e;
     if (!(fabsf((float)*x) < __builtin_huge_valf())) *x = (T)0.0f;
   }

@@ -18,11 +18,12 @@ constexpr int kFewSplits = 8;
 // row tile (their sums are joined at the end), 4 / KW row tiles.
 template <typename T, int DP, int KW, int HB>
 struct Fwd {
-  static constexpr int RW = 4 / KW;                       // row tiles of a workgroup
+  static constexpr int kWaves = KW == 8 ? 8 : 4, kThreads = 64 * kWaves;
+  static constexpr int RW = kWaves / KW;                       // row tiles of a workgroup
   static constexpr int KT = KW == 1 ? 64 : 32 * KW;       // keys staged at a time
   static constexpr size_t kTile = (size_t)KT * Tile<T, DP>::kRowBytes;
   static constexpr size_t kTiles = 2 * HB * kTile;
-  static constexpr size_t kMerge = (size_t)4 * 32 * (DP + 4) * 4 + 4 * 32 * 8;
+  static constexpr size_t kMerge = (size_t)KW * 32 * (DP + 4) * 4 + KW * 32 * 8;
   static constexpr size_t kBytes = KW == 1 || kTiles > kMerge ? kTiles : kMerge;
 };
 
@@ -36,6 +37,7 @@ constexpr int min_waves(int hb) {
 template <typename T, int DP, int KW, int HB>
 __device__ __forceinline__ void finish(const AttnArgs& a, const Row& w, int first, int split, int64_t bh, int hd, int kw,
                                        int lane, f32x16 (&acc)[DP / 32], float m, float l, char* smem) {
+  using C = Fwd<T, DP, KW, HB>;
   constexpr int NB = DP / 32;
   const int n = lane & 31, h = lane >> 5, head = w.head + hd;
   const int b = (int)(bh / a.Hk), hk = (int)(bh - (int64_t)b * a.Hk);
@@ -75,18 +77,18 @@ __device__ __forceinline__ void finish(const AttnArgs& a, const Row& w, int firs
       }
     }
   } else {
-    // the four waves' sums over their keys, added in wave order
-    float* mo = (float*)smem;                       // [4][32][DP + 4]
-    float* ml = mo + 4 * 32 * (DP + 4);             // [4][32][2]
+    // the waves' sums over their keys, added in wave order
+    float* mo = (float*)smem;                       // [KW][32][DP + 4]
+    float* ml = mo + KW * 32 * (DP + 4);            // [KW][32][2]
     __syncthreads();
     if (h == 0) ml[(kw * 32 + n) * 2] = m, ml[(kw * 32 + n) * 2 + 1] = l;
     __syncthreads();
     float top = kNegInf;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[(k * 32 + n) * 2]);
+    for (int k = 0; k < KW; ++k) top = fmaxf(top, ml[(k * 32 + n) * 2]);
     float tot = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < KW; ++k) {
       const float mk = ml[(k * 32 + n) * 2];
       tot += ml[(k * 32 + n) * 2 + 1] * (mk == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(mk - top));
     }
@@ -112,12 +114,12 @@ __device__ __forceinline__ void finish(const AttnArgs& a, const Row& w, int firs
     if (kw == 0 && h == 0) ml[n * 2] = part ? 1.0f : (tot > 0.0f || tot != tot ? 1.0f / tot : 0.0f);
     __syncthreads();
     const int rows = min(32, a.R - first);
-    for (int e = threadIdx.x; e < rows * DP; e += kThreads) {
+    for (int e = threadIdx.x; e < rows * DP; e += C::kThreads) {
       const int r = e / DP, c = e - r * DP;
       if (c >= a.D) continue;
       float o = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o += mo[(k * 32 + r) * (DP + 4) + c];
+      for (int k = 0; k < KW; ++k) o += mo[(k * 32 + r) * (DP + 4) + c];
       const int row = first + r, t = row / a.G, hh = hk * a.G + (row - t * a.G);
       if (part)
         a.part[(((int64_t)split * a.B * a.Hk + bh) * a.R + row) * (a.D + 2) + c] = o;
@@ -128,7 +130,7 @@ __device__ __forceinline__ void finish(const AttnArgs& a, const Row& w, int firs
 }
 
 template <typename T, int DP, int KW, int HB, bool BIAS>
-__global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_fwd(AttnArgs a,
+__global__ __launch_bounds__((Fwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(HB))) void attn_fwd(AttnArgs a,
                                                                                                    int tiles) {
   using C = Fwd<T, DP, KW, HB>;
   using M = Mma<T, DP>;
@@ -136,7 +138,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_fwd(Att
   __shared__ alignas(16) char smem[C::kBytes];
   __shared__ alignas(16) float pos[BIAS ? 3 * KT : 1];   // [key][axis]
   __shared__ alignas(16) int docs[KT];
-  __shared__ int doc_range[4][2];
+  __shared__ int doc_range[C::kWaves][2];
   __shared__ uint32_t stage_bits;
   char* Ks = smem;                                        // HB tiles each
   char* Vs = smem + HB * C::kTile;
@@ -165,7 +167,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_fwd(Att
 #pragma unroll
     for (int i = 0; i < HB; ++i) slope[i] = a.slope[((int64_t)b * a.Tq + w.t) * a.Hq + w.head + i] / un.raw;
   }
-  for (int e = threadIdx.x; e < KT; e += kThreads) docs[e] = 0;
+  for (int e = threadIdx.x; e < KT; e += C::kThreads) docs[e] = 0;
   // the keys the workgroup's and the wave's rows can see by order
   const int lim_lo = row_limit(a, b, min(first, a.R - 1) / a.G);
   const int lim_hi = row_limit(a, b, min(first + 31, a.R - 1) / a.G);
@@ -177,8 +179,9 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_fwd(Att
     dmax = wave_max(w.doc);
     if (lane == 0) doc_range[wave][0] = dmin, doc_range[wave][1] = dmax;
     __syncthreads();
-    bmin = min(min(doc_range[0][0], doc_range[1][0]), min(doc_range[2][0], doc_range[3][0]));
-    bmax = max(max(doc_range[0][1], doc_range[1][1]), max(doc_range[2][1], doc_range[3][1]));
+    bmin = doc_range[0][0], bmax = doc_range[0][1];
+#pragma unroll
+    for (int i = 1; i < C::kWaves; ++i) bmin = min(bmin, doc_range[i][0]), bmax = max(bmax, doc_range[i][1]);
   }
   const bool one_doc = dmin == dmax && wave_min(w.doc) == dmin;   // every row of the wave in one document
 
@@ -196,7 +199,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_fwd(Att
     if (a.doc_q) {
       const int stage = (s0 - k_begin) / KT & 31;
       if (stage == 0)
-        stages = stages_with<KT>(&stage_bits, s0, k_end, bmin, bmax, [&](int k) { return a.doc_k[(int64_t)b * a.Tk + k]; });
+        stages = stages_with<KT, C::kThreads>(&stage_bits, s0, k_end, bmin, bmax, [&](int k) { return a.doc_k[(int64_t)b * a.Tk + k]; });
       if (!((stages >> stage) & 1)) continue;
       if ((int)threadIdx.x < nk) my_doc = a.doc_k[(int64_t)b * a.Tk + s0 + threadIdx.x];
     }
@@ -205,13 +208,13 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_fwd(Att
     const bool mixed = a.doc_q != nullptr || (a.causal && s0 + KT - 1 > blk_lo);
 #pragma unroll
     for (int i = 0; i < HB; ++i) {
-      stage_rows<T, DP, KT>(Ks + i * C::kTile, (const T*)a.k + b * a.ks[0] + s0 * a.ks[1] + (hk + i) * a.ks[2], a.ks[1],
+      stage_rows<T, DP, KT, C::kThreads>(Ks + i * C::kTile, (const T*)a.k + b * a.ks[0] + s0 * a.ks[1] + (hk + i) * a.ks[2], a.ks[1],
                             nk, a.vec, a.D, st);
-      stage_rows<T, DP, KT>(Vs + i * C::kTile, (const T*)a.v + b * a.vs[0] + s0 * a.vs[1] + (hk + i) * a.vs[2], a.vs[1],
+      stage_rows<T, DP, KT, C::kThreads>(Vs + i * C::kTile, (const T*)a.v + b * a.vs[0] + s0 * a.vs[1] + (hk + i) * a.vs[2], a.vs[1],
                             nk, a.vec, a.D, st);
     }
     if (a.doc_q && (int)threadIdx.x < KT) docs[threadIdx.x] = my_doc;
-    if constexpr (BIAS) stage_floats(pos, a.pos_k + ((int64_t)b * a.Tk + s0) * a.dims, nk * a.dims, KT * a.dims);
+    if constexpr (BIAS) stage_floats<C::kThreads>(pos, a.pos_k + ((int64_t)b * a.Tk + s0) * a.dims, nk * a.dims, KT * a.dims);
     // which of the tile's keys (16 of the lane's half) the lane's row sees
     auto visible = [&](int at) {
       uint32_t vis = 0;
@@ -225,7 +228,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_fwd(Att
     };
     wait_staged();
     __syncthreads();
-    if (mixed && __builtin_expect(__syncthreads_or(holds_odd<T, DP, HB * KT>(Vs)), 0)) {
+    if (mixed && __builtin_expect(__syncthreads_or(holds_odd<T, DP, HB * KT, C::kThreads>(Vs)), 0)) {
 #pragma unroll 1
       for (int at = 32 * kw; at < KT; at += 32 * KW) {
         const uint32_t vis = visible(at);
@@ -235,7 +238,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP>(HB))) void attn_fwd(Att
           for (int blk = 0; blk < NB; ++blk) odd[hd][blk] |= find_odd<T, DP>(Vs + hd * C::kTile, at, blk, vis, lane);
       }
       __syncthreads();
-      clean_rows<T, DP, HB * KT>(Vs);
+      clean_rows<T, DP, HB * KT, C::kThreads>(Vs);
       __syncthreads();
     }
 #pragma unroll 1
@@ -392,13 +395,21 @@ Plan make_plan(const AttnArgs& a) {
   p.hb = a.dims > 0 && a.G == 1 && a.Hk % 2 == 0 && a.D <= 32 && bh * ((a.R + 31) / 32) >= 1024 ? 2 : 1;
   // row tiles that share staged keys when they fill the card several times over, else keys over the waves
   p.kw = bh / p.hb * ((a.R + 127) / 128) >= (a.D <= 64 ? 2048 : 512) ? 1 : 4;
-  const int rows = 32 * (4 / p.kw), kt = p.kw == 1 ? 64 : 128;
+  const int64_t row_tiles = bh * ((a.R + 31) / 32);
+  // under 512 workgroups of four waves a SIMD has one wave or none: eight a workgroup (900 fp32 queries, 232 workgroups:
+  // 22.4 us against 25.7 us with the keys in two splits); 928 workgroups lose by it (32.1 against 27.3 us)
+  const int dp = a.D <= 32 ? 32 : a.D <= 64 ? 64 : 128;
+  if (p.kw == 4 && p.hb == 1 && (a.elem_bytes == 4 ? eight_waves<float>(dp) : eight_waves<__bf16>(dp)) &&
+      row_tiles >= 128 && row_tiles < 512)
+    p.kw = 8;
+  const int rows = p.kw == 1 ? 128 : 32, kt = p.kw == 1 ? 64 : 32 * p.kw;
   p.tiles = (a.R + rows - 1) / rows;
+  // under 128 workgroups the keys are split over several (at least 512 each, four workgroups a CU at most) and joined
   const int64_t blocks = bh / p.hb * p.tiles;
   p.splits = 1;
-  if (blocks < 256) {
+  if (blocks < 128) {
     int64_t want = (1024 + blocks - 1) / blocks;
-    const int64_t most = (a.Tk + 4 * kt - 1) / (4 * kt);
+    const int64_t most = (a.Tk + 511) / 512;
     if (want > most) want = most;
     p.splits = want < 1 ? 1 : (int)want;
   }
@@ -412,10 +423,13 @@ Plan make_plan(const AttnArgs& a) {
 template <typename T, int DP, int HB, bool BIAS>
 void launch(const AttnArgs& a, const Plan& p, hipStream_t stream) {
   const dim3 grid((unsigned)((int64_t)a.B * a.Hk / HB * p.tiles * p.splits));
-  if (p.kw == 1)
-    attn_fwd<T, DP, 1, HB, BIAS><<<grid, kThreads, 0, stream>>>(a, p.tiles);
-  else
-    attn_fwd<T, DP, 4, HB, BIAS><<<grid, kThreads, 0, stream>>>(a, p.tiles);
+  if (p.kw == 1) {
+    attn_fwd<T, DP, 1, HB, BIAS><<<grid, 256, 0, stream>>>(a, p.tiles);
+  } else if (p.kw == 4) {
+    attn_fwd<T, DP, 4, HB, BIAS><<<grid, 256, 0, stream>>>(a, p.tiles);
+  } else {
+    if constexpr (HB == 1 && eight_waves<T>(DP)) attn_fwd<T, DP, 8, HB, BIAS><<<grid, 512, 0, stream>>>(a, p.tiles);
+  }
 }
 
 template <typename T, int DP>

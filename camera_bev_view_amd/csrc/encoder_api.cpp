@@ -325,7 +325,15 @@ fbev_status fbev_attention_workspace(const fbev_attention_desc* ad, int32_t back
   if (s != FBEV_OK) return s;
   *bytes = 0;
   if ((int64_t)a.B * a.R == 0) return FBEV_OK;
-  *bytes = backward ? fbev::attention_backward_workspace_bytes(a) : fbev::attention_forward_workspace_bytes(a);
+  if (backward) {
+    *bytes = fbev::attention_backward_workspace_bytes(a);
+    return FBEV_OK;
+  }
+  // the split of the keys depends on the type: the size covers both
+  for (a.elem_bytes = 4; a.elem_bytes >= 2; a.elem_bytes -= 2) {
+    const size_t n = fbev::attention_forward_workspace_bytes(a);
+    if (n > *bytes) *bytes = n;
+  }
   return FBEV_OK;
 }
 
