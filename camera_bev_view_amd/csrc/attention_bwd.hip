@@ -21,7 +21,7 @@ template <typename T, int DP, int KW, int HB>
 struct Bwd {
   static constexpr int kWaves = KW == 8 ? 8 : 4, kThreads = 64 * kWaves;
   static constexpr int RW = kWaves / KW;
-  static constexpr int MT = KW == 1 ? 64 : 32 * KW;       // moving rows staged at a time
+  static constexpr int MT = KW == 1 ? shared_rows<T>(DP) : 32 * KW;   // moving rows staged at a time
   static constexpr size_t kTile = (size_t)MT * Tile<T, DP>::kRowBytes;
   static constexpr size_t kTiles = 2 * HB * kTile;
   static constexpr size_t kMerge = (size_t)KW * 32 * (DP + 4) * 4;

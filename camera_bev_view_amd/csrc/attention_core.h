@@ -75,6 +75,12 @@ constexpr bool eight_waves(int dp) {
   return 2 * 256 * dp * sizeof(T) <= (128 << 10);
 }
 
+// Moving rows that four row tiles share: 128, where two workgroups' tiles fit a CU's LDS.
+template <typename T>
+constexpr int shared_rows(int dp) {
+  return 2 * 128 * dp * sizeof(T) <= (64 << 10) ? 128 : 64;
+}
+
 // A staged tile of N rows: 16-byte pieces, P to a row, piece p of row r in slot r P + (p ^ turn(r)).  There is no padding,
 // so global memory moves straight into LDS (a wave's instruction fills 64 neighbouring slots, each lane fetching the piece
 // that belongs there); the turn spreads the rows over the banks, both for a row's pieces read by 32 lanes (all 16 bank

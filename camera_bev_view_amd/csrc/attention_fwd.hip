@@ -20,7 +20,7 @@ template <typename T, int DP, int KW, int HB>
 struct Fwd {
   static constexpr int kWaves = KW == 8 ? 8 : 4, kThreads = 64 * kWaves;
   static constexpr int RW = kWaves / KW;                       // row tiles of a workgroup
-  static constexpr int KT = KW == 1 ? 64 : 32 * KW;       // keys staged at a time
+  static constexpr int KT = KW == 1 ? shared_rows<T>(DP) : 32 * KW;   // keys staged at a time
   static constexpr size_t kTile = (size_t)KT * Tile<T, DP>::kRowBytes;
   static constexpr size_t kTiles = 2 * HB * kTile;
   static constexpr size_t kMerge = (size_t)KW * 32 * (DP + 4) * 4 + KW * 32 * 8;
@@ -256,7 +256,7 @@ __global__ __launch_bounds__((Fwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
       if constexpr (BIAS) distances(pos, at, a.dims, own, lane, d);
 #pragma unroll
       for (int hd = 0; hd < HB; ++hd) {
-        __builtin_amdgcn_sched_barrier(0);      // one head's registers at a time
+        if constexpr (HB > 1) __builtin_amdgcn_sched_barrier(0);      // one head's registers at a time
         f32x16 s = tile_dot<T, DP>(Ks + hd * C::kTile, at, q[hd], lane);
         if (a.cap > 0.0f) cap_scores<T>(s, un.inv_cap);
         if constexpr (BIAS) {
@@ -268,7 +268,7 @@ __global__ __launch_bounds__((Fwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
 #pragma unroll
           for (int i = 0; i < 16; ++i) s[i] = (vis >> i) & 1 ? s[i] : kNegInf;
         }
-        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (HB > 1) __builtin_amdgcn_sched_barrier(0);
         float top = fmaxf(s[0], s[1]);
 #pragma unroll
         for (int i = 2; i < 16; i += 2) top = fmaxf(fmaxf(top, s[i]), s[i + 1]);
@@ -293,7 +293,7 @@ __global__ __launch_bounds__((Fwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
         }
         l[hd] += sum;
         pin(l[hd]);
-        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (HB > 1) __builtin_amdgcn_sched_barrier(0);
         M::template accumulate<NB>(acc[hd], M::pack(s), Vs + hd * C::kTile, at, lane);
       }
     }
@@ -402,7 +402,7 @@ Plan make_plan(const AttnArgs& a) {
   if (p.kw == 4 && p.hb == 1 && (a.elem_bytes == 4 ? eight_waves<float>(dp) : eight_waves<__bf16>(dp)) &&
       row_tiles >= 128 && row_tiles < 512)
     p.kw = 8;
-  const int rows = p.kw == 1 ? 128 : 32, kt = p.kw == 1 ? 64 : 32 * p.kw;
+  const int rows = p.kw == 1 ? 128 : 32, kt = p.kw == 1 ? 128 : 32 * p.kw;
   p.tiles = (a.R + rows - 1) / rows;
   // under 128 workgroups the keys are split over several (at least 512 each, four workgroups a CU at most) and joined
   const int64_t blocks = bh / p.hb * p.tiles;

@@ -116,6 +116,18 @@ def test_many_heads_share_staged_keys(D, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+def test_every_number_of_waves_and_rows(dtype):
+    """Grids that take eight waves a row tile (forward too), and narrow heads in 128-row workgroups."""
+    docs = [runs([40, 33, 20], 95)] * 4
+    for D in (32, 64, 128):
+        check(*draw(4, 95, 300, 16, 16, D, dtype, 53, dims=1, cap=6.0), f"eight waves D={D}")
+        check(*draw(4, 95, 95, 16, 16, D, dtype, 54, docs=(docs, docs), causal=True), f"eight waves documents D={D}")
+    check(*draw(16, 21, 40, 128, 128, 16, dtype, 55), "128-row workgroups, dense")
+    check(*draw(16, 40, 40, 128, 128, 16, dtype, 56, causal=True, dims=2, cap=3.0), "128-row workgroups, causal")
+    check(*draw(16, 35, 21, 256, 128, 40, dtype, 57, causal=True), "128-row workgroups, grouped heads")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("form", ["dense", "causal", "documents"])
 def test_two_heads_share_their_distances(form, dtype):
     """Enough heads with a distance bias that a wave takes two: dense, causal and packed, 1 to 3 axes."""
