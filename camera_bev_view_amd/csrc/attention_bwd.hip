@@ -90,17 +90,18 @@ __device__ __forceinline__ void write_own(f32x16 (&acc)[DP / 32], float scale, f
   }
 }
 
-// A (sample, key head)'s rows in the workspace: delta and lse, with a bias slope and position (lse and slope in score
-// units).
+// A (sample, key head)'s rows in the workspace, for the keys' launch: delta, the exponents' offset (fp32: the maximum m;
+// bf16: m + log2 l, in score units unless a cap comes between) and 1 / l, with a bias slope and position.
 struct RowStats {
-  float *delta, *lse, *slope, *pos;
+  float *delta, *off, *inv, *slope, *pos;
 };
 
-__host__ __device__ __forceinline__ int64_t stat_floats(const AttnArgs& a) { return a.dims ? 3 + a.dims : 2; }
+__host__ __device__ __forceinline__ int64_t stat_floats(const AttnArgs& a) { return a.dims ? 4 + a.dims : 3; }
 
 __device__ __forceinline__ RowStats row_stats(const AttnArgs& a, int64_t bh) {
   float* p = a.delta + bh * a.R * stat_floats(a);
-  return RowStats{p, p + a.R, p + 2 * (int64_t)a.R, p + 3 * (int64_t)a.R};
+  const int64_t R = a.R;
+  return RowStats{p, p + R, p + 2 * R, p + 3 * R, p + 4 * R};
 }
 
 // ---- query rows: delta, gq, gslope
@@ -115,7 +116,7 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
   __shared__ alignas(16) int docs[MT];
   __shared__ int doc_range[C::kWaves][2];
   __shared__ uint32_t stage_bits;
-  __shared__ float slopes[KW > 1 && BIAS ? KW : 1][3][32];
+  __shared__ float slopes[KW][3][32];
   char* Ks = smem;                                        // HB tiles each
   char* Vs = smem + HB * C::kTile;
 
@@ -132,7 +133,7 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
   __shared__ alignas(16) char own_frags[C::kOwnLds ? RW * HB * 2 * C::kOwn : 16];   // [row tile][head][q, go]
   char* own_at = own_frags + rw * HB * 2 * C::kOwn;
   typename M::Frag q[C::kOwnLds ? 1 : HB][M::kFrags], go[C::kOwnLds ? 1 : HB][M::kFrags];
-  float delta[HB], lse2[HB], slope[HB] = {};
+  float delta[HB], neg_m[HB], inv_l[HB], slope[HB] = {};
 #pragma unroll
   for (int i = 0; i < HB; ++i) {
     const int64_t row_at = (((int64_t)b * a.Tq + w.t) * a.Hq + w.head + i) * a.D;
@@ -157,19 +158,21 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
       }
     }
     delta[i] = pair_sum(sum);
-    float lse = a.lse[((int64_t)b * a.Hq + w.head + i) * a.Tq + w.t];
-    if (lse == kNegInf) lse = -kNegInf;                   // a row without weights: all p are 0
-    lse2[i] = lse * kLog2e;
+    // exponentials are taken around the forward's maximum and divided by its sum at the end: a logarithm of the sum
+    // would be off by its own size times 2^-24.  A row without weights: all p are 0.
+    const float2 ml = a.stats[((int64_t)b * a.Hq + w.head + i) * a.Tq + w.t];
+    neg_m[i] = ml.y == 0.0f ? kNegInf : -ml.x;
+    inv_l[i] = ml.y == 0.0f ? 0.0f : 1.0f / ml.y;
     if constexpr (BIAS) slope[i] = a.slope[((int64_t)b * a.Tq + w.t) * a.Hq + w.head + i] / un.raw;
-    // what the keys' launch needs of its moving rows, in the order it walks them
     if (kw == 0 && h == 0 && first + n < a.R) {
-      const RowStats st = row_stats(a, (int64_t)b * a.Hk + hk + i);
-      st.delta[w.r] = delta[i];
-      st.lse[w.r] = CAP ? lse2[i] : lse / un.raw;
+      const RowStats rs = row_stats(a, (int64_t)b * a.Hk + hk + i);
+      const float lse2 = ml.y == 0.0f ? -kNegInf : ml.x + __builtin_amdgcn_logf(ml.y);
+      rs.off[w.r] = sizeof(T) == 4 ? -neg_m[i] : CAP ? lse2 : lse2 / un.unit;
+      rs.inv[w.r] = inv_l[i];
       if constexpr (BIAS) {
-        st.slope[w.r] = slope[i];
+        rs.slope[w.r] = slope[i];
         for (int ax = 0; ax < a.dims; ++ax)
-          st.pos[(int64_t)w.r * a.dims + ax] = a.pos_q[((int64_t)b * a.Tq + w.t) * a.dims + ax];
+          rs.pos[(int64_t)w.r * a.dims + ax] = a.pos_q[((int64_t)b * a.Tq + w.t) * a.dims + ax];
       }
     }
   }
@@ -295,32 +298,38 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
             dp[i] = (vis >> i) & 1 ? dp[i] : 0.0f;
           }
         }
+        float t_ds = 0.0f, t_dsd = 0.0f, t_pd = 0.0f;     // a tile's sums first: thousands of keys in one chain add up errors
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float p = __builtin_amdgcn_exp2f(fmaf(s[i], un.unit, -lse2[hd]));
+          const float p = __builtin_amdgcn_exp2f(fmaf(s[i], un.unit, neg_m[hd]));
           s[i] = p * dp[i];
+          t_ds += s[i];
           if constexpr (BIAS) {
-            sum_ds[hd] += s[i];
-            sum_dsd[hd] = fmaf(s[i], d[i], sum_dsd[hd]);
-            sum_pd[hd] = fmaf(p, d[i], sum_pd[hd]);
+            t_dsd = fmaf(s[i], d[i], t_dsd);
+            t_pd = fmaf(p, d[i], t_pd);
           }
         }
+        pin(sum_ds[hd] += t_ds);
         if constexpr (BIAS) {
-          pin(sum_ds[hd]);
-          pin(sum_dsd[hd]);
-          pin(sum_pd[hd]);
+          pin(sum_dsd[hd] += t_dsd);
+          pin(sum_pd[hd] += t_pd);
         }
         if constexpr (CAP) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) s[i] = whole || (seen >> i) & 1 ? s[i] * fmaf(-th[i], th[i], 1.0f) : 0.0f;
         }
         __builtin_amdgcn_sched_barrier(0);
-        M::template accumulate<NB>(acc[hd], M::pack(s), kt, at, lane);
+        // a bf16 ds would be as far off as the result's own rounding: it goes in two parts
+        M::template accumulate_fine<NB>(acc[hd], s, kt, at, lane);
       }
     }
   }
 #pragma unroll
   for (int hd = 0; hd < HB; ++hd) {
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[hd][blk][i] *= inv_l[hd];
     make_nan<NB>(acc[hd], odd[hd]);
     // the queries' sign is in s, not in k: a zero scale gives zeros
     write_own<T, DP, KW>(acc[hd], a.scale, (float*)smem, a.D, a.vec_out, kw, lane, [&](int r) -> T* {
@@ -328,22 +337,26 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
       const int t = (first + r) / a.G, head = hk * a.G + (first + r - t * a.G) + hd;
       return (T*)a.gq + (((int64_t)b * a.Tq + t) * a.Hq + head) * a.D;
     });
+    // delta came from the rounded output; ds sums to the error it made (sum_j p_ij = 1): the keys' launch gets delta
+    // without it, and the distances' mean takes it out of the slope's gradient, which is fp32 whatever the type
+    float sd = pair_sum(sum_ds[hd]) * inv_l[hd], sdd = 0.0f, pd = 0.0f;
     if constexpr (BIAS) {
-      if (a.gslope == nullptr) continue;
-      // delta came from the rounded output; ds sums to the error it made (sum_j p_ij = 1), which the distances'
-      // mean takes back out: the slope's gradient is fp32 whatever the tensors' type
-      float sd = pair_sum(sum_ds[hd]), sdd = pair_sum(sum_dsd[hd]), pd = pair_sum(sum_pd[hd]);
-      bool bad = odd[hd];
-      if constexpr (KW > 1) {
-        __syncthreads();
-        if (h == 0) slopes[kw][0][n] = sd, slopes[kw][1][n] = bad ? __builtin_nanf("") : sdd, slopes[kw][2][n] = pd;
-        __syncthreads();
-        sd = sdd = pd = 0.0f;
+      sdd = pair_sum(sum_dsd[hd]) * inv_l[hd];
+      pd = pair_sum(sum_pd[hd]) * inv_l[hd];
+    }
+    bool bad = odd[hd];
+    if constexpr (KW > 1) {
+      __syncthreads();
+      if (h == 0) slopes[kw][0][n] = sd, slopes[kw][1][n] = bad ? __builtin_nanf("") : sdd, slopes[kw][2][n] = pd;
+      __syncthreads();
+      sd = sdd = pd = 0.0f;
 #pragma unroll
-        for (int k = 0; k < KW; ++k) sd += slopes[k][0][n], sdd += slopes[k][1][n], pd += slopes[k][2][n];
-        bad = false;
-      }
-      if (kw == 0 && h == 0 && first + n < a.R)
+      for (int k = 0; k < KW; ++k) sd += slopes[k][0][n], sdd += slopes[k][1][n], pd += slopes[k][2][n];
+      bad = false;
+    }
+    if (kw == 0 && h == 0 && first + n < a.R) {
+      row_stats(a, (int64_t)b * a.Hk + hk + hd).delta[w.r] = delta[hd] + sd;
+      if (BIAS && a.gslope)
         a.gslope[((int64_t)b * a.Tq + w.t) * a.Hq + w.head + hd] = bad ? __builtin_nanf("") : fmaf(sd, pd, -sdd);
     }
   }
@@ -358,7 +371,9 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
   constexpr int NB = DP / 32, MT = C::MT, RW = C::RW;
   __shared__ alignas(16) char smem[C::kBytes];
   __shared__ alignas(16) float pos[BIAS ? 3 * MT : 1];   // [row][axis]
-  __shared__ alignas(16) float lse2s[HB][MT], deltas[HB][MT], slopes[HB][BIAS ? MT : 4];
+  constexpr bool EXACT = sizeof(T) == 4;                  // p from the maximum and 1 / l, not from their logarithm
+  __shared__ alignas(16) float offs[HB][MT], invs[EXACT ? HB : 1][EXACT ? MT : 4], deltas[HB][MT];
+  __shared__ alignas(16) float slopes[HB][BIAS ? MT : 4];
   __shared__ alignas(16) int docs[MT], lims[MT];
   __shared__ int doc_range[C::kWaves][2];
   __shared__ uint32_t stage_bits;
@@ -459,12 +474,13 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
     }
 #pragma unroll
     for (int i = 0; i < HB; ++i) {
-      const RowStats st = row_stats(a, (int64_t)b * a.Hk + hk + i);
-      stage_floats<C::kThreads>(lse2s[i], st.lse + s0, nr, MT);
-      stage_floats<C::kThreads>(deltas[i], st.delta + s0, nr, MT);
+      const RowStats rs = row_stats(a, (int64_t)b * a.Hk + hk + i);
+      stage_floats<C::kThreads>(offs[i], rs.off + s0, nr, MT);
+      if constexpr (EXACT) stage_floats<C::kThreads>(invs[i], rs.inv + s0, nr, MT);
+      stage_floats<C::kThreads>(deltas[i], rs.delta + s0, nr, MT);
       if constexpr (BIAS) {
-        stage_floats<C::kThreads>(slopes[i], st.slope + s0, nr, MT);
-        if (i == 0) stage_floats<C::kThreads>(pos, st.pos + (int64_t)s0 * a.dims, nr * a.dims, MT * a.dims);
+        stage_floats<C::kThreads>(slopes[i], rs.slope + s0, nr, MT);
+        if (i == 0) stage_floats<C::kThreads>(pos, rs.pos + (int64_t)s0 * a.dims, nr * a.dims, MT * a.dims);
       }
     }
     auto visible = [&](int at) {
@@ -519,11 +535,12 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
         __builtin_amdgcn_sched_barrier(0);                // one head's registers at a time
         const char* qt = Qs + hd * C::kTile;
         const char* gt = Gs + hd * C::kTile;
-        // the sums start from -lse (in score units; a cap comes between) and -delta of the moving row
+        // the sums start from the exponents' offset (bf16 without a cap) and -delta of the moving row
+        constexpr bool FOLD = !CAP && !EXACT;
         const float one = h == 0 ? 1.0f : 0.0f;
-        const float l2 = CAP || h != 0 ? 0.0f : -lse2s[hd][at + n];
+        const float l2 = !FOLD || h != 0 ? 0.0f : -offs[hd][at + n];
         f32x16 s = {}, dp = outer_sum(h == 0 ? -deltas[hd][at + n] : 0.0f, one);
-        if constexpr (!CAP) s = outer_sum(l2, one);
+        if constexpr (FOLD) s = outer_sum(l2, one);
         if constexpr (C::kOwnLds) {
           s = tile_dot<T, DP>(qt, at, own_at + 2 * hd * C::kOwn, lane, s);
           dp = tile_dot<T, DP>(gt, at, own_at + (2 * hd + 1) * C::kOwn, lane, dp);
@@ -539,14 +556,16 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int r = at + 8 * u + 4 * h;
-          f32x4 sl = {}, l2 = {};
-          if constexpr (CAP) l2 = *(const f32x4*)&lse2s[hd][r];
+          f32x4 sl = {}, l2 = {}, inv = {};
+          if constexpr (!FOLD) l2 = *(const f32x4*)&offs[hd][r];
+          if constexpr (EXACT) inv = *(const f32x4*)&invs[hd][r];
           if constexpr (BIAS) sl = *(const f32x4*)&slopes[hd][r];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int i = 4 * u + j;
             if constexpr (BIAS) s[i] = fmaf(-sl[j], d[i], s[i]);
-            s[i] = __builtin_amdgcn_exp2f(CAP ? fmaf(s[i], un.unit, -l2[j]) : s[i] * un.unit);
+            s[i] = __builtin_amdgcn_exp2f(FOLD ? s[i] * un.unit : fmaf(s[i], un.unit, -l2[j]));
+            if constexpr (EXACT) s[i] *= inv[j];
             dp[i] *= s[i];
             if constexpr (CAP) dp[i] *= fmaf(-th[i], th[i], 1.0f);
           }

@@ -163,6 +163,26 @@ struct Mma<__bf16, DP> {
       for (int c = 0; c < 2; ++c)
         acc[blk] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(columns(tile, r0, c, blk, lane), p.v[c], acc[blk], 0, 0, 0);
   }
+
+  // The same with each value as the sum of two bf16 (16 bits of it).
+  template <int NB>
+  static __device__ __forceinline__ void accumulate_fine(f32x16 (&acc)[NB], const f32x16& p, const char* tile, int r0,
+                                                         int lane) {
+    const Values hi = pack(p);
+    Values lo;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) lo.v[c][j] = (__bf16)(p[8 * c + j] - (float)hi.v[c][j]);
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const bf16x8 x = columns(tile, r0, c, blk, lane);
+        acc[blk] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, hi.v[c], acc[blk], 0, 0, 0);
+        acc[blk] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, lo.v[c], acc[blk], 0, 0, 0);
+      }
+  }
 };
 
 // fp32: contraction in steps of two; a fragment is four channels (the half-waves' share of eight).
@@ -194,6 +214,11 @@ struct Mma<float, DP> {
       for (int i = 0; i < 16; ++i)
         acc[blk] = __builtin_amdgcn_mfma_f32_32x32x2f32(
             *Tl::at(tile + r0 * Tl::kRowBytes, acc_row(i, lane >> 5), 32 * blk + (lane & 31)), p.v[i], acc[blk], 0, 0, 0);
+  }
+  template <int NB>
+  static __device__ __forceinline__ void accumulate_fine(f32x16 (&acc)[NB], const f32x16& p, const char* tile, int r0,
+                                                         int lane) {
+    accumulate<NB>(acc, pack(p), tile, r0, lane);
   }
 };
 

@@ -1,7 +1,7 @@
 // Attention between queries, cells and tokens, forward.
 //
 //   s_ij = cap tanh(scale q_i . k_j / cap) - slope_i |pos_i - pos_j|     (cap and bias optional)
-//   o_i  = sum_j p_ij v_j,  p = softmax of s over the keys row i sees,  lse_i = log sum_j exp(s_ij)
+//   o_i  = sum_j p_ij v_j,  p = softmax of s over the keys row i sees
 //
 // One pass over the keys with a running maximum and sum per row (in fp32, base-2 exponentials).  A key
 // head's G query heads are rows of one problem (row = token G + head), so single tokens with grouped heads
@@ -73,7 +73,7 @@ __device__ __forceinline__ void finish(const AttnArgs& a, const Row& w, int firs
         if (part)
           po[a.D] = m, po[a.D + 1] = l;
         else
-          a.lse[((int64_t)b * a.Hq + head) * a.Tq + w.t] = l == 0.0f ? kNegInf : m * kLn2 + logf(l);
+          a.stats[((int64_t)b * a.Hq + head) * a.Tq + w.t] = make_float2(m, l);
       }
     }
   } else {
@@ -107,7 +107,7 @@ __device__ __forceinline__ void finish(const AttnArgs& a, const Row& w, int firs
         float* po = a.part + (((int64_t)split * a.B * a.Hk + bh) * a.R + w.r) * (a.D + 2);
         po[a.D] = top, po[a.D + 1] = tot;
       } else {
-        a.lse[((int64_t)b * a.Hq + head) * a.Tq + w.t] = tot == 0.0f ? kNegInf : top * kLn2 + logf(tot);
+        a.stats[((int64_t)b * a.Hq + head) * a.Tq + w.t] = make_float2(top, tot);
       }
     }
     __syncthreads();
@@ -340,7 +340,7 @@ __global__ __launch_bounds__(kThreads) void attn_join_few(AttnArgs a) {
 #pragma unroll
   for (int j = 0; j < 2; ++j)
     if (lane + 64 * j < a.D) out[lane + 64 * j] = (T)(o[j] * inv);
-  if (lane == 0) a.lse[((int64_t)b * a.Hq + head) * a.Tq + t] = tot == 0.0f ? kNegInf : top * kLn2 + logf(tot);
+  if (lane == 0) a.stats[((int64_t)b * a.Hq + head) * a.Tq + t] = make_float2(top, tot);
 }
 
 // Many: one workgroup a row, the maximum and the weights over all threads, then wave w adds up
@@ -381,7 +381,7 @@ __global__ __launch_bounds__(kThreads) void attn_join(AttnArgs a) {
   if (c < a.D)
     ((T*)a.out)[(((int64_t)b * a.Tq + t) * a.Hq + head) * a.D + c] =
         (T)(((part[0][c] + part[1][c]) + (part[2][c] + part[3][c])) * inv);
-  if (c == 0) a.lse[((int64_t)b * a.Hq + head) * a.Tq + t] = tot == 0.0f ? kNegInf : top * kLn2 + logf(tot);
+  if (c == 0) a.stats[((int64_t)b * a.Hq + head) * a.Tq + t] = make_float2(top, tot);
 }
 
 struct Plan {

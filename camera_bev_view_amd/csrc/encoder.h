@@ -60,7 +60,7 @@ struct AttnArgs {
   int causal;
   const int32_t* prefix;   // [B] or NULL
   void* out;               // [B, Tq, Hq, D] (backward: read)
-  float* lse;              // [B, Hq, Tq] (backward: read)
+  float2* stats;           // [B, Hq, Tq] (backward: read): a row's maximum m (base-2 units) and sum l of 2^(s - m)
   int elem_bytes;
   bool vec;                // q, k, v rows move as 16-byte pieces
   bool vec_out;            // rows of out (and of the gradients) move as pieces of four channels

@@ -338,18 +338,19 @@ fbev_status fbev_attention_workspace(const fbev_attention_desc* ad, int32_t back
 }
 
 fbev_status fbev_attention_forward(const void* q, const void* k, const void* v, fbev_dtype dtype,
-                                   const fbev_attention_desc* ad, void* out, float* lse, void* workspace,
+                                   const fbev_attention_desc* ad, void* out, float* stats, void* workspace,
                                    size_t workspace_bytes, void* stream) {
   fbev::AttnArgs a{};
   fbev_status s = check_attention(ad, a);
   if (s == FBEV_OK) s = check_attention_data(a, q, k, v, dtype);
   if (s != FBEV_OK) return s;
   if ((int64_t)a.B * a.R == 0) return FBEV_OK;
-  if (out == nullptr || lse == nullptr) return fail(FBEV_ERR_INVALID_ARGUMENT, "out and lse must be non-NULL");
+  if (out == nullptr || stats == nullptr) return fail(FBEV_ERR_INVALID_ARGUMENT, "out and stats must be non-NULL");
+  if (!aligned(stats, 8)) return fail(FBEV_ERR_INVALID_ARGUMENT, "stats must be 8-byte aligned");
   s = check_workspace(workspace, workspace_bytes, fbev::attention_forward_workspace_bytes(a));
   if (s != FBEV_OK) return s;
   a.out = out;
-  a.lse = lse;
+  a.stats = reinterpret_cast<float2*>(stats);
   a.part = static_cast<float*>(workspace);
   a.vec_out = a.D % 4 == 0 && aligned(out, 4 * a.elem_bytes);
   return device_status(fbev::launch_attention_forward(a, static_cast<hipStream_t>(stream)),
@@ -358,7 +359,7 @@ fbev_status fbev_attention_forward(const void* q, const void* k, const void* v, 
 
 fbev_status fbev_attention_backward(const void* grad_out, const void* q, const void* k, const void* v,
                                     fbev_dtype dtype, const fbev_attention_desc* ad, const void* out,
-                                    const float* lse, void* grad_q, void* grad_k, void* grad_v, float* grad_slope,
+                                    const float* stats, void* grad_q, void* grad_k, void* grad_v, float* grad_slope,
                                     void* workspace, size_t workspace_bytes, void* stream) {
   fbev::AttnArgs a{};
   fbev_status s = check_attention(ad, a);
@@ -366,8 +367,9 @@ fbev_status fbev_attention_backward(const void* grad_out, const void* q, const v
   if (s != FBEV_OK) return s;
   const bool rows = (int64_t)a.B * a.R > 0, keys = (int64_t)a.B * a.Tk > 0;
   if (!rows && !keys) return FBEV_OK;
-  if (rows && (grad_out == nullptr || out == nullptr || lse == nullptr || grad_q == nullptr))
-    return fail(FBEV_ERR_INVALID_ARGUMENT, "grad_out, out, lse and grad_q must be non-NULL");
+  if (rows && (grad_out == nullptr || out == nullptr || stats == nullptr || grad_q == nullptr))
+    return fail(FBEV_ERR_INVALID_ARGUMENT, "grad_out, out, stats and grad_q must be non-NULL");
+  if (!aligned(stats, 8)) return fail(FBEV_ERR_INVALID_ARGUMENT, "stats must be 8-byte aligned");
   if (keys && (grad_k == nullptr || grad_v == nullptr))
     return fail(FBEV_ERR_INVALID_ARGUMENT, "grad_k and grad_v must be non-NULL");
   if (grad_slope != nullptr && a.dims == 0)
@@ -379,7 +381,7 @@ fbev_status fbev_attention_backward(const void* grad_out, const void* q, const v
               aligned(grad_v, 4 * a.elem_bytes);
   a.gout = grad_out;
   a.out = const_cast<void*>(out);
-  a.lse = const_cast<float*>(lse);
+  a.stats = reinterpret_cast<float2*>(const_cast<float*>(stats));
   a.gq = grad_q;
   a.gk = grad_k;
   a.gv = grad_v;

@@ -383,43 +383,44 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scal
     slope times the Euclidean distance of the two positions.  ``doc_q`` [B,Tq], ``doc_k`` [B,Tk] int32: only keys of
     the query's own document are seen, negative ones (padding) by none.  ``causal``: key j is seen by query i when
     j <= i + Tk - Tq, or j < ``prefix`` [B] (int32).  Queries that see no key get zeros.
-    Returns (out [B,Tq,Hq,D], lse [B,Hq,Tq] fp32)."""
+    Returns (out [B,Tq,Hq,D], stats [B,Hq,Tq,2] fp32): the softmax's m and l, sum_j exp(s_j) = 2^m l, which the
+    backward takes (m = -inf, l = 0 where no key is seen)."""
     q, k, v, ad, keep = _attention_desc(q, k, v, scale, cap, pos_q, pos_k, slope, doc_q, doc_k, causal, prefix)
     dev = q.device
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=dev)
     else:
         _check_plain("out", out, q.shape, q.dtype, dev)
-    lse = torch.empty((ad.B, ad.Hq, ad.Tq), dtype=torch.float32, device=dev)
+    stats = torch.empty((ad.B, ad.Hq, ad.Tq, 2), dtype=torch.float32, device=dev)
     workspace, have = _scratch(_attention_scratch(ad.B, ad.Tq, ad.Tk, ad.Hq, ad.Hk, ad.D, ad.dims, 0), workspace, dev)
-    _call("fbev_attention_forward", dev, _data(q), _data(k), _data(v), _DTYPES[q.dtype], ad, _data(out), _data(lse),
+    _call("fbev_attention_forward", dev, _data(q), _data(k), _data(v), _DTYPES[q.dtype], ad, _data(out), _data(stats),
           _data(workspace), have)
     del keep
-    return out, lse
+    return out, stats
 
 
 def attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
-                       lse: torch.Tensor, *, scale: Optional[float] = None, cap: Optional[float] = None,
+                       stats: torch.Tensor, *, scale: Optional[float] = None, cap: Optional[float] = None,
                        pos_q: Optional[torch.Tensor] = None, pos_k: Optional[torch.Tensor] = None,
                        slope: Optional[torch.Tensor] = None, doc_q: Optional[torch.Tensor] = None,
                        doc_k: Optional[torch.Tensor] = None, causal: bool = False,
                        prefix: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
     """fbev_attention_backward: (grad_q, grad_k, grad_v, grad_slope [B,Tq,Hq] fp32 or None without positions) from
-    dL/dout and the forward's inputs, out and lse."""
+    dL/dout and the forward's inputs, out and stats."""
     q, k, v, ad, keep = _attention_desc(q, k, v, scale, cap, pos_q, pos_k, slope, doc_q, doc_k, causal, prefix)
     dev, dtype = q.device, q.dtype
     if grad_out.shape != q.shape or grad_out.dtype != dtype or grad_out.device != dev:
         raise ValueError(f"grad_out must be a {dtype} tensor of shape {list(q.shape)} on {dev}")
     grad_out = grad_out.contiguous()
     _check_plain("out", out, q.shape, dtype, dev)
-    _check_plain("lse", lse, (ad.B, ad.Hq, ad.Tq), torch.float32, dev)
+    _check_plain("stats", stats, (ad.B, ad.Hq, ad.Tq, 2), torch.float32, dev)
     gq = torch.empty(q.shape, dtype=dtype, device=dev)
     gk = torch.empty(k.shape, dtype=dtype, device=dev)
     gv = torch.empty(v.shape, dtype=dtype, device=dev)
     gslope = torch.empty((ad.B, ad.Tq, ad.Hq), dtype=torch.float32, device=dev) if ad.dims else None
     workspace, have = _scratch(_attention_scratch(ad.B, ad.Tq, ad.Tk, ad.Hq, ad.Hk, ad.D, ad.dims, 1), workspace, dev)
     _call("fbev_attention_backward", dev, _data(grad_out), _data(q), _data(k), _data(v), _DTYPES[dtype], ad,
-          _data(out), _data(lse), _data(gq), _data(gk), _data(gv), _data(gslope), _data(workspace), have)
+          _data(out), _data(stats), _data(gq), _data(gk), _data(gv), _data(gslope), _data(workspace), have)
     del keep
     return gq, gk, gv, gslope
 
@@ -429,18 +430,18 @@ class QueryAttention(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, slope, scale, cap, pos_q, pos_k, doc_q, doc_k, causal, prefix):
-        out, lse = attention_forward(q, k, v, scale=scale, cap=cap, pos_q=pos_q, pos_k=pos_k, slope=slope,
-                                     doc_q=doc_q, doc_k=doc_k, causal=causal, prefix=prefix)
-        ctx.save_for_backward(q, k, v, slope, pos_q, pos_k, doc_q, doc_k, prefix, out, lse)
+        out, stats = attention_forward(q, k, v, scale=scale, cap=cap, pos_q=pos_q, pos_k=pos_k, slope=slope,
+                                       doc_q=doc_q, doc_k=doc_k, causal=causal, prefix=prefix)
+        ctx.save_for_backward(q, k, v, slope, pos_q, pos_k, doc_q, doc_k, prefix, out, stats)
         ctx.meta = (scale, cap, causal)
         return out
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_out):
-        q, k, v, slope, pos_q, pos_k, doc_q, doc_k, prefix, out, lse = ctx.saved_tensors
+        q, k, v, slope, pos_q, pos_k, doc_q, doc_k, prefix, out, stats = ctx.saved_tensors
         scale, cap, causal = ctx.meta
-        gq, gk, gv, gs = attention_backward(grad_out, q, k, v, out, lse, scale=scale, cap=cap, pos_q=pos_q,
+        gq, gk, gv, gs = attention_backward(grad_out, q, k, v, out, stats, scale=scale, cap=cap, pos_q=pos_q,
                                             pos_k=pos_k, slope=slope, doc_q=doc_q, doc_k=doc_k, causal=causal,
                                             prefix=prefix)
         return (gq, gk, gv, gs) + (None,) * 8

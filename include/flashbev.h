@@ -467,8 +467,8 @@ fbev_status fbev_rotary(const void* q, const void* k, fbev_dtype dtype, const fb
  *
  * Key j is seen when doc_q[b,i] == doc_k[b,j] >= 0 (without documents:
  * always) and, when `causal`, j <= i + Tk - Tq or j < prefix[b].  A query
- * that sees no key gets zeros (and lse = -inf); what masked keys hold, NaN and
- * infinities among it, reaches no query that does not see them.
+ * that sees no key gets zeros; what masked keys hold, NaN and infinities among
+ * it, reaches no query that does not see them.
  *
  *   q [B,Tq,Hq,D], k, v [B,Tk,Hk,D] : by element strides (batch, token, head), channels
  *       contiguous; 16-byte aligned rows take the wide-load path.  Hq a
@@ -478,16 +478,21 @@ fbev_status fbev_rotary(const void* q, const void* k, fbev_dtype dtype, const fb
  *   doc_q [B,Tq], doc_k [B,Tk] : int32, both or neither; in any order, but
  *       documents that lie together are skipped tile by tile.
  *   prefix : [B] int32 or NULL; needs `causal`.
- *   out [B,Tq,Hq,D] of dtype, lse [B,Hq,Tq] fp32 (log of the sum of exp(s)) : contiguous.
+ *   out [B,Tq,Hq,D] of dtype, contiguous.
+ *   stats [B,Hq,Tq,2] fp32, 8-byte aligned: m and l with sum_j exp(s_j) = 2^m l (no
+ *       key: -inf and 0), what the backward needs of the softmax.  m is within 8 of
+ *       the row's largest s log2(e); the pair keeps what one logarithm would round.
  *   workspace : as for group norm.  Few rows over many keys are split along the
  *       keys and joined from there.
  *
- * The backward takes grad_out, out [B,Tq,Hq,D] (contiguous, of dtype) and lse
+ * The backward takes grad_out, out [B,Tq,Hq,D] (contiguous, of dtype) and stats
  * and gives grad_q, grad_k, grad_v (contiguous, of dtype; a key head's
  * gradient is the sum over its query heads) and grad_slope [B,Tq,Hq] fp32
- * (NULL skips it).  Positions are not differentiated.  Probabilities and score
- * gradients of bf16 tensors are rounded to bf16 before the matrix products
- * that use them.
+ * (NULL skips it).  Positions are not differentiated.  For bf16 tensors
+ * the probabilities, and the score gradients that give grad_k, are rounded to
+ * bf16 before their matrix products; those that give grad_q keep 16 bits.  A
+ * query, key or slope whose masked tiles it sees hold an infinity or a NaN gets
+ * NaN gradients.
  */
 typedef struct {
   int32_t B, Tq, Tk, Hq, Hk, D;
@@ -500,11 +505,11 @@ typedef struct {
 
 fbev_status fbev_attention_workspace(const fbev_attention_desc* ad, int32_t backward, size_t* bytes);
 fbev_status fbev_attention_forward(const void* q, const void* k, const void* v, fbev_dtype dtype,
-                                   const fbev_attention_desc* ad, void* out, float* lse, void* workspace,
+                                   const fbev_attention_desc* ad, void* out, float* stats, void* workspace,
                                    size_t workspace_bytes, void* stream);
 fbev_status fbev_attention_backward(const void* grad_out, const void* q, const void* k, const void* v,
                                     fbev_dtype dtype, const fbev_attention_desc* ad, const void* out,
-                                    const float* lse, void* grad_q, void* grad_k, void* grad_v, float* grad_slope,
+                                    const float* stats, void* grad_q, void* grad_k, void* grad_v, float* grad_slope,
                                     void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static text for a status code. */

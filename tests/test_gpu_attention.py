@@ -37,10 +37,11 @@ def check(q, k, v, go, how, label, backward=True):
     out, lse = ops.attention_forward(q, k, v, **how)
     ref, bd = oracle_attention(q, k, v, how, go if backward else None)
     close(label + " out", out, ref["out"], bd["out"])
-    empty = np.isneginf(ref["lse"])
-    got = lse.double().cpu().numpy()
-    assert (np.isneginf(got) == empty).all(), f"{label}: rows without keys differ"
-    close(label + " lse", torch.where(torch.isinf(lse), 0.0, lse), np.where(empty, 0.0, ref["lse"]), bd["lse"])
+    empty = torch.from_numpy(np.isneginf(ref["lse"])).cuda()
+    assert torch.equal(lse[..., 1] == 0, empty) and torch.equal(torch.isneginf(lse[..., 0]), empty), \
+        f"{label}: rows without keys differ"
+    log = lse[..., 0].double() * np.log(2.0) + torch.log(lse[..., 1].double())
+    close(label + " m, l", torch.where(empty, 0.0, log), np.where(empty.cpu(), 0.0, ref["lse"]), bd["lse"])
     if not backward:
         return
     gq, gk, gv, gs = ops.attention_backward(go, q, k, v, out, lse, **how)
