@@ -155,6 +155,11 @@ fbev_status check_attention(const fbev_attention_desc* ad, fbev::AttnArgs& a) {
     return fail(FBEV_ERR_UNSUPPORTED, "D=%d exceeds FBEV_MAX_HEAD_DIM=%d", ad->D, FBEV_MAX_HEAD_DIM);
   if (!std::isfinite(ad->scale) || !std::isfinite(ad->cap) || ad->cap < 0.0f)
     return fail(FBEV_ERR_INVALID_ARGUMENT, "scale and cap must be finite, cap not negative");
+  // slopes and exponents are divided by the one or the other: their quotients stay within fp32
+  const auto far = [](float x) { return x != 0.0f && !(std::fabs(x) >= 1e-12f && std::fabs(x) <= 1e12f); };
+  if (far(ad->scale) || far(ad->cap))
+    return fail(FBEV_ERR_UNSUPPORTED, "scale=%g and cap=%g must be 0 or of a size within [1e-12, 1e12]", ad->scale,
+                ad->cap);
   if (ad->dims < 0 || ad->dims > 3) return fail(FBEV_ERR_INVALID_ARGUMENT, "dims=%d outside [0, 3]", ad->dims);
   if ((ad->doc_q == nullptr) != (ad->doc_k == nullptr) && ad->B > 0 && ad->Tq > 0 && ad->Tk > 0)
     return fail(FBEV_ERR_INVALID_ARGUMENT, "doc_q and doc_k come together");

@@ -82,6 +82,24 @@ def _scratch(need: int, workspace: Optional[torch.Tensor], device) -> Tuple[Opti
     return workspace, 0 if workspace is None else workspace.numel()
 
 
+def _check_sizes(*sizes: int) -> None:
+    if max(sizes) >= 1 << 31:                         # the descriptors' 32-bit fields would cut them short
+        raise ValueError(f"sizes must be below 2^31, got {max(sizes)}")
+
+
+def _span(t: torch.Tensor) -> Tuple[int, int]:
+    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
+
+def _check_apart(name: str, out: torch.Tensor, *inputs: torch.Tensor) -> None:
+    """Refuses an output on memory that another workgroup may still read."""
+    lo, hi = _span(out)
+    for x in inputs:
+        if out.numel() and x.numel() and _span(x)[0] < hi and lo < _span(x)[1]:
+            raise ValueError(f"{name} must not overlap an input")
+
+
 # ---- group norm with an activation
 
 def _collapse(shape: Sequence[int], stride: Sequence[int]) -> Optional[int]:
@@ -111,6 +129,7 @@ def _norm_desc(x: torch.Tensor, groups: int, eps: float, activation: str, image_
     if not 0 <= lead < x.dim():
         raise ValueError(f"image_dims={lead} does not fit a tensor of {x.dim()} dimensions")
     shape, stride = x.shape, x.stride()
+    _check_sizes(shape[-1], groups)
     si, sp = _collapse(shape[:lead], stride[:lead]), _collapse(shape[lead:-1], stride[lead:-1])
     if si is None or sp is None or (shape[-1] > 1 and stride[-1] != 1):
         x = x.contiguous()
@@ -144,6 +163,7 @@ def group_norm_forward(x: torch.Tensor, groups: int, weight: Optional[torch.Tens
         out = torch.empty(x.shape, dtype=x.dtype, device=dev)
     else:
         _check_plain("out", out, x.shape, x.dtype, dev)
+        _check_apart("out", out, x)
     stats = torch.empty((nd.images, max(groups, 0), 2), dtype=torch.float32, device=dev)
     dt = _DTYPES[x.dtype]
     workspace, have = _scratch(_norm_scratch(nd.images, nd.pixels, nd.C, groups, dt, 0), workspace, dev)
@@ -239,6 +259,7 @@ def _rotary(q, k, pos, freqs, interleaved, inverse, q_out, k_out):
     for name, x in (("pos", pos), ("freqs", freqs)):
         if x.dtype != torch.float32 or x.device != dev:
             raise ValueError(f"{name} must be a float32 tensor on {dev}")
+    _check_sizes(B, T, D, 0 if q is None else q.shape[2], 0 if k is None else k.shape[2], *freqs.shape)
     pos, freqs = pos.contiguous(), freqs.contiguous()
     outs = []
     ins = []
@@ -259,6 +280,8 @@ def _rotary(q, k, pos, freqs, interleaved, inverse, q_out, k_out):
                              "channels contiguous")
         elif out.numel() and any(s == 0 and n > 1 for n, s in zip(out.shape, out.stride())):
             raise ValueError(f"{name}_out must not be a broadcast tensor")
+        elif out.data_ptr() != x.data_ptr() or out.stride() != x.stride():
+            _check_apart(f"{name}_out, unless it is {name} itself,", out, x)
         ins.append(x)
         outs.append(out)
     none = (0, 0, 0, 0)
@@ -325,6 +348,7 @@ def _attention_desc(q, k, v, scale, cap, pos_q, pos_k, slope, doc_q, doc_k, caus
     Tk, Hk = k.shape[1], k.shape[2]
     if k.shape[0] != B or k.shape[3] != D or v.shape != k.shape:
         raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must be [B={B}, Tk, Hk, D={D}]")
+    _check_sizes(B, Tq, Tk, Hq, Hk, D)
     if D > 1:
         q = q if q.stride(3) == 1 else q.contiguous()
         k = k if k.stride(3) == 1 else k.contiguous()
@@ -391,6 +415,7 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scal
         out = torch.empty(q.shape, dtype=q.dtype, device=dev)
     else:
         _check_plain("out", out, q.shape, q.dtype, dev)
+        _check_apart("out", out, q, k, v)
     stats = torch.empty((ad.B, ad.Hq, ad.Tq, 2), dtype=torch.float32, device=dev)
     workspace, have = _scratch(_attention_scratch(ad.B, ad.Tq, ad.Tk, ad.Hq, ad.Hk, ad.D, ad.dims, 0), workspace, dev)
     _call("fbev_attention_forward", dev, _data(q), _data(k), _data(v), _DTYPES[q.dtype], ad, _data(out), _data(stats),

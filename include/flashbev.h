@@ -396,7 +396,7 @@ fbev_status fbev_deform_backward(const float* grad_out, const float* features, f
  *   xh = (x - mean) / sqrt(var + eps),  z = weight xh + bias,  y = act(z)
  *
  *   weight, bias : [C] fp32, device, or NULL (ones / zeros).
- *   y            : [images, pixels, C] of dtype, contiguous.
+ *   y            : [images, pixels, C] of dtype, contiguous, not on x.
  *   stats        : [images, groups, 2] fp32: mean and 1 / sqrt(var + eps).
  *   workspace    : device scratch of the size the workspace call reports
  *                  (NULL when 0), 16-byte aligned; not needed before or after
@@ -478,7 +478,8 @@ fbev_status fbev_rotary(const void* q, const void* k, fbev_dtype dtype, const fb
  *   doc_q [B,Tq], doc_k [B,Tk] : int32, both or neither; in any order, but
  *       documents that lie together are skipped tile by tile.
  *   prefix : [B] int32 or NULL; needs `causal`.
- *   out [B,Tq,Hq,D] of dtype, contiguous.
+ *   scale, cap : 0 or of a size within [1e-12, 1e12] (cap 0: none).
+ *   out [B,Tq,Hq,D] of dtype, contiguous, on memory of its own.
  *   stats [B,Hq,Tq,2] fp32, 8-byte aligned: m and l with sum_j exp(s_j) = 2^m l (no
  *       key: -inf and 0), what the backward needs of the softmax.  m is within 8 of
  *       the row's largest s log2(e); the pair keeps what one logarithm would round.
@@ -490,9 +491,8 @@ fbev_status fbev_rotary(const void* q, const void* k, fbev_dtype dtype, const fb
  * gradient is the sum over its query heads) and grad_slope [B,Tq,Hq] fp32
  * (NULL skips it).  Positions are not differentiated.  For bf16 tensors
  * the probabilities, and the score gradients that give grad_k, are rounded to
- * bf16 before their matrix products; those that give grad_q keep 16 bits.  A
- * query, key or slope whose masked tiles it sees hold an infinity or a NaN gets
- * NaN gradients.
+ * bf16 before their matrix products; those that give grad_q keep 16 bits.  An
+ * infinity or a NaN reaches the gradients of what sees it and no others.
  */
 typedef struct {
   int32_t B, Tq, Tk, Hq, Hk, D;

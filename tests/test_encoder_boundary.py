@@ -43,13 +43,13 @@ def attn_desc(B=1, Tq=4, Tk=6, Hq=4, Hk=2, D=32, stride=(1024, 128, 32), scale=0
                               slope, doc_q, doc_k, prefix)
 
 
-def attn(lib, q=FAKE, k=FAKE, v=FAKE, dtype=0, out=FAKE, lse=FAKE, ws=FAKE, have=1 << 30, **kw):
-    return lib.fbev_attention_forward(q, k, v, dtype, attn_desc(**kw), out, lse, ws, have, None)
+def attn(lib, q=FAKE, k=FAKE, v=FAKE, dtype=0, out=FAKE, stats=FAKE, ws=FAKE, have=1 << 30, **kw):
+    return lib.fbev_attention_forward(q, k, v, dtype, attn_desc(**kw), out, stats, ws, have, None)
 
 
-def attn_bwd(lib, go=FAKE, q=FAKE, k=FAKE, v=FAKE, dtype=0, out=FAKE, lse=FAKE, gq=FAKE, gk=FAKE, gv=FAKE, gs=None,
+def attn_bwd(lib, go=FAKE, q=FAKE, k=FAKE, v=FAKE, dtype=0, out=FAKE, stats=FAKE, gq=FAKE, gk=FAKE, gv=FAKE, gs=None,
              ws=FAKE, have=1 << 30, **kw):
-    return lib.fbev_attention_backward(go, q, k, v, dtype, attn_desc(**kw), out, lse, gq, gk, gv, gs, ws, have, None)
+    return lib.fbev_attention_backward(go, q, k, v, dtype, attn_desc(**kw), out, stats, gq, gk, gv, gs, ws, have, None)
 
 
 @pytest.mark.parametrize("call,kw,status,text", [
@@ -89,6 +89,9 @@ def attn_bwd(lib, go=FAKE, q=FAKE, k=FAKE, v=FAKE, dtype=0, out=FAKE, lse=FAKE, 
     (attn, dict(Tq=-1), INVALID, "bad size"),
     (attn, dict(scale=float("inf")), INVALID, "scale"),
     (attn, dict(cap=-1.0), INVALID, "cap"),
+    (attn, dict(scale=1e-20), UNSUPPORTED, "scale"),
+    (attn, dict(scale=-1e20), UNSUPPORTED, "scale"),
+    (attn, dict(cap=1e-30), UNSUPPORTED, "cap"),
     (attn, dict(dims=4), INVALID, "dims"),
     (attn, dict(dims=2, slope=None), INVALID, "slope"),
     (attn, dict(doc_q=FAKE), INVALID, "together"),
@@ -104,6 +107,7 @@ def attn_bwd(lib, go=FAKE, q=FAKE, k=FAKE, v=FAKE, dtype=0, out=FAKE, lse=FAKE, 
     (attn_bwd, dict(gk=None), INVALID, "non-NULL"),
     (attn_bwd, dict(gs=FAKE), INVALID, "grad_slope"),
     (attn_bwd, dict(have=4), INVALID, "workspace"),
+    (attn_bwd, dict(stats=FAKE + 4), INVALID, "8-byte"),
 ])
 def test_refusals(lib, call, kw, status, text):
     assert call(lib, **kw) == status
@@ -119,8 +123,8 @@ def test_null_descriptors_and_sizes(lib):
     # nothing to do needs no buffers
     assert norm(lib, images=0, x=None, y=None, stats=None, ws=None, have=0) == 0
     assert rotary(lib, T=0, q=None, k=None, pos=None, freqs=None, qo=None, ko=None) == 0
-    assert attn(lib, B=0, q=None, k=None, v=None, out=None, lse=None, ws=None, have=0) == 0
-    assert attn(lib, Tq=0, q=None, out=None, lse=None, ws=None, have=0) == 0
+    assert attn(lib, B=0, q=None, k=None, v=None, out=None, stats=None, ws=None, have=0) == 0
+    assert attn(lib, Tq=0, q=None, out=None, stats=None, ws=None, have=0) == 0
     # few rows over many keys need a workspace, many rows none
     assert lib.fbev_attention_workspace(attn_desc(Tq=1, Tk=40000), 0, ctypes.byref(n)) == 0 and n.value > 0
     assert lib.fbev_attention_workspace(attn_desc(B=64, Tq=4000, Tk=4000), 0, ctypes.byref(n)) == 0 and n.value == 0

@@ -190,6 +190,44 @@ def test_masked_keys_may_hold_anything(dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [32, 64, 128, 40, 33])
+def test_rows_behind_the_last_are_not_read(D, dtype):
+    """Every tensor is the front of a memory of NaN: a tile that reaches behind the last row sees zeros."""
+    for Tq, Tk, H, G in ((1, 1, 2, 1), (5, 3, 1, 1), (33, 65, 1, 2), (130, 100, 40, 1), (2, 70, 1, 3), (200, 300, 1, 1)):
+        q, k, v, go, _ = draw(1, Tq, Tk, H * G, H, D, dtype, 52)
+        print(f"[case] attention before NaN: {Tq} {Tk} {H} {G} {D} {dtype}", flush=True)
+        want = ops.attention_forward(q, k, v)
+        grads = ops.attention_backward(go, q, k, v, *want)
+
+        def front(t):
+            room = torch.full((1, t.shape[1] + 520, *t.shape[2:]), float("nan"), dtype=dtype, device="cuda")
+            room[:, :t.shape[1]] = t
+            return room[:, :t.shape[1]]
+
+        q, k, v, go = (front(t) for t in (q, k, v, go))
+        out = front(want[0])
+        got = ops.attention_forward(q, k, v)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert go.is_contiguous() and out.is_contiguous()
+        for a, b in zip(ops.attention_backward(go, q, k, v, out, want[1])[:3], grads[:3]):
+            assert torch.equal(a, b)
+
+
+def test_refused_outputs_and_scales():
+    q, k, v, go, _ = draw(1, 40, 40, 2, 2, 32, F32, 53)
+    packed = torch.zeros((1, 40, 3, 2, 32), device="cuda")
+    for kw in (dict(out=q), dict(out=k), dict(scale=1e-20), dict(scale=1e20), dict(cap=1e-30)):
+        with pytest.raises((ValueError, RuntimeError)):
+            ops.attention_forward(q, k, v, **kw)
+    room = torch.zeros(40 * 64 + 4, device="cuda")
+    with pytest.raises(ValueError):
+        ops.attention_forward(room[4:].view(1, 40, 2, 32), k, v, out=room[:-4].view(1, 40, 2, 32))
+    check(q, k, v, go, dict(scale=1e-12), "smallest scale")
+    check(q, k, v, go, dict(scale=0.0), "no scale")
+    check(packed[:, :, 0], packed[:, :, 1], packed[:, :, 2], go, {}, "all zeros")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_views(dtype):
     B, T, H, D = 2, 60, 4, 32
     g = torch.Generator().manual_seed(47)

@@ -91,6 +91,9 @@ def test_strided_maps_and_odd_addresses():
     check(first, gy.cuda(), w.cuda(), b.cuda(), 4, "silu", "one image twice")
     check(x.cuda().reshape(24, 20, 32), gy.cuda().reshape(24, 20, 32), w.cuda(), b.cuda(), 4, "silu", "rows as images")
     check(x.cuda(), gy.cuda(), w.cuda(), b.cuda(), 4, "silu", "all as one image", image_dims=0)
+    same = x.cuda()
+    with pytest.raises(ValueError):
+        ops.group_norm_forward(same, 4, out=same)
 
 
 def test_empty_and_nan():

@@ -94,6 +94,12 @@ def test_one_tensor_views_and_in_place():
     wide = torch.zeros((2, 31, 4, 40), device="cuda", dtype=BF16)
     ops.rotary_forward(q, None, pos, freqs, q_out=wide[..., :32])
     assert torch.equal(wide[..., :32], want[0]) and (wide[..., 32:] == 0).all()
+    # memory that another token's turn still reads
+    room = torch.zeros((2 * 31 * 4 * 32 + 8,), device="cuda", dtype=BF16)
+    first, later = (room[at:at + 2 * 31 * 4 * 32].view(2, 31, 4, 32) for at in (0, 8))
+    for x, out in ((first, later), (q, q.view(2, 31, 4, 32).as_strided((2, 31, 4, 32), (4 * 31 * 32, 32, 31 * 32, 1)))):
+        with pytest.raises(ValueError):
+            ops.rotary_forward(x, None, pos, freqs, q_out=out)
 
 
 def test_empty_and_table():
