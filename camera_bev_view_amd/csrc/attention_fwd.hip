@@ -343,44 +343,68 @@ __global__ __launch_bounds__(kThreads) void attn_join_few(AttnArgs a) {
   if (lane == 0) a.stats[((int64_t)b * a.Hq + head) * a.Tq + t] = make_float2(top, tot);
 }
 
-// Many: one workgroup a row, the maximum and the weights over all threads, then wave w adds up
-// splits w, w + 4, ... (their loads do not depend on each other) and the four sums are added in wave order.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void attn_join(AttnArgs a) {
-  __shared__ float red[4], sums[4], part[4][128];
+// Many: one workgroup a row.  Wave w joins splits w, w + WAVES, ... with a running maximum, kJoinRun of them at a time whose
+// loads all go out at once (what they wait for is the time: 79 splits of 16 rows took 13 us when the maximum, and then four
+// splits at a time, were waited for in turn); the waves' results are joined in wave order.
+constexpr int kJoinRun = 8;
+
+template <typename T, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void attn_join(AttnArgs a) {
+  __shared__ float tops[WAVES], sums[WAVES], part[WAVES][128];
   const int64_t rows = (int64_t)a.B * a.Hk * a.R, row = blockIdx.x;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t stride = rows * (a.D + 2);
   const float* p = a.part + row * (a.D + 2);
-  float top = kNegInf;
-  for (int s = threadIdx.x; s < a.splits; s += kThreads) top = fmaxf(top, p[s * stride + a.D]);
-  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-  if (lane == 0) red[wave] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  const float base = top == kNegInf ? 0.0f : top;
-  float tot = 0.0f, o[2] = {0.0f, 0.0f};
-#pragma unroll 4
-  for (int s = wave; s < a.splits; s += 4) {
-    const float f = __builtin_amdgcn_exp2f(p[s * stride + a.D] - base);
-    tot = fmaf(p[s * stride + a.D + 1], f, tot);
+  float top = kNegInf, tot = 0.0f, o[2] = {0.0f, 0.0f};
+#pragma unroll 1
+  for (int s0 = wave; s0 < a.splits; s0 += WAVES * kJoinRun) {
+    float m[kJoinRun], l[kJoinRun], x[kJoinRun][2];
+    float next = top;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (lane + 64 * j < a.D) o[j] = fmaf(p[s * stride + lane + 64 * j], f, o[j]);
+    for (int i = 0; i < kJoinRun; ++i) {
+      const int s = s0 + i * WAVES;
+      const bool in = s < a.splits;
+      const float* q = p + (in ? s : s0) * stride;
+      m[i] = in ? q[a.D] : kNegInf;
+      l[i] = q[a.D + 1];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) x[i][j] = lane + 64 * j < a.D ? q[lane + 64 * j] : 0.0f;
+      next = fmaxf(next, m[i]);
+      if (!in) l[i] = x[i][0] = x[i][1] = 0.0f;
+    }
+    const float base = next == kNegInf ? 0.0f : next, back = __builtin_amdgcn_exp2f(top - base);
+    top = next;
+    tot *= back, o[0] *= back, o[1] *= back;
+#pragma unroll
+    for (int i = 0; i < kJoinRun; ++i) {
+      const float f = __builtin_amdgcn_exp2f(m[i] - base);
+      tot = fmaf(l[i], f, tot);
+      o[0] = fmaf(x[i][0], f, o[0]);
+      o[1] = fmaf(x[i][1], f, o[1]);
+    }
   }
-  if (lane == 0) sums[wave] = tot;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) part[wave][lane + 64 * j] = o[j];
+  if (lane == 0) tops[wave] = top, sums[wave] = tot;
+  part[wave][lane] = o[0], part[wave][lane + 64] = o[1];
   __syncthreads();
-  tot = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+  const int c = threadIdx.x;
+  if (c >= 128) return;
+  top = tops[0];
+#pragma unroll
+  for (int w = 1; w < WAVES; ++w) top = fmaxf(top, tops[w]);
+  const float base = top == kNegInf ? 0.0f : top;
+  float sum = 0.0f;
+  tot = 0.0f;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    const float f = __builtin_amdgcn_exp2f(tops[w] - base);
+    tot = fmaf(sums[w], f, tot);
+    sum = fmaf(part[w][c], f, sum);
+  }
   const int64_t bh = row / a.R;
   const int r = (int)(row - bh * a.R), t = r / a.G, b = (int)(bh / a.Hk);
   const int head = (int)(bh - (int64_t)b * a.Hk) * a.G + (r - t * a.G);
   const float inv = tot > 0.0f || tot != tot ? 1.0f / tot : 0.0f;
-  const int c = threadIdx.x;
-  if (c < a.D)
-    ((T*)a.out)[(((int64_t)b * a.Tq + t) * a.Hq + head) * a.D + c] =
-        (T)(((part[0][c] + part[1][c]) + (part[2][c] + part[3][c])) * inv);
+  if (c < a.D) ((T*)a.out)[(((int64_t)b * a.Tq + t) * a.Hq + head) * a.D + c] = (T)(sum * inv);
   if (c == 0) a.stats[((int64_t)b * a.Hq + head) * a.Tq + t] = make_float2(top, tot);
 }
 
@@ -404,14 +428,18 @@ Plan make_plan(const AttnArgs& a) {
     p.kw = 8;
   const int rows = p.kw == 1 ? 128 : 32, kt = p.kw == 1 ? 128 : 32 * p.kw;
   p.tiles = (a.R + rows - 1) / rows;
-  // under 128 workgroups the keys are split over several (at least 512 each, four workgroups a CU at most) and joined
+  // under 128 workgroups the keys are split over several and joined: at least 512 keys each and four workgroups a CU at most,
+  // but down to a stage of 128 keys while there is not a workgroup a CU (one token over 8000 keys of 2 heads: 32 workgroups
+  // take 10.9 us, 126 take 8.8 us; beyond that the join costs what shorter walks gain)
   const int64_t blocks = bh / p.hb * p.tiles;
   p.splits = 1;
   if (blocks < 128) {
-    int64_t want = (1024 + blocks - 1) / blocks;
-    const int64_t most = (a.Tk + 511) / 512;
-    if (want > most) want = most;
-    p.splits = want < 1 ? 1 : (int)want;
+    const auto at_most = [](int64_t x, int64_t y) { return x < y ? x : y; };
+    const int64_t keys = a.Tk;
+    const int64_t want = at_most((1024 + blocks - 1) / blocks, (keys + 511) / 512);
+    const int64_t fill = at_most((256 + blocks - 1) / blocks, (keys + 127) / 128);
+    p.splits = (int)(want > fill ? want : fill);
+    if (p.splits < 1) p.splits = 1;
   }
   const int per = (a.Tk + p.splits - 1) / p.splits;
   p.split_keys = (per + kt - 1) / kt * kt;
@@ -446,8 +474,10 @@ hipError_t run(AttnArgs& a, const Plan& p, hipStream_t stream) {
   const int64_t rows = (int64_t)a.B * a.Hk * a.R;
   if (p.splits <= kFewSplits)
     attn_join_few<T><<<dim3((unsigned)((rows + 3) / 4)), kThreads, 0, stream>>>(a);
+  else if (p.splits <= 4 * kJoinRun)
+    attn_join<T, 4><<<dim3((unsigned)rows), 256, 0, stream>>>(a);
   else
-    attn_join<T><<<dim3((unsigned)rows), kThreads, 0, stream>>>(a);
+    attn_join<T, 16><<<dim3((unsigned)rows), 1024, 0, stream>>>(a);
   return hipGetLastError();
 }
 

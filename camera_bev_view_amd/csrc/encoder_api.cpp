@@ -173,7 +173,7 @@ fbev_status check_attention(const fbev_attention_desc* ad, fbev::AttnArgs& a) {
     return fail(FBEV_ERR_UNSUPPORTED, "Tq Hq / Hk = %lld rows or Tk = %d keys (limit 2^30 - 1)", (long long)rows,
                 ad->Tk);
   const int64_t longest = (rows > ad->Tk ? rows : ad->Tk) / 32 + 1;
-  // (heads of the whole batch) x (tiles of 32) x (splits of at least 512 keys) blocks
+  // (heads of the whole batch) x (tiles of 32) blocks; splits come only where these are under 128
   if ((int64_t)ad->B * ad->Hk >= limit / longest || (int64_t)ad->B * ad->Hk * longest >= (int64_t)1 << 26)
     return fail(FBEV_ERR_UNSUPPORTED, "B Hk = %lld heads of %lld tiles of 32: above 2^26",
                 (long long)ad->B * ad->Hk, (long long)longest);

@@ -143,6 +143,7 @@ def test_two_heads_share_their_distances(form, dtype):
 def test_few_rows_over_many_keys(Tq, G, D, dtype):
     check(*draw(2, Tq, 5000, 2 * G, 2, D, dtype, 42, dims=2), f"split {Tq} x {G}", backward=False)
     check(*draw(1, Tq, 4097, G, 1, D, dtype, 43, causal=True, cap=10.0), f"split causal {Tq} x {G}")
+    check(*draw(1, Tq, 70001, G, 1, min(D, 40), dtype, 54), f"many splits {Tq} x {G}", backward=False)
     docs = ([[3] * Tq], [runs([1500, 700, 900, 4], 4100)])
     check(*draw(1, Tq, 4100, G, 1, D, dtype, 44, docs=docs), f"split documents {Tq} x {G}")
 
