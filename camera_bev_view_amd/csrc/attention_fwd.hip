@@ -7,7 +7,7 @@
 // head's G query heads are rows of one problem (row = token G + head), so single tokens with grouped heads
 // still fill a tile and keys are read once for the group.
 //
-// What bounds it (bf16, D = 128, 16 heads over 4, 2 x 3100 tokens with a prefix of 2816: 195 us, 735 TFLOP/s of
+// What bounds it (bf16, D = 128, 16 heads over 4, 2 x 3100 tokens with a prefix of 2816: 198 us, 725 TFLOP/s of
 // 1147 a large library product reaches): the exponentials' vector instructions between the matrix ones; at
 // D = 32 with distances (10000 x 10000 cells of 8 heads: 395 us) mostly those: the counters see 8.9 a score (half a
 // distance and its root, as two heads a wave share them, bias, maximum, exponential, sum, rounding), 180 us of issue
