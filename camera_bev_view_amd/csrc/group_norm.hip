@@ -13,7 +13,8 @@
 //     workgroups are at work and the other form is faster although it reads twice;
 //   - otherwise one launch leaves each chunk's (mean, sum of squares around it) in the workspace, and the
 //     next merges an image's chunks (pairwise formula, in their order) and normalises; its blocks take the
-//     chunks in the same order, so the second read finds much of them in the same L2.
+//     chunks in the same order, so the second read finds much of them in the same L2.  Many chunks are merged by a
+//     launch between the two.
 // The backward has the same two forms with the per-channel sums of dz and dz xh; the parameters'
 // gradients are column sums over chunks and images in a fixed order.  All results are deterministic.
 //
@@ -291,12 +292,50 @@ __global__ __launch_bounds__(BLOCK) void norm_moments(NormArgs a, int nch, int s
   }
 }
 
+// An image's chunks joined once, for all workgroups that normalise it: a wave a group, its lanes as share_moments joins
+// threads.  Writes the statistics.
+__global__ __launch_bounds__(512) void norm_join(NormArgs a, int chunk, int chunks) {
+  const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 6);
+  if (at >= (int64_t)a.images * a.groups) return;
+  const int img = (int)(at / a.groups), g = (int)(at - (int64_t)img * a.groups), lane = threadIdx.x & 63;
+  const int cg = a.C / a.groups;
+  const float2* p = (const float2*)a.part + (int64_t)img * chunks * a.groups + g;
+  const float n = (float)a.pixels * (float)cg;
+  const float full = (float)chunk * (float)cg, rest = (float)(a.pixels - (chunks - 1) * chunk) * (float)cg;
+  auto size = [&](int k) { return k < chunks - 1 ? full : (k == chunks - 1 ? rest : 0.0f); };
+  float mean = 0.0f, m2 = 0.0f;
+  for (int k0 = lane; k0 < chunks; k0 += 64 * 8) {        // eight loads in flight at once
+    float2 c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = p[(int64_t)min(k0 + 64 * i, chunks - 1) * a.groups];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mean = fmaf(size(k0 + 64 * i), c[i].x, mean);
+  }
+  for (int o = 32; o > 0; o >>= 1) mean += __shfl_xor(mean, o);
+  mean /= n;
+  for (int k0 = lane; k0 < chunks; k0 += 64 * 8) {
+    float2 c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = p[(int64_t)min(k0 + 64 * i, chunks - 1) * a.groups];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float d = c[i].x - mean, q = fmaf(size(k0 + 64 * i) * d, d, c[i].y);
+      if (k0 + 64 * i < chunks) m2 += q;
+    }
+  }
+  for (int o = 32; o > 0; o >>= 1) m2 += __shfl_xor(m2, o);
+  if (lane == 0) {
+    a.stats[2 * at] = mean;
+    a.stats[2 * at + 1] = 1.0f / sqrtf(m2 / n + a.eps);
+  }
+}
+
 constexpr int kKeep = 12;
 
 // The second: merges the image's chunks and normalises.
 template <int BLOCK, typename T, int V, int R, int ACT>
 __global__ __launch_bounds__(BLOCK) void norm_apply(NormArgs a, int nch, int slabs, int chunk, int chunks, int share,
-                                                   int shares) {
+                                                   int shares, bool joined) {
   __shared__ Groups<BLOCK, V> L;
   const int per_img = slabs * shares, img = blockIdx.x / per_img, rest = blockIdx.x - img * per_img;
   const int slab = rest / shares, ch = rest - slab * shares, c0 = slab * nch;
@@ -311,7 +350,14 @@ __global__ __launch_bounds__(BLOCK) void norm_apply(NormArgs a, int nch, int sla
   int gt = 64;
   while (gt > 1 && gt * ng > BLOCK) gt >>= 1;
   const float n = (float)a.pixels * (float)cg;
-  for (int g0 = 0; g0 < ng; g0 += BLOCK / gt) {
+  if (joined) {
+    for (int g = threadIdx.x; g < ng; g += BLOCK) {
+      const float* st = a.stats + ((int64_t)img * a.groups + c0 / cg + g) * 2;
+      L.g1[g] = st[0];
+      L.g2[g] = st[1];
+    }
+  }
+  for (int g0 = joined ? ng : 0; g0 < ng; g0 += BLOCK / gt) {
     const int g = g0 + (int)threadIdx.x / gt, l = threadIdx.x & (gt - 1);
     const float2* p = (const float2*)a.part + (int64_t)img * chunks * a.groups + c0 / cg + g;
     float mean = 0.0f, m2 = 0.0f;
@@ -536,34 +582,63 @@ __global__ __launch_bounds__(BLOCK) void norm_bwd_sums(NormArgs a, int nch, int 
 // Sums of one column of the [rows][2 C] partial sums, by a wave.
 __device__ __forceinline__ float wave_column(const float* part, int64_t rows, int stride, int col) {
   float s = 0.0f;
-#pragma unroll 8
-  for (int64_t r = threadIdx.x & 63; r < rows; r += 64) s += part[r * stride + col];
+  for (int64_t r0 = threadIdx.x & 63; r0 < rows; r0 += 64 * 8) {      // eight loads in flight at once
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = part[(r0 + 64 * i < rows ? r0 + 64 * i : rows - 1) * stride + col];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += r0 + 64 * i < rows ? v[i] : 0.0f;
+  }
   for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
   return s;
 }
 
 template <int BLOCK>
-__device__ __forceinline__ void param_grads(const NormArgs& a, int64_t rows, int block) {
+__device__ __forceinline__ void param_grads(const NormArgs& a, const float* sums, int64_t rows, int block) {
   const int col = block * (BLOCK / 64) + (int)(threadIdx.x >> 6);     // 0 .. 2 C - 1
   if (col >= 2 * a.C) return;
   float* out = col < a.C ? a.gbias : a.gweight;
   if (out == nullptr) return;
-  const float s = wave_column(a.part, rows, 2 * a.C, col);
+  const float s = wave_column(sums, rows, 2 * a.C, col);
   if ((threadIdx.x & 63) == 0) out[col < a.C ? col : col - a.C] = s;
 }
 
 template <int BLOCK>
 __global__ __launch_bounds__(BLOCK) void norm_param_grads(NormArgs a, int64_t rows) {
-  param_grads<BLOCK>(a, rows, blockIdx.x);
+  param_grads<BLOCK>(a, a.part, rows, blockIdx.x);
 }
 
 // The second: gx from the image's sums; the blocks behind the last chunk add up the parameters' gradients.
+// An image's chunks joined once, for all workgroups of the next launch: 32 columns by 32 chunks a workgroup.
+__global__ __launch_bounds__(1024) void norm_bwd_join(NormArgs a, int chunks, float* sums) {
+  __shared__ float part[32][33];
+  const int per_img = (2 * a.C + 31) / 32, img = blockIdx.x / per_img;
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, col = (blockIdx.x - img * per_img) * 32 + x;
+  const float* p = a.part + (int64_t)img * chunks * 2 * a.C + min(col, 2 * a.C - 1);
+  float s = 0.0f;
+  for (int k0 = y; k0 < chunks; k0 += 32 * 8) {           // eight loads in flight at once
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = p[(int64_t)min(k0 + 32 * i, chunks - 1) * 2 * a.C];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += k0 + 32 * i < chunks ? v[i] : 0.0f;
+  }
+  part[y][x] = s;
+  __syncthreads();
+  if (y > 0 || col >= 2 * a.C) return;
+  s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) s += part[i][x];
+  sums[(int64_t)img * 2 * a.C + col] = s;
+}
+
 template <int BLOCK, typename T, int V, int R, int ACT>
-__global__ __launch_bounds__(BLOCK) void norm_bwd_apply(NormArgs a, int nch, int slabs, int chunk, int chunks) {
+__global__ __launch_bounds__(BLOCK) void norm_bwd_apply(NormArgs a, int nch, int slabs, int chunk, int chunks,
+                                                       const float* sums, int rows) {
   __shared__ Groups<BLOCK, V> L;
   const int per_img = slabs * chunks, img = blockIdx.x / per_img, rest = blockIdx.x - img * per_img;
   if (img >= a.images) {
-    param_grads<BLOCK>(a, (int64_t)a.images * chunks, blockIdx.x - a.images * per_img);
+    param_grads<BLOCK>(a, sums, (int64_t)a.images * rows, blockIdx.x - a.images * per_img);
     return;
   }
   const int slab = rest / chunks, ch = rest - slab * chunks, c0 = slab * nch;
@@ -575,9 +650,15 @@ __global__ __launch_bounds__(BLOCK) void norm_bwd_apply(NormArgs a, int nch, int
   const Channel<V> p = load_channel<V>(a, w, cg);
   for (int c = threadIdx.x; c < 2 * cols; c += BLOCK) {
     const int col = c < cols ? c : a.C + c - cols;
+    const float* q = sums + (int64_t)img * rows * 2 * a.C + c0 + col;
     float s = 0.0f;
-#pragma unroll 16
-    for (int k = 0; k < chunks; ++k) s += a.part[((int64_t)img * chunks + k) * 2 * a.C + c0 + col];
+    for (int k0 = 0; k0 < rows; k0 += 16) {               // sixteen loads in flight at once
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = q[(int64_t)min(k0 + i, rows - 1) * 2 * a.C];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s += k0 + i < rows ? v[i] : 0.0f;
+    }
     (c < cols ? L.g1 : L.g2)[c < cols ? c : c - cols] = s;
   }
   __syncthreads();
@@ -595,6 +676,12 @@ constexpr int kWhole = 2;       // pieces a thread of a kBig workgroup holds of 
 constexpr int kR = 8;           // pieces a thread holds of a chunk (forward)
 constexpr int kRA = 8;          // pieces a thread normalises (forward, the second launch)
 constexpr int kRB = 4;          // pieces of x and of gy a thread holds of a chunk (backward)
+
+// An image's chunks are joined by a launch of their own above so many of them: every workgroup of the next launch joins them
+// by itself below, which is a launch less but grows with the square (bf16, 200 x 200 cells, 128 channels, 313 and 625 chunks:
+// forward 30.8 -> 21.7 us, backward 72 -> 33 us; four maps with 256 channels, backward 1119 -> 173 us; 88 chunks forward
+// 27.7 and 28.0 us, 29 backward 29.9 and 31.2 us, 79 backward 16.5 and 17.0 us).
+constexpr int kJoinMoments = 96, kJoinSums = 64;
 
 struct Plan {
   bool whole;
@@ -641,8 +728,11 @@ void forward(const NormArgs& a, const Plan& p, hipStream_t stream) {
   const int share = kRA * (BLOCK / (p.nch / V)), shares = (a.pixels + share - 1) / share;
   norm_moments<BLOCK, T, V, kR><<<dim3((unsigned)(a.images * p.slabs * p.chunks)), BLOCK, 0, stream>>>(
       a, p.nch, p.slabs, p.chunk, p.chunks);
+  const bool joined = p.chunks > kJoinMoments;
+  if (joined)
+    norm_join<<<dim3((unsigned)(((int64_t)a.images * a.groups + 7) / 8)), 512, 0, stream>>>(a, p.chunk, p.chunks);
   norm_apply<BLOCK, T, V, kRA, ACT><<<dim3((unsigned)(a.images * p.slabs * shares)), BLOCK, 0, stream>>>(
-      a, p.nch, p.slabs, p.chunk, p.chunks, share, shares);
+      a, p.nch, p.slabs, p.chunk, p.chunks, share, shares, joined);
 }
 
 template <int BLOCK, typename T, int V, int ACT>
@@ -650,7 +740,16 @@ void backward(const NormArgs& a, const Plan& p, hipStream_t stream) {
   const unsigned extra = a.gweight || a.gbias ? (unsigned)((2 * a.C + BLOCK / 64 - 1) / (BLOCK / 64)) : 0;
   const unsigned n = (unsigned)(a.images * p.slabs * p.chunks);
   norm_bwd_sums<BLOCK, T, V, kRB, ACT><<<dim3(n), BLOCK, 0, stream>>>(a, p.nch, p.slabs, p.chunk, p.chunks);
-  norm_bwd_apply<BLOCK, T, V, kRB, ACT><<<dim3(n + extra), BLOCK, 0, stream>>>(a, p.nch, p.slabs, p.chunk, p.chunks);
+  const float* sums = a.part;
+  int rows = p.chunks;
+  if (p.chunks > kJoinSums) {
+    float* joined = a.part + (int64_t)a.images * p.chunks * 2 * a.C;
+    norm_bwd_join<<<dim3((unsigned)(a.images * ((2 * a.C + 31) / 32))), 1024, 0, stream>>>(a, p.chunks, joined);
+    sums = joined;
+    rows = 1;
+  }
+  norm_bwd_apply<BLOCK, T, V, kRB, ACT><<<dim3(n + extra), BLOCK, 0, stream>>>(a, p.nch, p.slabs, p.chunk, p.chunks,
+                                                                               sums, rows);
 }
 
 template <typename T, int V, int ACT>
@@ -697,7 +796,8 @@ hipError_t by_type(const NormArgs& a, bool bwd, hipStream_t stream) {
 
 size_t group_norm_workspace_bytes(const NormArgs& a, bool backward) {
   const Plan p = make_plan(a, backward ? kRB : kR);
-  if (backward) return (size_t)a.images * (p.whole ? 1 : p.chunks) * 2 * a.C * sizeof(float);
+  if (backward)
+    return (size_t)a.images * (p.whole ? 1 : p.chunks + (p.chunks > kJoinSums ? 1 : 0)) * 2 * a.C * sizeof(float);
   return p.whole ? 0 : (size_t)a.images * p.chunks * 2 * a.groups * sizeof(float);
 }
 

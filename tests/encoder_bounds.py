@@ -3,7 +3,8 @@
 U = 2^-24 is half a step of fp32.  A rounding to a tensor's type is off by at most finfo(type).eps / 2 of the value.
 An fp32 sum whose longest chain of additions has n terms is off by at most n U times the sum of magnitudes; CHAIN
 bounds the chains of the norm kernels at the tested sizes (16 pieces of a thread, 8 channels of a piece, up to 128
-terms of a lane's share of the workgroup's sums, 6 lane steps and the merge of at most 64 chunks).
+terms of a lane's share of the workgroup's sums, 6 lane steps and the merge of at most 64 chunks, which lanes share
+where there are more).
 """
 import numpy as np
 import torch

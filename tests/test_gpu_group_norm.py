@@ -48,7 +48,9 @@ def check(x, gy, w, b, groups, kind, label, image_dims=None, eps=1e-5):
 # in one workgroup, images in chunks (the last one short), more channels than a workgroup has pieces, one group
 SHAPES = [((1, 1, 4), 1), ((3, 5, 7, 6), 6), ((2, 3, 4, 5, 80), 16), ((2, 9, 13, 81), 27), ((1, 8, 22, 64), 8),
           ((3, 300, 12), 4), ((1, 2, 64, 176, 32), 4), ((2, 70, 70, 20), 4), ((1, 5, 9, 2064), 16), ((2, 40, 40, 36), 1),
-          ((1, 3000, 10), 5)]
+          ((1, 3000, 10), 5),
+          # more chunks than a workgroup joins by itself: forward and backward, backward alone, a wide slab, odd channels
+          ((1, 100, 130, 128), 32), ((2, 90, 150, 36), 9), ((2, 1, 700, 1, 1032), 3), ((1, 150, 150, 27), 9)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
