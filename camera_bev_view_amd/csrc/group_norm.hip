@@ -672,10 +672,11 @@ __global__ __launch_bounds__(BLOCK) void norm_bwd_apply(NormArgs a, int nch, int
 constexpr int kSmall = 256, kBig = 1024;
 constexpr int kWhole = 2;       // pieces a thread of a kBig workgroup holds of a whole slab (32 KB)
 // Eight pieces were faster than 16 in the moments (which leave CUs idle) and than 2 or 4 in the second launch (more
-// workgroups, each of which merges the chunks).  The backward holds two tensors, four pieces of each.
+// workgroups, each of which merges the chunks).  The backward holds two tensors, four or six
+// pieces of each.
 constexpr int kR = 8;           // pieces a thread holds of a chunk (forward)
 constexpr int kRA = 8;          // pieces a thread normalises (forward, the second launch)
-constexpr int kRB = 4;          // pieces of x and of gy a thread holds of a chunk (backward)
+constexpr int kRB = 4, kRBMany = 6;       // pieces of x and of gy a thread holds of a chunk (backward)
 
 // An image's chunks are joined by a launch of their own above so many of them: every workgroup of the next launch joins them
 // by itself below, which is a launch less but grows with the square (bf16, 200 x 200 cells, 128 channels, 313 and 625 chunks:
@@ -723,6 +724,15 @@ Plan make_plan(const NormArgs& a, int R) {
   return p;
 }
 
+// The backward's plan, and the pieces it was made for: six of each tensor where there are workgroups enough with four (bf16,
+// six maps of 64 x 176, 128 channels: 53 -> 41 us; four of 200 x 200, 256 channels: 177 -> 158 us), four where there are
+// not (six of 32 x 88, 80 channels: 18.9 us against 21.2 us; 174 workgroups).
+Plan backward_plan(const NormArgs& a, int* pieces) {
+  const Plan p = make_plan(a, kRB);
+  *pieces = !p.whole && (int64_t)a.images * p.slabs * p.chunks >= 512 ? kRBMany : kRB;
+  return *pieces == kRB ? p : make_plan(a, kRBMany);
+}
+
 template <int BLOCK, typename T, int V, int ACT>
 void forward(const NormArgs& a, const Plan& p, hipStream_t stream) {
   const int share = kRA * (BLOCK / (p.nch / V)), shares = (a.pixels + share - 1) / share;
@@ -735,11 +745,11 @@ void forward(const NormArgs& a, const Plan& p, hipStream_t stream) {
       a, p.nch, p.slabs, p.chunk, p.chunks, share, shares, joined);
 }
 
-template <int BLOCK, typename T, int V, int ACT>
+template <int BLOCK, typename T, int V, int ACT, int R>
 void backward(const NormArgs& a, const Plan& p, hipStream_t stream) {
   const unsigned extra = a.gweight || a.gbias ? (unsigned)((2 * a.C + BLOCK / 64 - 1) / (BLOCK / 64)) : 0;
   const unsigned n = (unsigned)(a.images * p.slabs * p.chunks);
-  norm_bwd_sums<BLOCK, T, V, kRB, ACT><<<dim3(n), BLOCK, 0, stream>>>(a, p.nch, p.slabs, p.chunk, p.chunks);
+  norm_bwd_sums<BLOCK, T, V, R, ACT><<<dim3(n), BLOCK, 0, stream>>>(a, p.nch, p.slabs, p.chunk, p.chunks);
   const float* sums = a.part;
   int rows = p.chunks;
   if (p.chunks > kJoinSums) {
@@ -748,13 +758,14 @@ void backward(const NormArgs& a, const Plan& p, hipStream_t stream) {
     sums = joined;
     rows = 1;
   }
-  norm_bwd_apply<BLOCK, T, V, kRB, ACT><<<dim3(n + extra), BLOCK, 0, stream>>>(a, p.nch, p.slabs, p.chunk, p.chunks,
+  norm_bwd_apply<BLOCK, T, V, R, ACT><<<dim3(n + extra), BLOCK, 0, stream>>>(a, p.nch, p.slabs, p.chunk, p.chunks,
                                                                                sums, rows);
 }
 
 template <typename T, int V, int ACT>
 hipError_t run(const NormArgs& a, bool bwd, hipStream_t stream) {
-  const Plan p = make_plan(a, bwd ? kRB : kR);
+  int pieces = kR;
+  const Plan p = bwd ? backward_plan(a, &pieces) : make_plan(a, kR);
   const dim3 whole((unsigned)(a.images * p.slabs));
   if (p.whole && !bwd) {
     norm_whole<kBig, T, V, kWhole, ACT><<<whole, kBig, 0, stream>>>(a, p.nch, p.slabs);
@@ -763,7 +774,11 @@ hipError_t run(const NormArgs& a, bool bwd, hipStream_t stream) {
     if (a.gweight || a.gbias)
       norm_param_grads<kSmall><<<dim3((unsigned)((2 * a.C + 3) / 4)), kSmall, 0, stream>>>(a, a.images);
   } else if (bwd) {
-    p.big ? backward<kBig, T, V, ACT>(a, p, stream) : backward<kSmall, T, V, ACT>(a, p, stream);
+    if (p.big)
+      pieces == kRB ? backward<kBig, T, V, ACT, kRB>(a, p, stream) : backward<kBig, T, V, ACT, kRBMany>(a, p, stream);
+    else
+      pieces == kRB ? backward<kSmall, T, V, ACT, kRB>(a, p, stream)
+                    : backward<kSmall, T, V, ACT, kRBMany>(a, p, stream);
   } else {
     p.big ? forward<kBig, T, V, ACT>(a, p, stream) : forward<kSmall, T, V, ACT>(a, p, stream);
   }
@@ -795,7 +810,8 @@ hipError_t by_type(const NormArgs& a, bool bwd, hipStream_t stream) {
 }  // namespace
 
 size_t group_norm_workspace_bytes(const NormArgs& a, bool backward) {
-  const Plan p = make_plan(a, backward ? kRB : kR);
+  int pieces;
+  const Plan p = backward ? backward_plan(a, &pieces) : make_plan(a, kR);
   if (backward)
     return (size_t)a.images * (p.whole ? 1 : p.chunks + (p.chunks > kJoinSums ? 1 : 0)) * 2 * a.C * sizeof(float);
   return p.whole ? 0 : (size_t)a.images * p.chunks * 2 * a.groups * sizeof(float);

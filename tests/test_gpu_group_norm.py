@@ -50,7 +50,9 @@ SHAPES = [((1, 1, 4), 1), ((3, 5, 7, 6), 6), ((2, 3, 4, 5, 80), 16), ((2, 9, 13,
           ((3, 300, 12), 4), ((1, 2, 64, 176, 32), 4), ((2, 70, 70, 20), 4), ((1, 5, 9, 2064), 16), ((2, 40, 40, 36), 1),
           ((1, 3000, 10), 5),
           # more chunks than a workgroup joins by itself: forward and backward, backward alone, a wide slab, odd channels
-          ((1, 100, 130, 128), 32), ((2, 90, 150, 36), 9), ((2, 1, 700, 1, 1032), 3), ((1, 150, 150, 27), 9)]
+          ((1, 100, 130, 128), 32), ((2, 90, 150, 36), 9), ((2, 1, 700, 1, 1032), 3), ((1, 150, 150, 27), 9),
+          # workgroups enough for longer chunks in the backward
+          ((9, 70, 60, 128), 32), ((40, 33, 31, 45), 9), ((3, 700, 1032), 43)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
