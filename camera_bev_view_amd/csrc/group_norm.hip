@@ -18,7 +18,7 @@
 // The backward has the same two forms with the per-channel sums of dz and dz xh; the parameters'
 // gradients are column sums over chunks and images in a fixed order.  All results are deterministic.
 //
-// Measured: bf16, 24 maps of 32 x 88 with 80 channels (10.8 MB): moments 9.4, apply 10.8, backward 13.3 and 19.3 us;
+// Measured: bf16, 24 maps of 32 x 88 with 80 channels (10.8 MB): moments 9.4, apply 10.3, backward 13.4 and 16.7 us;
 // six maps of 64 x 176 with 128 channels (17.3 MB): 9.4 and 18.1 us.  The second read comes out of the caches (the
 // counters see each kernel fetch its input once); a launch costs about 4 us of each, the rest is one round of
 // loads and stores by all workgroups at once (1.9 TB/s while it runs).
