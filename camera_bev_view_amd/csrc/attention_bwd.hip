@@ -115,10 +115,22 @@ __device__ __forceinline__ RowStats row_stats(const AttnArgs& a, int64_t bh) {
   return RowStats{p, p + R, p + 2 * R, p + 3 * R, p + 4 * R};
 }
 
+// Where few own tiles stand against a long other side, its rows are split over `splits` workgroups, `per` (a multiple of
+// every stage) each; their fp32 sums are joined in split order (one token of 8 heads over 40000 keys of 2: 357 -> 66 us;
+// 40000 x 8 rows over 900 keys of one head: 3786 -> 704 us).
+struct Split {
+  int splits, per;
+  float* part;
+};
+
+// Floats of a partial row: gq with the sums of ds, ds d and p d; gk or gv.
+__host__ __device__ __forceinline__ int row_floats(int D) { return (D + 6) / 4 * 4; }
+__host__ __device__ __forceinline__ int key_floats(int D) { return (D + 3) / 4 * 4; }
+
 // ---- query rows: delta, gq, gslope
 
 template <typename T, int DP, int KW, int HB, bool BIAS, bool CAP>
-__global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(HB))) void attn_bwd_rows(AttnArgs a, int tiles) {
+__global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(HB))) void attn_bwd_rows(AttnArgs a, int tiles, Split sp) {
   using C = Bwd<T, DP, KW, HB>;
   using M = Mma<T, DP>;
   constexpr int NB = DP / 32, MT = C::MT, RW = C::RW;
@@ -175,7 +187,7 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
     neg_m[i] = ml.y == 0.0f ? kNegInf : -ml.x;
     inv_l[i] = ml.y == 0.0f ? 0.0f : 1.0f / ml.y;
     if constexpr (BIAS) slope[i] = a.slope[((int64_t)b * a.Tq + w.t) * a.Hq + w.head + i] / un.raw;
-    if (kw == 0 && h == 0 && first + n < a.R) {
+    if (kw == 0 && h == 0 && first + n < a.R && blockIdx.y == 0) {
       const RowStats rs = row_stats(a, (int64_t)b * a.Hk + hk + i);
       const float lse2 = ml.y == 0.0f ? -kNegInf : ml.x + __builtin_amdgcn_logf(ml.y);
       rs.off[w.r] = sizeof(T) == 4 ? -neg_m[i] : CAP ? lse2 : lse2 / un.unit;
@@ -211,13 +223,14 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
   f32x16 acc[HB][NB] = {};
   bool odd[HB] = {};                                      // the row sees a key with an infinite or NaN element
   float sum_ds[HB] = {}, sum_dsd[HB] = {}, sum_pd[HB] = {};
-  const int k_end = min(a.Tk, blk_hi + 1);
+  const int k_begin = (int)blockIdx.y * sp.per;
+  const int k_end = min(min(a.Tk, blk_hi + 1), k_begin + sp.per);
   uint32_t stages = 0;
-  for (int s0 = 0; s0 < k_end; s0 += MT) {
+  for (int s0 = k_begin; s0 < k_end; s0 += MT) {
     const int nk = min(MT, a.Tk - s0);
     int my_doc = -1;
     if (a.doc_q) {
-      const int stage = s0 / MT & 31;
+      const int stage = (s0 - k_begin) / MT & 31;
       if (stage == 0)
         stages = stages_with<MT, C::kThreads>(&stage_bits, s0, k_end, bmin, bmax, [&](int j) { return a.doc_k[(int64_t)b * a.Tk + j]; });
       if (!((stages >> stage) & 1)) continue;
@@ -343,11 +356,21 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
       for (int i = 0; i < 16; ++i) acc[hd][blk][i] *= inv_l[hd];
     make_nan<NB>(acc[hd], odd[hd]);
     // the queries' sign is in s, not in k: a zero scale gives zeros
-    write_own<T, DP, KW>(acc[hd], a.scale, (float*)smem, a.D, a.vec_out, kw, lane, [&](int r) -> T* {
-      if (first + r >= a.R) return nullptr;
-      const int t = (first + r) / a.G, head = hk * a.G + (first + r - t * a.G) + hd;
-      return (T*)a.gq + (((int64_t)b * a.Tq + t) * a.Hq + head) * a.D;
-    });
+    float* part = nullptr;                                // of the tile's first row
+    if constexpr (KW > 1 && HB == 1) {
+      if (sp.splits > 1)
+        part = sp.part + (((int64_t)blockIdx.y * a.B * a.Hk + bh) * a.R + first) * row_floats(a.D);
+    }
+    if (part != nullptr)
+      write_own<float, DP, KW>(acc[hd], a.scale, (float*)smem, a.D, false, kw, lane, [&](int r) -> float* {
+        return first + r < a.R ? part + (int64_t)r * row_floats(a.D) : nullptr;
+      });
+    else
+      write_own<T, DP, KW>(acc[hd], a.scale, (float*)smem, a.D, a.vec_out, kw, lane, [&](int r) -> T* {
+        if (first + r >= a.R) return nullptr;
+        const int t = (first + r) / a.G, head = hk * a.G + (first + r - t * a.G) + hd;
+        return (T*)a.gq + (((int64_t)b * a.Tq + t) * a.Hq + head) * a.D;
+      });
     // delta came from the rounded output; ds sums to the error it made (sum_j p_ij = 1): the keys' launch gets delta
     // without it, and the distances' mean takes it out of the slope's gradient, which is fp32 whatever the type
     float sd = pair_sum(sum_ds[hd]) * inv_l[hd], sdd = 0.0f, pd = 0.0f;
@@ -365,7 +388,13 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
       for (int k = 0; k < KW; ++k) sd += slopes[k][0][n], sdd += slopes[k][1][n], pd += slopes[k][2][n];
       bad = false;
     }
-    if (kw == 0 && h == 0 && first + n < a.R) {
+    if (part != nullptr) {
+      if (kw == 0 && h == 0 && first + n < a.R) {
+        float* sums = part + (int64_t)n * row_floats(a.D) + a.D;
+        sums[0] = sd, sums[1] = sdd, sums[2] = pd;
+        if (blockIdx.y == 0) row_stats(a, (int64_t)b * a.Hk + hk + hd).delta[w.r] = delta[hd];
+      }
+    } else if (kw == 0 && h == 0 && first + n < a.R) {
       row_stats(a, (int64_t)b * a.Hk + hk + hd).delta[w.r] = delta[hd] + sd;
       if (BIAS && a.gslope)
         a.gslope[((int64_t)b * a.Tq + w.t) * a.Hq + w.head + hd] = bad ? __builtin_nanf("") : fmaf(sd, pd, -sdd);
@@ -376,7 +405,7 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
 // ---- keys: gk, gv
 
 template <typename T, int DP, int KW, int HB, bool BIAS, bool CAP>
-__global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(HB))) void attn_bwd_keys(AttnArgs a, int tiles) {
+__global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(HB))) void attn_bwd_keys(AttnArgs a, int tiles, Split sp) {
   using C = Bwd<T, DP, KW, HB>;
   using M = Mma<T, DP>;
   constexpr int NB = DP / 32, MT = C::MT, RW = C::RW;
@@ -446,8 +475,10 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
     const int64_t t0 = (int64_t)blk_key - a.Tk + a.Tq;
     if (t0 > 0) r_begin = (int)((t0 < a.Tq ? t0 : a.Tq) * a.G) / MT * MT;
   }
+  r_begin = max(r_begin, (int)blockIdx.y * sp.per);
+  const int r_end = min(a.R, (int)blockIdx.y * sp.per + sp.per);
   uint32_t stages = 0;
-  for (int s0 = r_begin; s0 < a.R; s0 += MT) {
+  for (int s0 = r_begin; s0 < r_end; s0 += MT) {
     const int nr = min(MT, a.R - s0);
     Row w;
     w.doc = -1, w.lim = -1;
@@ -603,9 +634,91 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
     };
     add_odd<NB>(gv[hd], odd[hd]);
     make_nan<NB>(gk[hd], odd_key[hd]);
+    if constexpr (KW > 1 && HB == 1) {
+      if (sp.splits > 1) {
+        const int pf = key_floats(a.D);
+        float* part = sp.part + (((int64_t)blockIdx.y * a.B * a.Hk + bh) * a.Tk + key0) * 2 * pf;
+        auto row = [&](int r, int which) { return key0 + r < a.Tk ? part + ((int64_t)r * 2 + which) * pf : nullptr; };
+        write_own<float, DP, KW>(gv[hd], 1.0f, (float*)smem, a.D, false, kw, lane, [&](int r) { return row(r, 1); });
+        write_own<float, DP, KW>(gk[hd], a.scale, (float*)smem, a.D, false, kw, lane, [&](int r) { return row(r, 0); });
+        return;
+      }
+    }
     write_own<T, DP, KW>(gv[hd], 1.0f, (float*)smem, a.D, a.vec_out, kw, lane, [&](int r) { return at_key(a.gv, r); });
     write_own<T, DP, KW>(gk[hd], a.scale, (float*)smem, a.D, a.vec_out, kw, lane, [&](int r) { return at_key(a.gk, r); });
   }
+}
+
+// ---- joins of the splits: a wave a row
+
+// Sum of element lane + 64 j of a row over the splits, eight of them in flight at once.
+template <int N>
+__device__ __forceinline__ void sum_splits(const float* row, int64_t stride, int splits, int floats, int lane,
+                                           float (&o)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) o[j] = 0.0f;
+  for (int s0 = 0; s0 < splits; s0 += 8) {
+    float v[8][N];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[i][j] = row[min(s0 + i, splits - 1) * stride + min(lane + 64 * j, floats - 1)];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < N; ++j) o[j] += s0 + i < splits ? v[i][j] : 0.0f;
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void attn_bwd_join_rows(AttnArgs a, Split sp) {
+  const int64_t rows = (int64_t)a.B * a.Hk * a.R, row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= rows) return;
+  const int lane = threadIdx.x & 63, pf = row_floats(a.D);
+  float o[3];
+  sum_splits<3>(sp.part + row * pf, rows * pf, sp.splits, a.D + 3, lane, o);
+  const int64_t bh = row / a.R;
+  const int r = (int)(row - bh * a.R), t = r / a.G, b = (int)(bh / a.Hk);
+  const int head = (int)(bh - (int64_t)b * a.Hk) * a.G + (r - t * a.G);
+  T* gq = (T*)a.gq + (((int64_t)b * a.Tq + t) * a.Hq + head) * a.D;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (lane + 64 * j < a.D) gq[lane + 64 * j] = (T)o[j];
+  auto at = [&](int i) { return __shfl(i < 64 ? o[0] : i < 128 ? o[1] : o[2], i & 63); };
+  const float sd = at(a.D), sdd = at(a.D + 1), pd = at(a.D + 2);
+  if (lane == 0) {
+    row_stats(a, bh).delta[r] += sd;
+    if (a.dims && a.gslope) a.gslope[((int64_t)b * a.Tq + t) * a.Hq + head] = fmaf(sd, pd, -sdd);
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void attn_bwd_join_keys(AttnArgs a, Split sp) {
+  const int64_t rows = (int64_t)a.B * a.Hk * a.Tk * 2, row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= rows) return;
+  const int lane = threadIdx.x & 63, pf = key_floats(a.D);
+  float o[2];
+  sum_splits<2>(sp.part + row * pf, rows * pf, sp.splits, a.D, lane, o);
+  const int64_t bh = row / 2 / a.Tk;
+  const int key = (int)(row / 2 - bh * a.Tk), b = (int)(bh / a.Hk), hk = (int)(bh - (int64_t)b * a.Hk);
+  T* out = (T*)(row & 1 ? a.gv : a.gk) + (((int64_t)b * a.Tk + key) * a.Hk + hk) * a.D;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (lane + 64 * j < a.D) out[lane + 64 * j] = (T)o[j];
+}
+
+// `own` rows a head against `len` others: split under 128 tiles of 32, as the forward's keys are.
+Split make_split(const AttnArgs& a, int own, int len) {
+  const int64_t tiles = (int64_t)a.B * a.Hk * ((own + 31) / 32);
+  Split sp{1, INT32_MAX / 256 * 256, nullptr};
+  if (tiles == 0 || tiles >= 128 || len <= 256) return sp;
+  const auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
+  const int64_t want = least((1024 + tiles - 1) / tiles, ((int64_t)len + 511) / 512);
+  const int64_t fill = least((256 + tiles - 1) / tiles, ((int64_t)len + 255) / 256);
+  const int64_t n = want > fill ? want : fill;
+  sp.per = (int)((((int64_t)len + n - 1) / n + 255) / 256 * 256);
+  sp.splits = (int)(((int64_t)len + sp.per - 1) / sp.per);
+  return sp;
 }
 
 // Waves that split the moving rows of a tile of own rows.
@@ -619,32 +732,44 @@ int pick_waves(const AttnArgs& a, int64_t heads, int rows) {
   return 4;
 }
 
+// The rows' figures, then the splits' partial rows (of one launch at a time).
+int64_t stats_size(const AttnArgs& a) { return ((int64_t)a.B * a.Hk * a.R * stat_floats(a) + 3) / 4 * 4; }
+float* split_part(const AttnArgs& a) { return a.delta == nullptr ? nullptr : a.delta + stats_size(a); }
+
 template <typename T, int DP, int HB, bool BIAS, bool CAP>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
   const int64_t heads = (int64_t)a.B * a.Hk / HB;
   if (a.R > 0) {
     const int kw = pick_waves<T, DP, HB>(a, heads, a.R), rows = kw == 1 ? 128 : 32;
     const int tiles = (a.R + rows - 1) / rows;
-    const dim3 grid((unsigned)(heads * tiles));
+    Split sp = make_split(a, a.R, a.Tk);
+    sp.part = split_part(a);
+    const dim3 grid((unsigned)(heads * tiles), (unsigned)sp.splits);
     if (kw == 1)
-      attn_bwd_rows<T, DP, 1, HB, BIAS, CAP><<<grid, 256, 0, stream>>>(a, tiles);
+      attn_bwd_rows<T, DP, 1, HB, BIAS, CAP><<<grid, 256, 0, stream>>>(a, tiles, sp);
     else if (kw == 4)
-      attn_bwd_rows<T, DP, 4, HB, BIAS, CAP><<<grid, 256, 0, stream>>>(a, tiles);
+      attn_bwd_rows<T, DP, 4, HB, BIAS, CAP><<<grid, 256, 0, stream>>>(a, tiles, sp);
     else if constexpr (HB == 1 && eight_waves<T>(DP))
-      attn_bwd_rows<T, DP, 8, HB, BIAS, CAP><<<grid, 512, 0, stream>>>(a, tiles);
+      attn_bwd_rows<T, DP, 8, HB, BIAS, CAP><<<grid, 512, 0, stream>>>(a, tiles, sp);
+    if (sp.splits > 1)
+      attn_bwd_join_rows<T><<<dim3((unsigned)(((int64_t)a.B * a.Hk * a.R + 3) / 4)), kThreads, 0, stream>>>(a, sp);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (a.Tk > 0) {
     const int kw = pick_waves<T, DP, HB>(a, heads, a.Tk), rows = kw == 1 ? 128 : 32;
     const int tiles = (a.Tk + rows - 1) / rows;
-    const dim3 grid((unsigned)(heads * tiles));
+    Split sp = make_split(a, a.Tk, a.R);
+    sp.part = split_part(a);
+    const dim3 grid((unsigned)(heads * tiles), (unsigned)sp.splits);
     if (kw == 1)
-      attn_bwd_keys<T, DP, 1, HB, BIAS, CAP><<<grid, 256, 0, stream>>>(a, tiles);
+      attn_bwd_keys<T, DP, 1, HB, BIAS, CAP><<<grid, 256, 0, stream>>>(a, tiles, sp);
     else if (kw == 4)
-      attn_bwd_keys<T, DP, 4, HB, BIAS, CAP><<<grid, 256, 0, stream>>>(a, tiles);
+      attn_bwd_keys<T, DP, 4, HB, BIAS, CAP><<<grid, 256, 0, stream>>>(a, tiles, sp);
     else if constexpr (HB == 1 && eight_waves<T>(DP))
-      attn_bwd_keys<T, DP, 8, HB, BIAS, CAP><<<grid, 512, 0, stream>>>(a, tiles);
+      attn_bwd_keys<T, DP, 8, HB, BIAS, CAP><<<grid, 512, 0, stream>>>(a, tiles, sp);
+    if (sp.splits > 1)
+      attn_bwd_join_keys<T><<<dim3((unsigned)(((int64_t)a.B * a.Hk * a.Tk * 2 + 3) / 4)), kThreads, 0, stream>>>(a, sp);
   }
   return hipGetLastError();
 }
@@ -673,7 +798,11 @@ hipError_t by_width(const AttnArgs& a, hipStream_t stream) {
 }  // namespace
 
 size_t attention_backward_workspace_bytes(const AttnArgs& a) {
-  return (size_t)a.B * a.Hk * a.R * stat_floats(a) * sizeof(float);
+  const int64_t heads = (int64_t)a.B * a.Hk;
+  const Split r = make_split(a, a.R, a.Tk), k = make_split(a, a.Tk, a.R);
+  const int64_t rows = r.splits > 1 ? heads * a.R * row_floats(a.D) * r.splits : 0;
+  const int64_t keys = k.splits > 1 ? heads * a.Tk * 2 * key_floats(a.D) * k.splits : 0;
+  return (size_t)(stats_size(a) + (rows > keys ? rows : keys)) * sizeof(float);
 }
 
 hipError_t launch_attention_backward(AttnArgs a, hipStream_t stream) {

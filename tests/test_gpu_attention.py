@@ -149,6 +149,15 @@ def test_few_rows_over_many_keys(Tq, G, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("Tk,G,D", [(1, 1, 64), (3, 4, 128), (40, 2, 33)])
+def test_many_rows_over_few_keys(Tk, G, D, dtype):
+    check(*draw(2, 2100, Tk, 2 * G, 2, D, dtype, 55, dims=2), f"rows split {Tk} x {G}")
+    check(*draw(1, 1500, Tk, G, 1, D, dtype, 56, causal=True, cap=10.0, prefix=[2]), f"rows split causal {Tk} x {G}")
+    docs = ([runs([700, 500, 300], 1600)], [[2] * (Tk - Tk // 2) + [0] * (Tk // 2)])
+    check(*draw(1, 1600, Tk, G, 1, D, dtype, 57, docs=docs, dims=1), f"rows split documents {Tk} x {G}")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_masked_keys_may_hold_anything(dtype):
     """NaN and infinities in keys, values and positions that a query does not see do not reach it, nor what shares a
     tile with it; queries that see no key keep their zeros."""
