@@ -7,13 +7,14 @@
 // head's G query heads are rows of one problem (row = token G + head), so single tokens with grouped heads
 // still fill a tile and keys are read once for the group.
 //
-// What bounds it (bf16, D = 128, 16 heads over 4, 2 x 3100 tokens with a prefix of 2816: 198 us, 725 TFLOP/s of
-// 1147 a large library product reaches): the exponentials' vector instructions between the matrix ones; at
-// D = 32 with distances (10000 x 10000 cells of 8 heads: 395 us) mostly those: the counters see 8.9 a score (half a
-// distance and its root, as two heads a wave share them, bias, maximum, exponential, sum, rounding), 180 us of issue
-// and 90 us more for the quarter rate of exponentials and roots, where the products take 90 us.  Probabilities of bf16 tensors are
-// rounded to bf16 for the second product (each is off by 2^-9 of itself at most, and those errors average over the
-// keys: outputs 0.0022 off against the 0.0017 of their own rounding); their sum l is of the unrounded ones.
+// What bounds it (bf16, D = 128, 16 heads over 4, 2 x 3100 tokens with a prefix of 2816: 255 us; the products alone, with the
+// second in two parts, would take 190 us at a large library product's rate): the exponentials' and roundings' vector
+// instructions between the matrix ones; at D = 32 with distances (10000 x 10000 cells of 8 heads: 470 us) mostly those (half
+// a distance and its root, as two heads a wave share them, bias, maximum, exponential, sum, rounding).
+//
+// Probabilities of bf16 tensors go into the second product as the sum of two bf16 (16 bits of each): one, rounded by up to
+// 2^-8, left outputs 0.0022 off where their own rounding leaves 0.0017.  The second part costs a product and three vector
+// instructions a score (the prefix case took 193 us without, the cells 395 us).
 #include "attention_core.h"
 
 namespace fbev {
@@ -304,7 +305,7 @@ __global__ __launch_bounds__((Fwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
         l[hd] += sum;
         pin(l[hd]);
         if constexpr (HB > 1) __builtin_amdgcn_sched_barrier(0);
-        M::template accumulate<NB>(acc[hd], M::pack(s), Vs + hd * C::kTile, at, lane);
+        M::template accumulate_fine<NB>(acc[hd], s, Vs + hd * C::kTile, at, lane);
       }
     }
   }
