@@ -154,20 +154,11 @@ struct Mma<__bf16, DP> {
     return u.v;
   }
 
+  // Adds the transposed tile's product with the values, each of them as the sum of two bf16: the first is off by up to 2^-8
+  // of it, the second by as much of the rest, so 16 bits go into the product.
   template <int NB>
-  static __device__ __forceinline__ void accumulate(f32x16 (&acc)[NB], const Values& p, const char* tile, int r0,
+  static __device__ __forceinline__ void accumulate(f32x16 (&acc)[NB], const f32x16& p, const char* tile, int r0,
                                                     int lane) {
-#pragma unroll
-    for (int blk = 0; blk < NB; ++blk)
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-        acc[blk] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(columns(tile, r0, c, blk, lane), p.v[c], acc[blk], 0, 0, 0);
-  }
-
-  // The same with each value as the sum of two bf16 (16 bits of it).
-  template <int NB>
-  static __device__ __forceinline__ void accumulate_fine(f32x16 (&acc)[NB], const f32x16& p, const char* tile, int r0,
-                                                         int lane) {
     const Values hi = pack(p);
     Values lo;
 #pragma unroll
@@ -200,25 +191,15 @@ struct Mma<float, DP> {
     return c;
   }
 
-  struct Values {
-    f32x16 v;
-  };
-  static __device__ __forceinline__ Values pack(const f32x16& p) { return Values{p}; }
-
   template <int NB>
-  static __device__ __forceinline__ void accumulate(f32x16 (&acc)[NB], const Values& p, const char* tile, int r0,
+  static __device__ __forceinline__ void accumulate(f32x16 (&acc)[NB], const f32x16& p, const char* tile, int r0,
                                                     int lane) {
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         acc[blk] = __builtin_amdgcn_mfma_f32_32x32x2f32(
-            *Tl::at(tile + r0 * Tl::kRowBytes, acc_row(i, lane >> 5), 32 * blk + (lane & 31)), p.v[i], acc[blk], 0, 0, 0);
-  }
-  template <int NB>
-  static __device__ __forceinline__ void accumulate_fine(f32x16 (&acc)[NB], const f32x16& p, const char* tile, int r0,
-                                                         int lane) {
-    accumulate<NB>(acc, pack(p), tile, r0, lane);
+            *Tl::at(tile + r0 * Tl::kRowBytes, acc_row(i, lane >> 5), 32 * blk + (lane & 31)), p[i], acc[blk], 0, 0, 0);
   }
 };
 

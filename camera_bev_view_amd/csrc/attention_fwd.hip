@@ -305,7 +305,7 @@ __global__ __launch_bounds__((Fwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
         l[hd] += sum;
         pin(l[hd]);
         if constexpr (HB > 1) __builtin_amdgcn_sched_barrier(0);
-        M::template accumulate_fine<NB>(acc[hd], s, Vs + hd * C::kTile, at, lane);
+        M::template accumulate<NB>(acc[hd], s, Vs + hd * C::kTile, at, lane);
       }
     }
   }

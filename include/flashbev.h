@@ -489,9 +489,9 @@ fbev_status fbev_rotary(const void* q, const void* k, fbev_dtype dtype, const fb
  * The backward takes grad_out, out [B,Tq,Hq,D] (contiguous, of dtype) and stats
  * and gives grad_q, grad_k, grad_v (contiguous, of dtype; a key head's
  * gradient is the sum over its query heads) and grad_slope [B,Tq,Hq] fp32
- * (NULL skips it).  Positions are not differentiated.  For bf16 tensors
- * the probabilities, and the score gradients that give grad_k, are rounded to
- * bf16 before their matrix products; those that give grad_q keep 16 bits.  An
+ * (NULL skips it).  Positions are not differentiated.  For bf16 tensors the
+ * probabilities and score gradients of forward and backward go into their
+ * matrix products as two bf16 each, which keeps 16 bits of them.  An
  * infinity or a NaN reaches the gradients of what sees it and no others.
  */
 typedef struct {

@@ -48,3 +48,14 @@ def test_outputs(label, kw, dtype):
     print(f"[case] attention outputs {label} {dtype}", flush=True)
     ref, bd = oracle(q, k, v, how)
     close(label + " out", ops.attention_forward(q, k, v, **how)[0], ref["out"], bd["out"])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("label,kw", FORMS, ids=[f[0] for f in FORMS])
+def test_key_and_value_gradients(label, kw, dtype):
+    q, k, v, go, how = make(kw, dtype, 72)
+    print(f"[case] attention gk, gv {label} {dtype}", flush=True)
+    ref, bd = oracle(q, k, v, how, go)
+    _, gk, gv, _ = ops.attention_backward(go, q, k, v, *ops.attention_forward(q, k, v, **how), **how)
+    close(label + " gk", gk, ref["gk"], bd["gk"])
+    close(label + " gv", gv, ref["gv"], bd["gv"])
