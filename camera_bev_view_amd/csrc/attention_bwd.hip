@@ -4,11 +4,11 @@
 //   gslope_i = - sum_j ds_ij |pos_i - pos_j|,   ds'_ij = ds_ij (1 - tanh^2)   (with a cap),
 //   gq_i = scale sum_j ds'_ij k_j,   gk_j = scale sum_i ds'_ij q_i,   gv_j = sum_i p_ij go_i.
 //
-// Two launches, each recomputing the scores tile by tile: one owns query rows and walks the keys (delta,
-// gq, gslope), one owns keys and walks the rows of all query heads that share them (gk, gv).  Every sum
-// stays in registers and is written once, so nothing is added by atomics and results are the same from
-// run to run; the price is seven matrix products a tile where five would do with atomics.  Distances
-// are not differentiated: positions are given.
+// Each launch recomputes the scores tile by tile: one owns query rows and walks the keys (delta, gq, gslope; for bf16 delta
+// comes from a launch before it), one owns keys and walks the rows of all query heads that share them (gk, gv).  Every sum
+// stays in registers and is written once (as an fp32 part where the walk is split over workgroups, which a launch behind
+// joins in order), so nothing is added by atomics and results are the same from run to run; the price is seven matrix
+// products a tile where five would do with atomics.  Distances are not differentiated: positions are given.
 //
 // What bounds it (bf16, D = 32, distances, 10000 x 10000 cells of 8 heads: 1120 us for both launches, of which the
 // eight products, one of them in two parts, would take 360 us at a large product's rate): vector instructions between the
@@ -123,17 +123,30 @@ struct Split {
   float* part;
 };
 
-// Floats of a partial row: gq with the sums of ds, ds d and p d; gk or gv.
-__host__ __device__ __forceinline__ int row_floats(int D) { return (D + 6) / 4 * 4; }
+// Floats of a partial row: gq with the sums of ds, ds d and p d (or the sum of ds alone); gk or gv.
+__host__ __device__ __forceinline__ int row_floats(bool grads, int D) { return grads ? (D + 6) / 4 * 4 : 1; }
 __host__ __device__ __forceinline__ int key_floats(int D) { return (D + 3) / 4 * 4; }
 
 // ---- query rows: delta, gq, gslope
 
-template <typename T, int DP, int KW, int HB, bool BIAS, bool CAP>
+// Delta is the mean of go . v over a row's weights, go . o with the output before its rounding.  Taken from the rounded
+// output it is off by up to half a step of that, which in a row that looks at one key is many times the differences
+// go . v - delta that make its gradients (bf16, 400 points of a 100 m square, slope 2: one row in twenty of gq off by more
+// than itself, with the exact delta by 0.002).  fp32 outputs are exact enough for gq (half a step is 2^-24, what the products
+// are off by too), and the sum of the row's ds corrects what the keys' launch and the slopes get.  For bf16 a launch of its
+// own (kDelta: the scores once more, no gradients) sums up ds first: 290 us of the 100 x 100 cells' 1605, 19 us of the 107 of
+// 4 x 900 queries.
+enum Pass { kDelta, kGradients };
+
+template <typename T>
+constexpr bool kOwnDelta = sizeof(T) == 4;                // the gradients' launch forms delta itself
+
+template <typename T, int DP, int KW, int HB, bool BIAS, bool CAP, Pass PASS>
 __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(HB))) void attn_bwd_rows(AttnArgs a, int tiles, Split sp) {
   using C = Bwd<T, DP, KW, HB>;
   using M = Mma<T, DP>;
   constexpr int NB = DP / 32, MT = C::MT, RW = C::RW;
+  constexpr bool SUM = PASS == kDelta || kOwnDelta<T>, GRADS = PASS == kGradients;
   __shared__ alignas(16) char smem[C::kBytes];
   __shared__ alignas(16) float pos[BIAS ? 3 * MT : 1];   // [key][axis]
   __shared__ alignas(16) int docs[MT];
@@ -166,13 +179,6 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
     load_row<T, DP>((const T*)a.q + b * a.qs[0] + w.t * a.qs[1] + (w.head + i) * a.qs[2], a.vec, a.D, h, qi);
     sign_row<T, DP>(a, qi);
     load_row<T, DP>((const T*)a.gout + row_at, a.vec, a.D, h, gi);
-    typename M::Frag o[M::kFrags];
-    load_row<T, DP>((const T*)a.out + row_at, a.vec, a.D, h, o);
-    float sum = 0.0f;
-#pragma unroll
-    for (int f = 0; f < M::kFrags; ++f)
-#pragma unroll
-      for (int j = 0; j < M::kFragElems; ++j) sum = fmaf((float)gi[f][j], (float)o[f][j], sum);
     if (L && kw == 0) {
 #pragma unroll
       for (int f = 0; f < M::kFrags; ++f) {
@@ -180,15 +186,26 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
         *(typename M::Frag*)(own_at + (2 * i + 1) * C::kOwn + (f * 64 + lane) * 16) = gi[f];
       }
     }
-    delta[i] = pair_sum(sum);
+    const RowStats rs = row_stats(a, (int64_t)b * a.Hk + hk + i);
+    if constexpr (SUM) {
+      typename M::Frag o[M::kFrags];
+      load_row<T, DP>((const T*)a.out + row_at, a.vec, a.D, h, o);
+      float sum = 0.0f;
+#pragma unroll
+      for (int f = 0; f < M::kFrags; ++f)
+#pragma unroll
+        for (int j = 0; j < M::kFragElems; ++j) sum = fmaf((float)gi[f][j], (float)o[f][j], sum);
+      delta[i] = pair_sum(sum);
+    } else {
+      delta[i] = rs.delta[w.r];
+    }
     // exponentials are taken around the forward's maximum and divided by its sum at the end: a logarithm of the sum
     // would be off by its own size times 2^-24.  A row without weights: all p are 0.
     const float2 ml = a.stats[((int64_t)b * a.Hq + w.head + i) * a.Tq + w.t];
     neg_m[i] = ml.y == 0.0f ? kNegInf : -ml.x;
     inv_l[i] = ml.y == 0.0f ? 0.0f : 1.0f / ml.y;
     if constexpr (BIAS) slope[i] = a.slope[((int64_t)b * a.Tq + w.t) * a.Hq + w.head + i] / un.raw;
-    if (kw == 0 && h == 0 && first + n < a.R && blockIdx.y == 0) {
-      const RowStats rs = row_stats(a, (int64_t)b * a.Hk + hk + i);
+    if (SUM && kw == 0 && h == 0 && first + n < a.R && blockIdx.y == 0) {
       const float lse2 = ml.y == 0.0f ? -kNegInf : ml.x + __builtin_amdgcn_logf(ml.y);
       rs.off[w.r] = sizeof(T) == 4 ? -neg_m[i] : CAP ? lse2 : lse2 / un.unit;
       rs.inv[w.r] = inv_l[i];
@@ -259,7 +276,7 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
     };
     wait_staged();
     __syncthreads();
-    if (mixed && __builtin_expect(__syncthreads_or(holds_odd<T, DP, HB * MT, C::kThreads>(Ks)), 0)) {
+    if (GRADS && mixed && __builtin_expect(__syncthreads_or(holds_odd<T, DP, HB * MT, C::kThreads>(Ks)), 0)) {
 #pragma unroll 1
       for (int at = 32 * kw; at < MT; at += 32 * KW) {
         const uint32_t vis = visible(at);
@@ -327,53 +344,53 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
         for (int i = 0; i < 16; ++i) {
           const float p = __builtin_amdgcn_exp2f(fmaf(s[i], un.unit, neg_m[hd]));
           s[i] = p * dp[i];
-          t_ds += s[i];
-          if constexpr (BIAS) {
-            t_dsd = fmaf(s[i], d[i], t_dsd);
-            t_pd = fmaf(p, d[i], t_pd);
-          }
+          if constexpr (SUM) t_ds += s[i];
+          if constexpr (BIAS && GRADS) t_dsd = fmaf(s[i], d[i], t_dsd);
+          if constexpr (BIAS && GRADS && SUM) t_pd = fmaf(p, d[i], t_pd);
         }
-        pin(sum_ds[hd] += t_ds);
-        if constexpr (BIAS) {
-          pin(sum_dsd[hd] += t_dsd);
-          pin(sum_pd[hd] += t_pd);
-        }
-        if constexpr (CAP) {
+        if constexpr (SUM) pin(sum_ds[hd] += t_ds);
+        if constexpr (BIAS && GRADS) pin(sum_dsd[hd] += t_dsd);
+        if constexpr (BIAS && GRADS && SUM) pin(sum_pd[hd] += t_pd);
+        if constexpr (GRADS) {
+          if constexpr (CAP) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) s[i] = whole || (seen >> i) & 1 ? s[i] * fmaf(-th[i], th[i], 1.0f) : 0.0f;
+            for (int i = 0; i < 16; ++i) s[i] = whole || (seen >> i) & 1 ? s[i] * fmaf(-th[i], th[i], 1.0f) : 0.0f;
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          M::template accumulate<NB>(acc[hd], s, kt, at, lane);
         }
-        __builtin_amdgcn_sched_barrier(0);
-        M::template accumulate<NB>(acc[hd], s, kt, at, lane);
       }
     }
   }
 #pragma unroll
   for (int hd = 0; hd < HB; ++hd) {
+    const bool split = KW > 1 && HB == 1 && sp.splits > 1;
+    const RowStats rs = row_stats(a, (int64_t)b * a.Hk + hk + hd);
+    // partial rows of a split, from the tile's first row on
+    float* part = nullptr;
+    if (split) part = sp.part + (((int64_t)blockIdx.y * a.B * a.Hk + bh) * a.R + first) * row_floats(GRADS, a.D);
+    if constexpr (GRADS) {
 #pragma unroll
-    for (int blk = 0; blk < NB; ++blk)
+      for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[hd][blk][i] *= inv_l[hd];
-    make_nan<NB>(acc[hd], odd[hd]);
-    // the queries' sign is in s, not in k: a zero scale gives zeros
-    float* part = nullptr;                                // of the tile's first row
-    if constexpr (KW > 1 && HB == 1) {
-      if (sp.splits > 1)
-        part = sp.part + (((int64_t)blockIdx.y * a.B * a.Hk + bh) * a.R + first) * row_floats(a.D);
+        for (int i = 0; i < 16; ++i) acc[hd][blk][i] *= inv_l[hd];
+      make_nan<NB>(acc[hd], odd[hd]);
+      // the queries' sign is in s, not in k: a zero scale gives zeros
+      if (split)
+        write_own<float, DP, KW>(acc[hd], a.scale, (float*)smem, a.D, false, kw, lane, [&](int r) -> float* {
+          return first + r < a.R ? part + (int64_t)r * row_floats(GRADS, a.D) : nullptr;
+        });
+      else
+        write_own<T, DP, KW>(acc[hd], a.scale, (float*)smem, a.D, a.vec_out, kw, lane, [&](int r) -> T* {
+          if (first + r >= a.R) return nullptr;
+          const int t = (first + r) / a.G, head = hk * a.G + (first + r - t * a.G) + hd;
+          return (T*)a.gq + (((int64_t)b * a.Tq + t) * a.Hq + head) * a.D;
+        });
     }
-    if (part != nullptr)
-      write_own<float, DP, KW>(acc[hd], a.scale, (float*)smem, a.D, false, kw, lane, [&](int r) -> float* {
-        return first + r < a.R ? part + (int64_t)r * row_floats(a.D) : nullptr;
-      });
-    else
-      write_own<T, DP, KW>(acc[hd], a.scale, (float*)smem, a.D, a.vec_out, kw, lane, [&](int r) -> T* {
-        if (first + r >= a.R) return nullptr;
-        const int t = (first + r) / a.G, head = hk * a.G + (first + r - t * a.G) + hd;
-        return (T*)a.gq + (((int64_t)b * a.Tq + t) * a.Hq + head) * a.D;
-      });
-    // delta came from the rounded output; ds sums to the error it made (sum_j p_ij = 1): the keys' launch gets delta
-    // without it, and the distances' mean takes it out of the slope's gradient, which is fp32 whatever the type
+    // ds sums to the error of delta (sum_j p_ij = 1): the keys' launch (and bf16 gradients) get delta without it, and the
+    // distances' mean takes it out of an fp32 slope's gradient
     float sd = pair_sum(sum_ds[hd]) * inv_l[hd], sdd = 0.0f, pd = 0.0f;
-    if constexpr (BIAS) {
+    if constexpr (BIAS && GRADS) {
       sdd = pair_sum(sum_dsd[hd]) * inv_l[hd];
       pd = pair_sum(sum_pd[hd]) * inv_l[hd];
     }
@@ -387,15 +404,15 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
       for (int k = 0; k < KW; ++k) sd += slopes[k][0][n], sdd += slopes[k][1][n], pd += slopes[k][2][n];
       bad = false;
     }
-    if (part != nullptr) {
-      if (kw == 0 && h == 0 && first + n < a.R) {
-        float* sums = part + (int64_t)n * row_floats(a.D) + a.D;
-        sums[0] = sd, sums[1] = sdd, sums[2] = pd;
-        if (blockIdx.y == 0) row_stats(a, (int64_t)b * a.Hk + hk + hd).delta[w.r] = delta[hd];
-      }
-    } else if (kw == 0 && h == 0 && first + n < a.R) {
-      row_stats(a, (int64_t)b * a.Hk + hk + hd).delta[w.r] = delta[hd] + sd;
-      if (BIAS && a.gslope)
+    if (kw != 0 || h != 0 || first + n >= a.R) continue;
+    if (split) {
+      float* sums = part + (int64_t)n * row_floats(GRADS, a.D) + (GRADS ? a.D : 0);
+      sums[0] = sd;
+      if constexpr (GRADS) sums[1] = sdd, sums[2] = pd;
+      if (SUM && blockIdx.y == 0) rs.delta[w.r] = delta[hd];
+    } else {
+      if constexpr (SUM) rs.delta[w.r] = delta[hd] + sd;
+      if (GRADS && BIAS && a.gslope)
         a.gslope[((int64_t)b * a.Tq + w.t) * a.Hq + w.head + hd] = bad ? __builtin_nanf("") : fmaf(sd, pd, -sdd);
     }
   }
@@ -673,7 +690,7 @@ template <typename T>
 __global__ __launch_bounds__(kThreads) void attn_bwd_join_rows(AttnArgs a, Split sp) {
   const int64_t rows = (int64_t)a.B * a.Hk * a.R, row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (row >= rows) return;
-  const int lane = threadIdx.x & 63, pf = row_floats(a.D);
+  const int lane = threadIdx.x & 63, pf = row_floats(true, a.D);
   float o[3];
   sum_splits<3>(sp.part + row * pf, rows * pf, sp.splits, a.D + 3, lane, o);
   const int64_t bh = row / a.R;
@@ -686,9 +703,19 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_join_rows(AttnArgs a, Split
   auto at = [&](int i) { return __shfl(i < 64 ? o[0] : i < 128 ? o[1] : o[2], i & 63); };
   const float sd = at(a.D), sdd = at(a.D + 1), pd = at(a.D + 2);
   if (lane == 0) {
-    row_stats(a, bh).delta[r] += sd;
+    if (kOwnDelta<T>) row_stats(a, bh).delta[r] += sd;
     if (a.dims && a.gslope) a.gslope[((int64_t)b * a.Tq + t) * a.Hq + head] = fmaf(sd, pd, -sdd);
   }
+}
+
+// The sums of ds alone: a lane a row.
+__global__ __launch_bounds__(kThreads) void attn_bwd_join_delta(AttnArgs a, Split sp) {
+  const int64_t rows = (int64_t)a.B * a.Hk * a.R, row = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (row >= rows) return;
+  float o[1];
+  sum_splits<1>(sp.part + row, rows, sp.splits, 1, 0, o);
+  const int64_t bh = row / a.R;
+  row_stats(a, bh).delta[row - bh * a.R] += o[0];
 }
 
 template <typename T>
@@ -735,6 +762,16 @@ int pick_waves(const AttnArgs& a, int64_t heads, int rows) {
 int64_t stats_size(const AttnArgs& a) { return ((int64_t)a.B * a.Hk * a.R * stat_floats(a) + 3) / 4 * 4; }
 float* split_part(const AttnArgs& a) { return a.delta == nullptr ? nullptr : a.delta + stats_size(a); }
 
+template <typename T, int DP, int HB, bool BIAS, bool CAP, Pass PASS>
+void launch_rows(const AttnArgs& a, int kw, dim3 grid, int tiles, const Split& sp, hipStream_t stream) {
+  if (kw == 1)
+    attn_bwd_rows<T, DP, 1, HB, BIAS, CAP, PASS><<<grid, 256, 0, stream>>>(a, tiles, sp);
+  else if (kw == 4)
+    attn_bwd_rows<T, DP, 4, HB, BIAS, CAP, PASS><<<grid, 256, 0, stream>>>(a, tiles, sp);
+  else if constexpr (HB == 1 && eight_waves<T>(DP))
+    attn_bwd_rows<T, DP, 8, HB, BIAS, CAP, PASS><<<grid, 512, 0, stream>>>(a, tiles, sp);
+}
+
 template <typename T, int DP, int HB, bool BIAS, bool CAP>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
   const int64_t heads = (int64_t)a.B * a.Hk / HB;
@@ -744,12 +781,12 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
     Split sp = make_split(a, a.R, a.Tk);
     sp.part = split_part(a);
     const dim3 grid((unsigned)(heads * tiles), (unsigned)sp.splits);
-    if (kw == 1)
-      attn_bwd_rows<T, DP, 1, HB, BIAS, CAP><<<grid, 256, 0, stream>>>(a, tiles, sp);
-    else if (kw == 4)
-      attn_bwd_rows<T, DP, 4, HB, BIAS, CAP><<<grid, 256, 0, stream>>>(a, tiles, sp);
-    else if constexpr (HB == 1 && eight_waves<T>(DP))
-      attn_bwd_rows<T, DP, 8, HB, BIAS, CAP><<<grid, 512, 0, stream>>>(a, tiles, sp);
+    if constexpr (!kOwnDelta<T>) {
+      launch_rows<T, DP, HB, BIAS, CAP, kDelta>(a, kw, grid, tiles, sp, stream);
+      if (sp.splits > 1)
+        attn_bwd_join_delta<<<dim3((unsigned)(((int64_t)a.B * a.Hk * a.R + kThreads - 1) / kThreads)), kThreads, 0, stream>>>(a, sp);
+    }
+    launch_rows<T, DP, HB, BIAS, CAP, kGradients>(a, kw, grid, tiles, sp, stream);
     if (sp.splits > 1)
       attn_bwd_join_rows<T><<<dim3((unsigned)(((int64_t)a.B * a.Hk * a.R + 3) / 4)), kThreads, 0, stream>>>(a, sp);
     const hipError_t e = hipGetLastError();
@@ -799,7 +836,7 @@ hipError_t by_width(const AttnArgs& a, hipStream_t stream) {
 size_t attention_backward_workspace_bytes(const AttnArgs& a) {
   const int64_t heads = (int64_t)a.B * a.Hk;
   const Split r = make_split(a, a.R, a.Tk), k = make_split(a, a.Tk, a.R);
-  const int64_t rows = r.splits > 1 ? heads * a.R * row_floats(a.D) * r.splits : 0;
+  const int64_t rows = r.splits > 1 ? heads * a.R * row_floats(true, a.D) * r.splits : 0;
   const int64_t keys = k.splits > 1 ? heads * a.Tk * 2 * key_floats(a.D) * k.splits : 0;
   return (size_t)(stats_size(a) + (rows > keys ? rows : keys)) * sizeof(float);
 }

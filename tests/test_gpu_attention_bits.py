@@ -59,3 +59,30 @@ def test_key_and_value_gradients(label, kw, dtype):
     _, gk, gv, _ = ops.attention_backward(go, q, k, v, *ops.attention_forward(q, k, v, **how), **how)
     close(label + " gk", gk, ref["gk"], bd["gk"])
     close(label + " gv", gv, ref["gv"], bd["gv"])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("label,kw", FORMS, ids=[f[0] for f in FORMS])
+def test_query_and_slope_gradients(label, kw, dtype):
+    q, k, v, go, how = make(kw, dtype, 73)
+    print(f"[case] attention gq {label} {dtype}", flush=True)
+    ref, bd = oracle(q, k, v, how, go)
+    gq, _, _, gs = ops.attention_backward(go, q, k, v, *ops.attention_forward(q, k, v, **how), **how)
+    close(label + " gq", gq, ref["gq"], bd["gq"])
+    if gs is not None:
+        close(label + " gslope", gs, ref["gslope"], bd["gslope"])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("slope", [0.25, 0.5, 2.0])
+def test_gradients_of_rows_that_look_at_one_key(slope, dtype):
+    """Distances that leave a row one key's weight: its gradients are small differences of large terms, and an output
+    rounded to bf16 in their place would be off by many times their size."""
+    print(f"[case] attention of peaked rows, slope {slope} {dtype}", flush=True)
+    q, k, v, go, how = draw(1, 400, 400, 2, 2, 64, dtype, 74, dims=2)
+    how["pos_k"] = how["pos_q"] = how["pos_q"] * 5
+    how["slope"] = torch.full_like(how["slope"], slope)
+    ref, bd = oracle(q, k, v, how, go)
+    gq, gk, gv, gs = ops.attention_backward(go, q, k, v, *ops.attention_forward(q, k, v, **how), **how)
+    for name, x in (("gq", gq), ("gk", gk), ("gv", gv), ("gslope", gs)):
+        close(f"slope {slope} {name}", x, ref[name], bd[name])
