@@ -138,6 +138,10 @@ __host__ __device__ __forceinline__ int key_floats(int D) { return (D + 3) / 4 *
 // 4 x 900 queries.
 enum Pass { kDelta, kGradients };
 
+// Delta and its error.  Without a sum of ds (NaN: a key of the row is infinite) it stays as it came from the output, which
+// knows what weight such a key has.
+__device__ __forceinline__ float corrected(float delta, float sd) { return sd == sd ? delta + sd : delta; }
+
 template <typename T>
 constexpr bool kOwnDelta = sizeof(T) == 4;                // the gradients' launch forms delta itself
 
@@ -389,20 +393,19 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
     }
     // ds sums to the error of delta (sum_j p_ij = 1): the keys' launch (and bf16 gradients) get delta without it, and the
     // distances' mean takes it out of an fp32 slope's gradient
-    float sd = pair_sum(sum_ds[hd]) * inv_l[hd], sdd = 0.0f, pd = 0.0f;
+    // (a row that sees an infinite or NaN key gets NaN: its scores here are those of the cleaned key)
+    float sd = odd[hd] ? __builtin_nanf("") : pair_sum(sum_ds[hd]) * inv_l[hd], sdd = 0.0f, pd = 0.0f;
     if constexpr (BIAS && GRADS) {
       sdd = pair_sum(sum_dsd[hd]) * inv_l[hd];
       pd = pair_sum(sum_pd[hd]) * inv_l[hd];
     }
-    bool bad = odd[hd];
     if constexpr (KW > 1) {
       __syncthreads();
-      if (h == 0) slopes[kw][0][n] = sd, slopes[kw][1][n] = bad ? __builtin_nanf("") : sdd, slopes[kw][2][n] = pd;
+      if (h == 0) slopes[kw][0][n] = sd, slopes[kw][1][n] = sdd, slopes[kw][2][n] = pd;
       __syncthreads();
       sd = sdd = pd = 0.0f;
 #pragma unroll
       for (int k = 0; k < KW; ++k) sd += slopes[k][0][n], sdd += slopes[k][1][n], pd += slopes[k][2][n];
-      bad = false;
     }
     if (kw != 0 || h != 0 || first + n >= a.R) continue;
     if (split) {
@@ -411,9 +414,9 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
       if constexpr (GRADS) sums[1] = sdd, sums[2] = pd;
       if (SUM && blockIdx.y == 0) rs.delta[w.r] = delta[hd];
     } else {
-      if constexpr (SUM) rs.delta[w.r] = delta[hd] + sd;
+      if constexpr (SUM) rs.delta[w.r] = corrected(delta[hd], sd);
       if (GRADS && BIAS && a.gslope)
-        a.gslope[((int64_t)b * a.Tq + w.t) * a.Hq + w.head + hd] = bad ? __builtin_nanf("") : fmaf(sd, pd, -sdd);
+        a.gslope[((int64_t)b * a.Tq + w.t) * a.Hq + w.head + hd] = fmaf(sd, pd, -sdd);
     }
   }
 }
@@ -703,7 +706,8 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_join_rows(AttnArgs a, Split
   auto at = [&](int i) { return __shfl(i < 64 ? o[0] : i < 128 ? o[1] : o[2], i & 63); };
   const float sd = at(a.D), sdd = at(a.D + 1), pd = at(a.D + 2);
   if (lane == 0) {
-    if (kOwnDelta<T>) row_stats(a, bh).delta[r] += sd;
+    float& delta = row_stats(a, bh).delta[r];
+    if (kOwnDelta<T>) delta = corrected(delta, sd);
     if (a.dims && a.gslope) a.gslope[((int64_t)b * a.Tq + t) * a.Hq + head] = fmaf(sd, pd, -sdd);
   }
 }
@@ -715,7 +719,8 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_join_delta(AttnArgs a, Spli
   float o[1];
   sum_splits<1>(sp.part + row, rows, sp.splits, 1, 0, o);
   const int64_t bh = row / a.R;
-  row_stats(a, bh).delta[row - bh * a.R] += o[0];
+  float& delta = row_stats(a, bh).delta[row - bh * a.R];
+  delta = corrected(delta, o[0]);
 }
 
 template <typename T>

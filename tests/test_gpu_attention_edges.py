@@ -1,0 +1,48 @@
+"""GPU: attention calls at the edges of what its documentation allows."""
+import numpy as np
+import pytest
+import torch
+
+from camera_bev_view_amd import ops
+from encoder_bounds import close
+from encoder_fine_bounds import oracle
+from test_gpu_attention import draw, runs
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def check(q, k, v, go, how, label, skip=()):
+    print(f"[case] attention {label}: {tuple(q.shape)} {q.dtype}", flush=True)
+    ref, bd = oracle(q, k, v, how, go)
+    out, stats = ops.attention_forward(q, k, v, **how)
+    grads = ops.attention_backward(go, q, k, v, out, stats, **how)
+    for name, x in zip(("out", "gq", "gk", "gv", "gslope"), (out, *grads)):
+        if x is not None and name not in skip:
+            close(f"{label} {name}", x, ref[name], bd[name])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("heads,B", [(2, 1), (96, 4)])
+def test_a_key_of_minus_infinity_takes_no_weight(heads, B, dtype):
+    """A key whose score is minus infinity for every query of its document is as good as masked: the document's other keys
+    get the gradients that they have without it."""
+    T = 90
+    ids = [runs([40, 30], T)] * B
+    q, k, v, go, how = draw(B, T, T, heads, heads, 32, dtype, 84, dims=2, docs=(ids, ids))
+    q[..., 5] = q[..., 5].abs() + 0.1
+    ref_docs = how["doc_k"].clone()
+    ref_docs[:, 50] = 99
+    ref, bd = oracle(q, k, v, {**how, "doc_k": ref_docs}, go)
+    print(f"[case] attention with a key of -inf, {heads} heads {dtype}", flush=True)
+    k[:, 50, :, 5] = -float("inf")
+    out, stats = ops.attention_forward(q, k, v, **how)
+    _, gk, gv, _ = ops.attention_backward(go, q, k, v, out, stats, **how)
+    for name, x in (("out", out), ("gk", gk), ("gv", gv)):
+        close(f"-inf key {name}", x, ref[name], bd[name])
