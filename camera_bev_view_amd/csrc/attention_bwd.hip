@@ -328,7 +328,7 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
           dp = tile_dot<T, DP>(Vs + hd * C::kTile, at, go[hd], lane, dp);
         f32x16 th;
         if constexpr (CAP) {
-          cap_scores<T>(s, un.inv_cap);
+          cap_scores<T>(s, un);
           th = s;
         }
         if constexpr (BIAS) {
@@ -611,7 +611,7 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
         }
         f32x16 th;
         if constexpr (CAP) {
-          cap_scores<T>(s, un.inv_cap);
+          cap_scores<T>(s, un);
           th = s;
         }
 #pragma unroll

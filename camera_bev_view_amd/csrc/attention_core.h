@@ -449,8 +449,8 @@ __device__ __forceinline__ void make_nan(f32x16 (&acc)[NB], bool odd) {
   }
 }
 
-// tanh(u).  Through e = exp(-2 |u|) as (1 - e) / (1 + e); near zero, where 1 - e cancels, fp32 scores take the odd
-// Taylor series instead (|u| < 1/4: the first term left out is below 1e-8 of the value).
+// tanh(u).  Through e = exp(-2 |u|) as (1 - e) / (1 + e); near zero, where 1 - e cancels, the odd Taylor series when EXACT
+// (|u| < 1/4: the first term left out is below 1e-8 of the value).
 template <bool EXACT>
 __device__ __forceinline__ float tanh_fast(float u) {
   const float e = __builtin_amdgcn_exp2f(fabsf(u) * (-2.0f * kLog2e));
@@ -541,8 +541,13 @@ __device__ __forceinline__ void own_point(const float* p, int dims, int h, float
 
 // Scores are kept in a unit that costs the loop no multiplication: the raw products (a negative scale turns
 // the queries' sign) or the cap's tanh.  `unit` takes them to base-2 exponents, a slope is divided by `raw`.
+// Without its series near zero tanh is off by up to 2^-24, whatever its own size, and a score by that much of the cap: up
+// to this cap by 4e-6, under what bf16 probabilities keep (2^-16).  fp32 tensors always take the series.
+constexpr float kCoarseCap = 64.0f;
+
 struct Unit {
   float unit, raw, inv_cap;
+  bool near;            // bf16: tanh takes its series near zero
 };
 
 __device__ __forceinline__ Unit make_unit(const AttnArgs& a) {
@@ -551,6 +556,7 @@ __device__ __forceinline__ Unit make_unit(const AttnArgs& a) {
   u.raw = a.cap > 0.0f ? a.cap : (sc > 0.0f ? sc : 1.0f);
   u.unit = u.raw * kLog2e;
   u.inv_cap = a.cap > 0.0f ? sc / a.cap : 0.0f;
+  u.near = a.cap > kCoarseCap;
   return u;
 }
 
@@ -566,9 +572,14 @@ __device__ __forceinline__ void sign_row(const AttnArgs& a, typename Mma<T, DP>:
 }
 
 template <typename T>
-__device__ __forceinline__ void cap_scores(f32x16& s, float inv_cap) {
+__device__ __forceinline__ void cap_scores(f32x16& s, const Unit& un) {
+  if (sizeof(T) == 4 || un.near) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) s[i] = tanh_fast<sizeof(T) == 4>(s[i] * inv_cap);
+    for (int i = 0; i < 16; ++i) s[i] = tanh_fast<true>(s[i] * un.inv_cap);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = tanh_fast<false>(s[i] * un.inv_cap);
+  }
 }
 
 }  // namespace fbev

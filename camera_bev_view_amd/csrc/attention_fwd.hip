@@ -268,7 +268,7 @@ __global__ __launch_bounds__((Fwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
       for (int hd = 0; hd < HB; ++hd) {
         if constexpr (HB > 1) __builtin_amdgcn_sched_barrier(0);      // one head's registers at a time
         f32x16 s = tile_dot<T, DP>(Ks + hd * C::kTile, at, q[hd], lane);
-        if (a.cap > 0.0f) cap_scores<T>(s, un.inv_cap);
+        if (a.cap > 0.0f) cap_scores<T>(s, un);
         if constexpr (BIAS) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) s[i] = fmaf(-slope[hd], d[i], s[i]);

@@ -46,3 +46,9 @@ def test_a_key_of_minus_infinity_takes_no_weight(heads, B, dtype):
     _, gk, gv, _ = ops.attention_backward(go, q, k, v, out, stats, **how)
     for name, x in (("out", out), ("gk", gk), ("gv", gv)):
         close(f"-inf key {name}", x, ref[name], bd[name])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cap", [65.0, 1e4, 1e6, 1e9, 1e12])
+def test_caps_far_above_the_scores(cap, dtype):
+    check(*draw(1, 50, 90, 4, 2, 32, dtype, 81, cap=cap, dims=1, sharp=2.0), f"cap {cap}")
