@@ -475,7 +475,7 @@ struct Row {
 
 __device__ __forceinline__ int row_limit(const AttnArgs& a, int b, int t) {
   if (!a.causal) return a.Tk - 1;
-  const int pre = a.prefix ? a.prefix[b] : 0;
+  const int pre = a.prefix ? max(a.prefix[b], 0) : 0;      // (pre - 1 of the lowest int would wrap)
   return min(a.Tk - 1, max(t + a.Tk - a.Tq, pre - 1));
 }
 

@@ -52,3 +52,10 @@ def test_a_key_of_minus_infinity_takes_no_weight(heads, B, dtype):
 @pytest.mark.parametrize("cap", [65.0, 1e4, 1e6, 1e9, 1e12])
 def test_caps_far_above_the_scores(cap, dtype):
     check(*draw(1, 50, 90, 4, 2, 32, dtype, 81, cap=cap, dims=1, sharp=2.0), f"cap {cap}")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("prefix", [-2 ** 31, -1, 2 ** 31 - 1])
+def test_prefixes_beyond_the_keys(prefix, dtype):
+    q, k, v, go, how = draw(1, 40, 70, 2, 1, 32, dtype, 82, causal=True, prefix=[prefix])
+    check(q, k, v, go, how, f"prefix {prefix}")
