@@ -217,6 +217,13 @@ fbev_status check_attention_data(fbev::AttnArgs& a, const void* q, const void* k
   const int e = 16 / a.elem_bytes;
   a.vec = a.D % e == 0 && aligned(q, 16) && aligned(k, 16) && aligned(v, 16);
   const int nq[3] = {a.B, a.Tq, a.Hq}, nk[3] = {a.B, a.Tk, a.Hk};
+  // rows behind the last are told by their offset, so staged tokens have to lie a row apart: broadcast ones (stride 0) move
+  // element by element
+  const auto apart = [&](int tokens, int64_t& stride) {
+    if (tokens <= 1) stride = a.D;
+    return stride >= a.D;
+  };
+  a.vec = a.vec && (a.G > 1 || apart(a.Tq, a.qs[1])) && apart(a.Tk, a.ks[1]) && apart(a.Tk, a.vs[1]);
   // a staged tile (128 tokens, all heads of a group) is addressed with 31 bits
   const int64_t far = ((int64_t)1 << 30) / (128 * a.elem_bytes);
   a.vec = a.vec && a.qs[1] < far && a.ks[1] < far && a.vs[1] < far && a.qs[2] < far / a.G * 64;

@@ -16,6 +16,9 @@ from encoder_bounds import HALF, U, f64
 import oracle.encoder as enc
 
 TWO_PARTS = 2.0 ** -16
+# fp32 and bf16 end at 2^-126: a weight, its product and its second part may each be flushed to zero below that, wherever the
+# largest weight of a row is 1 or more (they are taken around a maximum that is never above the row's)
+TINY = 2.0 ** -124
 
 
 def oracle(q, k, v, how, go=None):
@@ -55,7 +58,7 @@ def bounds(q, k, v, ref, how, dtype, go=None):
             # the weights' own errors and those of their sum
             rel = 2 * es.max(axis=1, keepdims=True, initial=0.0) + 2 * (Tk + 16) * U
             pv = p @ vb
-            eo = (rel + low) * pv * 1.01
+            eo = (rel + low) * pv * 1.01 + TINY * vb.sum(axis=0)
             o = np.abs(ref["out"][b, :, h])
             res["out"][b, :, h] = eo + half * (o + eo)
             if go is None:
@@ -71,7 +74,7 @@ def bounds(q, k, v, ref, how, dtype, go=None):
                 edelta = (p * (relp * span + edp)).sum(-1, keepdims=True) + (Tk + D + 16) * U * mean
             else:
                 edelta = (ga * res["out"][b, :, h]).sum(-1, keepdims=True) + (D + 4) * U * (ga * o).sum(-1, keepdims=True)
-            eds = p * (edelta + edp) + relp * p * span
+            eds = p * (edelta + edp) + relp * p * span + TINY * (1 + span)
             sum_ds = np.abs(ref["dsc"][b, h]) + eds * 1.01
             edsc = (eds + low * ds) * 1.02 + (16 * U + 4 * es) * ds
             if "dist" in ref:
@@ -88,7 +91,7 @@ def bounds(q, k, v, ref, how, dtype, go=None):
             e = scale * ((edsc + acc * sum_ds) @ kb)
             res["gq"][b, :, h] = e + half * (g + e)
             res["gk"][b, :, h // G] += scale * ((edsc + acc * sum_ds).T @ np.abs(q[b, :, h]))
-            res["gv"][b, :, h // G] += ((relp + low + acc) * p * 1.01).T @ ga
+            res["gv"][b, :, h // G] += ((relp + low + acc) * p * 1.01 + TINY).T @ ga
     if go is not None:
         res["gk"] += half * (np.abs(ref["gk"]) + res["gk"])
         res["gv"] += half * (np.abs(ref["gv"]) + res["gv"])

@@ -59,3 +59,14 @@ def test_caps_far_above_the_scores(cap, dtype):
 def test_prefixes_beyond_the_keys(prefix, dtype):
     q, k, v, go, how = draw(1, 40, 70, 2, 1, 32, dtype, 82, causal=True, prefix=[prefix])
     check(q, k, v, go, how, f"prefix {prefix}")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_one_query_row_for_all_tokens(dtype):
+    """Queries broadcast over the tokens (stride 0), with scores far beyond what an exponential holds."""
+    q, k, v, go, how = draw(1, 33, 45, 2, 2, 32, dtype, 83, sharp=1.0)
+    row = k[:, 7:8] * 40
+    check(row.expand(1, 33, 2, 32), k, v, go, how, "one row")
+    one = k[:, 3:4].expand(1, 45, 2, 32)
+    check(q, one, v[:, :1].expand(1, 45, 2, 32), go, how, "one key")
+    check(row.as_strided((1, 1, 2, 32), (0, 0, 32, 1)), k, v, go[:, :1].contiguous(), how, "one token of stride 0")
