@@ -87,17 +87,49 @@ def _check_sizes(*sizes: int) -> None:
         raise ValueError(f"sizes must be below 2^31, got {max(sizes)}")
 
 
-def _span(t: torch.Tensor) -> Tuple[int, int]:
-    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
-    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+def _walk(t: torch.Tensor):
+    """The tensor's bytes as (count, stride) dimensions, widest stride first, without those that stay in place."""
+    es = t.element_size()
+    dims = [(n, s * es) for n, s in zip(t.shape, t.stride()) if n > 1 and s > 0]
+    return sorted(dims + [(es, 1)], key=lambda d: -d[1])
 
 
-def _check_apart(name: str, out: torch.Tensor, *inputs: torch.Tensor) -> None:
-    """Refuses an output on memory that another workgroup may still read."""
-    lo, hi = _span(out)
-    for x in inputs:
-        if out.numel() and x.numel() and _span(x)[0] < hi and lo < _span(x)[1]:
-            raise ValueError(f"{name} must not overlap an input")
+def _extent(dims) -> int:
+    return sum((n - 1) * s for n, s in dims) + 1
+
+
+def _disjoint(off: int, a, b) -> bool:
+    """Whether walk b, begun `off` bytes behind walk a, shares no byte with it.  Exact where one steps over the other's
+    inner dimensions (slices of packed tensors); False where that takes more than comparing extents."""
+    if off >= _extent(a) or -off >= _extent(b):
+        return True
+    if not a or not b:
+        return False                                  # a single byte within the other's extent
+    step = max(a[0][1], b[0][1])
+    if step <= 1:
+        return False
+    inner_a, inner_b = a[a[0][1] == step:], b[b[0][1] == step:]
+    if _extent(inner_a) > step or _extent(inner_b) > step:
+        return False
+    off %= step                                       # of any two blocks that can meet
+    return _disjoint(off, inner_a, inner_b) and _disjoint(off - step, inner_a, inner_b)
+
+
+def _steps_over(dims) -> bool:
+    """Whether every dimension steps over those inside it: no byte is walked twice."""
+    return all(dims[i][1] >= _extent(dims[i + 1:]) for i in range(len(dims) - 1))
+
+
+def _overlap(x: torch.Tensor, y: torch.Tensor) -> bool:
+    if x.numel() == 0 or y.numel() == 0:
+        return False
+    return not _disjoint(y.data_ptr() - x.data_ptr(), _walk(x), _walk(y))
+
+
+def _check_apart(name: str, out: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
+    """Refuses an output on memory that another workgroup may still read (or write)."""
+    if any(x is not None and _overlap(out, x) for x in others):
+        raise ValueError(f"{name} must not overlap another tensor of the call")
 
 
 # ---- group norm with an activation
@@ -280,10 +312,15 @@ def _rotary(q, k, pos, freqs, interleaved, inverse, q_out, k_out):
                              "channels contiguous")
         elif out.numel() and any(s == 0 and n > 1 for n, s in zip(out.shape, out.stride())):
             raise ValueError(f"{name}_out must not be a broadcast tensor")
+        elif not _steps_over(_walk(out)):
+            raise ValueError(f"{name}_out must not overlap itself")
         elif out.data_ptr() != x.data_ptr() or out.stride() != x.stride():
             _check_apart(f"{name}_out, unless it is {name} itself,", out, x)
         ins.append(x)
         outs.append(out)
+    for given, name, out, other in ((q_out, "q_out", outs[0], 1), (k_out, "k_out", outs[1], 0)):
+        if given is not None and out is not None:
+            _check_apart(name, out, ins[other], outs[other], pos, freqs)
     none = (0, 0, 0, 0)
     strides = [none if x is None else x.stride() for x in ins + outs]
     rd = _lib.RotaryDesc(B, T, D, pos.shape[2], freqs.shape[1], 0 if q is None else q.shape[2],
@@ -299,7 +336,8 @@ def rotary_forward(q: Optional[torch.Tensor], k: Optional[torch.Tensor], pos: to
                    k_out: Optional[torch.Tensor] = None):
     """fbev_rotary: queries [B,T,Hq,D] and keys [B,T,Hk,D] (fp32 or bf16, either may be None) turned by
     theta = pos [B,T,axes] . freqs [axes,pairs] (fp32; angles in double).  Pair i is channels (i, i + pairs), or
-    (2i, 2i + 1) when ``interleaved``.  ``q_out`` / ``k_out`` may be q / k themselves.  Returns (q', k')."""
+    (2i, 2i + 1) when ``interleaved``.  ``q_out`` / ``k_out`` may be q / k themselves (slices of a packed tensor among
+    them), but share no memory with anything else of the call.  Returns (q', k')."""
     return _rotary(q, k, pos, freqs, interleaved, False, q_out, k_out)
 
 

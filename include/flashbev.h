@@ -442,8 +442,10 @@ fbev_status fbev_group_norm_backward(const void* grad_y, const void* x, fbev_dty
  *
  *   q, k       : [B, T, heads, D] by element strides (batch, token, head), channels
  *                contiguous; a tensor with 0 heads may be NULL.
- *   q_out, k_out : the results, by their own strides; may be q and k themselves
- *                (same strides), but must not overlap them otherwise.
+ *   q_out, k_out : the results, by their own strides.  q_out may be q and k_out k
+ *                (same strides); apart from that no output may share memory with
+ *                an input, the other output or itself: one launch turns both, and
+ *                its workgroups read and write in any order.
  *   pos        : [B, T, A] fp32;  freqs : [A, P] fp32, device; 1 <= A <= 8,
  *                1 <= P <= min(D / 2, FBEV_MAX_ROTARY_PAIRS).
  */

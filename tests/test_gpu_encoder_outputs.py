@@ -1,0 +1,48 @@
+"""GPU: outputs on memory that something else of the call uses are refused; those that lie apart are not."""
+import pytest
+import torch
+
+from camera_bev_view_amd import ops
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rotary_outputs(dtype):
+    print(f"[case] rotary outputs on the call's memory {dtype}", flush=True)
+    g = torch.Generator().manual_seed(91)
+    packed = torch.randn((2, 31, 3, 4, 32), generator=g).to(dtype).cuda()
+    q, k, v = (packed[:, :, i] for i in range(3))
+    pos, freqs = torch.randn((2, 31, 3), generator=g).cuda(), ops.rotary_freqs((6, 5, 5), device="cuda")
+    want = ops.rotary_forward(q, k, pos, freqs)
+    free = torch.empty((2, 31, 4, 32), dtype=dtype, device="cuda")
+    refused = [dict(q_out=k), dict(k_out=q), dict(q_out=k, k_out=q), dict(q_out=free, k_out=free),
+               dict(q_out=packed.view(2, 31, 12, 32)[:, :, 2:6]), dict(q_out=free.as_strided(free.shape, (3968, 64, 32, 1)))]
+    held = packed.clone()
+    for kw in refused:
+        with pytest.raises(ValueError):
+            ops.rotary_forward(q, k, pos, freqs, **kw)
+    same = q.clone()
+    with pytest.raises(ValueError):
+        ops.rotary_forward(same, same, pos, freqs, q_out=same)        # other threads read it as k
+    if dtype == F32:
+        for hold in (pos, freqs):
+            x = torch.zeros((1, 3, 1, 4) if hold is pos else (1, 1, 1, 4), device="cuda")
+            t = dict(pos=torch.zeros((1, x.shape[1], 1), device="cuda"), freqs=torch.zeros((1, 2), device="cuda"))
+            name = "pos" if hold is pos else "freqs"
+            t[name] = x.view(-1)[:t[name].numel()].view(t[name].shape)
+            with pytest.raises(ValueError):
+                ops.rotary_forward(torch.ones_like(x), None, t["pos"], t["freqs"], q_out=x)
+    assert torch.equal(packed, held)
+    # what lies apart: in place within a packed tensor, the third slice as an output, both at once
+    got = ops.rotary_forward(q, None, pos, freqs, q_out=v)
+    assert got[0].data_ptr() == v.data_ptr() and torch.equal(v, want[0])
+    ops.rotary_forward(q, k, pos, freqs, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
