@@ -195,7 +195,7 @@ def group_norm_forward(x: torch.Tensor, groups: int, weight: Optional[torch.Tens
         out = torch.empty(x.shape, dtype=x.dtype, device=dev)
     else:
         _check_plain("out", out, x.shape, x.dtype, dev)
-        _check_apart("out", out, x)
+        _check_apart("out", out, x, weight, bias, workspace)
     stats = torch.empty((nd.images, max(groups, 0), 2), dtype=torch.float32, device=dev)
     dt = _DTYPES[x.dtype]
     workspace, have = _scratch(_norm_scratch(nd.images, nd.pixels, nd.C, groups, dt, 0), workspace, dev)
@@ -453,7 +453,7 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scal
         out = torch.empty(q.shape, dtype=q.dtype, device=dev)
     else:
         _check_plain("out", out, q.shape, q.dtype, dev)
-        _check_apart("out", out, q, k, v)
+        _check_apart("out", out, q, k, v, *keep, workspace)
     stats = torch.empty((ad.B, ad.Hq, ad.Tq, 2), dtype=torch.float32, device=dev)
     workspace, have = _scratch(_attention_scratch(ad.B, ad.Tq, ad.Tk, ad.Hq, ad.Hk, ad.D, ad.dims, 0), workspace, dev)
     _call("fbev_attention_forward", dev, _data(q), _data(k), _data(v), _DTYPES[q.dtype], ad, _data(out), _data(stats),

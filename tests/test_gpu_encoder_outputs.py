@@ -46,3 +46,31 @@ def test_rotary_outputs(dtype):
     assert got[0].data_ptr() == v.data_ptr() and torch.equal(v, want[0])
     ops.rotary_forward(q, k, pos, freqs, q_out=q, k_out=k)
     assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+
+
+def test_norm_and_attention_outputs():
+    print("[case] norm and attention outputs on parameters, positions, slopes, documents, workspaces", flush=True)
+    x = torch.randn((2, 30, 16), device="cuda")
+    out = torch.empty_like(x)
+    for name in ("weight", "bias"):
+        with pytest.raises(ValueError):
+            ops.group_norm_forward(x, 4, out=out, **{name: out.view(-1)[32:48]})
+    with pytest.raises(ValueError):
+        ops.group_norm_forward(x, 4, out=out, workspace=out.view(torch.uint8).view(-1)[:256])
+    ops.group_norm_forward(x, 4, torch.ones(16, device="cuda"), out=out)
+    q, k, v = (torch.randn((1, 40, 2, 32), device="cuda") for _ in range(3))
+    out = torch.empty_like(q)
+    flat = out.view(-1)
+    tables = dict(pos_q=torch.zeros((1, 40, 2), device="cuda"), pos_k=torch.zeros((1, 40, 2), device="cuda"),
+                  slope=torch.zeros((1, 40, 2), device="cuda"), doc_q=torch.zeros((1, 40), dtype=torch.int32, device="cuda"),
+                  doc_k=torch.zeros((1, 40), dtype=torch.int32, device="cuda"))
+    for name, t in tables.items():
+        with pytest.raises(ValueError):
+            ops.attention_forward(q, k, v, out=out, **{**tables, name: flat[:t.numel()].view(t.dtype).view(t.shape)})
+    with pytest.raises(ValueError):
+        ops.attention_forward(q, k, v, out=out, causal=True, prefix=flat[:1].view(torch.int32))
+    with pytest.raises(ValueError):
+        ops.attention_forward(q, k, v, out=out, workspace=flat.view(torch.uint8))
+    want = ops.attention_forward(q, k, v, **tables)
+    got = ops.attention_forward(q, k, v, out=out, **tables)
+    assert got[0] is out and torch.equal(out, want[0])
