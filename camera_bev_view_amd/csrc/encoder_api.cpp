@@ -264,13 +264,15 @@ fbev_status fbev_group_norm_forward(const void* x, fbev_dtype dtype, const fbev_
   fbev::NormArgs a{};
   fbev_status s = check_norm(nd, dtype, a);
   if (s != FBEV_OK) return s;
-  if ((int64_t)a.images * a.pixels == 0) return FBEV_OK;
-  if (x == nullptr || y == nullptr || stats == nullptr)
+  if (a.images == 0) return FBEV_OK;
+  if (stats == nullptr || (a.pixels > 0 && (x == nullptr || y == nullptr)))
     return fail(FBEV_ERR_INVALID_ARGUMENT, "x, y and stats must be non-NULL");
-  s = pick_norm_width(a, x, y, y);
-  if (s != FBEV_OK) return s;
-  s = check_workspace(workspace, workspace_bytes, fbev::group_norm_workspace_bytes(a, false));
-  if (s != FBEV_OK) return s;
+  if (a.pixels > 0) {
+    s = pick_norm_width(a, x, y, y);
+    if (s != FBEV_OK) return s;
+    s = check_workspace(workspace, workspace_bytes, fbev::group_norm_workspace_bytes(a, false));
+    if (s != FBEV_OK) return s;
+  }
   a.x = x;
   a.weight = weight;
   a.bias = bias;

@@ -404,6 +404,14 @@ __global__ __launch_bounds__(BLOCK) void norm_apply(NormArgs a, int nch, int sla
   write_normed<T, V, R, ACT>(a, w, x, af.mul, af.add);
 }
 
+// Images without pixels: mean 0, variance 0.
+__global__ __launch_bounds__(256) void norm_empty_stats(NormArgs a) {
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (at >= (int64_t)a.images * a.groups) return;
+  a.stats[2 * at] = 0.0f;
+  a.stats[2 * at + 1] = 1.0f / sqrtf(a.eps);
+}
+
 // ---- backward
 
 // dz and xh of element j of piece r, from the group's mean / rstd and the channel's weight / bias.
@@ -817,7 +825,11 @@ size_t group_norm_workspace_bytes(const NormArgs& a, bool backward) {
   return p.whole ? 0 : (size_t)a.images * p.chunks * 2 * a.groups * sizeof(float);
 }
 
-hipError_t launch_group_norm_forward(const NormArgs& a, hipStream_t stream) { return by_type(a, false, stream); }
+hipError_t launch_group_norm_forward(const NormArgs& a, hipStream_t stream) {
+  if (a.pixels > 0) return by_type(a, false, stream);
+  norm_empty_stats<<<dim3((unsigned)(((int64_t)a.images * a.groups + kSmall - 1) / kSmall)), kSmall, 0, stream>>>(a);
+  return hipGetLastError();
+}
 
 hipError_t launch_group_norm_backward(const NormArgs& a, hipStream_t stream) {
   if ((int64_t)a.images * a.pixels > 0) return by_type(a, true, stream);

@@ -397,7 +397,8 @@ fbev_status fbev_deform_backward(const float* grad_out, const float* features, f
  *
  *   weight, bias : [C] fp32, device, or NULL (ones / zeros).
  *   y            : [images, pixels, C] of dtype, contiguous, not on x.
- *   stats        : [images, groups, 2] fp32: mean and 1 / sqrt(var + eps).
+ *   stats        : [images, groups, 2] fp32: mean and 1 / sqrt(var + eps)
+ *                  (without pixels: 0 and 1 / sqrt(eps)).
  *   workspace    : device scratch of the size the workspace call reports
  *                  (NULL when 0), 16-byte aligned; not needed before or after
  *                  the call.  Calls that share it must not overlap.
