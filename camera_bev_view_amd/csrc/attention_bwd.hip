@@ -146,7 +146,7 @@ template <typename T>
 constexpr bool kOwnDelta = sizeof(T) == 4;                // the gradients' launch forms delta itself
 
 template <typename T, int DP, int KW, int HB, bool BIAS, bool CAP, Pass PASS>
-__global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(HB))) void attn_bwd_rows(AttnArgs a, int tiles, Split sp) {
+__global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(HB))) void attn_bwd_rows(AttnArgs a, int tiles, int blocks, Split sp) {
   using C = Bwd<T, DP, KW, HB>;
   using M = Mma<T, DP>;
   constexpr int NB = DP / 32, MT = C::MT, RW = C::RW;
@@ -160,7 +160,9 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
   char* Ks = smem;                                        // HB tiles each
   char* Vs = smem + HB * C::kTile;
 
-  const int bid = xcd_block(blockIdx.x, gridDim.x);
+  const int block = blockIdx.z * gridDim.x + blockIdx.x;
+  if (block >= blocks) return;
+  const int bid = xcd_block(block, blocks);
   const int bh = bid / tiles, order = bid - bh * tiles;
   const int tile = a.causal ? tiles - 1 - order : order;  // causal rows: those with the most keys first
   const int b = bh / (a.Hk / HB), hk = (bh - b * (a.Hk / HB)) * HB;
@@ -424,7 +426,7 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
 // ---- keys: gk, gv
 
 template <typename T, int DP, int KW, int HB, bool BIAS, bool CAP>
-__global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(HB))) void attn_bwd_keys(AttnArgs a, int tiles, Split sp) {
+__global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(HB))) void attn_bwd_keys(AttnArgs a, int tiles, int blocks, Split sp) {
   using C = Bwd<T, DP, KW, HB>;
   using M = Mma<T, DP>;
   constexpr int NB = DP / 32, MT = C::MT, RW = C::RW;
@@ -439,7 +441,9 @@ __global__ __launch_bounds__((Bwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
   char* Qs = smem;                                        // HB tiles each
   char* Gs = smem + HB * C::kTile;
 
-  const int bid = xcd_block(blockIdx.x, gridDim.x);
+  const int block = blockIdx.z * gridDim.x + blockIdx.x;
+  if (block >= blocks) return;
+  const int bid = xcd_block(block, blocks);
   const int tile = bid % tiles, bh = bid / tiles;
   const int b = bh / (a.Hk / HB), hk = (bh - b * (a.Hk / HB)) * HB;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 31, h = lane >> 5;
@@ -763,18 +767,24 @@ int pick_waves(const AttnArgs& a, int64_t heads, int rows) {
   return 4;
 }
 
+// Workgroups by splits, rows of workgroups in the third dimension.
+dim3 split_grid(int blocks, const Split& sp) {
+  const dim3 rows = grid_rows(blocks);
+  return dim3(rows.x, (unsigned)sp.splits, rows.y);
+}
+
 // The rows' figures, then the splits' partial rows (of one launch at a time).
 int64_t stats_size(const AttnArgs& a) { return ((int64_t)a.B * a.Hk * a.R * stat_floats(a) + 3) / 4 * 4; }
 float* split_part(const AttnArgs& a) { return a.delta == nullptr ? nullptr : a.delta + stats_size(a); }
 
 template <typename T, int DP, int HB, bool BIAS, bool CAP, Pass PASS>
-void launch_rows(const AttnArgs& a, int kw, dim3 grid, int tiles, const Split& sp, hipStream_t stream) {
+void launch_rows(const AttnArgs& a, int kw, dim3 grid, int tiles, int blocks, const Split& sp, hipStream_t stream) {
   if (kw == 1)
-    attn_bwd_rows<T, DP, 1, HB, BIAS, CAP, PASS><<<grid, 256, 0, stream>>>(a, tiles, sp);
+    attn_bwd_rows<T, DP, 1, HB, BIAS, CAP, PASS><<<grid, 256, 0, stream>>>(a, tiles, blocks, sp);
   else if (kw == 4)
-    attn_bwd_rows<T, DP, 4, HB, BIAS, CAP, PASS><<<grid, 256, 0, stream>>>(a, tiles, sp);
+    attn_bwd_rows<T, DP, 4, HB, BIAS, CAP, PASS><<<grid, 256, 0, stream>>>(a, tiles, blocks, sp);
   else if constexpr (HB == 1 && eight_waves<T>(DP))
-    attn_bwd_rows<T, DP, 8, HB, BIAS, CAP, PASS><<<grid, 512, 0, stream>>>(a, tiles, sp);
+    attn_bwd_rows<T, DP, 8, HB, BIAS, CAP, PASS><<<grid, 512, 0, stream>>>(a, tiles, blocks, sp);
 }
 
 template <typename T, int DP, int HB, bool BIAS, bool CAP>
@@ -785,13 +795,14 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
     const int tiles = (a.R + rows - 1) / rows;
     Split sp = make_split(a, a.R, a.Tk);
     sp.part = split_part(a);
-    const dim3 grid((unsigned)(heads * tiles), (unsigned)sp.splits);
+    const int blocks = (int)(heads * tiles);
+    const dim3 grid = split_grid(blocks, sp);
     if constexpr (!kOwnDelta<T>) {
-      launch_rows<T, DP, HB, BIAS, CAP, kDelta>(a, kw, grid, tiles, sp, stream);
+      launch_rows<T, DP, HB, BIAS, CAP, kDelta>(a, kw, grid, tiles, blocks, sp, stream);
       if (sp.splits > 1)
         attn_bwd_join_delta<<<dim3((unsigned)(((int64_t)a.B * a.Hk * a.R + kThreads - 1) / kThreads)), kThreads, 0, stream>>>(a, sp);
     }
-    launch_rows<T, DP, HB, BIAS, CAP, kGradients>(a, kw, grid, tiles, sp, stream);
+    launch_rows<T, DP, HB, BIAS, CAP, kGradients>(a, kw, grid, tiles, blocks, sp, stream);
     if (sp.splits > 1)
       attn_bwd_join_rows<T><<<dim3((unsigned)(((int64_t)a.B * a.Hk * a.R + 3) / 4)), kThreads, 0, stream>>>(a, sp);
     const hipError_t e = hipGetLastError();
@@ -802,13 +813,14 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
     const int tiles = (a.Tk + rows - 1) / rows;
     Split sp = make_split(a, a.Tk, a.R);
     sp.part = split_part(a);
-    const dim3 grid((unsigned)(heads * tiles), (unsigned)sp.splits);
+    const int blocks = (int)(heads * tiles);
+    const dim3 grid = split_grid(blocks, sp);
     if (kw == 1)
-      attn_bwd_keys<T, DP, 1, HB, BIAS, CAP><<<grid, 256, 0, stream>>>(a, tiles, sp);
+      attn_bwd_keys<T, DP, 1, HB, BIAS, CAP><<<grid, 256, 0, stream>>>(a, tiles, blocks, sp);
     else if (kw == 4)
-      attn_bwd_keys<T, DP, 4, HB, BIAS, CAP><<<grid, 256, 0, stream>>>(a, tiles, sp);
+      attn_bwd_keys<T, DP, 4, HB, BIAS, CAP><<<grid, 256, 0, stream>>>(a, tiles, blocks, sp);
     else if constexpr (HB == 1 && eight_waves<T>(DP))
-      attn_bwd_keys<T, DP, 8, HB, BIAS, CAP><<<grid, 512, 0, stream>>>(a, tiles, sp);
+      attn_bwd_keys<T, DP, 8, HB, BIAS, CAP><<<grid, 512, 0, stream>>>(a, tiles, blocks, sp);
     if (sp.splits > 1)
       attn_bwd_join_keys<T><<<dim3((unsigned)(((int64_t)a.B * a.Hk * a.Tk * 2 + 3) / 4)), kThreads, 0, stream>>>(a, sp);
   }

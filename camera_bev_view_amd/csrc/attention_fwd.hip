@@ -140,8 +140,8 @@ __device__ __forceinline__ void finish(const AttnArgs& a, const Row& w, int firs
 }
 
 template <typename T, int DP, int KW, int HB, bool BIAS>
-__global__ __launch_bounds__((Fwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(HB))) void attn_fwd(AttnArgs a,
-                                                                                                   int tiles) {
+__global__ __launch_bounds__((Fwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(HB))) void attn_fwd(AttnArgs a, int tiles,
+                                                                                                   int blocks) {
   using C = Fwd<T, DP, KW, HB>;
   using M = Mma<T, DP>;
   constexpr int NB = DP / 32, KT = C::KT, RW = C::RW;
@@ -153,7 +153,9 @@ __global__ __launch_bounds__((Fwd<T, DP, KW, HB>::kThreads), (min_waves<T, DP>(H
   char* Ks = smem;                                        // HB tiles each
   char* Vs = smem + HB * C::kTile;
 
-  const int bid = xcd_block(blockIdx.x, gridDim.x);
+  const int block = blockIdx.y * gridDim.x + blockIdx.x;
+  if (block >= blocks) return;
+  const int bid = xcd_block(block, blocks);
   const int split = bid % a.splits, bh = bid / a.splits / tiles;
   const int order = bid / a.splits - bh * tiles;
   const int tile = a.causal ? tiles - 1 - order : order;  // causal rows: those with the most keys first
@@ -461,13 +463,14 @@ Plan make_plan(const AttnArgs& a) {
 
 template <typename T, int DP, int HB, bool BIAS>
 void launch(const AttnArgs& a, const Plan& p, hipStream_t stream) {
-  const dim3 grid((unsigned)((int64_t)a.B * a.Hk / HB * p.tiles * p.splits));
+  const int blocks = (int)((int64_t)a.B * a.Hk / HB * p.tiles * p.splits);
+  const dim3 grid = grid_rows(blocks);
   if (p.kw == 1) {
-    attn_fwd<T, DP, 1, HB, BIAS><<<grid, 256, 0, stream>>>(a, p.tiles);
+    attn_fwd<T, DP, 1, HB, BIAS><<<grid, 256, 0, stream>>>(a, p.tiles, blocks);
   } else if (p.kw == 4) {
-    attn_fwd<T, DP, 4, HB, BIAS><<<grid, 256, 0, stream>>>(a, p.tiles);
+    attn_fwd<T, DP, 4, HB, BIAS><<<grid, 256, 0, stream>>>(a, p.tiles, blocks);
   } else {
-    if constexpr (HB == 1 && eight_waves<T>(DP)) attn_fwd<T, DP, 8, HB, BIAS><<<grid, 512, 0, stream>>>(a, p.tiles);
+    if constexpr (HB == 1 && eight_waves<T>(DP)) attn_fwd<T, DP, 8, HB, BIAS><<<grid, 512, 0, stream>>>(a, p.tiles, blocks);
   }
 }
 

@@ -7,6 +7,14 @@
 
 namespace fbev {
 
+// A launch has at most 2^32 - 1 threads in a dimension: beyond kGridRow workgroups (of up to 1024 threads) they lie in rows
+// of so many, the last one padded, which the kernels number through.
+constexpr int64_t kGridRow = (int64_t)1 << 21;
+inline dim3 grid_rows(int64_t blocks) {
+  if (blocks <= kGridRow) return dim3((unsigned)blocks);
+  return dim3((unsigned)kGridRow, (unsigned)((blocks + kGridRow - 1) / kGridRow));
+}
+
 // Group norm over channels-last images x[i][s][c] (i < images, s < pixels, c < C), `groups` groups of
 // C / groups neighbouring channels.  y, gy and gx are contiguous.
 struct NormArgs {

@@ -46,7 +46,6 @@ fbev_status check_norm(const fbev_norm_desc* nd, fbev_dtype dtype, fbev::NormArg
     return fail(FBEV_ERR_INVALID_ARGUMENT, "eps must be finite and not negative");
   if (nd->image_stride < 0 || nd->pixel_stride < 0)
     return fail(FBEV_ERR_INVALID_ARGUMENT, "negative stride");
-  // blocks (at most one a pixel, image and channel group) and their products stay within 31 bits
   if (nd->images >= (int64_t)1 << 31 || nd->pixels >= (int64_t)1 << 31 ||
       nd->images * nd->pixels >= ((int64_t)1 << 40) / nd->C)
     return fail(FBEV_ERR_UNSUPPORTED, "%lld images of %lld pixels of %d channels: above 2^40 elements",
@@ -77,6 +76,7 @@ fbev_status pick_norm_width(fbev::NormArgs& a, const void* x, const void* y, con
   const int cg = a.C / a.groups;
   if (cg / gcd(cg, a.vec) > 1024)
     return fail(FBEV_ERR_UNSUPPORTED, "groups of %d channels moved %d at a time: more than 1024 pieces", cg, a.vec);
+  // workgroups hold at least six pixels of a group: their numbers stay within 32 bits
   const size_t blocks = (size_t)a.images * a.groups * ((size_t)a.pixels / 8 + 1);
   if (blocks >= (size_t)1 << 31)
     return fail(FBEV_ERR_UNSUPPORTED, "%d images of %d pixels in %d groups: too many", a.images, a.pixels, a.groups);

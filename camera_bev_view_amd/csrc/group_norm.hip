@@ -32,6 +32,9 @@ namespace {
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__bf16 x) { return (float)x; }
 
+// The workgroup's number in a grid_rows() launch.
+__device__ __forceinline__ uint32_t row_block() { return blockIdx.y * gridDim.x + blockIdx.x; }
+
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Piece {
   T e[V];
@@ -251,7 +254,9 @@ struct Affine {
 template <int BLOCK, typename T, int V, int R, int ACT>
 __global__ __launch_bounds__(BLOCK) void norm_whole(NormArgs a, int nch, int slabs) {
   __shared__ Lds<BLOCK, V> L;
-  const int img = blockIdx.x / slabs, c0 = (blockIdx.x - img * slabs) * nch;
+  const uint32_t block = row_block();
+  const int img = block / slabs, c0 = (block - img * slabs) * nch;
+  if (img >= a.images) return;
   const Share w = make_share<BLOCK, V>(img, c0, min(nch, a.C - c0), 0, a.pixels);
   const int cg = a.C / a.groups, per = cg % V == 0 ? 1 : V;
   Piece<T, V> x[R];
@@ -277,7 +282,9 @@ __global__ __launch_bounds__(BLOCK) void norm_whole(NormArgs a, int nch, int sla
 template <int BLOCK, typename T, int V, int R>
 __global__ __launch_bounds__(BLOCK) void norm_moments(NormArgs a, int nch, int slabs, int chunk, int chunks) {
   __shared__ Lds<BLOCK, V> L;
-  const int per_img = slabs * chunks, img = blockIdx.x / per_img, rest = blockIdx.x - img * per_img;
+  const uint32_t block = row_block();
+  const int per_img = slabs * chunks, img = block / per_img, rest = block - img * per_img;
+  if (img >= a.images) return;
   const int slab = rest / chunks, ch = rest - slab * chunks, c0 = slab * nch;
   const Share w = make_share<BLOCK, V>(img, c0, min(nch, a.C - c0), ch * chunk, min(chunk, a.pixels - ch * chunk));
   const int cg = a.C / a.groups, per = cg % V == 0 ? 1 : V;
@@ -295,7 +302,7 @@ __global__ __launch_bounds__(BLOCK) void norm_moments(NormArgs a, int nch, int s
 // An image's chunks joined once, for all workgroups that normalise it: a wave a group, its lanes as share_moments joins
 // threads.  Writes the statistics.
 __global__ __launch_bounds__(512) void norm_join(NormArgs a, int chunk, int chunks) {
-  const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 6);
+  const int64_t at = (int64_t)row_block() * 8 + (threadIdx.x >> 6);
   if (at >= (int64_t)a.images * a.groups) return;
   const int img = (int)(at / a.groups), g = (int)(at - (int64_t)img * a.groups), lane = threadIdx.x & 63;
   const int cg = a.C / a.groups;
@@ -337,7 +344,9 @@ template <int BLOCK, typename T, int V, int R, int ACT>
 __global__ __launch_bounds__(BLOCK) void norm_apply(NormArgs a, int nch, int slabs, int chunk, int chunks, int share,
                                                    int shares, bool joined) {
   __shared__ Groups<BLOCK, V> L;
-  const int per_img = slabs * shares, img = blockIdx.x / per_img, rest = blockIdx.x - img * per_img;
+  const uint32_t block = row_block();
+  const int per_img = slabs * shares, img = block / per_img, rest = block - img * per_img;
+  if (img >= a.images) return;
   const int slab = rest / shares, ch = rest - slab * shares, c0 = slab * nch;
   const Share w = make_share<BLOCK, V>(img, c0, min(nch, a.C - c0), ch * share, min(share, a.pixels - ch * share));
   const int cg = a.C / a.groups;
@@ -406,7 +415,7 @@ __global__ __launch_bounds__(BLOCK) void norm_apply(NormArgs a, int nch, int sla
 
 // Images without pixels: mean 0, variance 0.
 __global__ __launch_bounds__(256) void norm_empty_stats(NormArgs a) {
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t at = (int64_t)row_block() * 256 + threadIdx.x;
   if (at >= (int64_t)a.images * a.groups) return;
   a.stats[2 * at] = 0.0f;
   a.stats[2 * at + 1] = 1.0f / sqrtf(a.eps);
@@ -545,7 +554,9 @@ __device__ __forceinline__ void group_means(const NormArgs& a, const Share& w, c
 template <int BLOCK, typename T, int V, int R, int ACT>
 __global__ __launch_bounds__(BLOCK) void norm_bwd_whole(NormArgs a, int nch, int slabs) {
   __shared__ Lds<BLOCK, V> L;
-  const int img = blockIdx.x / slabs, c0 = (blockIdx.x - img * slabs) * nch;
+  const uint32_t block = row_block();
+  const int img = block / slabs, c0 = (block - img * slabs) * nch;
+  if (img >= a.images) return;
   const Share w = make_share<BLOCK, V>(img, c0, min(nch, a.C - c0), 0, a.pixels);
   const int cg = a.C / a.groups, cols = w.nv * V;
   Piece<T, V> x[R], gy[R];
@@ -569,7 +580,9 @@ __global__ __launch_bounds__(BLOCK) void norm_bwd_whole(NormArgs a, int nch, int
 template <int BLOCK, typename T, int V, int R, int ACT>
 __global__ __launch_bounds__(BLOCK) void norm_bwd_sums(NormArgs a, int nch, int slabs, int chunk, int chunks) {
   __shared__ Lds<BLOCK, V> L;
-  const int per_img = slabs * chunks, img = blockIdx.x / per_img, rest = blockIdx.x - img * per_img;
+  const uint32_t block = row_block();
+  const int per_img = slabs * chunks, img = block / per_img, rest = block - img * per_img;
+  if (img >= a.images) return;
   const int slab = rest / chunks, ch = rest - slab * chunks, c0 = slab * nch;
   const Share w = make_share<BLOCK, V>(img, c0, min(nch, a.C - c0), ch * chunk, min(chunk, a.pixels - ch * chunk));
   const int cg = a.C / a.groups, cols = w.nv * V;
@@ -620,8 +633,10 @@ __global__ __launch_bounds__(BLOCK) void norm_param_grads(NormArgs a, int64_t ro
 // An image's chunks joined once, for all workgroups of the next launch: 32 columns by 32 chunks a workgroup.
 __global__ __launch_bounds__(1024) void norm_bwd_join(NormArgs a, int chunks, float* sums) {
   __shared__ float part[32][33];
-  const int per_img = (2 * a.C + 31) / 32, img = blockIdx.x / per_img;
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, col = (blockIdx.x - img * per_img) * 32 + x;
+  const uint32_t block = row_block();
+  const int per_img = (2 * a.C + 31) / 32, img = block / per_img;
+  if (img >= a.images) return;
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, col = (block - img * per_img) * 32 + x;
   const float* p = a.part + (int64_t)img * chunks * 2 * a.C + min(col, 2 * a.C - 1);
   float s = 0.0f;
   for (int k0 = y; k0 < chunks; k0 += 32 * 8) {           // eight loads in flight at once
@@ -644,9 +659,10 @@ template <int BLOCK, typename T, int V, int R, int ACT>
 __global__ __launch_bounds__(BLOCK) void norm_bwd_apply(NormArgs a, int nch, int slabs, int chunk, int chunks,
                                                        const float* sums, int rows) {
   __shared__ Groups<BLOCK, V> L;
-  const int per_img = slabs * chunks, img = blockIdx.x / per_img, rest = blockIdx.x - img * per_img;
+  const uint32_t block = row_block();
+  const int per_img = slabs * chunks, img = block / per_img, rest = block - img * per_img;
   if (img >= a.images) {
-    param_grads<BLOCK>(a, sums, (int64_t)a.images * rows, blockIdx.x - a.images * per_img);
+    param_grads<BLOCK>(a, sums, (int64_t)a.images * rows, (int)(block - (uint32_t)a.images * per_img));
     return;
   }
   const int slab = rest / chunks, ch = rest - slab * chunks, c0 = slab * nch;
@@ -744,29 +760,29 @@ Plan backward_plan(const NormArgs& a, int* pieces) {
 template <int BLOCK, typename T, int V, int ACT>
 void forward(const NormArgs& a, const Plan& p, hipStream_t stream) {
   const int share = kRA * (BLOCK / (p.nch / V)), shares = (a.pixels + share - 1) / share;
-  norm_moments<BLOCK, T, V, kR><<<dim3((unsigned)(a.images * p.slabs * p.chunks)), BLOCK, 0, stream>>>(
+  norm_moments<BLOCK, T, V, kR><<<grid_rows((int64_t)a.images * p.slabs * p.chunks), BLOCK, 0, stream>>>(
       a, p.nch, p.slabs, p.chunk, p.chunks);
   const bool joined = p.chunks > kJoinMoments;
   if (joined)
-    norm_join<<<dim3((unsigned)(((int64_t)a.images * a.groups + 7) / 8)), 512, 0, stream>>>(a, p.chunk, p.chunks);
-  norm_apply<BLOCK, T, V, kRA, ACT><<<dim3((unsigned)(a.images * p.slabs * shares)), BLOCK, 0, stream>>>(
+    norm_join<<<grid_rows(((int64_t)a.images * a.groups + 7) / 8), 512, 0, stream>>>(a, p.chunk, p.chunks);
+  norm_apply<BLOCK, T, V, kRA, ACT><<<grid_rows((int64_t)a.images * p.slabs * shares), BLOCK, 0, stream>>>(
       a, p.nch, p.slabs, p.chunk, p.chunks, share, shares, joined);
 }
 
 template <int BLOCK, typename T, int V, int ACT, int R>
 void backward(const NormArgs& a, const Plan& p, hipStream_t stream) {
-  const unsigned extra = a.gweight || a.gbias ? (unsigned)((2 * a.C + BLOCK / 64 - 1) / (BLOCK / 64)) : 0;
-  const unsigned n = (unsigned)(a.images * p.slabs * p.chunks);
-  norm_bwd_sums<BLOCK, T, V, R, ACT><<<dim3(n), BLOCK, 0, stream>>>(a, p.nch, p.slabs, p.chunk, p.chunks);
+  const int64_t extra = a.gweight || a.gbias ? (2 * a.C + BLOCK / 64 - 1) / (BLOCK / 64) : 0;
+  const int64_t n = (int64_t)a.images * p.slabs * p.chunks;
+  norm_bwd_sums<BLOCK, T, V, R, ACT><<<grid_rows(n), BLOCK, 0, stream>>>(a, p.nch, p.slabs, p.chunk, p.chunks);
   const float* sums = a.part;
   int rows = p.chunks;
   if (p.chunks > kJoinSums) {
     float* joined = a.part + (int64_t)a.images * p.chunks * 2 * a.C;
-    norm_bwd_join<<<dim3((unsigned)(a.images * ((2 * a.C + 31) / 32))), 1024, 0, stream>>>(a, p.chunks, joined);
+    norm_bwd_join<<<grid_rows((int64_t)a.images * ((2 * a.C + 31) / 32)), 1024, 0, stream>>>(a, p.chunks, joined);
     sums = joined;
     rows = 1;
   }
-  norm_bwd_apply<BLOCK, T, V, R, ACT><<<dim3(n + extra), BLOCK, 0, stream>>>(a, p.nch, p.slabs, p.chunk, p.chunks,
+  norm_bwd_apply<BLOCK, T, V, R, ACT><<<grid_rows(n + extra), BLOCK, 0, stream>>>(a, p.nch, p.slabs, p.chunk, p.chunks,
                                                                                sums, rows);
 }
 
@@ -774,7 +790,7 @@ template <typename T, int V, int ACT>
 hipError_t run(const NormArgs& a, bool bwd, hipStream_t stream) {
   int pieces = kR;
   const Plan p = bwd ? backward_plan(a, &pieces) : make_plan(a, kR);
-  const dim3 whole((unsigned)(a.images * p.slabs));
+  const dim3 whole = grid_rows((int64_t)a.images * p.slabs);
   if (p.whole && !bwd) {
     norm_whole<kBig, T, V, kWhole, ACT><<<whole, kBig, 0, stream>>>(a, p.nch, p.slabs);
   } else if (p.whole) {
@@ -827,7 +843,7 @@ size_t group_norm_workspace_bytes(const NormArgs& a, bool backward) {
 
 hipError_t launch_group_norm_forward(const NormArgs& a, hipStream_t stream) {
   if (a.pixels > 0) return by_type(a, false, stream);
-  norm_empty_stats<<<dim3((unsigned)(((int64_t)a.images * a.groups + kSmall - 1) / kSmall)), kSmall, 0, stream>>>(a);
+  norm_empty_stats<<<grid_rows(((int64_t)a.images * a.groups + kSmall - 1) / kSmall), kSmall, 0, stream>>>(a);
   return hipGetLastError();
 }
 

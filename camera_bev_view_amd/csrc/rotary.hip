@@ -117,8 +117,10 @@ struct Item {
 template <typename T, int V, bool IL>
 __global__ __launch_bounds__(kBlock) void rotary_kernel(RotaryArgs a, int tokens, int blocks_per_sample) {
   __shared__ float2 table[kTableMax];
-  const int b = blockIdx.x / blocks_per_sample;
-  const int t0 = (blockIdx.x - b * blocks_per_sample) * tokens;
+  const uint32_t block = blockIdx.y * gridDim.x + blockIdx.x;
+  const int b = block / blocks_per_sample;
+  const int t0 = (block - b * blocks_per_sample) * tokens;
+  if (b >= a.B) return;
   const int nt = min(tokens, a.T - t0);
   // pieces of a head's row: rotated ones first (a half-split piece is V channels and their V partners)
   const int turned = (IL && V > 1) ? 2 * a.P / V : a.P / V;
@@ -159,7 +161,7 @@ hipError_t launch(const RotaryArgs& a, hipStream_t stream) {
   if (tokens > (int64_t)a.B * a.T / 512) tokens = (int64_t)a.B * a.T / 512;
   if (tokens < 1) tokens = 1;
   const int per = (int)((a.T + tokens - 1) / tokens);
-  const dim3 grid((unsigned)((int64_t)a.B * per));
+  const dim3 grid = grid_rows((int64_t)a.B * per);
   if (a.interleaved)
     rotary_kernel<T, V, true><<<grid, kBlock, 0, stream>>>(a, (int)tokens, per);
   else
