@@ -7,7 +7,7 @@
 
 namespace fbev {
 
-// A launch has at most 2^32 - 1 threads in a dimension: beyond kGridRow workgroups (of up to 1024 threads) they lie in rows
+// A launch has at most 2^32 - 1 threads in a dimension (the runtime cuts more to 32 bits without an error): beyond kGridRow workgroups (of up to 1024 threads) they lie in rows
 // of so many, the last one padded, which the kernels number through.
 constexpr int64_t kGridRow = (int64_t)1 << 21;
 inline dim3 grid_rows(int64_t blocks) {
