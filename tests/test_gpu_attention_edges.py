@@ -1,5 +1,4 @@
 """GPU: attention calls at the edges of what its documentation allows."""
-import numpy as np
 import pytest
 import torch
 
@@ -70,3 +69,44 @@ def test_one_query_row_for_all_tokens(dtype):
     one = k[:, 3:4].expand(1, 45, 2, 32)
     check(q, one, v[:, :1].expand(1, 45, 2, 32), go, how, "one key")
     check(row.as_strided((1, 1, 2, 32), (0, 0, 32, 1)), k, v, go[:, :1].contiguous(), how, "one token of stride 0")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_masked_places_hold_anything_where_a_wave_takes_two_heads(dtype):
+    T, B, H = 75, 4, 96
+    ids = [runs([40, 9, 20], T)] * B
+    q, k, v, go, how = draw(B, T, T, H, H, 32, dtype, 85, dims=2, docs=(ids, ids), causal=True)
+    print(f"[case] attention, two heads a wave, padding {dtype}", flush=True)
+    want = ops.attention_forward(q, k, v, **how)
+    grads = ops.attention_backward(go, q, k, v, *want, **how)
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        for t in (k, v, q, go):
+            t[:, 69:] = bad
+        how["pos_k"][:, 69:] = bad
+        how["pos_q"][:, 69:] = bad
+        out, stats = ops.attention_forward(q, k, v, **how)
+        assert torch.equal(out, want[0]) and torch.equal(stats, want[1]), bad
+        for a, b in zip(ops.attention_backward(go, q, k, v, out, stats, **how), grads):
+            assert torch.equal(a, b), bad
+    # one value of a document: the others' rows and gradients stay
+    q, k, v, go, how = draw(B, T, T, H, H, 32, dtype, 86, dims=2, docs=(ids, ids))
+    want = ops.attention_forward(q, k, v, **how)
+    grads = ops.attention_backward(go, q, k, v, *want, **how)
+    other = torch.tensor([i < 40 or i >= 49 for i in range(T)], device="cuda")
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        k2, v2, q2, go2 = (t.clone() for t in (k, v, q, go))
+        v2[:, 41, :, 3] = k2[:, 42, :, 1] = q2[:, 43, :, 2] = go2[:, 44, :, 2] = bad
+        out, stats = ops.attention_forward(q2, k2, v2, **how)
+        assert torch.equal(out[:, other], want[0][:, other]), bad
+        for a, b in zip(ops.attention_backward(go2, q2, k2, v2, out, stats, **how), grads):
+            assert torch.equal(a[:, other], b[:, other]), bad
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_no_queries(dtype):
+    print(f"[case] attention without queries {dtype}", flush=True)
+    q, k, v, go, how = draw(2, 0, 50, 4, 2, 32, dtype, 87, dims=2, docs=([[]] * 2, [[0] * 50] * 2))
+    out, stats = ops.attention_forward(q, k, v, **how)
+    gq, gk, gv, gs = ops.attention_backward(go, q, k, v, out, stats, **how)
+    assert out.shape == q.shape and gq.shape == q.shape and gs.shape == (2, 0, 4)
+    assert gk.shape == k.shape and (gk == 0).all() and (gv == 0).all()

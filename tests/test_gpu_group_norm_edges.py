@@ -1,5 +1,4 @@
 """GPU: group norm calls at the edges of what its documentation allows."""
-import numpy as np
 import pytest
 import torch
 
@@ -25,3 +24,30 @@ def test_statistics_of_images_without_pixels(dtype):
         del held
         y, stats = ops.group_norm_forward(x, 2, eps=0.25)
         assert y.shape == x.shape and (stats[..., 0] == 0).all() and (stats[..., 1] == 2).all()
+
+
+# groups of more pieces than a small workgroup has threads: (shape, groups).  Whole slabs, chunks of four pieces a thread
+# without and with the launch that joins them, chunks of six, one channel a piece, two slabs of a group each, the widest
+# group; last chunks are short
+WIDE = [((5, 2, 2056), 1), ((1, 101, 2056), 1), ((1, 701, 2056), 1), ((3, 701, 2056), 1), ((2, 303, 771), 1),
+        ((5, 611, 771), 1), ((2, 77, 4112), 2)]
+WIDE = [(*c, t) for c in WIDE for t in (F32, BF16)] + [((1, 50, 8192), 1, BF16)]
+
+
+@pytest.mark.parametrize("shape,groups,dtype", WIDE)
+def test_wide_groups(shape, groups, dtype, monkeypatch):
+    import encoder_bounds
+    from test_gpu_group_norm import check, draw
+    # a group's channels are added one after the other in the backward
+    monkeypatch.setattr(encoder_bounds, "CHAIN", shape[-1] // groups + 256)
+    print(f"[case] group norm of wide groups {shape} {dtype}", flush=True)
+    x, gy, w, b = draw(shape, dtype, 17)
+    check(x.cuda(), gy.cuda(), w.cuda(), b.cuda(), groups, "silu", f"{shape}/{groups}")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_map_one_pixel_wide(dtype):
+    from test_gpu_group_norm import check, draw
+    print(f"[case] group norm of a map one pixel wide {dtype}", flush=True)
+    x, gy, w, b = draw((2, 1, 700, 1, 1032), dtype, 18)
+    check(x.cuda(), gy.cuda(), w.cuda(), b.cuda(), 3, "silu", "one pixel wide")
