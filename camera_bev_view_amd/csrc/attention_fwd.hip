@@ -51,21 +51,16 @@ __device__ __forceinline__ void finish(const AttnArgs& a, const Row& w, int firs
   constexpr int NB = DP / 32;
   const int n = lane & 31, h = lane >> 5, head = w.head + hd;
   const int b = (int)(bh / a.Hk), hk = (int)(bh - (int64_t)b * a.Hk);
-  const bool part = a.splits > 1;
-  if constexpr (KW == 1) {
+  if constexpr (KW == 1) {                          // 128 rows a workgroup: so many of them that no keys are split
     if (first + n < a.R) {
-      float* po = part ? a.part + (((int64_t)split * a.B * a.Hk + bh) * a.R + w.r) * (a.D + 2) : nullptr;
       T* out = (T*)a.out + (((int64_t)b * a.Tq + w.t) * a.Hq + head) * a.D;
-      const float inv = part ? 1.0f : (l > 0.0f || l != l ? 1.0f / l : 0.0f);
+      const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
 #pragma unroll
       for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int c = 32 * blk + 8 * u + 4 * h;
-          if (part) {
-            for (int j = 0; j < 4; ++j)
-              if (c + j < a.D) po[c + j] = acc[blk][4 * u + j];
-          } else if (a.vec_out) {
+          if (a.vec_out) {
             if (c < a.D) {
               typedef T V4 __attribute__((ext_vector_type(4)));
               V4 o;
@@ -79,15 +74,11 @@ __device__ __forceinline__ void finish(const AttnArgs& a, const Row& w, int firs
               if (c + j < a.D) out[c + j] = (T)(acc[blk][4 * u + j] * inv);
           }
         }
-      if (h == 0) {
-        if (part)
-          po[a.D] = m, po[a.D + 1] = l;
-        else
-          a.stats[((int64_t)b * a.Hq + head) * a.Tq + w.t] = make_float2(m, l);
-      }
+      if (h == 0) a.stats[((int64_t)b * a.Hq + head) * a.Tq + w.t] = make_float2(m, l);
     }
   } else {
     // the waves' sums over their keys, added in wave order
+    const bool part = a.splits > 1;
     float* mo = (float*)smem;                       // [KW][32][DP + 4]
     float* ml = mo + KW * 32 * (DP + 4);            // [KW][32][2]
     __syncthreads();

@@ -15,6 +15,8 @@ inline dim3 grid_rows(int64_t blocks) {
   return dim3((unsigned)kGridRow, (unsigned)((blocks + kGridRow - 1) / kGridRow));
 }
 
+inline int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
+
 // Group norm over channels-last images x[i][s][c] (i < images, s < pixels, c < C), `groups` groups of
 // C / groups neighbouring channels.  y, gy and gx are contiguous.
 struct NormArgs {

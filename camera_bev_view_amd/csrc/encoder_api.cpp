@@ -12,6 +12,7 @@
 namespace {
 
 using fbev::fail;
+using fbev::gcd;
 
 fbev_status device_status(hipError_t e, const char* what) {
   if (e == hipSuccess) return FBEV_OK;
@@ -28,8 +29,6 @@ fbev_status check_workspace(const void* workspace, size_t have, size_t need) {
   if (!aligned(workspace, 16)) return fail(FBEV_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
   return FBEV_OK;
 }
-
-int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
 // ---- group norm
 
@@ -339,15 +338,12 @@ fbev_status fbev_attention_workspace(const fbev_attention_desc* ad, int32_t back
   if (s != FBEV_OK) return s;
   *bytes = 0;
   if ((int64_t)a.B * a.R == 0) return FBEV_OK;
+  a.elem_bytes = 4;      // neither size depends on the type
   if (backward) {
     *bytes = fbev::attention_backward_workspace_bytes(a);
     return FBEV_OK;
   }
-  // the split of the keys depends on the type: the size covers both
-  for (a.elem_bytes = 4; a.elem_bytes >= 2; a.elem_bytes -= 2) {
-    const size_t n = fbev::attention_forward_workspace_bytes(a);
-    if (n > *bytes) *bytes = n;
-  }
+  *bytes = fbev::attention_forward_workspace_bytes(a);
   return FBEV_OK;
 }
 

@@ -25,20 +25,13 @@
 #include "encoder.h"
 
 #include "../../include/flashbev.h"
+#include "pieces.h"
 
 namespace fbev {
 namespace {
 
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__bf16 x) { return (float)x; }
-
 // The workgroup's number in a grid_rows() launch.
 __device__ __forceinline__ uint32_t row_block() { return blockIdx.y * gridDim.x + blockIdx.x; }
-
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Piece {
-  T e[V];
-};
 
 template <int ACT>
 __device__ __forceinline__ float act_fwd(float z) {
@@ -629,7 +622,6 @@ __global__ __launch_bounds__(BLOCK) void norm_param_grads(NormArgs a, int64_t ro
   param_grads<BLOCK>(a, a.part, rows, blockIdx.x);
 }
 
-// The second: gx from the image's sums; the blocks behind the last chunk add up the parameters' gradients.
 // An image's chunks joined once, for all workgroups of the next launch: 32 columns by 32 chunks a workgroup.
 __global__ __launch_bounds__(1024) void norm_bwd_join(NormArgs a, int chunks, float* sums) {
   __shared__ float part[32][33];
@@ -655,6 +647,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_join(NormArgs a, int chunks, fl
   sums[(int64_t)img * 2 * a.C + col] = s;
 }
 
+// The second: gx from the image's sums; the blocks behind the last chunk add up the parameters' gradients.
 template <int BLOCK, typename T, int V, int R, int ACT>
 __global__ __launch_bounds__(BLOCK) void norm_bwd_apply(NormArgs a, int nch, int slabs, int chunk, int chunks,
                                                        const float* sums, int rows) {
@@ -714,8 +707,6 @@ struct Plan {
   int chunk, chunks;            // pixels of a chunk
   bool big;
 };
-
-int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
 // A slab is a multiple of `unit` channels, the least that holds whole groups and whole pieces.
 Plan make_plan(const NormArgs& a, int R) {

@@ -16,6 +16,7 @@
 // copy reaches; fp32, 3 x 10007 tokens of four heads of 40, interleaved (38 MB, in the caches): 12 us; 900 tokens of
 // 16 heads of 32: 3.9 us, a launch.
 #include "encoder.h"
+#include "pieces.h"
 
 namespace fbev {
 namespace {
@@ -44,14 +45,6 @@ __device__ __forceinline__ float2 sincos_turns(double turns) {
   const float ss = (n & 1) ? c : s, cc = (n & 1) ? s : c;
   return make_float2((n & 2) ? -ss : ss, ((n + 1) & 2) ? -cc : cc);
 }
-
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Piece {
-  T e[V];
-};
-
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__bf16 x) { return (float)x; }
 
 constexpr int kAhead = 4;             // items a thread loads before the angles are ready
 
