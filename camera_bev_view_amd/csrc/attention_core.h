@@ -21,7 +21,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -121,16 +121,22 @@ struct Mma<__bf16, DP> {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
 
-  // The B operand: values of tile rows 16 c .. 16 c + 15 (accumulator registers 8 c .. 8 c + 7).
+  // The B operand: values of tile rows 16 c .. 16 c + 15 (accumulator registers 8 c .. 8 c + 7), each as the sum of two bf16:
+  // the first is off by up to 2^-8 of it, the second by as much of the rest, so 16 bits go into the product.
   struct Values {
-    bf16x8 v[2];
+    bf16x8 hi, lo;
   };
-  static __device__ __forceinline__ Values pack(const f32x16& p) {
+  static __device__ __forceinline__ Values split(const f32x16& p, int c) {
     Values r;
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) r.v[c][j] = (__bf16)p[8 * c + j];
+    for (int j = 0; j < 4; ++j) {
+      const float x = p[8 * c + 2 * j], y = p[8 * c + 2 * j + 1];
+      const bf16x2 hi = {(__bf16)x, (__bf16)y};
+      const uint32_t both = opaque(__builtin_bit_cast(uint32_t, hi));     // (the compiler would convert both again)
+      r.hi[2 * j] = hi[0], r.hi[2 * j + 1] = hi[1];
+      r.lo[2 * j] = (__bf16)(x - __builtin_bit_cast(float, both << 16));
+      r.lo[2 * j + 1] = (__bf16)(y - __builtin_bit_cast(float, both & 0xFFFF0000u));
+    }
     return r;
   }
 
@@ -153,25 +159,19 @@ struct Mma<__bf16, DP> {
     return u.v;
   }
 
-  // Adds the transposed tile's product with the values, each of them as the sum of two bf16: the first is off by up to 2^-8
-  // of it, the second by as much of the rest, so 16 bits go into the product.
   template <int NB>
   static __device__ __forceinline__ void accumulate(f32x16 (&acc)[NB], const f32x16& p, const char* tile, int r0,
                                                     int lane) {
-    const Values hi = pack(p);
-    Values lo;
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int c = 0; c < 2; ++c) {
+      const Values v = split(p, c);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) lo.v[c][j] = (__bf16)(p[8 * c + j] - (float)hi.v[c][j]);
-#pragma unroll
-    for (int blk = 0; blk < NB; ++blk)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int blk = 0; blk < NB; ++blk) {
         const bf16x8 x = columns(tile, r0, c, blk, lane);
-        acc[blk] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, hi.v[c], acc[blk], 0, 0, 0);
-        acc[blk] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, lo.v[c], acc[blk], 0, 0, 0);
+        acc[blk] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, v.hi, acc[blk], 0, 0, 0);
+        acc[blk] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, v.lo, acc[blk], 0, 0, 0);
       }
+    }
   }
 };
 
