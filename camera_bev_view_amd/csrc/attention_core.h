@@ -162,16 +162,15 @@ struct Mma<__bf16, DP> {
   template <int NB>
   static __device__ __forceinline__ void accumulate(f32x16 (&acc)[NB], const f32x16& p, const char* tile, int r0,
                                                     int lane) {
+    const Values v[2] = {split(p, 0), split(p, 1)};
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const Values v = split(p, c);
+    for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
-      for (int blk = 0; blk < NB; ++blk) {
+      for (int c = 0; c < 2; ++c) {
         const bf16x8 x = columns(tile, r0, c, blk, lane);
-        acc[blk] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, v.hi, acc[blk], 0, 0, 0);
-        acc[blk] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, v.lo, acc[blk], 0, 0, 0);
+        acc[blk] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, v[c].hi, acc[blk], 0, 0, 0);
+        acc[blk] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, v[c].lo, acc[blk], 0, 0, 0);
       }
-    }
   }
 };
 
