@@ -10,15 +10,16 @@
 // joins in order), so nothing is added by atomics and results are the same from run to run; the price is seven matrix
 // products a tile where five would do with atomics.  Distances are not differentiated: positions are given.
 //
-// What bounds it (bf16, D = 32, distances, 10000 x 10000 cells of 8 heads: 1120 us for both launches, of which the
-// eight products, one of them in two parts, would take 360 us at a large product's rate): vector instructions between the
-// products, as in the forward.  The counters see 14.5 a score in the rows' launch and 9.5 in the keys'.  fp32 (2 x 2048 packed rows of 8 heads over 4, D = 64, a
-// cap: rows 105 us, keys 165 us) runs on the fp32 matrix instructions, near their rate in the tiles that are not
-// masked out.
+// What bounds it.  bf16, D = 32, distances, 10000 x 10000 cells of 8 heads: 1550 us, a trace 377 (delta), 545 (rows) and
+// 811 us (keys), of which vector instructions, with the quarter rate of exponentials and roots, issue for 227, 340 and 426
+// us and matrix ones for 82, 123 and 184; the rest is stages that are waited for in full, 1252 workgroups on 768 places, and
+// in the keys' launch a few spilled registers.  fp32, 2 x 2048 packed rows of 8 heads over 4, D = 64, a cap: rows 109 us,
+// keys 176 us, of which matrix and vector instructions issue for 27 + 25 and 35 + 38 us: the tiles' LDS leaves one or two
+// workgroups a CU, whose work is unequal, and nothing hides their waits.
 //
 // Roundings of bf16 tensors: probabilities and score gradients go into their products as two bf16 each (16 bits).  With
 // one each, gk and gv were 0.0024 off where their own rounding leaves 0.0017; the second part took the cells' backward from
-// 1111 to 1315 us and that of 4 x 900 queries from 77 to 89 us.
+// 1111 to 1280 us and that of 4 x 900 queries from 77 to 87 us.
 #include "attention_core.h"
 
 namespace fbev {
@@ -116,8 +117,8 @@ __device__ __forceinline__ RowStats row_stats(const AttnArgs& a, int64_t bh) {
 }
 
 // Where few own tiles stand against a long other side, its rows are split over `splits` workgroups, `per` (a multiple of
-// every stage) each; their fp32 sums are joined in split order (one token of 8 heads over 40000 keys of 2: 357 -> 66 us;
-// 40000 x 8 rows over 900 keys of one head: 3786 -> 704 us).
+// every stage) each; their fp32 sums are joined in split order (bf16, D = 64: one token of 8 heads over 40000 keys of 2
+// heads 587 -> 84 us; D = 32, distances: 40000 tokens of 8 heads over 900 keys of one head 4157 -> 838 us).
 struct Split {
   int splits, per;
   float* part;
@@ -134,7 +135,7 @@ __host__ __device__ __forceinline__ int key_floats(int D) { return (D + 3) / 4 *
 // go . v - delta that make its gradients (bf16, 400 points of a 100 m square, slope 2: one row in twenty of gq off by more
 // than itself, with the exact delta by 0.002).  fp32 outputs are exact enough for gq (half a step is 2^-24, what the products
 // are off by too), and the sum of the row's ds corrects what the keys' launch and the slopes get.  For bf16 a launch of its
-// own (kDelta: the scores once more, no gradients) sums up ds first: 290 us of the 100 x 100 cells' 1605, 19 us of the 107 of
+// own (kDelta: the scores once more, no gradients) sums up ds first: 290 us of the 100 x 100 cells' 1550, 19 us of the 106 of
 // 4 x 900 queries.
 enum Pass { kDelta, kGradients };
 

@@ -7,10 +7,11 @@
 // head's G query heads are rows of one problem (row = token G + head), so single tokens with grouped heads
 // still fill a tile and keys are read once for the group.
 //
-// What bounds it (bf16, D = 128, 16 heads over 4, 2 x 3100 tokens with a prefix of 2816: 255 us; the products alone, with the
-// second in two parts, would take 190 us at a large library product's rate): the exponentials' and roundings' vector
-// instructions between the matrix ones; at D = 32 with distances (10000 x 10000 cells of 8 heads: 470 us) mostly those (half
-// a distance and its root, as two heads a wave share them, bias, maximum, exponential, sum, rounding).
+// What bounds it.  bf16, D = 128, 16 heads over 4, 2 x 3100 tokens with a prefix of 2816: 254 us; the counters see matrix
+// instructions issue for 86 us and vector ones for 79 us, which alternate within a wave, and every stage waits for its tile
+// in full, with two workgroups a CU to fill the waits.  D = 32 with distances (10000 x 10000 cells of 8 heads): 466 us, of
+// which vector instructions issue for 256 us (12.6 a score: half a distance and its root, as two heads a wave share them,
+// bias, maximum, exponential, sum, two roundings), the quarter rate of exponentials and roots for 90 and matrix ones for 82.
 //
 // Probabilities of bf16 tensors go into the second product as the sum of two bf16 (16 bits of each): one, rounded by up to
 // 2^-8, left outputs 0.0022 off where their own rounding leaves 0.0017.  The second part costs a product and three vector

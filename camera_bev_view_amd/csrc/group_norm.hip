@@ -20,8 +20,8 @@
 //
 // Measured: bf16, 24 maps of 32 x 88 with 80 channels (10.8 MB): moments 9.4, apply 10.3, backward 13.4 and 16.7 us;
 // six maps of 64 x 176 with 128 channels (17.3 MB): 9.4 and 18.1 us.  The second read comes out of the caches (the
-// counters see each kernel fetch its input once); a launch costs about 4 us of each, the rest is one round of
-// loads and stores by all workgroups at once (1.9 TB/s while it runs).
+// counters see each kernel fetch its input once); a launch costs about 4 us of each, the chunks' merge by every workgroup
+// about 7 us of the 18 (20 us forward with it left out), the rest is one round of loads and stores by all workgroups at once.
 #include "encoder.h"
 
 #include "../../include/flashbev.h"
@@ -696,9 +696,10 @@ constexpr int kRA = 8;          // pieces a thread normalises (forward, the seco
 constexpr int kRB = 4, kRBMany = 6;       // pieces of x and of gy a thread holds of a chunk (backward)
 
 // An image's chunks are joined by a launch of their own above so many of them: every workgroup of the next launch joins them
-// by itself below, which is a launch less but grows with the square (bf16, 200 x 200 cells, 128 channels, 313 and 625 chunks:
-// forward 30.8 -> 21.7 us, backward 72 -> 33 us; four maps with 256 channels, backward 1119 -> 173 us; 88 chunks forward
-// 27.7 and 28.0 us, 29 backward 29.9 and 31.2 us, 79 backward 16.5 and 17.0 us).
+// by itself below, which is a launch less but grows with the square (bf16, 200 x 200 cells, 128 channels, 313 chunks forward
+// and 417 backward: 31.3 -> 21.9 us and 48.7 -> 30.3 us; four maps with 256 channels 232.6 -> 75.6 us and 630 -> 157 us;
+// 400 x 400 cells, 128 channels, 220 -> 55 us and 329 -> 91 us; 88 chunks forward 27.7 and 28.0 us, 29 backward 29.9 and
+// 31.2 us, 79 backward 16.5 and 17.0 us).
 constexpr int kJoinMoments = 96, kJoinSums = 64;
 
 struct Plan {

@@ -187,7 +187,9 @@ def group_norm_forward(x: torch.Tensor, groups: int, weight: Optional[torch.Tens
                        workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """fbev_group_norm_forward on channels-last maps x [images..., pixels..., C] (fp32 or bf16; the first
     ``image_dims`` dimensions count images: two of [B,N,H,W,C], one otherwise).  ``activation``: "none", "relu",
-    "silu" or "gelu".  Returns (y like x, contiguous; stats [images, groups, 2] fp32: mean and 1 / sqrt(var + eps))."""
+    "silu" or "gelu".  ``weight`` and ``bias`` [C] are contiguous fp32.  Maps whose channels are not contiguous (a permuted
+    [B,C,X,Y]) or whose pixels have more than one stride are copied first.  Returns (y like x, contiguous; stats
+    [images, groups, 2] fp32: mean and 1 / sqrt(var + eps))."""
     dev = x.device
     x, nd = _norm_desc(x, groups, eps, activation, image_dims)
     _check_affine(nd.C, weight, bias, dev)
