@@ -19,11 +19,18 @@ FBEV_DTYPE_F32 = 0
 FBEV_DTYPE_BF16 = 1
 FBEV_MAX_CAMERAS = 64
 FBEV_MAX_LEVELS = 4
-ABI_VERSION = 9
+ABI_VERSION = 10
 FBEV_MAX_KEYPOINTS = 256
 FBEV_MAX_HEAD_DIM = 128
 FBEV_MAX_ROTARY_PAIRS = 2048
 FBEV_ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+FBEV_CODES_INT8 = 0
+FBEV_CODES_E4M3 = 1
+FBEV_CACHE_PAGE = 64
+FBEV_MAX_RMS_CHANNELS = 16384
+FBEV_DRAFT_NONE = 0
+FBEV_DRAFT_CHAIN = 1
+FBEV_DRAFT_TREE = 2
 FBEV_NOALLOC_SCRATCH_BYTES = 4 << 20
 
 EXPORTED = ("fbev_forward", "fbev_backward", "fbev_forward_levels", "fbev_backward_levels", "fbev_lss_forward",
@@ -32,7 +39,9 @@ EXPORTED = ("fbev_forward", "fbev_backward", "fbev_forward_levels", "fbev_backwa
             "fbev_backward_cameras", "fbev_backward_cameras_noalloc", "fbev_forward_temporal", "fbev_backward_temporal", "fbev_status_string",
             "fbev_last_error", "fbev_abi_version", "fbev_group_norm_workspace", "fbev_group_norm_forward",
             "fbev_group_norm_backward", "fbev_rotary", "fbev_attention_workspace", "fbev_attention_forward",
-            "fbev_attention_backward")
+            "fbev_attention_backward", "fbev_rms_norm_forward", "fbev_rms_norm_codes", "fbev_rms_norm_workspace",
+            "fbev_rms_norm_backward", "fbev_cache_write", "fbev_cache_read", "fbev_cache_attention_workspace",
+            "fbev_cache_attention")
 
 
 class FeatDesc(ctypes.Structure):
@@ -66,6 +75,28 @@ class AttentionDesc(ctypes.Structure):
                 ("cap", ctypes.c_float), ("dims", ctypes.c_int32), ("causal", ctypes.c_int32),
                 ("pos_q", ctypes.c_void_p), ("pos_k", ctypes.c_void_p), ("slope", ctypes.c_void_p),
                 ("doc_q", ctypes.c_void_p), ("doc_k", ctypes.c_void_p), ("prefix", ctypes.c_void_p)]
+
+
+class RmsDesc(ctypes.Structure):
+    _fields_ = [("outer", ctypes.c_int64), ("inner", ctypes.c_int64), ("x_stride", ctypes.c_int64 * 2),
+                ("residual_stride", ctypes.c_int64 * 2), ("C", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class CacheDesc(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int32), ("Hk", ctypes.c_int32), ("D", ctypes.c_int32), ("codes", ctypes.c_int32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
+class CacheRows(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("W", ctypes.c_int32), ("table", ctypes.c_void_p),
+                ("start", ctypes.c_void_p), ("count", ctypes.c_void_p)]
+
+
+class CacheAttentionDesc(ctypes.Structure):
+    _fields_ = [("Hq", ctypes.c_int32), ("drafts", ctypes.c_int32), ("words", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64 * 3), ("ancestors", ctypes.c_void_p), ("scale", ctypes.c_float),
+                ("cap", ctypes.c_float)]
 
 
 class FlashBevError(RuntimeError):
@@ -140,6 +171,20 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.fbev_attention_workspace.argtypes = [adp, i32, szp]
         lib.fbev_attention_forward.argtypes = [vp, vp, vp, i, adp, vp, f32p, vp, sz, vp]
         lib.fbev_attention_backward.argtypes = [vp, vp, vp, vp, i, adp, vp, f32p, vp, vp, vp, f32p, vp, sz, vp]
+        rmp, cdp, crp, cap = (ctypes.POINTER(t) for t in (RmsDesc, CacheDesc, CacheRows, CacheAttentionDesc))
+        stp = ctypes.POINTER(ctypes.c_int64)
+        lib.fbev_rms_norm_forward.argtypes = [vp, vp, i, rmp, f32p, vp, vp, f32p, vp]
+        lib.fbev_rms_norm_codes.argtypes = [vp, vp, i, rmp, f32p, i, i32, vp, f32p, vp, vp]
+        lib.fbev_rms_norm_workspace.argtypes = [rmp, i, szp]
+        lib.fbev_rms_norm_backward.argtypes = [vp, vp, vp, i, rmp, f32p, f32p, vp, f32p, vp, sz, vp]
+        lib.fbev_cache_write.argtypes = [cdp, crp, vp, vp, i, stp, stp, vp]
+        lib.fbev_cache_read.argtypes = [cdp, crp, i, vp, vp, vp]
+        lib.fbev_cache_attention_workspace.argtypes = [cdp, crp, cap, i, szp]
+        lib.fbev_cache_attention.argtypes = [cdp, crp, cap, vp, i, vp, vp, sz, vp]
+        for name in ("fbev_rms_norm_forward", "fbev_rms_norm_codes", "fbev_rms_norm_workspace",
+                     "fbev_rms_norm_backward", "fbev_cache_write", "fbev_cache_read",
+                     "fbev_cache_attention_workspace", "fbev_cache_attention"):
+            getattr(lib, name).restype = i
         for name in ("fbev_group_norm_workspace", "fbev_group_norm_forward", "fbev_group_norm_backward", "fbev_rotary",
                      "fbev_attention_workspace", "fbev_attention_forward", "fbev_attention_backward"):
             getattr(lib, name).restype = i

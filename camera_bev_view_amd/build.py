@@ -20,7 +20,9 @@ SOURCES = [os.path.join(CSRC, "flashbev_api.cpp"), os.path.join(CSRC, "sampling_
            os.path.join(CSRC, "camera_grad.hip"), os.path.join(CSRC, "temporal.hip"),
            os.path.join(CSRC, "sampling_vt_runs.hip"), os.path.join(CSRC, "encoder_api.cpp"),
            os.path.join(CSRC, "group_norm.hip"), os.path.join(CSRC, "rotary.hip"),
-           os.path.join(CSRC, "attention_fwd.hip"), os.path.join(CSRC, "attention_bwd.hip")]
+           os.path.join(CSRC, "attention_fwd.hip"), os.path.join(CSRC, "attention_bwd.hip"),
+           os.path.join(CSRC, "decoder_api.cpp"), os.path.join(CSRC, "rms_norm.hip"),
+           os.path.join(CSRC, "cache_rows.hip"), os.path.join(CSRC, "cache_attention.hip")]
 ARCH = "gfx950"
 
 # Packed-fp32 VALU forms are switched off for all device code.

@@ -1,0 +1,480 @@
+// Root-mean-square norm of rows of C channels, with the residual's addition in front of it and, where asked for, an
+// output in 8 bits behind it.
+//
+//   h = x + residual (rounded once to the type: what the backward reads is what was normalised)
+//   y = h r w,  r = 1 / sqrt(mean_c h^2 + eps)
+//   backward, with u = gy w:   gx = r (u - h r^2 mean_c(u h)) + gh,   gw = sum_rows gy h r
+//
+// Memory bounds it: each tensor once.  A row belongs to a team of 4 to 1024 lanes that keeps it in registers as fp32 between
+// the reduction and the output (at most four 16-byte pieces a lane), so nothing is read twice; teams of up to 64 lanes
+// reduce by lane exchanges alone, wider ones once through LDS.  The team is the narrowest that holds the row in one piece a
+// lane up to 64 lanes: short rows (heads of 32) then fill the wave with rows instead of idle lanes.  Pieces are moved at
+// any alignment (the card's global loads and stores take any address), the piece across a row's end element by element.
+// The backward's workgroups walk many rows and keep their share of gw in registers; partial sums go to the workspace once
+// per workgroup and a second launch adds them in a fixed order.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "codes.h"
+#include "decoder.h"
+#include "encoder.h"
+#include "pieces.h"
+#include "wave_ops.h"
+
+namespace fbev {
+namespace {
+
+template <typename T>
+constexpr int kVec = 16 / (int)sizeof(T);
+
+// Channels c .. c + kVec of a row (`left` of them exist) as fp32, zeros behind the end.
+template <typename T>
+__device__ __forceinline__ void load_piece(const T* p, int left, float (&v)[kVec<T>]) {
+  constexpr int V = kVec<T>;
+  T e[V];
+  if (left >= V) {
+    __builtin_memcpy(e, p, 16);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = to_f32(e[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = i < left ? to_f32(p[i]) : 0.0f;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store_piece(T* p, int left, const float (&v)[kVec<T>]) {
+  constexpr int V = kVec<T>;
+  if (left >= V) {
+    T e[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) e[i] = (T)v[i];
+    __builtin_memcpy(p, e, 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < left) p[i] = (T)v[i];
+  }
+}
+
+__device__ __forceinline__ void load_weight(const float* w, int c, int left, float* v, int n) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) v[i] = 1.0f;
+  if (w == nullptr || left <= 0) return;
+  if (left >= n) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 4)
+      if (j < n) __builtin_memcpy(v + j, w + c + j, 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n && i < left) v[i] = w[c + i];
+  }
+}
+
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// The largest over aligned groups of N lanes (a power of two up to 64).
+__device__ __forceinline__ uint32_t lanes_max(uint32_t x, int n) {
+  if (n >= 2) x = umax(x, dpp<kQuadSwap1>(x));
+  if (n >= 4) x = umax(x, dpp<kQuadSwap2>(x));
+  if (n >= 8) x = umax(x, dpp<kHalfMirror>(x));
+  if (n >= 16) x = umax(x, dpp<kRowMirror>(x));
+  if (n >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    x = umax(r[0], r[1]);
+  }
+  if (n >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    x = umax(r[0], r[1]);
+  }
+  return x;
+}
+
+// x of the lane that DPP control Ctrl names (32 or 64 bits).
+template <int Ctrl, typename X>
+__device__ __forceinline__ X dpp_any(X x) {
+  if constexpr (sizeof(X) == 4) {
+    return dpp<Ctrl>(x);
+  } else {
+    const uint64_t v = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)dpp<Ctrl>((int)(uint32_t)v), hi = (uint32_t)dpp<Ctrl>((int)(uint32_t)(v >> 32));
+    return __builtin_bit_cast(X, (uint64_t)hi << 32 | lo);
+  }
+}
+template <bool HALVES>
+__device__ __forceinline__ double swap_add(double x) {
+  const uint64_t v = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)v, hi = (uint32_t)(v >> 32);
+  uint32_t a[2], b[2];
+  if constexpr (HALVES) {
+    const auto p = __builtin_amdgcn_permlane32_swap(lo, lo, false, false), q = __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
+    a[0] = p[0], a[1] = p[1], b[0] = q[0], b[1] = q[1];
+  } else {
+    const auto p = __builtin_amdgcn_permlane16_swap(lo, lo, false, false), q = __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+    a[0] = p[0], a[1] = p[1], b[0] = q[0], b[1] = q[1];
+  }
+  return __builtin_bit_cast(double, (uint64_t)b[0] << 32 | a[0]) + __builtin_bit_cast(double, (uint64_t)b[1] << 32 | a[1]);
+}
+template <bool HALVES>
+__device__ __forceinline__ float swap_add(float x) {
+  return HALVES ? swap32_add(x, x) : swap16_add(x, x);
+}
+
+template <int L, typename X>
+__device__ __forceinline__ X lanes_sum(X x) {
+  x += dpp_any<kQuadSwap1>(x);
+  x += dpp_any<kQuadSwap2>(x);
+  if constexpr (L >= 8) x += dpp_any<kHalfMirror>(x);
+  if constexpr (L >= 16) x += dpp_any<kRowMirror>(x);
+  if constexpr (L >= 32) x = swap_add<false>(x);
+  if constexpr (L >= 64) x = swap_add<true>(x);
+  return x;
+}
+
+// The team's sum in each of its lanes.  `slots`: LDS for one number of each wave, used by teams of several waves.
+template <int L, typename X>
+__device__ __forceinline__ X team_sum(X x, double* slots) {
+  if constexpr (L <= 64) return lanes_sum<L>(x);
+  x = lanes_sum<64>(x);
+  X* mine = (X*)slots;
+  __syncthreads();          // the last use of the slots is over
+  if ((threadIdx.x & 63) == 0) mine[threadIdx.x >> 6] = x;
+  __syncthreads();
+  x = 0;
+#pragma unroll
+  for (int i = 0; i < L / 64; ++i) x += mine[i];
+  return x;
+}
+
+template <int L>
+__device__ __forceinline__ uint32_t team_max(uint32_t x, double* slots) {
+  if constexpr (L <= 64) return lanes_max(x, L);
+  x = lanes_max(x, 64);
+  __syncthreads();
+  uint32_t* mine = (uint32_t*)slots;
+  if ((threadIdx.x & 63) == 0) mine[threadIdx.x >> 6] = x;
+  __syncthreads();
+  x = 0;
+#pragma unroll
+  for (int i = 0; i < L / 64; ++i) x = umax(x, mine[i]);
+  return x;
+}
+
+constexpr int team_threads(int L) { return L > 256 ? L : 256; }
+
+__device__ __forceinline__ int64_t row_offset(int64_t row, int64_t inner, const int64_t (&s)[2]) {
+  if (inner == 1) return row * s[0];
+  const uint32_t o = (uint32_t)row / (uint32_t)inner;
+  return o * s[0] + (row - (int64_t)o * inner) * s[1];
+}
+
+// y of a row in 8 bits: a scale for each `block` channels.  Blocks are narrower than the row only where a lane's pieces lie
+// L apart and a block's 4 to 32 lanes side by side.
+template <int KIND, int L, int K, int V>
+__device__ __forceinline__ void store_codes(const RmsArgs& a, int64_t row, int lane, bool mine, double (&y)[K][V],
+                                            double* slots) {
+  using Cd = Codes<KIND>;
+  const int nb = a.block < a.C ? a.block / V : 0;       // lanes of a block (0: the row)
+  const int blocks = nb ? (a.C + a.block - 1) / a.block : 1;
+  uint8_t* out = (uint8_t*)a.y + row * a.C;
+  uint32_t top[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    top[k] = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) top[k] = umax(top[k], abs_bits((float)y[k][i]));
+  }
+  if (nb == 0) {
+    uint32_t t = top[0];
+#pragma unroll
+    for (int k = 1; k < K; ++k) t = umax(t, top[k]);
+    t = team_max<L>(t, slots);
+#pragma unroll
+    for (int k = 0; k < K; ++k) top[k] = t;
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k) top[k] = lanes_max(top[k], nb);
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (lane + L * k) * V, left = a.C - c;
+    if (left <= 0 || !mine) continue;
+    const float scale = Cd::scale_of(top[k]);
+    const bool odd = top[k] >= 0x7f800000u;
+    const float inverse = odd ? 0.0f : 1.0f / scale;
+    uint32_t w[V / 4];
+#pragma unroll
+    for (int j = 0; j < V / 4; ++j) {
+      double x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = odd ? 0.0 : y[k][4 * j + i];
+      w[j] = Cd::pack(x, scale, inverse);
+    }
+    if (left >= V) {
+      __builtin_memcpy(out + c, w, V);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i < left) out[c + i] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
+    }
+    if (nb ? (lane & (nb - 1)) == 0 : c == 0) a.scales[row * blocks + (nb ? c / a.block : 0)] = scale;
+  }
+}
+
+// CODES: the sum of squares, 1 / sqrt and y are fp64 in front of the codes, which have no other rounding than their own.
+template <typename T, int L, int K, bool CODES>
+__global__ __launch_bounds__(team_threads(L)) void rms_fwd(RmsArgs a) {
+  constexpr int V = kVec<T>, kThreads = team_threads(L), kTeams = kThreads / L;
+  __shared__ double slots[kThreads / 64];
+  const int lane = threadIdx.x % L;
+  const int64_t first = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kTeams + threadIdx.x / L;
+  if (L > 64 && first >= a.rows) return;                // the whole workgroup; narrower teams stay for the lane exchanges
+  const int64_t row = first < a.rows ? first : a.rows - 1;
+  const bool mine = first < a.rows;
+  const T* x = (const T*)a.x + row_offset(row, a.inner, a.xs);
+  const T* res = a.residual ? (const T*)a.residual + row_offset(row, a.inner, a.rs) : nullptr;
+  float v[K][V], sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (lane + L * k) * V;
+    load_piece(x + c, a.C - c, v[k]);
+  }
+  if (res) {
+    float r[K][V];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (lane + L * k) * V;
+      load_piece(res + c, a.C - c, r[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (lane + L * k) * V;
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[k][i] = to_f32((T)(v[k][i] + r[k][i]));
+      if (mine) store_piece((T*)a.h + row * a.C + c, a.C - c, v[k]);
+    }
+  }
+  if constexpr (CODES) {
+    double squares = 0.0;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) squares = fma((double)v[k][i], (double)v[k][i], squares);
+    squares = team_sum<L>(squares, slots);
+    const double r = 1.0 / sqrt(squares / (double)a.C + (double)a.eps);
+    double y[K][V];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (lane + L * k) * V;
+      float w[V];
+      load_weight(a.weight, c, a.C - c, w, V);
+#pragma unroll
+      for (int i = 0; i < V; ++i) y[k][i] = (double)v[k][i] * (double)w[i] * r;
+    }
+    if (a.codes == FBEV_CODES_E4M3)
+      store_codes<FBEV_CODES_E4M3, L, K, V>(a, row, lane, mine, y, slots);
+    else
+      store_codes<FBEV_CODES_INT8, L, K, V>(a, row, lane, mine, y, slots);
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum = fmaf(v[k][i], v[k][i], sum);
+    sum = team_sum<L>(sum, slots);
+    const float r = 1.0f / sqrtf(sum / (float)a.C + a.eps);
+    if (a.rstd && lane == 0 && mine) a.rstd[row] = r;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (lane + L * k) * V, left = a.C - c;
+      float w[V];
+      load_weight(a.weight, c, left, w, V);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[k][i] = v[k][i] * r * w[i];
+      if (mine) store_piece((T*)a.y + row * a.C + c, left, v[k]);
+    }
+  }
+}
+
+// gx of the rows, and each workgroup's share of gw in `part` [gridDim.x][C].
+template <typename T, int L, int K>
+__global__ __launch_bounds__(team_threads(L)) void rms_bwd(RmsArgs a) {
+  constexpr int V = kVec<T>, kThreads = team_threads(L), kTeams = kThreads / L;
+  __shared__ double slots[kThreads / 64];
+  const int lane = threadIdx.x % L;
+  float w[K][V], gw[K][V];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (lane + L * k) * V;
+    load_weight(a.weight, c, a.C - c, w[k], V);
+#pragma unroll
+    for (int i = 0; i < V; ++i) gw[k][i] = 0.0f;
+  }
+  // every team of a workgroup makes the same number of rounds
+  for (int64_t base = (int64_t)blockIdx.x * kTeams; base < a.rows; base += (int64_t)gridDim.x * kTeams) {
+    const int64_t at = base + threadIdx.x / L;
+    const bool mine = at < a.rows;
+    const int64_t row = mine ? at : a.rows - 1;
+    const T* x = (const T*)a.x + row_offset(row, a.inner, a.xs);
+    const T* gy = (const T*)a.gy + row * a.C;
+    float h[K][V], g[K][V], dot = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (lane + L * k) * V;
+      load_piece(x + c, a.C - c, h[k]);
+      load_piece(gy + c, a.C - c, g[k]);
+    }
+    float more[K][V];
+    if (a.gh) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int c = (lane + L * k) * V;
+        load_piece((const T*)a.gh + row * a.C + c, a.C - c, more[k]);
+      }
+    }
+    const float r = a.rstd[row];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) dot = fmaf(g[k][i] * w[k][i], h[k][i], dot);
+    dot = team_sum<L>(dot, slots);
+    const float along = dot / (float)a.C * r * r;
+    if (!mine) continue;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (lane + L * k) * V;
+      float gx[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        gx[i] = r * (g[k][i] * w[k][i] - h[k][i] * along);
+        if (a.gh) gx[i] += more[k][i];
+        gw[k][i] = fmaf(g[k][i], h[k][i] * r, gw[k][i]);
+      }
+      store_piece((T*)a.gx + row * a.C + c, a.C - c, gx);
+    }
+  }
+  if (a.gweight == nullptr) return;
+  float* part = a.part + (int64_t)blockIdx.x * a.C;
+  if constexpr (L < 256) {
+    // the teams of a wave by lane exchanges, the waves through LDS
+    __shared__ float joined[4][L <= 64 ? L * K * V : 1];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float s = gw[k][i];
+        if constexpr (L <= 4) s += dpp<kRowRor4>(s);
+        if constexpr (L <= 8) s += dpp<kRowRor8>(s);
+        if constexpr (L <= 16) s = swap16_add(s, s);
+        if constexpr (L <= 32) s = swap32_add(s, s);
+        if ((threadIdx.x & 63) < L) joined[threadIdx.x >> 6][(k * V + i) * L + lane] = s;
+      }
+    __syncthreads();
+    for (int n = threadIdx.x; n < L * K * V; n += kThreads) {
+      const int l = n % L, i = n / L % V, k = n / L / V, c = (l + L * k) * V + i;
+      if (c < a.C) part[c] = joined[0][n] + joined[1][n] + joined[2][n] + joined[3][n];
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (lane + L * k) * V;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (c + i < a.C) part[c + i] = gw[k][i];
+    }
+  }
+}
+
+// gw from the workgroups' shares: 32 channels by 32 runs of shares a workgroup, every run in order.
+__global__ __launch_bounds__(1024) void rms_join(const float* part, float* gw, int C, int shares) {
+  __shared__ float sums[32][33];
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), run = threadIdx.x >> 5;
+  float s = 0.0f;
+  if (c < C) {
+#pragma unroll 8
+    for (int i = run; i < shares; i += 32) s += part[(int64_t)i * C + c];
+  }
+  sums[run][threadIdx.x & 31] = s;
+  __syncthreads();
+  if (run != 0 || c >= C) return;
+  s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) s += sums[i][threadIdx.x];
+  gw[c] = s;
+}
+
+// The team of a row of `pieces` pieces: f(lanes, pieces a lane).
+template <typename F>
+hipError_t with_team(int pieces, F f) {
+  if (pieces <= 4) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
+  if (pieces <= 8) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
+  if (pieces <= 16) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
+  if (pieces <= 32) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{});
+  if (pieces <= 64) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
+  if (pieces <= 128) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
+  if (pieces <= 256) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 4>{});
+  if (pieces <= 512) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
+  if (pieces <= 1024) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
+  if (pieces <= 2048) return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+  return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
+}
+
+int pieces_of(const RmsArgs& a) { return (int)(((int64_t)a.C * a.elem_bytes + 15) / 16); }
+
+// Workgroups of the backward: up to four a CU, each with eight rounds of rows at least so that the shares stay few
+// against the data.
+int backward_blocks(const RmsArgs& a, int teams) {
+  const int64_t rounds = (a.rows + teams - 1) / teams;
+  const int64_t n = rounds / 8 > 256 ? rounds / 8 : (rounds < 256 ? rounds : 256);
+  return (int)(n < 1024 ? n : 1024);
+}
+
+}  // namespace
+
+size_t rms_norm_workspace_bytes(const RmsArgs& a) {
+  if (a.rows == 0) return 0;
+  size_t need = 0;
+  with_team(pieces_of(a), [&](auto L, auto) {
+    need = (size_t)backward_blocks(a, team_threads(L) / L) * a.C * sizeof(float);
+    return hipSuccess;
+  });
+  return need;
+}
+
+hipError_t launch_rms_norm_forward(const RmsArgs& a, hipStream_t stream) {
+  return with_team(pieces_of(a), [&](auto L, auto K) {
+    constexpr int kTeams = team_threads(L) / L;
+    const dim3 grid = grid_rows((a.rows + kTeams - 1) / kTeams);
+    const auto run = [&](auto codes) {
+      if (a.elem_bytes == 4)
+        rms_fwd<float, L, K, codes><<<grid, team_threads(L), 0, stream>>>(a);
+      else if constexpr (!(L == 1024 && K == 4))        // FBEV_MAX_RMS_CHANNELS bf16 are 2048 pieces
+        rms_fwd<__bf16, L, K, codes><<<grid, team_threads(L), 0, stream>>>(a);
+    };
+    if (a.codes < 0)
+      run(std::false_type{});
+    else
+      run(std::true_type{});
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_rms_norm_backward(const RmsArgs& a, hipStream_t stream) {
+  if (a.rows == 0) {      // no rows: gw is zero
+    rms_join<<<(a.C + 31) / 32, 1024, 0, stream>>>(a.part, a.gweight, a.C, 0);
+    return hipGetLastError();
+  }
+  return with_team(pieces_of(a), [&](auto L, auto K) {
+    const int blocks = backward_blocks(a, team_threads(L) / L);
+    if (a.elem_bytes == 4)
+      rms_bwd<float, L, K><<<blocks, team_threads(L), 0, stream>>>(a);
+    else if constexpr (!(L == 1024 && K == 4))
+      rms_bwd<__bf16, L, K><<<blocks, team_threads(L), 0, stream>>>(a);
+    if (a.gweight) rms_join<<<(a.C + 31) / 32, 1024, 0, stream>>>(a.part, a.gweight, a.C, blocks);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace fbev

@@ -1,0 +1,370 @@
+"""PyTorch-facing calls of the decoder operators: argument marshalling only.
+
+Root-mean-square norm with the residual's addition (and an output in 8 bits), the token cache in 8 bits, and attention
+of query tokens, trees of drafted ones among others, over that cache.  ``camera_bev_view_amd.ops`` re-exports them beside
+the encoder operators.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+from typing import Optional, Sequence, Tuple
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _lib
+from .encoder import (_DTYPES, _call, _check_apart, _check_plain, _check_sizes, _check_values, _collapse, _data,
+                      _scratch)
+
+_CODES = {torch.int8: _lib.FBEV_CODES_INT8, torch.float8_e4m3fn: _lib.FBEV_CODES_E4M3}
+_PAGE = _lib.FBEV_CACHE_PAGE
+_I64x3 = ctypes.c_int64 * 3
+
+
+# ---- root-mean-square norm
+
+@functools.lru_cache(maxsize=1024)
+def _rms_scratch(rows: int, C: int, dtype: int) -> int:
+    lib, need = _lib.load(), ctypes.c_size_t()
+    _lib.check(lib.fbev_rms_norm_workspace(_lib.RmsDesc(rows, 1, (0, 0), (0, 0), C, 0.0), dtype, ctypes.byref(need)))
+    return need.value
+
+
+def _rows(x: torch.Tensor, other: Optional[torch.Tensor]):
+    """(outer, inner, their strides in x and in other): how to walk the rows of both, or None."""
+    lead = x.dim() - 1
+    if x.is_contiguous() and (other is None or other.is_contiguous()):
+        C = x.shape[-1]
+        return (x.numel() // C if C else 0), 1, (C, 0), (C, 0)
+    for t in (x, other):
+        if t is not None and t.shape[-1] > 1 and t.stride(-1) != 1:
+            return None
+    for cut in range(lead, -1, -1):
+        strides = []
+        for t in (x, other):
+            if t is None:
+                strides.append((0, 0))
+                continue
+            so, si = _collapse(t.shape[:cut], t.stride()[:cut]), _collapse(t.shape[cut:lead], t.stride()[cut:lead])
+            if so is None or si is None:
+                break
+            strides.append((so, si))
+        if len(strides) == 2:
+            outer = inner = 1
+            for n in x.shape[:cut]:
+                outer *= n
+            for n in x.shape[cut:lead]:
+                inner *= n
+            return outer, inner, strides[0], strides[1]
+    return None
+
+
+def _rms_desc(x: torch.Tensor, residual: Optional[torch.Tensor], weight, eps: float):
+    if x.dim() < 1:
+        raise ValueError("x must be [..., C]")
+    if not x.is_cuda:
+        raise ValueError("x must be a device tensor")
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"x must be float32 or bfloat16, got {x.dtype}")
+    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype
+                                 or residual.device != x.device):
+        raise ValueError(f"residual must be a {x.dtype} tensor of shape {list(x.shape)} on {x.device}")
+    C = x.shape[-1]
+    _check_sizes(C)
+    if weight is not None:
+        _check_plain("weight", weight, (C,), torch.float32, x.device)
+    walk = _rows(x, residual)
+    if walk is None:
+        x = x.contiguous()
+        residual = None if residual is None else residual.contiguous()
+        walk = _rows(x, residual)
+    return x, residual, _lib.RmsDesc(*walk, C, eps)
+
+
+def rms_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
+                     residual: Optional[torch.Tensor] = None, eps: float = 1e-6, out: Optional[torch.Tensor] = None,
+                     h_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """fbev_rms_norm_forward on rows of channels x [..., C] (fp32 or bf16): h = x + residual (like x; rounded once), y = h
+    weight / sqrt(mean h^2 + eps).  ``weight`` [C] is contiguous fp32.  Rows may lie at two strides (heads of a packed
+    projection); other layouts are copied first.  ``h_out`` may be x or residual themselves, where contiguous.
+    Returns (y, h, rstd [...] fp32); h is x without a residual.  The backward takes h and rstd."""
+    dev = x.device
+    x, residual, rd = _rms_desc(x, residual, weight, eps)
+    y = _given("out", out, x, x, residual, weight, h_out)
+    h = x
+    if residual is not None:
+        h = _sum_out(h_out, x, residual, weight)
+    elif h_out is not None:
+        raise ValueError("h_out comes with a residual")
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    _call("fbev_rms_norm_forward", dev, _data(x), _data(residual), _DTYPES[x.dtype], rd, _data(weight), _data(y),
+          None if residual is None else _data(h), _data(rstd))
+    return y, h, rstd
+
+
+def _given(name: str, out: Optional[torch.Tensor], like: torch.Tensor, *others) -> torch.Tensor:
+    if out is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    _check_plain(name, out, like.shape, like.dtype, like.device)
+    _check_apart(name, out, *others)
+    return out
+
+
+def _sum_out(h_out, x, residual, weight) -> torch.Tensor:
+    if h_out is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _check_plain("h_out", h_out, x.shape, x.dtype, x.device)
+    for t in (x, residual):
+        if not (t.data_ptr() == h_out.data_ptr() and t.is_contiguous()):
+            _check_apart("h_out, unless it is x or residual itself,", h_out, t)
+    _check_apart("h_out", h_out, weight)
+    return h_out
+
+
+def rms_norm_codes(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
+                   residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                   codes: torch.dtype = torch.float8_e4m3fn, block: int = 128, h_out: Optional[torch.Tensor] = None
+                   ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """fbev_rms_norm_codes: rms_norm_forward with y in 8 bits (``codes``: torch.int8 or torch.float8_e4m3fn) and a scale for each ``block``
+    channels (32, 64 or 128; 0: one for the row).  Returns (codes like x, scales [..., blocks] fp32, h): a code stands for
+    code * scale."""
+    if codes not in _CODES:
+        raise ValueError(f"codes must be torch.int8 or torch.float8_e4m3fn, got {codes}")
+    dev = x.device
+    x, residual, rd = _rms_desc(x, residual, weight, eps)
+    _check_sizes(block)
+    C = x.shape[-1]
+    out = torch.empty(x.shape, dtype=codes, device=dev)
+    blocks = -(-C // block) if 0 < block < C else 1
+    scales = torch.empty((*x.shape[:-1], blocks), dtype=torch.float32, device=dev)
+    h = x
+    if residual is not None:
+        h = _sum_out(h_out, x, residual, weight)
+    elif h_out is not None:
+        raise ValueError("h_out comes with a residual")
+    _call("fbev_rms_norm_codes", dev, _data(x), _data(residual), _DTYPES[x.dtype], rd, _data(weight), _CODES[codes],
+          block, _data(out), _data(scales), None if residual is None else _data(h))
+    return out, scales, h
+
+
+def rms_norm_backward(grad_y: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
+                      weight: Optional[torch.Tensor] = None, *, grad_h: Optional[torch.Tensor] = None,
+                      with_weight: bool = True, workspace: Optional[torch.Tensor] = None
+                      ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """fbev_rms_norm_backward: (grad_x, which is the residual's gradient too, contiguous; grad_weight [C] fp32, or None
+    without ``with_weight``) from dL/dy, the forward's h and rstd, and ``grad_h``, dL/dh from elsewhere (the residual stream)."""
+    dev = h.device
+    h, _, rd = _rms_desc(h, None, weight, 0.0)
+    for name, g in (("grad_y", grad_y), ("grad_h", grad_h)):
+        if g is not None and (g.shape != h.shape or g.dtype != h.dtype or g.device != dev):
+            raise ValueError(f"{name} must be a {h.dtype} tensor of shape {list(h.shape)} on {dev}")
+    grad_y = grad_y.contiguous()
+    grad_h = None if grad_h is None else grad_h.contiguous()
+    _check_plain("rstd", rstd, h.shape[:-1], torch.float32, dev)
+    gx = torch.empty(h.shape, dtype=h.dtype, device=dev)
+    gw = torch.empty(h.shape[-1], dtype=torch.float32, device=dev) if with_weight else None
+    need = _rms_scratch(rd.outer * rd.inner, rd.C, _DTYPES[h.dtype]) if with_weight else 0
+    workspace, have = _scratch(need, workspace, dev)
+    _call("fbev_rms_norm_backward", dev, _data(grad_y), _data(grad_h), _data(h), _DTYPES[h.dtype], rd, _data(weight),
+          _data(rstd), _data(gx), _data(gw), _data(workspace), have)
+    return gx, gw
+
+
+class RmsNorm(torch.autograd.Function):
+    """Autograd wrapper of the root-mean-square norm; with a residual it returns (y, x + residual)."""
+
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps):
+        y, h, rstd = rms_norm_forward(x, weight, residual=residual, eps=eps)
+        ctx.save_for_backward(h, rstd, weight)
+        ctx.set_materialize_grads(False)
+        ctx.both = residual is not None
+        return (y, h) if ctx.both else y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_y, grad_h=None):
+        h, rstd, weight = ctx.saved_tensors
+        want = ctx.needs_input_grad
+        if grad_y is None:
+            return grad_h if want[0] else None, grad_h if want[1] else None, None, None
+        gx, gw = rms_norm_backward(grad_y, h, rstd, weight, grad_h=grad_h, with_weight=want[2])
+        return gx if want[0] else None, gx if want[1] else None, gw, None
+
+
+def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, eps: float = 1e-6) -> torch.Tensor:
+    """Differentiable x weight / sqrt(mean x^2 + eps) over the last dimension (see rms_norm_forward)."""
+    return RmsNorm.apply(x, None, weight, eps)
+
+
+def rms_norm_add(x: torch.Tensor, residual: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
+                 eps: float = 1e-6) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Differentiable (rms_norm(h), h) of h = x + residual: a layer's output joins the residual stream and is normalised
+    for the next one."""
+    return RmsNorm.apply(x, residual, weight, eps)
+
+
+# ---- token cache
+
+class TokenCache:
+    """Keys and values of many sequences in 8 bits, in pages of 64 tokens: codes k [pages, Hk, 64, Dp] and v [pages, Hk,
+    Dp, 64] (torch.int8 or torch.float8_e4m3fn; Dp: D rounded up to a multiple of 16, zeros behind D) and k_scale, v_scale
+    [pages, Hk, 64] fp32, contiguous tensors of one device.  Which page belongs to which sequence is the caller's table."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "D", "Hk", "pages", "device", "desc")
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor, D: int):
+        if k.dim() != 4 or k.dtype not in _CODES:
+            raise ValueError(f"k must be [pages, Hk, {_PAGE}, Dp] of torch.int8 or torch.float8_e4m3fn")
+        if not k.is_cuda:
+            raise ValueError("k must be a device tensor")
+        pages, Hk, Dp = k.shape[0], k.shape[1], -(-D // 16) * 16
+        _check_sizes(pages, Hk, D)
+        for name, t, shape, dtype in (("k", k, (pages, Hk, _PAGE, Dp), k.dtype),
+                                      ("v", v, (pages, Hk, Dp, _PAGE), k.dtype),
+                                      ("k_scale", k_scale, (pages, Hk, _PAGE), torch.float32),
+                                      ("v_scale", v_scale, (pages, Hk, _PAGE), torch.float32)):
+            _check_plain(name, t, shape, dtype, k.device)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.D, self.Hk, self.pages, self.device = D, Hk, pages, k.device
+        self.desc = _lib.CacheDesc(pages, Hk, D, _CODES[k.dtype], _data(k), _data(v), _data(k_scale), _data(v_scale))
+
+
+def token_cache(pages: int, Hk: int, D: int, *, codes: torch.dtype = torch.float8_e4m3fn, device="cuda") -> TokenCache:
+    """An empty cache of ``pages`` pages for ``Hk`` key heads of ``D`` channels."""
+    Dp = -(-D // 16) * 16
+    if codes not in _CODES:
+        raise ValueError(f"codes must be torch.int8 or torch.float8_e4m3fn, got {codes}")
+    return TokenCache(torch.zeros((pages, Hk, _PAGE, Dp), dtype=torch.uint8, device=device).view(codes),
+                      torch.zeros((pages, Hk, Dp, _PAGE), dtype=torch.uint8, device=device).view(codes),
+                      torch.zeros((pages, Hk, _PAGE), dtype=torch.float32, device=device),
+                      torch.zeros((pages, Hk, _PAGE), dtype=torch.float32, device=device), D)
+
+
+def _cache_rows(cache: TokenCache, table, start, count, B: int, T: int):
+    dev = cache.device
+    if table.dim() != 2 or table.shape[0] != B:
+        raise ValueError(f"table must be [B={B}, pages of a sequence], got {tuple(table.shape)}")
+    _check_sizes(B, T, table.shape[1])
+    for name, t in (("table", table), ("start", start), ("count", count)):
+        if t is not None and (t.dtype != torch.int32 or t.device != dev or not t.is_contiguous()
+                              or (t is not table and tuple(t.shape) != (B,))):
+            raise ValueError(f"{name} must be a contiguous int32 tensor" + ("" if t is table else f" of shape [{B}]")
+                             + f" on {dev}")
+    return _lib.CacheRows(B, T, table.shape[1], _data(table), _data(start), _data(count))
+
+
+def cache_write(cache: TokenCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, start: torch.Tensor, *,
+                count: Optional[torch.Tensor] = None) -> None:
+    """fbev_cache_write: rows k, v [B,T,Hk,D] (fp32 or bf16) become the tokens start[b] .. start[b] + count[b] (T without
+    ``count``) of their sequences, whose pages ``table`` [B,W] names (all int32).  Padding and rows without a page are
+    dropped.  No token may be written twice in a call."""
+    dev = cache.device
+    _check_values("k", k, 4, dev)
+    _check_values("v", v, 4, dev, k.dtype)
+    B, T = k.shape[:2]
+    if v.shape != k.shape or k.shape[2] != cache.Hk or k.shape[3] != cache.D:
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must be [B, T, Hk={cache.Hk}, D={cache.D}]")
+    if cache.D > 1:
+        k = k if k.stride(3) == 1 else k.contiguous()
+        v = v if v.stride(3) == 1 else v.contiguous()
+    cr = _cache_rows(cache, table, start, count, B, T)
+    _call("fbev_cache_write", dev, cache.desc, cr, _data(k), _data(v), _DTYPES[k.dtype], _I64x3(*k.stride()[:3]),
+          _I64x3(*v.stride()[:3]))
+
+
+def cache_read(cache: TokenCache, table: torch.Tensor, start: torch.Tensor, T: int, *,
+               count: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16
+               ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """fbev_cache_read: (k, v) [B,T,Hk,D] of ``dtype``, what the codes of the tokens start[b] .. start[b] + T stand for; zeros
+    from count[b] on and where there is no page."""
+    if dtype not in _DTYPES:
+        raise ValueError(f"dtype must be float32 or bfloat16, got {dtype}")
+    dev, B = cache.device, table.shape[0]
+    cr = _cache_rows(cache, table, start, count, B, T)
+    k = torch.empty((B, T, cache.Hk, cache.D), dtype=dtype, device=dev)
+    v = torch.empty((B, T, cache.Hk, cache.D), dtype=dtype, device=dev)
+    _call("fbev_cache_read", dev, cache.desc, cr, _DTYPES[dtype], _data(k), _data(v))
+    return k, v
+
+
+# ---- attention over the cache
+
+@functools.lru_cache(maxsize=1024)
+def _cache_attention_scratch(B: int, T: int, W: int, Hq: int, Hk: int, D: int, dtype: int) -> int:
+    lib, need = _lib.load(), ctypes.c_size_t()
+    cd = _lib.CacheDesc(0, Hk, D, 0, None, None, None, None)
+    cr = _lib.CacheRows(B, T, W, 16, 16, None)            # not dereferenced
+    ad = _lib.CacheAttentionDesc(Hq, _lib.FBEV_DRAFT_NONE, 0, (0, 0, 0), None, 1.0, 0.0)
+    _lib.check(lib.fbev_cache_attention_workspace(cd, cr, ad, dtype, ctypes.byref(need)))
+    return need.value
+
+
+def tree_ancestors(parents: Sequence, *, device="cuda") -> torch.Tensor:
+    """The ``ancestors`` of cache_attention from each drafted token's parent among them (-1: none, it follows the cache):
+    [T] parents give [1, T, words], [B, T] give [B, T, words] (int64 bits).  A token sees its ancestors and itself."""
+    rows = parents.tolist() if torch.is_tensor(parents) else [list(p) if hasattr(p, "__len__") else p for p in parents]
+    if not rows or not isinstance(rows[0], list):
+        rows = [rows]
+    T = len(rows[0])
+    if any(len(r) != T for r in rows):
+        raise ValueError("every tree must have the same number of tokens")
+    words, out = max(1, -(-T // 64)), []
+    for r in rows:
+        masks = []
+        for j, p in enumerate(r):
+            if not -1 <= p < j:
+                raise ValueError(f"token {j} has parent {p}: a parent comes before its children (-1: none)")
+            masks.append((masks[p] if p >= 0 else 0) | 1 << j)
+        cut = [[m >> 64 * w & (1 << 64) - 1 for w in range(words)] for m in masks]
+        out.append([[x - (1 << 64) if x >> 63 else x for x in m] for m in cut])
+    return torch.tensor(out, dtype=torch.int64).reshape(len(rows), T, words).to(device)
+
+
+def cache_attention(q: torch.Tensor, cache: TokenCache, table: torch.Tensor, start: torch.Tensor, *,
+                    count: Optional[torch.Tensor] = None, ancestors: Optional[torch.Tensor] = None,
+                    drafted: bool = True, scale: Optional[float] = None, cap: Optional[float] = None,
+                    out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """fbev_cache_attention: queries q [B,T,Hq,D] (fp32 or bf16; Hq a multiple of the cache's Hk) over the tokens of their
+    sequences, out [B,T,Hq,D].
+
+    Every query sees the start[b] tokens of the cache.  The call's own tokens, written to the cache before as start[b] ..
+    start[b] + T, are seen up to the query's own (a prompt, a single token), or as ``ancestors`` [B or 1,T,words] int64 says: bit j % 64
+    of word j / 64 for token j (a tree of drafted tokens; see tree_ancestors), or not at all when not ``drafted``
+    (queries that are not tokens of the cache).  Tokens and queries from count[b] on are padding; they, and queries that
+    see nothing, get zeros.  ``scale``: 1 / sqrt(D) unless given; ``cap``: scores become cap tanh(score / cap) (0 or None:
+    no cap).  Forward only: the cache holds no gradients."""
+    dev = cache.device
+    _check_values("q", q, 4, dev)
+    B, T, Hq, D = q.shape
+    if D != cache.D:
+        raise ValueError(f"q {tuple(q.shape)} must have the cache's D={cache.D} channels")
+    _check_sizes(Hq)
+    if D > 1 and q.stride(3) != 1:
+        q = q.contiguous()
+    cr = _cache_rows(cache, table, start, count, B, T)
+    mode, words = (_lib.FBEV_DRAFT_CHAIN if drafted else _lib.FBEV_DRAFT_NONE), 0
+    if ancestors is not None:
+        if not drafted:
+            raise ValueError("ancestors come with drafted tokens")
+        if ancestors.dtype != torch.int64 or ancestors.device != dev or ancestors.dim() != 3 \
+                or ancestors.shape[0] not in (1, B) or ancestors.shape[1] != T or ancestors.shape[2] * 64 < T:
+            raise ValueError(f"ancestors must be an int64 tensor of shape [{B} or 1, {T}, words >= {-(-T // 64)}] on {dev}")
+        if ancestors.shape[0] != B:
+            ancestors = ancestors.expand(B, T, ancestors.shape[2])
+        ancestors = ancestors.contiguous()
+        mode, words = _lib.FBEV_DRAFT_TREE, ancestors.shape[2]
+    if out is None:
+        out = torch.empty((B, T, Hq, D), dtype=q.dtype, device=dev)
+    else:
+        _check_plain("out", out, q.shape, q.dtype, dev)
+        _check_apart("out", out, q, cache.k, cache.v, cache.k_scale, cache.v_scale, table, start, count, ancestors,
+                     workspace)
+    if scale is None:
+        scale = D ** -0.5 if D else 1.0
+    dt = _DTYPES[q.dtype]
+    ad = _lib.CacheAttentionDesc(Hq, mode, words, q.stride()[:3], _data(ancestors), scale, cap or 0.0)
+    workspace, have = _scratch(_cache_attention_scratch(B, T, cr.W, Hq, cache.Hk, D, dt), workspace, dev)
+    _call("fbev_cache_attention", dev, cache.desc, cr, ad, _data(q), dt, _data(out), _data(workspace), have)
+    return out

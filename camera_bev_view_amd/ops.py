@@ -470,3 +470,9 @@ def deform_backward(grad_out: torch.Tensor, features: torch.Tensor, K: torch.Ten
 from .encoder import (GroupNormAct, QueryAttention, RotaryAxes, attention_backward,  # noqa: E402,F401
                       attention_forward, group_norm_act, group_norm_backward, group_norm_forward,
                       query_attention, rotary_axes, rotary_backward, rotary_forward, rotary_freqs)
+
+
+# ---- decoder operators (root-mean-square norm, token cache in 8 bits, attention over it)
+
+from .decoder import (RmsNorm, TokenCache, cache_attention, cache_read, cache_write, rms_norm,  # noqa: E402,F401
+                      rms_norm_add, rms_norm_backward, rms_norm_codes, rms_norm_forward, token_cache, tree_ancestors)

@@ -46,7 +46,7 @@
 extern "C" {
 #endif
 
-#define FBEV_ABI_VERSION 9
+#define FBEV_ABI_VERSION 10
 #define FBEV_MAX_CAMERAS 64
 #define FBEV_MAX_GRID 65536
 #define FBEV_MAX_LEVELS 4
@@ -514,6 +514,160 @@ fbev_status fbev_attention_backward(const void* grad_out, const void* q, const v
                                     fbev_dtype dtype, const fbev_attention_desc* ad, const void* out,
                                     const float* stats, void* grad_q, void* grad_k, void* grad_v, float* grad_slope,
                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Decoder operators: what a decoder over a scene's tokens runs around its
+ * projections, from training to one drafted token at a time.  Tensors are fp32
+ * or bf16 (`dtype`); sums, statistics and softmax are fp32.  All of them are
+ * deterministic and allocate nothing; the work runs on `stream`, whose device
+ * must be the current one.
+ *
+ * Numbers in 8 bits: signed integers (int8, up to 127) or e4m3 (four
+ * significant bits, up to 448, no infinities).  Values that share a scale have
+ *
+ *   scale = max(max_j |x_j| / most, 2^-126)      (a quotient of fp32)
+ *   code  = the format's number nearest to x / scale, ties to the even one,
+ *
+ * decided on the exact quotient.  Where an x is infinite or NaN the scale is
+ * NaN and the codes are 0.  A code stands for code * scale.
+ */
+typedef enum { FBEV_CODES_INT8 = 0, FBEV_CODES_E4M3 = 1 } fbev_codes;
+
+/*
+ * Root-mean-square norm with the residual's addition: per row of C channels
+ *
+ *   h = x + residual (rounded once to dtype; without a residual h is x)
+ *   y = h w / sqrt(mean_c h^2 + eps)
+ *
+ *   x, residual : rows o < outer, i < inner at the given element strides,
+ *                 channels contiguous, any alignment; residual may be NULL.
+ *   weight      : [C] fp32 or NULL (ones).
+ *   y, h        : [rows, C] of dtype, contiguous, rows = outer inner; h is NULL
+ *                 without a residual.  h may be x or residual itself where that
+ *                 one is contiguous; no other output may share memory with the call's tensors.
+ *   rstd        : [rows] fp32, 1 / sqrt(mean h^2 + eps), what the backward needs; may be NULL.
+ *
+ * fbev_rms_norm_codes gives y in 8 bits instead (before any rounding to dtype):
+ *   out    : [rows, C] codes;  scales : [rows, ceil(C / block)] fp32, one for each
+ *            `block` channels (32, 64 or 128), or [rows, 1] with block 0 or >= C.
+ *
+ * The backward takes h (the forward's x without a residual, by x's strides),
+ * rstd, grad_y and grad_h (dL/dh from elsewhere, may be NULL), both [rows, C]
+ * contiguous of dtype, and gives grad_x (dL/dx and dL/dresidual are the same;
+ * contiguous, may be grad_y or grad_h) and grad_weight [C] fp32 (NULL skips it).
+ *   workspace : device scratch of the size the workspace call reports, 16-byte
+ *               aligned; not needed before or after the call, not shared by
+ *               calls that overlap; NULL is fine without grad_weight.
+ *
+ * C up to FBEV_MAX_RMS_CHANNELS; 0 rows are allowed (grad_weight is zero then).
+ */
+#define FBEV_MAX_RMS_CHANNELS 16384
+
+typedef struct {
+  int64_t outer, inner;
+  int64_t x_stride[2], residual_stride[2]; /* of outer and of inner rows, in elements */
+  int32_t C;
+  float eps;
+} fbev_rms_desc;
+
+fbev_status fbev_rms_norm_forward(const void* x, const void* residual, fbev_dtype dtype, const fbev_rms_desc* rd,
+                                  const float* weight, void* y, void* h, float* rstd, void* stream);
+fbev_status fbev_rms_norm_codes(const void* x, const void* residual, fbev_dtype dtype, const fbev_rms_desc* rd,
+                                const float* weight, fbev_codes codes, int32_t block, void* out, float* scales,
+                                void* h, void* stream);
+fbev_status fbev_rms_norm_workspace(const fbev_rms_desc* rd, fbev_dtype dtype, size_t* bytes);
+fbev_status fbev_rms_norm_backward(const void* grad_y, const void* grad_h, const void* h, fbev_dtype dtype,
+                                   const fbev_rms_desc* rd, const float* weight, const float* rstd, void* grad_x,
+                                   float* grad_weight, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Token cache: keys and values of many sequences in 8 bits, in pages of
+ * FBEV_CACHE_PAGE tokens that any sequence may hold in any order.
+ *
+ *   k       : [pages, Hk, 64, Dp] codes,  v : [pages, Hk, Dp, 64] codes (tokens
+ *             side by side), Dp = D rounded up to a multiple of 16, zeros behind D;
+ *             both 16-byte aligned.  1 <= D <= FBEV_MAX_HEAD_DIM.
+ *   k_scale, v_scale : [pages, Hk, 64] fp32, 16-byte aligned: one scale for each token and key head.
+ *
+ * A call's rows:
+ *   table   : [B, W] int32, page of the sequence's tokens 64 w .. 64 w + 63.
+ *   start   : [B] int32, the tokens the cache holds for the sequence; the call's
+ *             row t < T of sequence b is its token start[b] + t.
+ *   count   : [B] int32 or NULL (T for all): rows t >= count[b] are padding.
+ *
+ * Nothing outside the cache is touched whatever these hold: a page that is not
+ * in [0, pages) and tokens beyond 64 W do not exist, and a sequence with a
+ * negative start has no tokens and no rows.
+ *
+ * fbev_cache_write quantises the rows k, v [B, T, Hk, D] (by element strides of
+ * batch, token, head, channels contiguous, any alignment) into their tokens;
+ * rows that are padding or have no page are dropped, and what they would
+ * have replaced stays.  Two rows of one call must not be the same token of the same page
+ * (sequences may share pages that none of them writes).
+ *
+ * fbev_cache_read gives the values that the codes of the rows' tokens stand
+ * for, rounded once to dtype: k_out, v_out [B, T, Hk, D], contiguous, zeros for
+ * rows that are padding or have no page.  Either may be NULL.
+ */
+#define FBEV_CACHE_PAGE 64
+
+typedef struct {
+  int32_t pages, Hk, D;
+  int32_t codes; /* fbev_codes */
+  void *k, *v;
+  float *k_scale, *v_scale;
+} fbev_cache_desc;
+
+typedef struct {
+  int32_t B, T, W;
+  const int32_t *table, *start, *count;
+} fbev_cache_rows;
+
+fbev_status fbev_cache_write(const fbev_cache_desc* cd, const fbev_cache_rows* cr, const void* k, const void* v,
+                             fbev_dtype dtype, const int64_t k_stride[3], const int64_t v_stride[3], void* stream);
+fbev_status fbev_cache_read(const fbev_cache_desc* cd, const fbev_cache_rows* cr, fbev_dtype dtype, void* k_out,
+                            void* v_out, void* stream);
+
+/*
+ * Attention of T query tokens a sequence over the cache, for query head n of
+ * key head n / (Hq / Hk), with the values that the cache's codes stand for:
+ *
+ *   s = scale q_i . k_j,   s = cap tanh(s / cap) when cap > 0,
+ *   o_i = sum_j softmax_j(s) v_j  over the tokens i sees.
+ *
+ * Every query sees the start[b] tokens of its sequence, and of the call's own
+ * rows, which are in the cache too (written before), `drafts` says which:
+ *   FBEV_DRAFT_NONE  : none (queries that are not tokens of the cache).
+ *   FBEV_DRAFT_CHAIN : those up to itself: a prompt, a single new token.
+ *   FBEV_DRAFT_TREE  : row j where bit j % 64 of ancestors[b, i, j / 64] is set
+ *                      (its own bit is up to the caller): several drafted continuations at once.
+ * With `count`, rows t >= count[b] are padding: nobody sees them and they get
+ * zeros, as does a query that sees no token.  What unseen tokens hold, NaN
+ * among it, reaches no query.
+ *
+ *   q   : [B, T, Hq, D] by element strides, channels contiguous, any alignment.
+ *   ancestors : [B, T, words] uint64, words >= ceil(T / 64); NULL without a tree.
+ *   scale, cap : as for fbev_attention_forward.
+ *   out : [B, T, Hq, D] of dtype, contiguous, on memory of its own.
+ *   workspace : as above; few queries over many tokens are split along the
+ *               tokens and joined from there.
+ */
+typedef enum { FBEV_DRAFT_NONE = 0, FBEV_DRAFT_CHAIN = 1, FBEV_DRAFT_TREE = 2 } fbev_drafts;
+
+typedef struct {
+  int32_t Hq;
+  int32_t drafts; /* fbev_drafts */
+  int32_t words;
+  int64_t q_stride[3];
+  const uint64_t* ancestors;
+  float scale, cap;
+} fbev_cache_attention_desc;
+
+fbev_status fbev_cache_attention_workspace(const fbev_cache_desc* cd, const fbev_cache_rows* cr,
+                                           const fbev_cache_attention_desc* ad, fbev_dtype dtype, size_t* bytes);
+fbev_status fbev_cache_attention(const fbev_cache_desc* cd, const fbev_cache_rows* cr,
+                                 const fbev_cache_attention_desc* ad, const void* q, fbev_dtype dtype, void* out,
+                                 void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static text for a status code. */
 const char* fbev_status_string(fbev_status s);

@@ -1,0 +1,288 @@
+"""GPU: rows into the token cache and back, bit for bit against the oracle."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.decoder as dec
+from camera_bev_view_amd import ops
+from decoder_bounds import HALF, KINDS, f64
+from gpu_helpers import say
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def draw(seed, *shape, dtype=F32):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(shape, generator=g).to(dtype).cuda()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def both(pages, Hk, D, kind, seed=7):
+    """A cache full of old bytes and its model (e4m3's NaN codes among them, as in memory never written)."""
+    rng = np.random.default_rng(seed)
+    model = dec.Cache(pages, Hk, D, kind)
+    for a in (model.k, model.v):
+        a[...] = rng.integers(0, 256, a.shape, dtype=np.uint8)
+    for a in (model.k_scale, model.v_scale):
+        a[...] = rng.normal(size=a.shape)
+    up = lambda a: torch.from_numpy(a.copy()).cuda()
+    cache = ops.TokenCache(up(model.k).view(KINDS[kind]), up(model.v).view(KINDS[kind]), up(model.k_scale),
+                           up(model.v_scale), D)
+    return cache, model
+
+
+def same_state(cache, model):
+    for name in ("k", "v", "k_scale", "v_scale"):
+        got = getattr(cache, name)
+        got = got.view(torch.uint8) if name in "kv" else got
+        got, want = got.cpu().numpy(), getattr(model, name)
+        assert np.array_equal(got, want, equal_nan=name not in "kv"), \
+            f"{name}: {int((got != want).sum())} differ, first at {np.argwhere(got != want)[:1].tolist()}"
+
+
+def same_read(cache, model, table, start, T, count, dtype):
+    k, v = ops.cache_read(cache, i32(table), i32(start), T, count=None if count is None else i32(count), dtype=dtype)
+    for name, got, want in (("k", k, 0), ("v", v, 1)):
+        want = model.read(np.array(table).reshape(len(start), -1), start, T, count)[want]
+        # code * scale has 31 bits: one rounding to fp32, one more to bf16
+        rounded = torch.from_numpy(want.astype(np.float32)).to(dtype)
+        assert torch.equal(got.cpu(), rounded) or torch.equal(got.cpu().isnan(), rounded.isnan()) and \
+            torch.equal(got.cpu().nan_to_num(), rounded.nan_to_num()), name
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [1, 7, 16, 17, 32, 40, 64, 80, 127, 128])
+def test_widths(D, dtype, kind):
+    say(f"[case] cache D={D} {dtype} {kind}")
+    cache, model = both(7, 3, D, kind)
+    table = [[5, 0, 3], [2, 6, 1]]
+    k, v = draw(D, 2, 90, 3, D, dtype=dtype), draw(D + 1, 2, 90, 3, D, dtype=dtype)
+    ops.cache_write(cache, k, v, i32(table), i32([0, 61]))
+    model.write(f64(k), f64(v), table, [0, 61])
+    same_state(cache, model)
+    same_read(cache, model, table, [0, 61], 90, None, dtype)
+    same_read(cache, model, table, [0, 61], 90, [90, 13], F32)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("T", [1, 2, 3, 5, 63, 64, 65, 129])
+@pytest.mark.parametrize("start", [0, 1, 62, 63, 64, 100])
+def test_lengths_and_places(T, start, kind):
+    cache, model = both(6, 2, 48, kind)
+    table = [[4, 1, 0, 5]]
+    k, v = draw(T, 1, T, 2, 48, dtype=BF16), draw(T + 1, 1, T, 2, 48, dtype=BF16)
+    ops.cache_write(cache, k, v, i32(table), i32([start]))
+    model.write(f64(k), f64(v), table, [start])
+    same_state(cache, model)
+    same_read(cache, model, table, [start], T, None, BF16)
+
+
+def test_what_is_dropped():
+    """Padding, pages that do not exist, tokens beyond the table, negative starts: nothing else is touched."""
+    for T in (1, 2, 70):
+        for kind in ("int8", "e4m3"):
+            cache, model = both(5, 2, 32, kind)
+            table = [[0, -1, 1], [5, 2, 99], [3, 4, 3], [4, 4, 4], [-2 ** 31, 2 ** 31 - 1, 0], [1, 1, 1]]
+            start = [50, 60, 191, -1, 10, 2 ** 31 - 1]
+            count = [T, T - 1, T, T, 5, 2 ** 31 - 1]
+            k, v = draw(1, 6, T, 2, 32), draw(2, 6, T, 2, 32)
+            ops.cache_write(cache, k, v, i32(table), i32(start), count=i32(count))
+            model.write(f64(k), f64(v), np.array(table), start, count)
+            same_state(cache, model)
+            same_read(cache, model, table, start, T, count, F32)
+            ops.cache_write(cache, k, v, i32(table), i32(start), count=i32([0, -5, -2 ** 31, 0, 0, 0]))
+            same_state(cache, model)
+
+
+def test_borders_between_codes():
+    """Quotients on a border go to the even code, one step of the type beside it to the nearer one; scales of every size."""
+    for kind in ("int8", "e4m3"):
+        n = dec.numbers(kind)[:127]
+        mid = ((n[:-1] + n[1:]) / 2).astype(np.float32)
+        around = np.stack([mid, np.nextafter(mid, np.float32(0)), np.nextafter(mid, np.float32(1e9)), -mid]).reshape(-1)
+        rows = []
+        for power in (-126, -100, -60, -59, 0, 1, 60, 100, 118):
+            x = np.pad(around, (0, -len(around) % 62)).reshape(-1, 62)
+            x = np.concatenate([x, np.full((len(x), 1), dec.MOST[kind], np.float32), -x[:, :1]], axis=1)
+            with np.errstate(under="ignore"):
+                rows.append((x.astype(np.float64) * 2.0 ** power).astype(np.float32))
+        # scales that are no powers of two: products of a border and a scale, rounded, and their neighbours
+        rng = np.random.default_rng(3)
+        for _ in range(40):
+            top = np.float32(rng.uniform(0.5, 900.0))
+            scale = np.float32(top / np.float32(dec.MOST[kind]))
+            x = (mid.astype(np.float64) * scale).astype(np.float32)
+            x = np.concatenate([x, np.nextafter(x, np.float32(0)), np.nextafter(x, np.float32(1e9))])
+            x = np.pad(np.minimum(x, top), (0, -len(x) % 63)).reshape(-1, 63)
+            rows.append(np.concatenate([x, np.full((len(x), 1), top, np.float32)], axis=1))
+        x = np.concatenate(rows)
+        say(f"[case] {len(x)} rows of borders, {kind}")
+        T = len(x)
+        pages = -(-T // 64)
+        cache, model = both(pages, 1, 64, kind)
+        k = torch.from_numpy(x).view(1, T, 1, 64).cuda()
+        v = torch.from_numpy(x[::-1].copy()).view(1, T, 1, 64).cuda()
+        table = [list(range(pages))]
+        ops.cache_write(cache, k, v, i32(table), i32([0]))
+        model.write(x.reshape(1, T, 1, 64), x[::-1].reshape(1, T, 1, 64), table, [0])
+        same_state(cache, model)
+        same_read(cache, model, table, [0], T, None, F32)
+
+
+def test_odd_values():
+    x = np.zeros((1, 12, 1, 16), np.float32)
+    x[0, 1, 0, 3] = np.nan
+    x[0, 2, 0, 15] = np.inf
+    x[0, 3, 0, 0] = -np.inf
+    x[0, 4] = 3.0e38
+    x[0, 5, 0, 2] = 1e-45
+    x[0, 6] = -2.0 ** -126
+    x[0, 7, 0, 1] = 2.0 ** -119
+    x[0, 8] = -0.0
+    x[0, 9, 0, ::2] = 3.4e38
+    for kind in ("int8", "e4m3"):
+        cache, model = both(2, 1, 16, kind)
+        t = torch.from_numpy(x).cuda()
+        ops.cache_write(cache, t, t, i32([[1]]), i32([5]))
+        model.write(x, x, [[1]], [5])
+        # a zero's sign is no part of what a code stands for
+        for name in ("k", "v"):
+            got = getattr(cache, name)
+            raw = got.view(torch.uint8)
+            if kind == "e4m3":
+                raw[raw == 128] = 0
+                a = getattr(model, name)
+                a[a == 128] = 0
+        same_state(cache, model)
+        k, v = ops.cache_read(cache, i32([[1]]), i32([5]), 12, dtype=F32)
+        for got in (k, v):
+            assert got[0, 1:4].isnan().all() and got[0, 4:].isfinite().all() and (got[0, 0] == 0).all()
+
+
+def test_views_and_addresses():
+    cache, model = both(6, 2, 24, "int8")
+    table = [[0, 1], [2, 3], [4, 5]]
+    packed = draw(1, 3, 50, 3, 2, 24, dtype=BF16)
+    k, v = packed[:, :, 1], packed[:, :, 2]
+    ops.cache_write(cache, k, v, i32(table), i32([3, 40, 70]))
+    model.write(f64(k), f64(v), table, [3, 40, 70])
+    same_state(cache, model)
+    flat = draw(2, 3 * 50 * 2 * 24 + 1)
+    k = flat[1:].view(3, 50, 2, 24)
+    v = flat[:-1].view(3, 2, 50, 24).transpose(1, 2)
+    ops.cache_write(cache, k, v, i32(table), i32([0, 0, 0]))
+    model.write(f64(k), f64(v), table, [0, 0, 0])
+    same_state(cache, model)
+    row = draw(3, 1, 1, 2, 24)
+    k, v = row.expand(3, 50, 2, 24), draw(4, 24, 2, 50, 3).permute(3, 2, 1, 0)
+    ops.cache_write(cache, k, v, i32(table), i32([7, 8, 9]))
+    model.write(f64(k), f64(v), table, [7, 8, 9])
+    same_state(cache, model)
+
+
+def test_shared_pages_and_new_caches():
+    cache = ops.token_cache(3, 2, 40, codes=torch.int8)
+    assert cache.k.shape == (3, 2, 64, 48) and cache.v.shape == (3, 2, 48, 64) and not cache.k.any()
+    k, v = draw(1, 1, 64, 2, 40), draw(2, 1, 64, 2, 40)
+    ops.cache_write(cache, k, v, i32([[2]]), i32([0]))
+    # two sequences that share the first page and go on in their own
+    k2, v2 = draw(3, 2, 4, 2, 40), draw(4, 2, 4, 2, 40)
+    ops.cache_write(cache, k2, v2, i32([[2, 0], [2, 1]]), i32([64, 64]))
+    rk, _ = ops.cache_read(cache, i32([[2, 0], [2, 1]]), i32([0, 0]), 68, dtype=F32)
+    assert torch.equal(rk[0, :64], rk[1, :64]) and not torch.equal(rk[0, 64:], rk[1, 64:])
+    step = k2.abs().amax(-1, keepdim=True) / 127
+    assert ((rk[:, 64:] - k2).abs() <= step * 0.5001).all()
+
+
+def test_offsets_beyond_31_bits():
+    pages, Hk, D = 33000, 8, 128
+    say(f"[case] cache of {pages} pages, {pages * Hk * 64 * D} bytes a side")
+    cache = ops.token_cache(pages, Hk, D, codes=torch.int8)
+    k, v = draw(1, 2, 65, Hk, D, dtype=BF16), draw(2, 2, 65, Hk, D, dtype=BF16)
+    small = ops.token_cache(4, Hk, D, codes=torch.int8)
+    ops.cache_write(cache, k, v, i32([[32999, 5], [32768, 32767]]), i32([0, 3]))
+    ops.cache_write(small, k, v, i32([[3, 0], [2, 1]]), i32([0, 3]))
+    for a, b in ((32999, 3), (5, 0), (32768, 2), (32767, 1)):
+        for name in ("k", "v", "k_scale", "v_scale"):
+            assert torch.equal(getattr(cache, name)[a], getattr(small, name)[b]), (a, name)
+    got = ops.cache_read(cache, i32([[32999, 5], [32768, 32767]]), i32([0, 3]), 65)
+    want = ops.cache_read(small, i32([[3, 0], [2, 1]]), i32([0, 3]), 65)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert not cache.k[6:32767].any() and not cache.v[:5].any()
+
+
+def test_empty_calls():
+    cache = ops.token_cache(2, 1, 16)
+    none = torch.empty((0, 3, 1, 16), device="cuda")
+    ops.cache_write(cache, none, none, i32([]).view(0, 2), i32([]))
+    none = torch.empty((2, 0, 1, 16), device="cuda")
+    ops.cache_write(cache, none, none, i32([[0], [1]]), i32([0, 0]))
+    k, v = ops.cache_read(cache, i32([[0], [1]]), i32([0, 0]), 0)
+    assert k.shape == (2, 0, 1, 16)
+    some = draw(1, 2, 3, 1, 16)
+    ops.cache_write(cache, some, some, i32([]).view(2, 0), i32([0, 0]))
+    k, v = ops.cache_read(cache, i32([]).view(2, 0), i32([0, 0]), 3)
+    assert not k.any() and not v.any() and not cache.k.view(torch.uint8).any()
+    empty = ops.token_cache(0, 1, 16)
+    ops.cache_write(empty, some, some, i32([[0], [1]]), i32([0, 0]))
+    k, v = ops.cache_read(empty, i32([[0], [1]]), i32([0, 0]), 3)
+    assert not k.any() and not v.any()
+
+
+def test_refusals():
+    cache = ops.token_cache(2, 2, 16)
+    k, table, start = draw(1, 1, 3, 2, 16), i32([[0, 1]]), i32([0])
+    for bad in (dict(k=k[:, :, :1]), dict(v=k.to(BF16)), dict(k=k.half(), v=k.half()), dict(table=table.long()),
+                dict(start=start.long()), dict(start=i32([0, 0])), dict(count=i32([1, 1])), dict(table=i32([0, 1])),
+                dict(table=i32([[0, 1], [0, 1]])), dict(k=k.cpu()), dict(table=i32([[0, 1, 0, 1]])[:, ::2])):
+        with pytest.raises(ValueError):
+            ops.cache_write(cache, **{**dict(k=k, v=k, table=table, start=start), **bad})
+    with pytest.raises(ValueError):
+        ops.cache_read(cache, table, start, 3, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        ops.TokenCache(cache.k, cache.v, cache.k_scale, cache.v_scale, 17)
+    with pytest.raises(ValueError):
+        ops.TokenCache(cache.k, cache.v.view(torch.int8), cache.k_scale, cache.v_scale, 16)
+    with pytest.raises(ValueError):
+        ops.TokenCache(cache.k, cache.v, cache.k_scale.double(), cache.v_scale, 16)
+
+
+def test_graph_replays_and_streams():
+    cache = ops.token_cache(8, 2, 64, codes=torch.int8)
+    table, start = i32([[0, 1, 2], [3, 4, 5]]), i32([10, 70])
+    k, v = draw(1, 2, 1, 2, 64, dtype=BF16), draw(2, 2, 1, 2, 64, dtype=BF16)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        ops.cache_write(cache, k, v, table, start)
+        first = ops.cache_read(cache, table, start, 1)
+    torch.cuda.current_stream().wait_stream(side)
+    again = ops.cache_read(cache, table, start, 1)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ops.cache_write(cache, k, v, table, start)
+        start.add_(1)
+    steps = []
+    for i in range(5):
+        k.copy_(draw(10 + i, 2, 1, 2, 64, dtype=BF16))
+        v.copy_(draw(20 + i, 2, 1, 2, 64, dtype=BF16))
+        steps.append((k.clone(), v.clone()))
+        graph.replay()
+        torch.cuda.synchronize()
+    assert start.tolist() == [15, 75]
+    other = ops.token_cache(8, 2, 64, codes=torch.int8)
+    ops.cache_write(other, torch.cat([s[0] for s in steps], 1), torch.cat([s[1] for s in steps], 1), table, i32([10, 70]))
+    for a, b in zip(ops.cache_read(cache, table, i32([10, 70]), 5), ops.cache_read(other, table, i32([10, 70]), 5)):
+        assert torch.equal(a, b)
