@@ -7,17 +7,18 @@
 // exact in bf16 goes in as parts: fp32 queries and weights as three (24 bits), the weights of bf16 tensors as two (16 bits:
 // one would add as much error as the result's own rounding), bf16 queries as they are.
 //
-// Memory bounds the calls of serving (few rows over a long cache): the cache's codes are read once and straight into the
-// registers that feed the matrix instructions, with no turn through LDS.  A wave takes a page of 64 tokens at a time, both
-// products with the tokens (or channels) as the instruction's rows and 16 queries as its columns:
-//   S^T = K Q^T:  lane (r, g) of r = lane mod 16, g = lane / 16 loads 16 bytes (channels 16 g ..) of token 16 (r / 4) + 4 u + r mod 4,
+// Both products have the tokens (or channels) as the matrix instruction's rows and 16 queries (times heads of a key head, a
+// row tile) as its columns, a page of 64 tokens at a time:
+//   S^T = K Q^T:  lane (r, g) of r = lane mod 16, g = lane / 16 takes 16 codes (channels 16 g ..) of token 16 (r / 4) + 4 u + r mod 4,
 //                 u = 0 .. 3, so that the result leaves it the scores of tokens 16 g .. 16 g + 15 of query r;
 //   O^T = V^T P^T: those 16 weights are its operand as they stand, and the values, kept with their tokens side by side, are
-//                 16 bytes (tokens 16 g ..) of channel r.
-// A page's keys are loaded while the one before is in its softmax and second product, its values under the first one.
-// The waves of a workgroup share the rows and take pages in turn; where rows are few, the pages are split over workgroups
-// as well and a second launch joins them.  Row tiles (16 queries times heads of a key head) are held RT at a time: each
-// code is read and converted once for all of them.
+//                 16 codes (tokens 16 g ..) of channel r.
+//
+// Two forms.  Up to one row tile (serving) memory bounds the call: every wave takes pages of its own, straight into the
+// registers that feed the matrix instructions, a page's keys while the one before is in its softmax and second product,
+// its values under the first one.  With more row tiles the arithmetic does: the waves of a workgroup hold row tiles of their
+// own and share every page, which they widen to bf16 once, a quarter each, into LDS, one page ahead.  Few rows over many pages
+// are split over workgroups as well, and a second launch joins them.
 #include <hip/hip_runtime.h>
 
 #include "attention_core.h"
@@ -29,7 +30,7 @@
 namespace fbev {
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kMostSplits = 512;
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -142,351 +143,642 @@ __device__ __forceinline__ float share(float m, float l, float top) {
 }
 
 // DC: channels held, 32, 64 or 128.
-template <typename T, int KIND, int DC, int RT>
+template <typename T, int DC>
 struct Shape {
   static constexpr int kQ = sizeof(T) == 4 ? 3 : 1;     // parts of a query
   static constexpr int kP = sizeof(T) == 4 ? 3 : 2;     // parts of a weight
   static constexpr int kSteps = DC / 32;                // of the first product
-  static constexpr int kChunk = DC >= 64 ? 16 : 8;      // bytes a lane loads of a key
+  static constexpr int kChunk = DC >= 64 ? 16 : 8;      // bytes a lane takes of a key at a time
   static constexpr int kChunks = DC >= 64 ? DC / 64 : 1;
   static constexpr int kTiles = DC / 16;                // of the second product's rows
-  static constexpr int kQBytes = RT * kSteps * kQ * 64 * 16;
   static constexpr int kRow = DC + 4;                   // floats of a row in the join
-  static constexpr int kJoinBytes = kWaves * 16 * kRow * 4;
-  static constexpr int kLds = kQBytes > kJoinBytes ? kQBytes : kJoinBytes;
 };
 
-template <typename T, int KIND, int DC, int RT>
-__global__ __launch_bounds__(64 * kWaves) void cache_attn(CacheAttnArgs a) {
-  using Sh = Shape<T, KIND, DC, RT>;
-  __shared__ alignas(16) char lds[Sh::kLds];
-  __shared__ float2 joined[kWaves][16 * RT];
+// A call's rows of one sequence and key head, as a workgroup sees them.
+struct Part {
+  int b, hk, bh, split;
+  int row0;               // first row
+  int start, rows;        // tokens in the cache; rows that are no padding
+  int end;                // tokens that any of the workgroup's rows sees
+  int p0, p1;             // its pages
+};
+
+__device__ __forceinline__ Part find_part(const CacheAttnArgs& a, int rows_held) {
   const CacheArgs& c = a.c;
-  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
-  const int r16 = lane & 15, g = lane >> 4;
-  const int heads = c.B * c.Hk;
+  Part p;
   int id = xcd_block(blockIdx.x, gridDim.x);
   const int rb = id % a.row_blocks;
   id /= a.row_blocks;
-  const int part = id % a.splits, bh = id / a.splits;
-  const int b = bh / c.Hk, hk = bh % c.Hk;
-  const int row0 = rb * 16 * RT;
+  p.split = id % a.splits;
+  p.bh = id / a.splits;
+  p.b = p.bh / c.Hk;
+  p.hk = p.bh % c.Hk;
+  p.row0 = (a.row_blocks - 1 - rb) * rows_held;         // the last rows see most: they begin first
+  p.start = min(c.start[p.b], c.W * kPage);             // (what lies beyond the table does not exist)
+  p.rows = p.start < 0 ? 0 : min(c.count ? max(c.count[p.b], 0) : c.T, c.T);
+  const int last_t = (min(p.row0 + rows_held, a.R) - 1) / a.G;
+  p.end = p.rows > 0 ? (int)visible_end(a, p.start, p.rows, last_t) : 0;
+  const int pages = (p.end + kPage - 1) / kPage;
+  p.p0 = (int)((int64_t)pages * p.split / a.splits);
+  p.p1 = (int)((int64_t)pages * (p.split + 1) / a.splits);
+  return p;
+}
 
-  // queries as the first product's columns: channel 64 c + 16 g + 8 h + j of step 2 c + h (8 g + j where one step is all)
-#pragma unroll
-  for (int i = 0; i < RT * Sh::kSteps / kWaves + (RT * Sh::kSteps % kWaves ? 1 : 0); ++i) {
-    const int item = i * kWaves + wave;
-    if (item < RT * Sh::kSteps) {
-      const int rt = item / Sh::kSteps, step = item % Sh::kSteps;
-      const int row = row0 + rt * 16 + r16, t = row / a.G, h = row - t * a.G;
-      const int ch = Sh::kChunk == 16 ? (step >> 1) * 64 + g * 16 + (step & 1) * 8 : g * 8;
-      const int left = row < a.R ? c.D - ch : 0;
-      const T* q = (const T*)a.q + b * a.qs[0] + (int64_t)t * a.qs[1] + (int64_t)(hk * a.G + h) * a.qs[2] + ch;
-      float x[8];
-      if (left >= 8) {
-        T e[8];
-        __builtin_memcpy(e, q, sizeof e);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = (float)e[j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = j < left ? (float)q[j] : 0.0f;
+// Walks the pages p0, p0 + STEP, .. of a part that exist.  A wave reads 64 of the table's entries at a time: one entry a page
+// would put a whole memory latency in front of each page's loads.
+template <int STEP>
+struct Walk {
+  const int32_t* table;
+  int end, pages;
+  int at, page = 0;       // the current page's place in the sequence (end: none) and its number
+  int first, ids;         // lane i: table[first + STEP i]
+
+  __device__ __forceinline__ Walk(const CacheArgs& c, const Part& p, int from)
+      : table(c.table + (int64_t)p.b * c.W), end(p.p1), pages(c.pages), at(from - STEP), first(from) {
+    fetch();
+    next();
+  }
+  __device__ __forceinline__ void fetch() {
+    const int i = first + STEP * ((int)threadIdx.x & 63);
+    ids = i < end ? table[i] : -1;
+  }
+  __device__ __forceinline__ void next() {
+    for (at += STEP; at < end; at += STEP) {
+      if (at >= first + 64 * STEP) {
+        first = at;
+        fetch();
       }
-      bf16x8 parts[Sh::kQ];
-      split<Sh::kQ>(x, parts);
-#pragma unroll
-      for (int p = 0; p < Sh::kQ; ++p) ((bf16x8*)lds)[(item * Sh::kQ + p) * 64 + lane] = parts[p];
+      page = __builtin_amdgcn_readlane(ids, (at - first) / STEP);
+      if (page >= 0 && page < pages) return;
     }
+    at = end;
+  }
+  __device__ __forceinline__ bool there() const { return at < end; }
+};
+
+// A row tile's queries as the first product's columns: step 2 c + h of lane group g has channels 64 c + 16 g + 8 h ..
+// (8 g .. where one step is all).
+template <typename T, int DC>
+__device__ __forceinline__ void load_queries(const CacheAttnArgs& a, const Part& p, int row, int step, int g,
+                                             bf16x8 (&parts)[Shape<T, DC>::kQ]) {
+  using Sh = Shape<T, DC>;
+  const int t = row / a.G, h = row - t * a.G;
+  const int ch = Sh::kChunk == 16 ? (step >> 1) * 64 + g * 16 + (step & 1) * 8 : g * 8;
+  const int left = row < a.R ? a.c.D - ch : 0;
+  const T* q = (const T*)a.q + p.b * a.qs[0] + (int64_t)t * a.qs[1] + (int64_t)(p.hk * a.G + h) * a.qs[2] + ch;
+  float x[8];
+  if (left >= 8) {
+    T e[8];
+    __builtin_memcpy(e, q, sizeof e);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = (float)e[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = j < left ? (float)q[j] : 0.0f;
+  }
+  split<Sh::kQ>(x, parts);
+}
+
+// A page's codes and scales of one key head, as buffers: what lies outside reads as zero, all of it where there is no
+// page.  So loads need no branches, whose joins would make the compiler wait for them on the spot.
+struct Page {
+  __amdgpu_buffer_rsrc_t k, v, ks, vs;
+};
+
+constexpr int kNowhere = 0x7fffff00;                    // an offset outside every page
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00020000);
+}
+
+__device__ __forceinline__ Page find_page(const CacheArgs& c, int hk, int page, bool there) {
+  const int64_t at = there ? (int64_t)page * c.Hk + hk : 0;
+  const int codes = there ? kPage * c.Dp : 0, scales = there ? kPage * 4 : 0;
+  Page p;
+  p.k = buffer_of((const uint8_t*)c.k + at * kPage * c.Dp, codes);
+  p.v = buffer_of((const uint8_t*)c.v + at * kPage * c.Dp, codes);
+  p.ks = buffer_of(c.k_scale + at * kPage, scales);
+  p.vs = buffer_of(c.v_scale + at * kPage, scales);
+  return p;
+}
+
+// Key codes of the token 16 (r / 4) + 4 u + r mod 4 of a page, channels 64 i + 16 g .. (8 g .. where eight are a lane's).
+template <typename Sh>
+__device__ __forceinline__ void load_key(const CacheArgs& c, const Page& p, int r16, int g, int u, int i,
+                                         uint32_t (&kw)[4]) {
+  const int ch = 64 * i + Sh::kChunk * g;
+  const int at = ch < c.Dp && u < 4 ? (16 * (r16 >> 2) + (r16 & 3) + 4 * u) * c.Dp + ch : kNowhere;
+  if constexpr (Sh::kChunk == 16) {
+    const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(p.k, at, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) kw[j] = x[j];
+  } else {
+    const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(p.k, at, 0, 0);
+    kw[0] = x[0];
+    kw[1] = x[1];
+  }
+}
+
+// Value codes of channel 16 i + r, tokens 16 g .. 16 g + 15.
+__device__ __forceinline__ void load_value(const Page& p, int r16, int g, int i, uint32_t (&vw)[4]) {
+  const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(p.v, (16 * i + r16) * kPage + 16 * g, 0, 0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) vw[j] = x[j];
+}
+
+// Scales of the tokens 16 g .. 16 g + 15.
+__device__ __forceinline__ void load_scales(__amdgpu_buffer_rsrc_t p, int g, float (&x)[16]) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const u32x4 w = __builtin_amdgcn_raw_buffer_load_b128(p, 64 * g + 16 * u, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[4 * u + j] = __builtin_bit_cast(float, (uint32_t)w[j]);
+  }
+}
+
+// Clears the codes behind the first `left` of 16: what was never written may be the code of a NaN.
+template <int KIND>
+__device__ __forceinline__ void keep_codes(uint32_t (&w)[4], int left) {
+  if constexpr (KIND != FBEV_CODES_E4M3) return;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int n = min(max(left - 4 * j, 0), 4);
+    w[j] &= n == 4 ? ~0u : (1u << (8 * n)) - 1u;
+  }
+}
+
+// Scores to weights for one row tile and page; m, l, o: the row's running maximum, this lane's share of the sum of
+// weights, and the sums.  `s` in base-2 units with the scale in it (or, with a cap, divided by the cap); it becomes the
+// values' weights.
+template <int TILES>
+__device__ __forceinline__ void weigh(float (&s)[16], const float (&vs)[16], bool masked, uint32_t bits, float cap,
+                                      float& m, float& l, f32x4 (&o)[TILES]) {
+  if (cap > 0) {
+    const float top = cap * kLog2e;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = top * tanh_fast<true>(s[i]);
+  }
+  if (masked) {
+    const uint32_t seen = opaque(bits);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (!(seen >> i & 1)) s[i] = kNegInf;
+  }
+  float top = s[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+  top = query_max(top);
+  // the maximum moves where it grows by 2^8 or more: weights stay below that, and sums in fp32 do not mind
+  if (__any(top > m + 8.0f)) {
+    const float to = top > m + 8.0f ? top : m;
+    const float less = to == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+    m = to;
+    l *= less;
+#pragma unroll
+    for (int i = 0; i < TILES; ++i) o[i] *= less;
+  }
+  const float base = m == kNegInf ? 0.0f : m;
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float p = __builtin_amdgcn_exp2f(s[i] - base);
+    sum += p;
+    s[i] = p * vs[i];
+  }
+  l += sum;
+  if (masked) {                                         // an unseen token's scale may be anything
+    const uint32_t seen = opaque(bits);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (!(seen >> i & 1)) s[i] = 0.0f;
+  }
+}
+
+// The weights of eight tokens in parts.
+template <int KP>
+__device__ __forceinline__ void split_weights(const float* w, bf16x8 (&parts)[KP]) {
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = w[i];
+  split<KP>(x, parts);
+}
+
+// Eight neighbouring channels (from 8 `lane` on, 16 lanes a row) of a row's results from what N sums hold of it: sums[w] + 8
+// lane, their maxima and sums of weights in ml.
+template <typename T, int N>
+__device__ __forceinline__ void finish_row(const CacheAttnArgs& a, const Part& p, int row, const float2 (&ml)[N],
+                                           const float* const (&sums)[N], int lane) {
+  const CacheArgs& c = a.c;
+  const int t = row / a.G, h = row - t * a.G;
+  const bool seen = t < p.rows;                         // padding sees nothing
+  float top = kNegInf;
+#pragma unroll
+  for (int w = 0; w < N; ++w) top = fmaxf(top, seen ? ml[w].x : kNegInf);
+  float total = 0.0f, x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  const int ch = 8 * lane, left = c.D - ch;
+  if (left <= 0) return;
+#pragma unroll
+  for (int w = 0; w < N; ++w) {
+    const float f = seen ? share(ml[w].x, ml[w].y, top) : 0.0f;
+    if (f == 0.0f) continue;
+    total += f * ml[w].y;
+    const f32x4 lo = *(const f32x4*)(sums[w] + ch), hi = *(const f32x4*)(sums[w] + ch + 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] += f * (i < 4 ? lo[i] : hi[i - 4]);
+  }
+  if (a.splits == 1) {
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    T* out = (T*)a.out + (((int64_t)p.b * c.T + t) * a.Hq + p.hk * a.G + h) * c.D + ch;
+    T y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = (T)(x[i] * inv);
+    if (left >= 8) {
+      __builtin_memcpy(out, y, sizeof y);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < left) out[i] = y[i];
+    }
+  } else {
+    float* keep = a.part + (((int64_t)p.split * c.B * c.Hk + p.bh) * a.R + row) * (c.D + 2);
+    if (left >= 8) {
+      __builtin_memcpy(keep + ch, x, sizeof x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < left) keep[ch + i] = x[i];
+    }
+    if (lane == 0) {
+      keep[c.D] = top;
+      keep[c.D + 1] = total;
+    }
+  }
+}
+
+// Up to 16 rows: every wave has pages of its own.
+template <typename T, int KIND, int DC, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void cache_attn_few(CacheAttnArgs a) {
+  using Sh = Shape<T, DC>;
+  constexpr int kQBytes = Sh::kSteps * Sh::kQ * 64 * 16, kSumBytes = WAVES * 16 * Sh::kRow * 4;
+  __shared__ alignas(16) char lds[kQBytes > kSumBytes ? kQBytes : kSumBytes];
+  __shared__ float2 joined[WAVES][16];
+  const CacheArgs& c = a.c;
+  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
+  const int r16 = lane & 15, g = lane >> 4;
+  const Part p = find_part(a, 16);
+  if (wave < Sh::kSteps) {
+    bf16x8 parts[Sh::kQ];
+    load_queries<T, DC>(a, p, p.row0 + r16, wave, g, parts);
+#pragma unroll
+    for (int i = 0; i < Sh::kQ; ++i) ((bf16x8*)lds)[(wave * Sh::kQ + i) * 64 + lane] = parts[i];
   }
   __syncthreads();
 
-  const int start = min(c.start[b], c.W * kPage);       // (what lies beyond the table does not exist)
-  const int rows = start < 0 ? 0 : min(c.count ? max(c.count[b], 0) : c.T, c.T);
-  const int last_t = (min(row0 + 16 * RT, a.R) - 1) / a.G;
-  const int end = rows > 0 ? (int)visible_end(a, start, rows, last_t) : 0;
-  const int pages = (end + kPage - 1) / kPage;
-  const int p0 = (int)((int64_t)pages * part / a.splits), p1 = (int)((int64_t)pages * (part + 1) / a.splits);
-  const int32_t* table = c.table + (int64_t)b * c.W;
-
-  f32x4 o[RT][Sh::kTiles];
-  float m[RT], l[RT];
+  f32x4 o[Sh::kTiles];
+  float m = kNegInf, l = 0.0f;
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    m[rt] = kNegInf;
-    l[rt] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < Sh::kTiles; ++i) o[rt][i] = f32x4{0, 0, 0, 0};
-  }
-
-  // a page's codes and scales of this lane
-  uint32_t kw[4][Sh::kChunks * Sh::kChunk / 4], vw[Sh::kTiles][4];
-  f32x4 ks[4], vs[4];
-  const int key = 16 * (r16 >> 2) + (r16 & 3);
-  const auto load_keys = [&](int page) {
-    const int64_t at = (int64_t)page * c.Hk + hk;
-    const uint8_t* p = (const uint8_t*)c.k + at * kPage * c.Dp + key * c.Dp + Sh::kChunk * g;
+  for (int i = 0; i < Sh::kTiles; ++i) o[i] = f32x4{0, 0, 0, 0};
+  uint32_t kw[4][Sh::kChunks][4], vw[Sh::kTiles][4];
+  float ks[16], vs[16];
+  const auto load_keys = [&](const Page& page) {
 #pragma unroll
     for (int u = 0; u < 4; ++u)
 #pragma unroll
-      for (int i = 0; i < Sh::kChunks; ++i) {
-        constexpr int kWordsOf = Sh::kChunk / 4;
-        const bool there = 64 * i + Sh::kChunk * g < c.Dp;
-#pragma unroll
-        for (int j = 0; j < kWordsOf; ++j) kw[u][i * kWordsOf + j] = 0;
-        if (there)
-          __builtin_memcpy(&kw[u][i * kWordsOf], __builtin_assume_aligned(p + 4 * u * c.Dp + 64 * i, Sh::kChunk),
-                           Sh::kChunk);
-      }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) ks[u] = *(const f32x4*)(c.k_scale + at * kPage + 16 * g + 4 * u);
+      for (int i = 0; i < Sh::kChunks; ++i) load_key<Sh>(c, page, r16, g, u, i, kw[u][i]);
+    load_scales(page.ks, g, ks);
   };
-  const auto load_values = [&](int page) {
-    const int64_t at = (int64_t)page * c.Hk + hk;
-    const uint8_t* p = (const uint8_t*)c.v + at * kPage * c.Dp + r16 * kPage + 16 * g;
+  const auto load_values = [&](const Page& page) {
 #pragma unroll
-    for (int i = 0; i < Sh::kTiles; ++i) {
-      const bool there = 16 * i < c.Dp;
-      u32x4 x = {0, 0, 0, 0};
-      if (there) x = *(const u32x4*)(p + 16 * kPage * i);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) vw[i][j] = x[j];
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) vs[u] = *(const f32x4*)(c.v_scale + at * kPage + 16 * g + 4 * u);
+    for (int i = 0; i < Sh::kTiles; ++i) load_value(page, r16, g, i, vw[i]);
+    load_scales(page.vs, g, vs);
   };
-  // the wave's next page that exists, from `at` on (p1: none); its number in `page`
-  int page = -1;
-  const auto next_page = [&](int at) {
-    for (; at < p1; at += kWaves) {
-      page = uniform(table[at]);
-      if (page >= 0 && page < c.pages) return at;
-    }
-    return p1;
-  };
-
   const float unit = a.cap > 0 ? a.scale / a.cap : a.scale * kLog2e;
-  int at = next_page(p0 + wave);
-  if (at < p1) {
-    load_keys(page);
-    load_values(page);
-  }
-  while (at < p1) {
-    f32x4 s[RT][4];
+  const int whole = a.mode == FBEV_DRAFT_NONE ? p.end : min(p.start, p.end);      // tokens below are seen by all
+  const int t = (p.row0 + r16) / a.G;
+  Walk<WAVES> walk(c, p, p.p0 + wave);
+  Page page = find_page(c, p.hk, walk.page, walk.there());
+  load_keys(page);
+  load_values(page);
+  while (walk.there()) {
+    float s[16];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      bf16x8 kf[Sh::kSteps];
+      f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < Sh::kSteps; ++i) kf[i] = widen<KIND>(kw[u][2 * i], kw[u][2 * i + 1]);
+      for (int i = 0; i < Sh::kSteps; ++i) {
+        const bf16x8 kf = widen<KIND>(kw[u][i / 2][2 * (i % 2)], kw[u][i / 2][2 * (i % 2) + 1]);
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        f32x4 acc = {0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < Sh::kSteps; ++i)
-#pragma unroll
-          for (int p = Sh::kQ - 1; p >= 0; --p)
-            acc = mfma(kf[i], ((const bf16x8*)lds)[((rt * Sh::kSteps + i) * Sh::kQ + p) * 64 + lane], acc);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[rt][u][i] = acc[i] * unit * ks[u][i];
+        for (int q = Sh::kQ - 1; q >= 0; --q) acc = mfma(kf, ((const bf16x8*)lds)[(i * Sh::kQ + q) * 64 + lane], acc);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[4 * u + i] = acc[i] * (unit * ks[4 * u + i]);
     }
-    const int pos = at * kPage;
-    at = next_page(at + kWaves);
-    if (at < p1) load_keys(page);
-
-    if (a.cap > 0) {
-      const float top = a.cap * kLog2e;
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[rt][u][i] = top * tanh_fast<true>(s[rt][u][i]);
-    }
-    // a page that holds a token which some query does not see
-    const bool masked = pos + kPage > (a.mode == FBEV_DRAFT_NONE ? end : min(start, end));
-    uint32_t bits[RT];
+    const int pos = walk.at * kPage;
+    walk.next();
+    page = find_page(c, p.hk, walk.page, walk.there());
+    load_keys(page);
+    const bool masked = pos + kPage > whole;
+    uint32_t bits = 0;
     if (masked) {
+      bits = t < p.rows ? seen_bits(a, p.b, t, p.start, p.rows, pos + 16 * g) : 0;
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const int row = row0 + rt * 16 + r16, t = row / a.G;
-        bits[rt] = t < rows ? seen_bits(a, b, t, start, rows, pos + 16 * g) : 0;
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (!(bits[rt] >> (4 * u + i) & 1)) s[rt][u][i] = kNegInf;
-      }
-      if constexpr (KIND == FBEV_CODES_E4M3) {          // what was never written may be the code of a NaN
-        const int left = end - pos - 16 * g;
-#pragma unroll
-        for (int i = 0; i < Sh::kTiles; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int n = min(max(left - 4 * j, 0), 4);
-            vw[i][j] &= n == 4 ? ~0u : (1u << (8 * n)) - 1u;
-          }
-      }
+      for (int i = 0; i < Sh::kTiles; ++i) keep_codes<KIND>(vw[i], p.end - pos - 16 * g);
     }
-    bf16x8 pf[RT][2][Sh::kP];
+    weigh<Sh::kTiles>(s, vs, masked, bits, a.cap, m, l, o);
+    bf16x8 pf[2][Sh::kP];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      float top = s[rt][0][0];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, s[rt][u][i]);
-      top = query_max(top);
-      // the maximum moves where it grows by 2^8 or more: weights stay below that, and sums in fp32 do not mind
-      if (__any(top > m[rt] + 8.0f)) {
-        const float to = top > m[rt] + 8.0f ? top : m[rt];
-        const float less = to == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - to);
-        m[rt] = to;
-        l[rt] *= less;
-#pragma unroll
-        for (int i = 0; i < Sh::kTiles; ++i) o[rt][i] *= less;
-      }
-      const float base = m[rt] == kNegInf ? 0.0f : m[rt];
-      float w[16], sum = 0.0f;
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float p = __builtin_amdgcn_exp2f(s[rt][u][i] - base);
-          sum += p;
-          w[4 * u + i] = p * vs[u][i];
-        }
-      l[rt] += sum;
-      if (masked) {                                     // an unseen token's scale may be anything
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (!(bits[rt] >> i & 1)) w[i] = 0.0f;
-      }
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = w[8 * kk + i];
-        split<Sh::kP>(x, pf[rt][kk]);
-      }
-    }
+    for (int kk = 0; kk < 2; ++kk) split_weights<Sh::kP>(s + 8 * kk, pf[kk]);
 #pragma unroll
     for (int i = 0; i < Sh::kTiles; ++i)
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
         const bf16x8 vf = widen<KIND>(vw[i][2 * kk], vw[i][2 * kk + 1]);
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-          for (int p = Sh::kP - 1; p >= 0; --p) o[rt][i] = mfma(vf, pf[rt][kk][p], o[rt][i]);
+        for (int q = Sh::kP - 1; q >= 0; --q) o[i] = mfma(vf, pf[kk][q], o[i]);
       }
-    if (at < p1) load_values(page);
+    load_values(page);
   }
 
-  // the waves' sums, row tile by row tile
+  l = query_sum(l);
+  if (g == 0) joined[wave][r16] = float2{m, l};
+  float* sums = (float*)lds;
+  __syncthreads();                                      // the queries have been read
+#pragma unroll
+  for (int i = 0; i < Sh::kTiles; ++i) *(f32x4*)(sums + (wave * 16 + r16) * Sh::kRow + 16 * i + 4 * g) = o[i];
+  __syncthreads();
+  const int mine = threadIdx.x >> 4, row = p.row0 + mine;
+  if (mine >= 16 || row >= a.R) return;
+  float2 ml[WAVES];
+  const float* of[WAVES];
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    ml[w] = joined[w][mine];
+    of[w] = sums + (w * 16 + mine) * Sh::kRow;
+  }
+  finish_row<T>(a, p, row, ml, of, r16);
+}
+
+// More rows: every wave has RT row tiles of its own, the pages are shared.
+template <typename T, int KIND, int DC, int RT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void cache_attn_many(CacheAttnArgs a) {
+  using Sh = Shape<T, DC>;
+  constexpr int kKeys = 4 * Sh::kSteps, kFrags = kKeys + 2 * Sh::kTiles;          // of a widened page
+  constexpr int kPageBytes = kFrags * 64 * 16, kSumBytes = WAVES * 16 * Sh::kRow * 4;
+  __shared__ alignas(16) char lds[2 * kPageBytes > kSumBytes ? 2 * kPageBytes : kSumBytes];
+  __shared__ alignas(16) float scales[2][2][kPage];
+  const CacheArgs& c = a.c;
+  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
+  const int r16 = lane & 15, g = lane >> 4;
+  const Part p = find_part(a, 16 * RT * WAVES);
+  const int row0 = p.row0 + wave * 16 * RT;
+  const bool idle = row0 >= a.R;                        // it moves pages for the others
+  bf16x8 qf[RT][Sh::kSteps][Sh::kQ];
+  f32x4 o[RT][Sh::kTiles];
+  float m[RT], l[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+    for (int i = 0; i < Sh::kSteps; ++i) load_queries<T, DC>(a, p, row0 + rt * 16 + r16, i, g, qf[rt][i]);
+    m[rt] = kNegInf;
+    l[rt] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < Sh::kTiles; ++i) o[rt][i] = f32x4{0, 0, 0, 0};
+  }
+
+  // a wave's part of a page: pieces of 16 codes a lane, keys (u and chunk) from the first wave on, value tiles from the last
+  constexpr int kKeyPieces = 4 * Sh::kChunks, kKeyMine = (kKeyPieces + WAVES - 1) / WAVES;
+  constexpr int kValueMine = (Sh::kTiles + WAVES - 1) / WAVES;
+  uint32_t kw[kKeyMine][4], vw[kValueMine][4];
+  float scale = 0.0f;
+  const int back = WAVES - 1 - wave;
+  const auto load_page = [&](int number, bool there) {
+    const Page page = find_page(c, p.hk, number, there);
+#pragma unroll
+    for (int j = 0; j < kKeyMine; ++j) {
+      const int piece = wave + WAVES * j;               // (one behind the last is outside the page)
+      load_key<Sh>(c, page, r16, g, piece / Sh::kChunks, piece % Sh::kChunks, kw[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kValueMine; ++j) load_value(page, r16, g, back + WAVES * j, vw[j]);
+    scale = __builtin_bit_cast(float, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(wave & 1 ? page.vs : page.ks, 4 * lane, 0, 0));
+  };
+  const float unit = a.cap > 0 ? a.scale / a.cap : a.scale * kLog2e;
+  const auto put_page = [&](int buf, int pos) {
+    bf16x8* to = (bf16x8*)(lds + buf * kPageBytes) + lane;
+#pragma unroll
+    for (int j = 0; j < kKeyMine; ++j) {
+      const int piece = wave + WAVES * j;
+      if (kKeyPieces % WAVES == 0 || piece < kKeyPieces) {
+        const int u = piece / Sh::kChunks, i = piece % Sh::kChunks;
+        to[(u * Sh::kSteps + 2 * i) * 64] = widen<KIND>(kw[j][0], kw[j][1]);
+        if constexpr (Sh::kChunk == 16) to[(u * Sh::kSteps + 2 * i + 1) * 64] = widen<KIND>(kw[j][2], kw[j][3]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kValueMine; ++j) {
+      const int tile = back + WAVES * j;
+      if (Sh::kTiles % WAVES == 0 || tile < Sh::kTiles) {
+        if (pos + kPage > p.end) keep_codes<KIND>(vw[j], p.end - pos - 16 * g);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) to[(kKeys + 2 * tile + kk) * 64] = widen<KIND>(vw[j][2 * kk], vw[j][2 * kk + 1]);
+      }
+    }
+    if (wave < 2) scales[buf][wave][lane] = wave ? scale : scale * unit;
+  };
+
+  const int whole = a.mode == FBEV_DRAFT_NONE ? p.end : min(p.start, p.end);      // tokens below are seen by all
+  Walk<1> walk(c, p, p.p0);                             // the page ahead of the one at work
+  int at = walk.at, buf = 0;
+  load_page(walk.page, walk.there());
+  put_page(0, at * kPage);
+  walk.next();
+  load_page(walk.page, walk.there());
+  while (at < p.p1) {
+    const int pos = at * kPage;
+    __syncthreads();                                    // this page is in; the other buffer has been read
+    const bf16x8* from = (const bf16x8*)(lds + buf * kPageBytes) + lane;
+    const float(&sc)[2][kPage] = scales[buf];
+    at = walk.at;
+    buf ^= 1;
+    put_page(buf, at * kPage);                          // (behind the last one: zeros that nobody reads)
+    walk.next();
+    load_page(walk.page, walk.there());
+    if (idle) continue;
+    float s[RT][16];
+    {
+      float ks[16];
+      __builtin_memcpy(ks, __builtin_assume_aligned(&sc[0][16 * g], 16), 64);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        f32x4 acc[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) acc[rt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < Sh::kSteps; ++i) {
+          const bf16x8 kf = from[(u * Sh::kSteps + i) * 64];
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int q = Sh::kQ - 1; q >= 0; --q) acc[rt] = mfma(kf, qf[rt][i][q], acc[rt]);
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[rt][4 * u + i] = acc[rt][i] * ks[4 * u + i];
+      }
+    }
+    const bool masked = pos + kPage > whole;
+    float vs[16];
+    __builtin_memcpy(vs, __builtin_assume_aligned(&sc[1][16 * g], 16), 64);
+    bf16x8 pf[RT][2][Sh::kP];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      uint32_t bits = 0;
+      if (masked) {
+        const int t = (row0 + rt * 16 + r16) / a.G;
+        bits = t < p.rows ? seen_bits(a, p.b, t, p.start, p.rows, pos + 16 * g) : 0;
+      }
+      weigh<Sh::kTiles>(s[rt], vs, masked, bits, a.cap, m[rt], l[rt], o[rt]);
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) split_weights<Sh::kP>(s[rt] + 8 * kk, pf[rt][kk]);
+    }
+#pragma unroll
+    for (int i = 0; i < Sh::kTiles; ++i)
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        const bf16x8 vf = from[(kKeys + 2 * i + kk) * 64];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int q = Sh::kP - 1; q >= 0; --q) o[rt][i] = mfma(vf, pf[rt][kk][q], o[rt][i]);
+      }
+  }
+
+  // a row's channels side by side again, by way of the pages' LDS, a tile of 16 rows at a time
+  float* sums = (float*)lds + wave * 16 * Sh::kRow;
+  __syncthreads();
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     l[rt] = query_sum(l[rt]);
-    if (g == 0) joined[wave][rt * 16 + r16] = float2{m[rt], l[rt]};
-  }
-  float* sums = (float*)lds;
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    __syncthreads();                                    // the queries, or the last tile, have been read
+    for (int i = 0; i < Sh::kTiles; ++i) *(f32x4*)(sums + r16 * Sh::kRow + 16 * i + 4 * g) = o[rt][i];
+    wave_lds_sync();
 #pragma unroll
-    for (int i = 0; i < Sh::kTiles; ++i)
-      *(f32x4*)(sums + (wave * 16 + r16) * Sh::kRow + 16 * i + 4 * g) = o[rt][i];
-    __syncthreads();
-    const int mine = threadIdx.x >> 4, row = row0 + rt * 16 + mine;
-    if (row < a.R) {
-      const int t = row / a.G, h = row - t * a.G;
-      float2 ml[kWaves];
-      float top = kNegInf;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        ml[w] = t < rows ? joined[w][rt * 16 + mine] : float2{kNegInf, 0.0f};     // padding sees nothing
-        top = fmaxf(top, ml[w].x);
-      }
-      float total = 0.0f, f[kWaves];
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        f[w] = share(ml[w].x, ml[w].y, top);
-        total += f[w] * ml[w].y;
-      }
-      const bool last = a.splits == 1;
-      const float inv = last ? (total == 0.0f ? 0.0f : 1.0f / total) : 1.0f;
-      T* out = (T*)a.out + (((int64_t)b * c.T + t) * a.Hq + hk * a.G + h) * c.D;
-      float* keep = a.part + (((int64_t)part * heads + bh) * a.R + row) * (c.D + 2);
-      for (int ch = (int)threadIdx.x & 15; ch < c.D; ch += 16) {
-        float x = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) x += f[w] == 0.0f ? 0.0f : f[w] * sums[(w * 16 + mine) * Sh::kRow + ch];
-        if (last)
-          out[ch] = (T)(x * inv);
-        else
-          keep[ch] = x;
-      }
-      if (!last && (threadIdx.x & 15) == 0) {
-        keep[c.D] = top;
-        keep[c.D + 1] = total;
-      }
+    for (int i = 0; i < 16; i += 4) {
+      const float2 ml[1] = {float2{__shfl(m[rt], i + g), __shfl(l[rt], i + g)}};
+      const float* const of[1] = {sums + (i + g) * Sh::kRow};
+      const int row = row0 + rt * 16 + i + g;
+      if (row < a.R) finish_row<T>(a, p, row, ml, of, r16);
     }
+    wave_lds_sync();
   }
 }
 
-// Rows split over the pages, a wave a row.
+// Rows split over the pages, a workgroup a row.  A wave takes every waves-th split, eight at a time; the first eight are on
+// their way before anything of the shares is known, so a call of few splits waits for memory once.
 template <typename T>
-__global__ __launch_bounds__(256) void cache_attn_join(CacheAttnArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t n = (int64_t)a.c.B * a.c.Hk * a.R, at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (at >= n) return;
+__global__ __launch_bounds__(1024) void cache_attn_join(CacheAttnArgs a) {
+  __shared__ float2 shares[kMostSplits];                // maximum and sum, then the share
+  __shared__ float sums[16][128];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int64_t n = (int64_t)a.c.B * a.c.Hk * a.R, at = blockIdx.x;
   const int D = a.c.D, stride = D + 2;
   const float* p = a.part + at * stride;
   const int64_t step = n * stride;
-  float top = kNegInf;
-  for (int s = lane; s < a.splits; s += 64) top = fmaxf(top, p[s * step + D]);
-  for (int i = 32; i > 0; i /= 2) top = fmaxf(top, __shfl_xor(top, i));
-  float x[2] = {0, 0}, total = 0.0f;
-  for (int s = 0; s < a.splits; ++s) {
-    const float l = p[s * step + D + 1], f = share(p[s * step + D], l, top);
-    total += f * l;
+  float held[8][2];
+  const auto load = [&](int s0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (lane + 64 * i < D && f != 0.0f) x[i] += f * p[s * step + lane + 64 * i];
+    for (int j = 0; j < 8; ++j) {
+      const int s = s0 + j * waves;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        held[j][i] = s < a.splits && lane + 64 * i < D ? p[s * step + lane + 64 * i] : 0.0f;
+    }
+  };
+  load(wave);
+  for (int s = threadIdx.x; s < a.splits; s += blockDim.x) shares[s] = float2{p[s * step + D], p[s * step + D + 1]};
+  __syncthreads();
+  // every wave finds the maximum and the total for itself
+  float top = kNegInf;
+  for (int s = lane; s < a.splits; s += 64) top = fmaxf(top, shares[s].x);
+#pragma unroll
+  for (int i = 32; i > 0; i /= 2) top = fmaxf(top, __shfl_xor(top, i));
+  float total = 0.0f;
+  for (int s = lane; s < a.splits; s += 64) total += share(shares[s].x, shares[s].y, top) * shares[s].y;
+  total = wave_sum(total);
+  float x[2] = {0, 0};
+  for (int s0 = wave; s0 < a.splits; s0 += 8 * waves) {
+    if (s0 != wave) load(s0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int s = s0 + j * waves;
+      const float2 ml = shares[s < a.splits ? s : 0];
+      const float f = s < a.splits ? share(ml.x, ml.y, top) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) x[i] += f == 0.0f ? 0.0f : f * held[j][i];
+    }
   }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) sums[wave][lane + 64 * i] = x[i];
+  __syncthreads();
+  const int ch = threadIdx.x;
+  if (ch >= D) return;
+  float y = 0.0f;
+  for (int w = 0; w < waves; ++w) y += sums[w][ch];
   const int64_t bh = at / a.R;
   const int row = (int)(at - bh * a.R), t = row / a.G, h = row - t * a.G;
   const int64_t b = bh / a.c.Hk, hk = bh - b * a.c.Hk;
-  T* out = (T*)a.out + ((b * a.c.T + t) * a.Hq + hk * a.G + h) * D;
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (lane + 64 * i < D) out[lane + 64 * i] = (T)(x[i] * inv);
+  ((T*)a.out)[((b * a.c.T + t) * a.Hq + hk * a.G + h) * D + ch] = (T)(total == 0.0f ? 0.0f : y / total);
 }
 
-// Row tiles a workgroup holds.
-int row_tiles(const CacheAttnArgs& a) {
-  if (a.R <= 16) return 1;
-  // fp32 (three parts a weight) and wide heads leave registers for two
-  if (a.R <= 32 || a.elem_bytes == 4 || a.c.D > 64) return 2;
-  return 4;
+// How a call's rows lie on workgroups.
+struct Plan {
+  bool few;               // up to one row tile: waves with pages of their own
+  int waves, tiles;       // of a workgroup, of a wave
+};
+
+// Few rows: eight waves where that alone gives most CUs a workgroup (no split, no join: 32 sequences of 4000 tokens, 8 key
+// heads of 128, 47 us against 52 with four waves and two splits), else four and splits (one sequence of 4000 tokens, 8 heads of
+// 64: 11 us against 21).  More rows: four waves up to 64 rows; beyond, eight share the widening of a page (64 rows of
+// 16 scenes x 4 heads of 128: 93 us against 116), but heads above 64 channels with rows enough for two workgroups a CU
+// take two row tiles a wave, whose products share each fragment's LDS read (8 x 4000 rows: 396 us against 456).
+Plan plan_of(const CacheAttnArgs& a) {
+  const int64_t heads = (int64_t)a.c.B * a.c.Hk;
+  if (a.R <= 16) return {true, heads >= 192 ? 8 : 4, 1};
+  if (a.R <= 64) return {false, 4, 1};
+  if (a.elem_bytes == 2 && a.c.D > 64 && heads * ((a.R + 127) / 128) >= 512) return {false, 4, 2};
+  return {false, 8, 1};
 }
 
 void set_splits(CacheAttnArgs& a) {
-  a.row_blocks = (a.R + 16 * row_tiles(a) - 1) / (16 * row_tiles(a));
+  const Plan plan = plan_of(a);
+  const int held = plan.few ? 16 : 16 * plan.waves * plan.tiles;
+  a.row_blocks = (a.R + held - 1) / held;
   const int64_t blocks = (int64_t)a.c.B * a.c.Hk * a.row_blocks;
-  // two workgroups a CU, where every wave of each still has a page
-  const int64_t want = blocks > 0 ? (512 + blocks - 1) / blocks : 1, most = (a.c.W + kWaves - 1) / kWaves;
-  a.splits = (int)(want < most ? want : most);
-  if (a.splits < 1) a.splits = 1;
+  // splits: eight waves a CU, where every four waves of few rows, or every workgroup of more, still have four pages
+  int64_t want = 1;
+  if (plan.waves == 4 ? blocks < 256 || plan.few : blocks < 192 && !plan.few) {
+    want = ((plan.waves == 4 ? 512 : 256) + blocks - 1) / blocks;
+    const int64_t most = (a.c.W + 3) / 4;
+    if (want > most) want = most;
+  }
+  a.splits = (int)(want < 1 ? 1 : want > kMostSplits ? kMostSplits : want);
 }
 
 template <typename T, int KIND, int DC>
 void launch_rows(const CacheAttnArgs& a, unsigned blocks, hipStream_t stream) {
-  switch (row_tiles(a)) {
-    case 1: cache_attn<T, KIND, DC, 1><<<blocks, 64 * kWaves, 0, stream>>>(a); break;
-    case 2: cache_attn<T, KIND, DC, 2><<<blocks, 64 * kWaves, 0, stream>>>(a); break;
-    default:
-      if constexpr (sizeof(T) == 2 && DC <= 64) cache_attn<T, KIND, DC, 4><<<blocks, 64 * kWaves, 0, stream>>>(a);
+  const Plan plan = plan_of(a);
+  if (plan.few) {
+    if (plan.waves == 8)
+      cache_attn_few<T, KIND, DC, 8><<<blocks, 512, 0, stream>>>(a);
+    else
+      cache_attn_few<T, KIND, DC, 4><<<blocks, 256, 0, stream>>>(a);
+  } else if (plan.waves == 8) {
+    cache_attn_many<T, KIND, DC, 1, 8><<<blocks, 512, 0, stream>>>(a);
+  } else if (plan.tiles == 1) {
+    cache_attn_many<T, KIND, DC, 1, 4><<<blocks, 256, 0, stream>>>(a);
+  } else if constexpr (sizeof(T) == 2 && DC == 128) {
+    cache_attn_many<T, KIND, DC, 2, 4><<<blocks, 256, 0, stream>>>(a);
   }
 }
 
@@ -509,8 +801,9 @@ hipError_t launch_type(const CacheAttnArgs& a, hipStream_t stream) {
     launch_width<T, FBEV_CODES_INT8>(a, blocks, stream);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  const int64_t rows = (int64_t)a.c.B * a.c.Hk * a.R;
-  cache_attn_join<T><<<(unsigned)((rows + 3) / 4), 256, 0, stream>>>(a);
+  // a wave for every eight splits; two at least, which have a thread for each channel
+  const int waves = a.splits >= 128 ? 16 : a.splits > 16 ? (a.splits + 7) / 8 : 2;
+  cache_attn_join<T><<<(unsigned)((int64_t)a.c.B * a.c.Hk * a.R), 64 * waves, 0, stream>>>(a);
   return hipGetLastError();
 }
 

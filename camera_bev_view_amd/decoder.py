@@ -8,18 +8,53 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import struct
 from typing import Optional, Sequence, Tuple
 
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from .encoder import (_DTYPES, _call, _check_apart, _check_plain, _check_sizes, _check_values, _collapse, _data,
-                      _scratch)
+from .encoder import (_DTYPES, _check_apart, _check_plain, _check_sizes, _check_values, _collapse, _data, _device,
+                      _raw_stream, _scratch)
 
 _CODES = {torch.int8: _lib.FBEV_CODES_INT8, torch.float8_e4m3fn: _lib.FBEV_CODES_E4M3}
 _PAGE = _lib.FBEV_CACHE_PAGE
-_I64x3 = ctypes.c_int64 * 3
+_F32, _I32 = torch.float32, torch.int32
+
+# A call's own time counts where a step of serving is a few small ones: descriptors are packed as bytes (a tenth of a
+# ctypes structure's time; the layouts are the structures' of _lib) and go as plain pointers.
+_pack_rms = struct.Struct("@6qif").pack
+_pack_cache = struct.Struct("@4i4P").pack
+_pack_rows = struct.Struct("@3i4x3P").pack
+_pack_attention = struct.Struct("@3i4x3qP2f").pack
+_pack_strides = struct.Struct("@3q").pack
+_P, _I, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_ARGS = {"fbev_rms_norm_forward": [_P, _P, _I, _P, _P, _P, _P, _P, _P],
+         "fbev_rms_norm_codes": [_P, _P, _I, _P, _P, _I, _I, _P, _P, _P, _P],
+         "fbev_rms_norm_backward": [_P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _Z, _P],
+         "fbev_cache_write": [_P, _P, _P, _P, _I, _P, _P, _P],
+         "fbev_cache_read": [_P, _P, _I, _P, _P, _P],
+         "fbev_cache_attention": [_P, _P, _P, _P, _I, _P, _P, _Z, _P]}
+
+
+@functools.lru_cache(maxsize=None)
+def _function(name: str):
+    fn = _lib.load()[name]              # a handle of its own: the library's takes structures
+    fn.argtypes, fn.restype = _ARGS[name], _I
+    return fn
+
+
+def _call(name: str, dev: torch.device, *args) -> None:
+    """The library's ``name``(*args, stream) on the current stream of ``dev``, with that device current."""
+    fn, index = _function(name), dev.index
+    if _device() == index:
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _raw_stream(index))
+    if status:
+        _lib.check(status)
 
 
 # ---- root-mean-square norm
@@ -32,11 +67,8 @@ def _rms_scratch(rows: int, C: int, dtype: int) -> int:
 
 
 def _rows(x: torch.Tensor, other: Optional[torch.Tensor]):
-    """(outer, inner, their strides in x and in other): how to walk the rows of both, or None."""
+    """(outer, inner, x's strides of them, other's strides): how to walk the rows of both, or None."""
     lead = x.dim() - 1
-    if x.is_contiguous() and (other is None or other.is_contiguous()):
-        C = x.shape[-1]
-        return (x.numel() // C if C else 0), 1, (C, 0), (C, 0)
     for t in (x, other):
         if t is not None and t.shape[-1] > 1 and t.stride(-1) != 1:
             return None
@@ -44,42 +76,44 @@ def _rows(x: torch.Tensor, other: Optional[torch.Tensor]):
         strides = []
         for t in (x, other):
             if t is None:
-                strides.append((0, 0))
+                strides += [0, 0]
                 continue
             so, si = _collapse(t.shape[:cut], t.stride()[:cut]), _collapse(t.shape[cut:lead], t.stride()[cut:lead])
             if so is None or si is None:
                 break
-            strides.append((so, si))
-        if len(strides) == 2:
+            strides += [so, si]
+        if len(strides) == 4:
             outer = inner = 1
             for n in x.shape[:cut]:
                 outer *= n
             for n in x.shape[cut:lead]:
                 inner *= n
-            return outer, inner, strides[0], strides[1]
+            return (outer, inner, *strides)
     return None
 
 
 def _rms_desc(x: torch.Tensor, residual: Optional[torch.Tensor], weight, eps: float):
-    if x.dim() < 1:
+    """(x, residual, rows, C, packed descriptor); x and residual copied where two strides do not walk their rows."""
+    shape, dev = x.shape, x.device
+    if not shape:
         raise ValueError("x must be [..., C]")
     if not x.is_cuda:
         raise ValueError("x must be a device tensor")
     if x.dtype not in _DTYPES:
         raise ValueError(f"x must be float32 or bfloat16, got {x.dtype}")
-    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype
-                                 or residual.device != x.device):
-        raise ValueError(f"residual must be a {x.dtype} tensor of shape {list(x.shape)} on {x.device}")
-    C = x.shape[-1]
+    if residual is not None and (residual.shape != shape or residual.dtype != x.dtype or residual.device != dev):
+        raise ValueError(f"residual must be a {x.dtype} tensor of shape {list(shape)} on {dev}")
+    C = shape[-1]
     _check_sizes(C)
     if weight is not None:
-        _check_plain("weight", weight, (C,), torch.float32, x.device)
+        _check_plain("weight", weight, (C,), _F32, dev)
+    if x.is_contiguous() and (residual is None or residual.is_contiguous()):
+        rows = x.numel() // C if C else 0
+        return x, residual, rows, C, _pack_rms(rows, 1, C, 0, C, 0, C, eps)
     walk = _rows(x, residual)
     if walk is None:
-        x = x.contiguous()
-        residual = None if residual is None else residual.contiguous()
-        walk = _rows(x, residual)
-    return x, residual, _lib.RmsDesc(*walk, C, eps)
+        return _rms_desc(x.contiguous(), None if residual is None else residual.contiguous(), weight, eps)
+    return x, residual, walk[0] * walk[1], C, _pack_rms(*walk, C, eps)
 
 
 def rms_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
@@ -90,30 +124,27 @@ def rms_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
     projection); other layouts are copied first.  ``h_out`` may be x or residual themselves, where contiguous.
     Returns (y, h, rstd [...] fp32); h is x without a residual.  The backward takes h and rstd."""
     dev = x.device
-    x, residual, rd = _rms_desc(x, residual, weight, eps)
-    y = _given("out", out, x, x, residual, weight, h_out)
-    h = x
-    if residual is not None:
-        h = _sum_out(h_out, x, residual, weight)
-    elif h_out is not None:
-        raise ValueError("h_out comes with a residual")
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    x, residual, _, _, rd = _rms_desc(x, residual, weight, eps)
+    if out is None:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    else:
+        y = out
+        _check_plain("out", out, x.shape, x.dtype, dev)
+        _check_apart("out", out, x, residual, weight, h_out)
+    h = _sum_out(h_out, x, residual, weight)
+    rstd = torch.empty(x.shape[:-1], dtype=_F32, device=dev)
     _call("fbev_rms_norm_forward", dev, _data(x), _data(residual), _DTYPES[x.dtype], rd, _data(weight), _data(y),
           None if residual is None else _data(h), _data(rstd))
     return y, h, rstd
 
 
-def _given(name: str, out: Optional[torch.Tensor], like: torch.Tensor, *others) -> torch.Tensor:
-    if out is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    _check_plain(name, out, like.shape, like.dtype, like.device)
-    _check_apart(name, out, *others)
-    return out
-
-
 def _sum_out(h_out, x, residual, weight) -> torch.Tensor:
+    if residual is None:
+        if h_out is not None:
+            raise ValueError("h_out comes with a residual")
+        return x
     if h_out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
     _check_plain("h_out", h_out, x.shape, x.dtype, x.device)
     for t in (x, residual):
         if not (t.data_ptr() == h_out.data_ptr() and t.is_contiguous()):
@@ -132,17 +163,12 @@ def rms_norm_codes(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
     if codes not in _CODES:
         raise ValueError(f"codes must be torch.int8 or torch.float8_e4m3fn, got {codes}")
     dev = x.device
-    x, residual, rd = _rms_desc(x, residual, weight, eps)
+    x, residual, _, C, rd = _rms_desc(x, residual, weight, eps)
     _check_sizes(block)
-    C = x.shape[-1]
-    out = torch.empty(x.shape, dtype=codes, device=dev)
+    out = torch.empty_like(x, dtype=codes, memory_format=torch.contiguous_format)
     blocks = -(-C // block) if 0 < block < C else 1
-    scales = torch.empty((*x.shape[:-1], blocks), dtype=torch.float32, device=dev)
-    h = x
-    if residual is not None:
-        h = _sum_out(h_out, x, residual, weight)
-    elif h_out is not None:
-        raise ValueError("h_out comes with a residual")
+    scales = torch.empty((*x.shape[:-1], blocks), dtype=_F32, device=dev)
+    h = _sum_out(h_out, x, residual, weight)
     _call("fbev_rms_norm_codes", dev, _data(x), _data(residual), _DTYPES[x.dtype], rd, _data(weight), _CODES[codes],
           block, _data(out), _data(scales), None if residual is None else _data(h))
     return out, scales, h
@@ -155,16 +181,16 @@ def rms_norm_backward(grad_y: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
     """fbev_rms_norm_backward: (grad_x, which is the residual's gradient too, contiguous; grad_weight [C] fp32, or None
     without ``with_weight``) from dL/dy, the forward's h and rstd, and ``grad_h``, dL/dh from elsewhere (the residual stream)."""
     dev = h.device
-    h, _, rd = _rms_desc(h, None, weight, 0.0)
+    h, _, rows, C, rd = _rms_desc(h, None, weight, 0.0)
     for name, g in (("grad_y", grad_y), ("grad_h", grad_h)):
         if g is not None and (g.shape != h.shape or g.dtype != h.dtype or g.device != dev):
             raise ValueError(f"{name} must be a {h.dtype} tensor of shape {list(h.shape)} on {dev}")
     grad_y = grad_y.contiguous()
     grad_h = None if grad_h is None else grad_h.contiguous()
     _check_plain("rstd", rstd, h.shape[:-1], torch.float32, dev)
-    gx = torch.empty(h.shape, dtype=h.dtype, device=dev)
-    gw = torch.empty(h.shape[-1], dtype=torch.float32, device=dev) if with_weight else None
-    need = _rms_scratch(rd.outer * rd.inner, rd.C, _DTYPES[h.dtype]) if with_weight else 0
+    gx = torch.empty_like(h, memory_format=torch.contiguous_format)
+    gw = torch.empty(C, dtype=_F32, device=dev) if with_weight else None
+    need = _rms_scratch(rows, C, _DTYPES[h.dtype]) if with_weight else 0
     workspace, have = _scratch(need, workspace, dev)
     _call("fbev_rms_norm_backward", dev, _data(grad_y), _data(grad_h), _data(h), _DTYPES[h.dtype], rd, _data(weight),
           _data(rstd), _data(gx), _data(gw), _data(workspace), have)
@@ -215,20 +241,26 @@ class TokenCache:
     __slots__ = ("k", "v", "k_scale", "v_scale", "D", "Hk", "pages", "device", "desc")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor, D: int):
-        if k.dim() != 4 or k.dtype not in _CODES:
+        shape, dtype, dev = k.shape, k.dtype, k.device
+        if len(shape) != 4 or dtype not in _CODES:
             raise ValueError(f"k must be [pages, Hk, {_PAGE}, Dp] of torch.int8 or torch.float8_e4m3fn")
         if not k.is_cuda:
             raise ValueError("k must be a device tensor")
-        pages, Hk, Dp = k.shape[0], k.shape[1], -(-D // 16) * 16
+        pages, Hk, Dp = shape[0], shape[1], -(-D // 16) * 16
         _check_sizes(pages, Hk, D)
-        for name, t, shape, dtype in (("k", k, (pages, Hk, _PAGE, Dp), k.dtype),
-                                      ("v", v, (pages, Hk, Dp, _PAGE), k.dtype),
-                                      ("k_scale", k_scale, (pages, Hk, _PAGE), torch.float32),
-                                      ("v_scale", v_scale, (pages, Hk, _PAGE), torch.float32)):
-            _check_plain(name, t, shape, dtype, k.device)
+        side = (pages, Hk, _PAGE)
+        if not (shape == (pages, Hk, _PAGE, Dp) and k.is_contiguous()
+                and v.shape == (pages, Hk, Dp, _PAGE) and v.is_contiguous() and v.dtype == dtype and v.device == dev
+                and k_scale.shape == side and k_scale.is_contiguous() and k_scale.dtype == _F32
+                and k_scale.device == dev and v_scale.shape == side and v_scale.is_contiguous()
+                and v_scale.dtype == _F32 and v_scale.device == dev):
+            for name, t, want, kind in (("k", k, (pages, Hk, _PAGE, Dp), dtype), ("v", v, (pages, Hk, Dp, _PAGE), dtype),
+                                        ("k_scale", k_scale, side, _F32), ("v_scale", v_scale, side, _F32)):
+                _check_plain(name, t, want, kind, dev)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.D, self.Hk, self.pages, self.device = D, Hk, pages, k.device
-        self.desc = _lib.CacheDesc(pages, Hk, D, _CODES[k.dtype], _data(k), _data(v), _data(k_scale), _data(v_scale))
+        self.D, self.Hk, self.pages, self.device = D, Hk, pages, dev
+        self.desc = _pack_cache(pages, Hk, D, _CODES[dtype], k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
+                                v_scale.data_ptr())
 
 
 def token_cache(pages: int, Hk: int, D: int, *, codes: torch.dtype = torch.float8_e4m3fn, device="cuda") -> TokenCache:
@@ -242,17 +274,19 @@ def token_cache(pages: int, Hk: int, D: int, *, codes: torch.dtype = torch.float
                       torch.zeros((pages, Hk, _PAGE), dtype=torch.float32, device=device), D)
 
 
-def _cache_rows(cache: TokenCache, table, start, count, B: int, T: int):
-    dev = cache.device
-    if table.dim() != 2 or table.shape[0] != B:
-        raise ValueError(f"table must be [B={B}, pages of a sequence], got {tuple(table.shape)}")
-    _check_sizes(B, T, table.shape[1])
-    for name, t in (("table", table), ("start", start), ("count", count)):
-        if t is not None and (t.dtype != torch.int32 or t.device != dev or not t.is_contiguous()
-                              or (t is not table and tuple(t.shape) != (B,))):
-            raise ValueError(f"{name} must be a contiguous int32 tensor" + ("" if t is table else f" of shape [{B}]")
-                             + f" on {dev}")
-    return _lib.CacheRows(B, T, table.shape[1], _data(table), _data(start), _data(count))
+def _cache_rows(cache: TokenCache, table, start, count, B: int, T: int) -> bytes:
+    dev, shape = cache.device, table.shape
+    if len(shape) != 2 or shape[0] != B:
+        raise ValueError(f"table must be [B={B}, pages of a sequence], got {tuple(shape)}")
+    _check_sizes(B, T, shape[1])
+    if not (table.dtype == _I32 and table.device == dev and table.is_contiguous()
+            and start.dtype == _I32 and start.device == dev and start.shape == (B,) and start.is_contiguous()
+            and (count is None or count.dtype == _I32 and count.device == dev and count.shape == (B,)
+                 and count.is_contiguous())):
+        for name, t, want in (("table", table, shape), ("start", start, (B,)), ("count", count, (B,))):
+            if t is not None:
+                _check_plain(name, t, want, _I32, dev)
+    return _pack_rows(B, T, shape[1], table.data_ptr(), start.data_ptr(), 0 if count is None else count.data_ptr())
 
 
 def cache_write(cache: TokenCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, start: torch.Tensor, *,
@@ -270,8 +304,8 @@ def cache_write(cache: TokenCache, k: torch.Tensor, v: torch.Tensor, table: torc
         k = k if k.stride(3) == 1 else k.contiguous()
         v = v if v.stride(3) == 1 else v.contiguous()
     cr = _cache_rows(cache, table, start, count, B, T)
-    _call("fbev_cache_write", dev, cache.desc, cr, _data(k), _data(v), _DTYPES[k.dtype], _I64x3(*k.stride()[:3]),
-          _I64x3(*v.stride()[:3]))
+    _call("fbev_cache_write", dev, cache.desc, cr, _data(k), _data(v), _DTYPES[k.dtype], _pack_strides(*k.stride()[:3]),
+          _pack_strides(*v.stride()[:3]))
 
 
 def cache_read(cache: TokenCache, table: torch.Tensor, start: torch.Tensor, T: int, *,
@@ -284,7 +318,7 @@ def cache_read(cache: TokenCache, table: torch.Tensor, start: torch.Tensor, T: i
     dev, B = cache.device, table.shape[0]
     cr = _cache_rows(cache, table, start, count, B, T)
     k = torch.empty((B, T, cache.Hk, cache.D), dtype=dtype, device=dev)
-    v = torch.empty((B, T, cache.Hk, cache.D), dtype=dtype, device=dev)
+    v = torch.empty_like(k)
     _call("fbev_cache_read", dev, cache.desc, cr, _DTYPES[dtype], _data(k), _data(v))
     return k, v
 
@@ -356,7 +390,7 @@ def cache_attention(q: torch.Tensor, cache: TokenCache, table: torch.Tensor, sta
         ancestors = ancestors.contiguous()
         mode, words = _lib.FBEV_DRAFT_TREE, ancestors.shape[2]
     if out is None:
-        out = torch.empty((B, T, Hq, D), dtype=q.dtype, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _check_plain("out", out, q.shape, q.dtype, dev)
         _check_apart("out", out, q, cache.k, cache.v, cache.k_scale, cache.v_scale, table, start, count, ancestors,
@@ -364,7 +398,7 @@ def cache_attention(q: torch.Tensor, cache: TokenCache, table: torch.Tensor, sta
     if scale is None:
         scale = D ** -0.5 if D else 1.0
     dt = _DTYPES[q.dtype]
-    ad = _lib.CacheAttentionDesc(Hq, mode, words, q.stride()[:3], _data(ancestors), scale, cap or 0.0)
-    workspace, have = _scratch(_cache_attention_scratch(B, T, cr.W, Hq, cache.Hk, D, dt), workspace, dev)
+    ad = _pack_attention(Hq, mode, words, *q.stride()[:3], _data(ancestors) or 0, scale, cap or 0.0)
+    workspace, have = _scratch(_cache_attention_scratch(B, T, table.shape[1], Hq, cache.Hk, D, dt), workspace, dev)
     _call("fbev_cache_attention", dev, cache.desc, cr, ad, _data(q), dt, _data(out), _data(workspace), have)
     return out
