@@ -24,19 +24,16 @@ struct Codes {
   static constexpr bool kFloat = KIND == FBEV_CODES_E4M3;
   static constexpr float kMost = kFloat ? 448.0f : 127.0f;
 
-  // From the largest abs_bits() of a row (NaN and infinity are the largest of all).
+  // From the largest abs_bits() of a row (NaN and infinity are the largest of all).  The quotient is the correctly rounded
+  // one: a product with the rounded reciprocal, corrected by its exact remainder (Markstein).
   static __device__ __forceinline__ float scale_of(uint32_t top) {
-    if (top >= 0x7f800000u) return __builtin_nanf("");
-    return fmaxf(__builtin_bit_cast(float, top) / kMost, kLeastScale);
+    constexpr float kInverse = 1.0f / kMost;
+    const float x = __builtin_bit_cast(float, top), q = x * kInverse;
+    const float scale = fmaxf(fmaf(fmaf(-q, kMost, x), kInverse, q), kLeastScale);
+    return top >= 0x7f800000u ? __builtin_nanf("") : scale;
   }
-
-  // Whether a quotient within 2^-21 of q (relative) might belong to another code than q does.
-  static __device__ __forceinline__ bool near_border(float q) {
-    if constexpr (!kFloat) return fabsf(q - rintf(q)) > 0.49996f;
-    const uint32_t low = __builtin_bit_cast(uint32_t, q) & 0xfffffu;      // what four significant bits drop
-    const float t = q * 512.0f;                                           // below 2^-6 the codes are 2^-9 apart
-    return low - 0x7fff0u <= 0x20u || (fabsf(q) < 0x1.0002p-6f && fabsf(t - rintf(t)) > 0.4999f);
-  }
+  // 1 / scale to a step of fp32: all that pack() asks for.
+  static __device__ __forceinline__ float inverse_of(float scale) { return __builtin_amdgcn_rcpf(scale); }
 
   // A number on the same side of every border as the exact x / scale: the quotient rounded to fp32, moved off itself by one
   // step towards the exact one where it is even (borders are even in fp32, so an odd one lies on none).  Where
@@ -50,28 +47,58 @@ struct Codes {
     return __builtin_bit_cast(float, b);
   }
 
-  // Four values' codes, one to a byte.  inverse = 1 / scale.  Values of fp64 are rounded for the quick quotient alone.
-  template <typename X>
-  static __device__ __forceinline__ uint32_t pack(const X (&x)[4], float scale, float inverse) {
+  // Four values' codes, one to a byte.  inverse: inverse_of(scale).
+  static __device__ __forceinline__ uint32_t pack(const float (&x)[4], float scale, float inverse) {
+    return pack(x, scale, inverse, [&](int i) { return x[i]; });
+  }
+  // The same where x[i] are rounded: exact(i) is the i-th value in fp64.
+  template <typename F>
+  static __device__ __forceinline__ uint32_t pack(const float (&x)[4], float scale, float inverse, F exact) {
     float q[4];
-    bool near = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      q[i] = (float)x[i] * inverse;
-      near |= near_border(q[i]);
-    }
-    if (near) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = side_of((double)x[i], scale);
-    }
+    for (int i = 0; i < 4; ++i) q[i] = x[i] * inverse;
     if constexpr (kFloat) {
+      // what four significant bits drop lies around the half; under 2^-6 codes are a fixed 2^-9 apart: all of those but 0
+      uint32_t half = ~0u, small = ~0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t b = __builtin_bit_cast(uint32_t, q[i]);
+        half = min(half, (b << 12) + 0x80010000u);
+        small = min(small, (b << 1) - 2u);
+      }
+      if (half <= 0x20000u || small < 0x79000000u - 2u) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = side_of(exact(i), scale);
+      }
       const int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
       return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
     } else {
-      uint32_t w = 0;
+      // 1.5 2^23 + q keeps q's nearest integer in its last byte
+      constexpr float kTurn = 12582912.0f;
+      uint32_t t[4];
+      float off = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w |= ((uint32_t)(int)rintf(q[i]) & 0xffu) << (8 * i);
-      return w;
+      for (int i = 0; i < 4; ++i) {
+        const float n = q[i] + kTurn;
+        off = fmaxf(off, fabsf(q[i] - (n - kTurn)));
+        t[i] = __builtin_bit_cast(uint32_t, n);
+      }
+      if (off > 0.49996f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (sizeof(exact(0)) == 8) {
+            t[i] = __builtin_bit_cast(uint32_t, side_of(exact(i), scale) + kTurn);
+          } else {
+            // the rest that the nearest integer n leaves of x is exact in fp32, and n off by one at most
+            const float n = __builtin_bit_cast(float, t[i]) - kTurn, rest = fmaf(-n, scale, x[i]);
+            const float over = fabsf(rest) - 0.5f * scale;
+            const bool move = over > 0.0f || (over == 0.0f && (t[i] & 1) != 0);
+            t[i] += !move ? 0u : rest > 0.0f ? 1u : ~0u;
+          }
+        }
+      }
+      const uint32_t lo = __builtin_amdgcn_perm(t[1], t[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(t[3], t[2], 0x0c0c0400u);
+      return hi << 16 | lo;
     }
   }
 

@@ -43,6 +43,18 @@ __device__ __forceinline__ void load_piece(const T* p, int left, float (&v)[kVec
   }
 }
 
+// The same in two steps, for pieces that are loaded a row ahead.
+template <typename T>
+__device__ __forceinline__ void load_raw(const T* p, int left, T (&e)[kVec<T>]) {
+  constexpr int V = kVec<T>;
+  if (left >= V) {
+    __builtin_memcpy(e, p, 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) e[i] = i < left ? p[i] : (T)0.0f;
+  }
+}
+
 template <typename T>
 __device__ __forceinline__ void store_piece(T* p, int left, const float (&v)[kVec<T>]) {
   constexpr int V = kVec<T>;
@@ -163,7 +175,7 @@ __device__ __forceinline__ uint32_t team_max(uint32_t x, double* slots) {
   return x;
 }
 
-constexpr int team_threads(int L) { return L > 256 ? L : 256; }
+constexpr int team_threads(int L) { return L > 64 ? L : 256; }
 
 __device__ __forceinline__ int64_t row_offset(int64_t row, int64_t inner, const int64_t (&s)[2]) {
   if (inner == 1) return row * s[0];
@@ -171,11 +183,11 @@ __device__ __forceinline__ int64_t row_offset(int64_t row, int64_t inner, const 
   return o * s[0] + (row - (int64_t)o * inner) * s[1];
 }
 
-// y of a row in 8 bits: a scale for each `block` channels.  Blocks are narrower than the row only where a lane's pieces lie
+// y of a row in 8 bits (y = h w r, rounded once): a scale for each `block` channels.  Blocks are narrower than the row only where a lane's pieces lie
 // L apart and a block's 4 to 32 lanes side by side.
 template <int KIND, int L, int K, int V>
-__device__ __forceinline__ void store_codes(const RmsArgs& a, int64_t row, int lane, bool mine, double (&y)[K][V],
-                                            double* slots) {
+__device__ __forceinline__ void store_codes(const RmsArgs& a, int64_t row, int lane, bool mine, const float (&y)[K][V],
+                                            const float (&h)[K][V], double r, double* slots) {
   using Cd = Codes<KIND>;
   const int nb = a.block < a.C ? a.block / V : 0;       // lanes of a block (0: the row)
   const int blocks = nb ? (a.C + a.block - 1) / a.block : 1;
@@ -185,7 +197,7 @@ __device__ __forceinline__ void store_codes(const RmsArgs& a, int64_t row, int l
   for (int k = 0; k < K; ++k) {
     top[k] = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) top[k] = umax(top[k], abs_bits((float)y[k][i]));
+    for (int i = 0; i < V; ++i) top[k] = umax(top[k], abs_bits(y[k][i]));
   }
   if (nb == 0) {
     uint32_t t = top[0];
@@ -204,14 +216,18 @@ __device__ __forceinline__ void store_codes(const RmsArgs& a, int64_t row, int l
     if (left <= 0 || !mine) continue;
     const float scale = Cd::scale_of(top[k]);
     const bool odd = top[k] >= 0x7f800000u;
-    const float inverse = odd ? 0.0f : 1.0f / scale;
+    const float inverse = Cd::inverse_of(scale);
     uint32_t w[V / 4];
 #pragma unroll
     for (int j = 0; j < V / 4; ++j) {
-      double x[4];
+      float x[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = odd ? 0.0 : y[k][4 * j + i];
-      w[j] = Cd::pack(x, scale, inverse);
+      for (int i = 0; i < 4; ++i) x[i] = y[k][4 * j + i];
+      w[j] = Cd::pack(x, scale, inverse, [&](int i) {
+        const int at = c + 4 * j + i;       // (read again: few come here, and it would hold registers)
+        return (double)h[k][4 * j + i] * (double)(a.weight && at < a.C ? a.weight[at] : 1.0f) * r;
+      });
+      if (odd) w[j] = 0;
     }
     if (left >= V) {
       __builtin_memcpy(out + c, w, V);
@@ -224,7 +240,16 @@ __device__ __forceinline__ void store_codes(const RmsArgs& a, int64_t row, int l
   }
 }
 
-// CODES: the sum of squares, 1 / sqrt and y are fp64 in front of the codes, which have no other rounding than their own.
+// h (head + tail) w, rounded once: both products with what their rounding drops.
+__device__ __forceinline__ float product(float h, float head, float tail, float w) {
+#pragma clang fp contract(off)
+  const float p = h * head, dp = fmaf(h, tail, fmaf(h, head, -p));
+  const float z = p * w;
+  return z + fmaf(dp, w, fmaf(p, w, -z));
+}
+
+// CODES: the codes have no other rounding than their own.  The sum of squares and 1 / sqrt are fp64, and y is rounded once;
+// where a code's border is near, it is taken in fp64.
 template <typename T, int L, int K, bool CODES>
 __global__ __launch_bounds__(team_threads(L)) void rms_fwd(RmsArgs a) {
   constexpr int V = kVec<T>, kThreads = team_threads(L), kTeams = kThreads / L;
@@ -236,7 +261,7 @@ __global__ __launch_bounds__(team_threads(L)) void rms_fwd(RmsArgs a) {
   const bool mine = first < a.rows;
   const T* x = (const T*)a.x + row_offset(row, a.inner, a.xs);
   const T* res = a.residual ? (const T*)a.residual + row_offset(row, a.inner, a.rs) : nullptr;
-  float v[K][V], sum = 0.0f;
+  float v[K][V];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int c = (lane + L * k) * V;
@@ -263,22 +288,28 @@ __global__ __launch_bounds__(team_threads(L)) void rms_fwd(RmsArgs a) {
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int i = 0; i < V; ++i) squares = fma((double)v[k][i], (double)v[k][i], squares);
-    squares = team_sum<L>(squares, slots);
-    const double r = 1.0 / sqrt(squares / (double)a.C + (double)a.eps);
-    double y[K][V];
+    // 1 / sqrt from the hardware's, two steps of Newton's method behind it
+    const double mean = team_sum<L>(squares, slots) / (double)a.C + (double)a.eps;
+    double r = __builtin_amdgcn_rsq(mean);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) r = fma(r, fma(-0.5 * mean * r, r, 0.5), r);
+    r = mean > 0.0 && mean < __builtin_huge_val() ? r : 1.0 / sqrt(mean);
+    const float head = (float)r, tail = (float)(r - (double)head);
+    float y[K][V];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = (lane + L * k) * V;
       float w[V];
       load_weight(a.weight, c, a.C - c, w, V);
 #pragma unroll
-      for (int i = 0; i < V; ++i) y[k][i] = (double)v[k][i] * (double)w[i] * r;
+      for (int i = 0; i < V; ++i) y[k][i] = product(v[k][i], head, tail, w[i]);
     }
     if (a.codes == FBEV_CODES_E4M3)
-      store_codes<FBEV_CODES_E4M3, L, K, V>(a, row, lane, mine, y, slots);
+      store_codes<FBEV_CODES_E4M3, L, K, V>(a, row, lane, mine, y, v, r, slots);
     else
-      store_codes<FBEV_CODES_INT8, L, K, V>(a, row, lane, mine, y, slots);
+      store_codes<FBEV_CODES_INT8, L, K, V>(a, row, lane, mine, y, v, r, slots);
   } else {
+    float sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -312,29 +343,41 @@ __global__ __launch_bounds__(team_threads(L)) void rms_bwd(RmsArgs a) {
 #pragma unroll
     for (int i = 0; i < V; ++i) gw[k][i] = 0.0f;
   }
-  // every team of a workgroup makes the same number of rounds
-  for (int64_t base = (int64_t)blockIdx.x * kTeams; base < a.rows; base += (int64_t)gridDim.x * kTeams) {
-    const int64_t at = base + threadIdx.x / L;
-    const bool mine = at < a.rows;
-    const int64_t row = mine ? at : a.rows - 1;
+  // every team of a workgroup makes the same number of rounds; where a lane has one piece, a row's are on their way while
+  // the row before is at work (rows of 1001 fp32 channels, both directions: 82 -> 67 us)
+  constexpr bool kAhead = K == 1;
+  const int64_t step = (int64_t)gridDim.x * kTeams;
+  T hr[K][V], gr[K][V], mr[K][V];
+  float rr;
+  const auto load_row = [&](int64_t at) {
+    const int64_t row = at < a.rows ? at : a.rows - 1;
     const T* x = (const T*)a.x + row_offset(row, a.inner, a.xs);
     const T* gy = (const T*)a.gy + row * a.C;
-    float h[K][V], g[K][V], dot = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = (lane + L * k) * V;
-      load_piece(x + c, a.C - c, h[k]);
-      load_piece(gy + c, a.C - c, g[k]);
+      load_raw(x + c, a.C - c, hr[k]);
+      load_raw(gy + c, a.C - c, gr[k]);
+      if (a.gh) load_raw((const T*)a.gh + row * a.C + c, a.C - c, mr[k]);
     }
-    float more[K][V];
-    if (a.gh) {
+    rr = a.rstd[row];
+  };
+  int64_t at = (int64_t)blockIdx.x * kTeams + threadIdx.x / L;
+  if (kAhead) load_row(at);
+  for (int64_t base = (int64_t)blockIdx.x * kTeams; base < a.rows; base += step, at += step) {
+    const bool mine = at < a.rows;
+    if (!kAhead) load_row(at);
+    float h[K][V], g[K][V], more[K][V], dot = 0.0f;
+    const float r = rr;
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int c = (lane + L * k) * V;
-        load_piece((const T*)a.gh + row * a.C + c, a.C - c, more[k]);
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        h[k][i] = to_f32(hr[k][i]);
+        g[k][i] = to_f32(gr[k][i]);
+        more[k][i] = a.gh ? to_f32(mr[k][i]) : 0.0f;
       }
-    }
-    const float r = a.rstd[row];
+    if (kAhead && base + step < a.rows) load_row(at + step);
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -352,14 +395,14 @@ __global__ __launch_bounds__(team_threads(L)) void rms_bwd(RmsArgs a) {
         if (a.gh) gx[i] += more[k][i];
         gw[k][i] = fmaf(g[k][i], h[k][i] * r, gw[k][i]);
       }
-      store_piece((T*)a.gx + row * a.C + c, a.C - c, gx);
+      store_piece((T*)a.gx + at * a.C + c, a.C - c, gx);
     }
   }
   if (a.gweight == nullptr) return;
   float* part = a.part + (int64_t)blockIdx.x * a.C;
-  if constexpr (L < 256) {
+  if constexpr (L <= 64) {
     // the teams of a wave by lane exchanges, the waves through LDS
-    __shared__ float joined[4][L <= 64 ? L * K * V : 1];
+    __shared__ float joined[4][L * K * V];
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -413,22 +456,23 @@ hipError_t with_team(int pieces, F f) {
   if (pieces <= 16) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
   if (pieces <= 32) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{});
   if (pieces <= 64) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
-  if (pieces <= 128) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
-  if (pieces <= 256) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 4>{});
-  if (pieces <= 512) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
-  if (pieces <= 1024) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
+  if (pieces <= 128) return f(std::integral_constant<int, 128>{}, std::integral_constant<int, 1>{});
+  if (pieces <= 256) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
+  if (pieces <= 512) return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 1>{});
+  if (pieces <= 1024) return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 1>{});
   if (pieces <= 2048) return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
   return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
 }
 
 int pieces_of(const RmsArgs& a) { return (int)(((int64_t)a.C * a.elem_bytes + 15) / 16); }
 
-// Workgroups of the backward: up to four a CU, each with eight rounds of rows at least so that the shares stay few
-// against the data.
-int backward_blocks(const RmsArgs& a, int teams) {
-  const int64_t rounds = (a.rows + teams - 1) / teams;
-  const int64_t n = rounds / 8 > 256 ? rounds / 8 : (rounds < 256 ? rounds : 256);
-  return (int)(n < 1024 ? n : 1024);
+// Workgroups of the backward: 1024 threads a CU (2048: 5000 rows of 2048 channels 48 against 44 us, for the shares), with four
+// rounds of rows each where that still leaves a workgroup a CU (eight: 46 us).
+int backward_blocks(const RmsArgs& a, int teams, int threads) {
+  const int64_t rounds = (a.rows + teams - 1) / teams, most = 256 * (1024 / threads);
+  int64_t n = rounds / 4 > 256 ? rounds / 4 : 256;
+  if (n > rounds) n = rounds;
+  return (int)(n < most ? n : most);
 }
 
 }  // namespace
@@ -437,7 +481,7 @@ size_t rms_norm_workspace_bytes(const RmsArgs& a) {
   if (a.rows == 0) return 0;
   size_t need = 0;
   with_team(pieces_of(a), [&](auto L, auto) {
-    need = (size_t)backward_blocks(a, team_threads(L) / L) * a.C * sizeof(float);
+    need = (size_t)backward_blocks(a, team_threads(L) / L, team_threads(L)) * a.C * sizeof(float);
     return hipSuccess;
   });
   return need;
@@ -467,7 +511,7 @@ hipError_t launch_rms_norm_backward(const RmsArgs& a, hipStream_t stream) {
     return hipGetLastError();
   }
   return with_team(pieces_of(a), [&](auto L, auto K) {
-    const int blocks = backward_blocks(a, team_threads(L) / L);
+    const int blocks = backward_blocks(a, team_threads(L) / L, team_threads(L));
     if (a.elem_bytes == 4)
       rms_bwd<float, L, K><<<blocks, team_threads(L), 0, stream>>>(a);
     else if constexpr (!(L == 1024 && K == 4))
