@@ -307,12 +307,12 @@ __device__ __forceinline__ void keep_codes(uint32_t (&w)[4], int left) {
   }
 }
 
-// Scores to weights for one row tile and page; m, l, o: the row's running maximum, this lane's share of the sum of
-// weights, and the sums.  `s` in base-2 units with the scale in it (or, with a cap, divided by the cap); it becomes the
-// values' weights.
-template <int TILES>
-__device__ __forceinline__ void weigh(float (&s)[16], const float (&vs)[16], bool masked, uint32_t bits, float cap,
-                                      float& m, float& l, f32x4 (&o)[TILES]) {
+// Scores to weights, in parts, for one row tile and page; m, l, o: the row's running maximum, this lane's share of the sum of
+// weights, and the sums.  `s` in base-2 units with the scale in it (or, with a cap, divided by the cap); vs(kk, x): scales of
+// the lane's tokens 8 kk .. 8 kk + 7.
+template <int KP, int TILES, typename F>
+__device__ __forceinline__ void weigh(float (&s)[16], F vs, bool masked, uint32_t bits, float cap, float& m, float& l,
+                                      f32x4 (&o)[TILES], bf16x8 (&pf)[2][KP]) {
   if (cap > 0) {
     const float top = cap * kLog2e;
 #pragma unroll
@@ -324,6 +324,8 @@ __device__ __forceinline__ void weigh(float (&s)[16], const float (&vs)[16], boo
     for (int i = 0; i < 16; ++i)
       if (!(seen >> i & 1)) s[i] = kNegInf;
   }
+  float x[2][8];
+  vs(0, x[0]);
   float top = s[0];
 #pragma unroll
   for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
@@ -338,29 +340,25 @@ __device__ __forceinline__ void weigh(float (&s)[16], const float (&vs)[16], boo
     for (int i = 0; i < TILES; ++i) o[i] *= less;
   }
   const float base = m == kNegInf ? 0.0f : m;
-  float sum = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float p = __builtin_amdgcn_exp2f(s[i] - base);
-    sum += p;
-    s[i] = p * vs[i];
+  for (int kk = 0; kk < 2; ++kk) {
+    if (kk == 0) vs(1, x[1]);                           // under the first half's work
+    float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float p = __builtin_amdgcn_exp2f(s[8 * kk + i] - base);
+      sum[i & 1] += p;
+      x[kk][i] *= p;
+    }
+    l += sum[0] + sum[1];
+    if (masked) {                                       // an unseen token's scale may be anything
+      const uint32_t seen = opaque(bits >> (8 * kk));
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (!(seen >> i & 1)) x[kk][i] = 0.0f;
+    }
+    split<KP>(x[kk], pf[kk]);
   }
-  l += sum;
-  if (masked) {                                         // an unseen token's scale may be anything
-    const uint32_t seen = opaque(bits);
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (!(seen >> i & 1)) s[i] = 0.0f;
-  }
-}
-
-// The weights of eight tokens in parts.
-template <int KP>
-__device__ __forceinline__ void split_weights(const float* w, bf16x8 (&parts)[KP]) {
-  float x[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = w[i];
-  split<KP>(x, parts);
 }
 
 // Eight neighbouring channels (from 8 `lane` on, 16 lanes a row) of a row's results from what N sums hold of it: sums[w] + 8
@@ -484,10 +482,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attn_few(CacheAttnArgs a)
 #pragma unroll
       for (int i = 0; i < Sh::kTiles; ++i) keep_codes<KIND>(vw[i], p.end - pos - 16 * g);
     }
-    weigh<Sh::kTiles>(s, vs, masked, bits, a.cap, m, l, o);
     bf16x8 pf[2][Sh::kP];
+    weigh<Sh::kP, Sh::kTiles>(
+        s,
+        [&](int kk, float(&x)[8]) {
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) split_weights<Sh::kP>(s + 8 * kk, pf[kk]);
+          for (int i = 0; i < 8; ++i) x[i] = vs[8 * kk + i];
+        },
+        masked, bits, a.cap, m, l, o, pf);
 #pragma unroll
     for (int i = 0; i < Sh::kTiles; ++i)
 #pragma unroll
@@ -518,9 +520,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attn_few(CacheAttnArgs a)
   finish_row<T>(a, p, row, ml, of, r16);
 }
 
-// More rows: every wave has RT row tiles of its own, the pages are shared.
-template <typename T, int KIND, int DC, int RT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, 2) void cache_attn_many(CacheAttnArgs a) {
+// More rows: every wave has a row tile of its own, the pages are shared.  SIMD_WAVES: waves a SIMD that the registers are meant
+// for.
+template <typename T, int KIND, int DC, int WAVES, int SIMD_WAVES>
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(SIMD_WAVES, SIMD_WAVES))) void cache_attn_many(CacheAttnArgs a) {
   using Sh = Shape<T, DC>;
   constexpr int kKeys = 4 * Sh::kSteps, kFrags = kKeys + 2 * Sh::kTiles;          // of a widened page
   constexpr int kPageBytes = kFrags * 64 * 16, kSumBytes = WAVES * 16 * Sh::kRow * 4;
@@ -529,21 +532,16 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attn_many(CacheAttnArgs a
   const CacheArgs& c = a.c;
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
-  const Part p = find_part(a, 16 * RT * WAVES);
-  const int row0 = p.row0 + wave * 16 * RT;
+  const Part p = find_part(a, 16 * WAVES);
+  const int row0 = p.row0 + wave * 16;
   const bool idle = row0 >= a.R;                        // it moves pages for the others
-  bf16x8 qf[RT][Sh::kSteps][Sh::kQ];
-  f32x4 o[RT][Sh::kTiles];
-  float m[RT], l[RT];
+  bf16x8 qf[Sh::kSteps][Sh::kQ];
+  f32x4 o[Sh::kTiles];
+  float m = kNegInf, l = 0.0f;
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
+  for (int i = 0; i < Sh::kSteps; ++i) load_queries<T, DC>(a, p, row0 + r16, i, g, qf[i]);
 #pragma unroll
-    for (int i = 0; i < Sh::kSteps; ++i) load_queries<T, DC>(a, p, row0 + rt * 16 + r16, i, g, qf[rt][i]);
-    m[rt] = kNegInf;
-    l[rt] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < Sh::kTiles; ++i) o[rt][i] = f32x4{0, 0, 0, 0};
-  }
+  for (int i = 0; i < Sh::kTiles; ++i) o[i] = f32x4{0, 0, 0, 0};
 
   // a wave's part of a page: pieces of 16 codes a lane, keys (u and chunk) from the first wave on, value tiles from the last
   constexpr int kKeyPieces = 4 * Sh::kChunks, kKeyMine = (kKeyPieces + WAVES - 1) / WAVES;
@@ -604,73 +602,56 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attn_many(CacheAttnArgs a
     walk.next();
     load_page(walk.page, walk.there());
     if (idle) continue;
-    float s[RT][16];
+    const bool masked = pos + kPage > whole;
+    uint32_t bits = 0;
+    if (masked) {
+      const int t = (int)(opaque(row0 + r16) / (uint32_t)a.G);
+      if (t < p.rows) bits = seen_bits(a, p.b, t, p.start, p.rows, pos + 16 * g);
+    }
+    float s[16];
     {
       float ks[16];
       __builtin_memcpy(ks, __builtin_assume_aligned(&sc[0][16 * g], 16), 64);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        f32x4 acc[RT];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) acc[rt] = f32x4{0, 0, 0, 0};
+        f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < Sh::kSteps; ++i) {
           const bf16x8 kf = from[(u * Sh::kSteps + i) * 64];
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int q = Sh::kQ - 1; q >= 0; --q) acc[rt] = mfma(kf, qf[rt][i][q], acc[rt]);
+          for (int q = Sh::kQ - 1; q >= 0; --q) acc = mfma(kf, qf[i][q], acc);
         }
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[rt][4 * u + i] = acc[rt][i] * ks[4 * u + i];
+        for (int i = 0; i < 4; ++i) s[4 * u + i] = acc[i] * ks[4 * u + i];
       }
     }
-    const bool masked = pos + kPage > whole;
-    float vs[16];
-    __builtin_memcpy(vs, __builtin_assume_aligned(&sc[1][16 * g], 16), 64);
-    bf16x8 pf[RT][2][Sh::kP];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      uint32_t bits = 0;
-      if (masked) {
-        const int t = (row0 + rt * 16 + r16) / a.G;
-        bits = t < p.rows ? seen_bits(a, p.b, t, p.start, p.rows, pos + 16 * g) : 0;
-      }
-      weigh<Sh::kTiles>(s[rt], vs, masked, bits, a.cap, m[rt], l[rt], o[rt]);
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) split_weights<Sh::kP>(s[rt] + 8 * kk, pf[rt][kk]);
-    }
+    bf16x8 pf[2][Sh::kP];
+    weigh<Sh::kP, Sh::kTiles>(
+        s, [&](int kk, float(&x)[8]) { __builtin_memcpy(x, __builtin_assume_aligned(&sc[1][16 * g + 8 * kk], 16), 32); },
+        masked, bits, a.cap, m, l, o, pf);
 #pragma unroll
     for (int i = 0; i < Sh::kTiles; ++i)
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
         const bf16x8 vf = from[(kKeys + 2 * i + kk) * 64];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-          for (int q = Sh::kP - 1; q >= 0; --q) o[rt][i] = mfma(vf, pf[rt][kk][q], o[rt][i]);
+        for (int q = Sh::kP - 1; q >= 0; --q) o[i] = mfma(vf, pf[kk][q], o[i]);
       }
   }
 
-  // a row's channels side by side again, by way of the pages' LDS, a tile of 16 rows at a time
+  // a row's channels side by side again, by way of the pages' LDS
   float* sums = (float*)lds + wave * 16 * Sh::kRow;
+  l = query_sum(l);
   __syncthreads();
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    l[rt] = query_sum(l[rt]);
+  for (int i = 0; i < Sh::kTiles; ++i) *(f32x4*)(sums + r16 * Sh::kRow + 16 * i + 4 * g) = o[i];
+  wave_lds_sync();
 #pragma unroll
-    for (int i = 0; i < Sh::kTiles; ++i) *(f32x4*)(sums + r16 * Sh::kRow + 16 * i + 4 * g) = o[rt][i];
-    wave_lds_sync();
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const float2 ml[1] = {float2{__shfl(m[rt], i + g), __shfl(l[rt], i + g)}};
-      const float* const of[1] = {sums + (i + g) * Sh::kRow};
-      const int row = row0 + rt * 16 + i + g;
-      if (row < a.R) finish_row<T>(a, p, row, ml, of, r16);
-    }
-    wave_lds_sync();
+  for (int i = 0; i < 16; i += 4) {
+    const float2 ml[1] = {float2{__shfl(m, i + g), __shfl(l, i + g)}};
+    const float* const of[1] = {sums + (i + g) * Sh::kRow};
+    const int row = row0 + i + g;
+    if (row < a.R) finish_row<T>(a, p, row, ml, of, r16);
   }
 }
 
@@ -734,71 +715,68 @@ __global__ __launch_bounds__(1024) void cache_attn_join(CacheAttnArgs a) {
 // How a call's rows lie on workgroups.
 struct Plan {
   bool few;               // up to one row tile: waves with pages of their own
-  int waves, tiles;       // of a workgroup, of a wave
+  int waves;              // of a workgroup
+  int row_blocks, splits;
 };
 
 // Few rows: eight waves where that alone gives most CUs a workgroup (no split, no join: 32 sequences of 4000 tokens, 8 key
-// heads of 128, 47 us against 52 with four waves and two splits), else four and splits (one sequence of 4000 tokens, 8 heads of
+// heads of 128, 46 us against 52 with four waves and two splits), else four and splits (one sequence of 4000 tokens, 8 heads of
 // 64: 11 us against 21).  More rows: four waves up to 64 rows; beyond, eight share the widening of a page (64 rows of
-// 16 scenes x 4 heads of 128: 93 us against 116), but heads above 64 channels with rows enough for two workgroups a CU
-// take two row tiles a wave, whose products share each fragment's LDS read (8 x 4000 rows: 396 us against 456).
+// 16 scenes x 4 heads of 128: 96 us against 116).  Splits make up eight waves a CU, where every four waves of few rows, or
+// every workgroup of more, still have four pages.
 Plan plan_of(const CacheAttnArgs& a) {
+  Plan p;
   const int64_t heads = (int64_t)a.c.B * a.c.Hk;
-  if (a.R <= 16) return {true, heads >= 192 ? 8 : 4, 1};
-  if (a.R <= 64) return {false, 4, 1};
-  if (a.elem_bytes == 2 && a.c.D > 64 && heads * ((a.R + 127) / 128) >= 512) return {false, 4, 2};
-  return {false, 8, 1};
-}
-
-void set_splits(CacheAttnArgs& a) {
-  const Plan plan = plan_of(a);
-  const int held = plan.few ? 16 : 16 * plan.waves * plan.tiles;
-  a.row_blocks = (a.R + held - 1) / held;
-  const int64_t blocks = (int64_t)a.c.B * a.c.Hk * a.row_blocks;
-  // splits: eight waves a CU, where every four waves of few rows, or every workgroup of more, still have four pages
+  p.few = a.R <= 16;
+  p.waves = (p.few ? heads >= 192 : a.R > 64) ? 8 : 4;
+  const int held = p.few ? 16 : 16 * p.waves;
+  p.row_blocks = (a.R + held - 1) / held;
+  const int64_t blocks = heads * p.row_blocks, full = p.waves == 4 ? 512 : 256;
   int64_t want = 1;
-  if (plan.waves == 4 ? blocks < 256 || plan.few : blocks < 192 && !plan.few) {
-    want = ((plan.waves == 4 ? 512 : 256) + blocks - 1) / blocks;
+  if (p.few ? p.waves == 4 : blocks < (p.waves == 4 ? 256 : 192)) {
     const int64_t most = (a.c.W + 3) / 4;
+    want = (full + blocks - 1) / blocks;
     if (want > most) want = most;
   }
-  a.splits = (int)(want < 1 ? 1 : want > kMostSplits ? kMostSplits : want);
+  p.splits = (int)(want < 1 ? 1 : want > kMostSplits ? kMostSplits : want);
+  return p;
 }
 
 template <typename T, int KIND, int DC>
-void launch_rows(const CacheAttnArgs& a, unsigned blocks, hipStream_t stream) {
-  const Plan plan = plan_of(a);
+void launch_rows(const CacheAttnArgs& a, const Plan& plan, unsigned blocks, hipStream_t stream) {
   if (plan.few) {
     if (plan.waves == 8)
       cache_attn_few<T, KIND, DC, 8><<<blocks, 512, 0, stream>>>(a);
     else
       cache_attn_few<T, KIND, DC, 4><<<blocks, 256, 0, stream>>>(a);
-  } else if (plan.waves == 8) {
-    cache_attn_many<T, KIND, DC, 1, 8><<<blocks, 512, 0, stream>>>(a);
-  } else if (plan.tiles == 1) {
-    cache_attn_many<T, KIND, DC, 1, 4><<<blocks, 256, 0, stream>>>(a);
-  } else if constexpr (sizeof(T) == 2 && DC == 128) {
-    cache_attn_many<T, KIND, DC, 2, 4><<<blocks, 256, 0, stream>>>(a);
+  } else if (plan.waves == 4) {
+    cache_attn_many<T, KIND, DC, 4, sizeof(T) == 2 && DC < 128 ? 4 : 2><<<blocks, 256, 0, stream>>>(a);
+  } else if (sizeof(T) == 2 && (DC < 128 || blocks >= 448)) {
+    // four waves a SIMD: with heads of 128 it takes tighter code, which pays where two workgroups a CU are there to
+    // use it (8 x 4000 rows: 371 us against 450; 2 x 4000 rows: 245 against 218)
+    if constexpr (sizeof(T) == 2) cache_attn_many<T, KIND, DC, 8, 4><<<blocks, 512, 0, stream>>>(a);
+  } else if constexpr (sizeof(T) == 4 || DC == 128) {
+    cache_attn_many<T, KIND, DC, 8, 2><<<blocks, 512, 0, stream>>>(a);
   }
 }
 
 template <typename T, int KIND>
-void launch_width(const CacheAttnArgs& a, unsigned blocks, hipStream_t stream) {
+void launch_width(const CacheAttnArgs& a, const Plan& plan, unsigned blocks, hipStream_t stream) {
   if (a.c.D <= 32)
-    launch_rows<T, KIND, 32>(a, blocks, stream);
+    launch_rows<T, KIND, 32>(a, plan, blocks, stream);
   else if (a.c.D <= 64)
-    launch_rows<T, KIND, 64>(a, blocks, stream);
+    launch_rows<T, KIND, 64>(a, plan, blocks, stream);
   else
-    launch_rows<T, KIND, 128>(a, blocks, stream);
+    launch_rows<T, KIND, 128>(a, plan, blocks, stream);
 }
 
 template <typename T>
-hipError_t launch_type(const CacheAttnArgs& a, hipStream_t stream) {
+hipError_t launch_type(const CacheAttnArgs& a, const Plan& plan, hipStream_t stream) {
   const unsigned blocks = (unsigned)((int64_t)a.c.B * a.c.Hk * a.row_blocks * a.splits);
   if (a.c.codes == FBEV_CODES_E4M3)
-    launch_width<T, FBEV_CODES_E4M3>(a, blocks, stream);
+    launch_width<T, FBEV_CODES_E4M3>(a, plan, blocks, stream);
   else
-    launch_width<T, FBEV_CODES_INT8>(a, blocks, stream);
+    launch_width<T, FBEV_CODES_INT8>(a, plan, blocks, stream);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   // a wave for every eight splits; two at least, which have a thread for each channel
@@ -809,16 +787,16 @@ hipError_t launch_type(const CacheAttnArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-size_t cache_attention_workspace_bytes(const CacheAttnArgs& args) {
-  CacheAttnArgs a = args;
-  set_splits(a);
-  if (a.splits == 1) return 0;
-  return (size_t)a.splits * a.c.B * a.c.Hk * a.R * (a.c.D + 2) * sizeof(float);
+size_t cache_attention_workspace_bytes(const CacheAttnArgs& a) {
+  const int splits = plan_of(a).splits;
+  return splits == 1 ? 0 : (size_t)splits * a.c.B * a.c.Hk * a.R * (a.c.D + 2) * sizeof(float);
 }
 
 hipError_t launch_cache_attention(CacheAttnArgs a, hipStream_t stream) {
-  set_splits(a);
-  return a.elem_bytes == 4 ? launch_type<float>(a, stream) : launch_type<__bf16>(a, stream);
+  const Plan plan = plan_of(a);
+  a.row_blocks = plan.row_blocks;
+  a.splits = plan.splits;
+  return a.elem_bytes == 4 ? launch_type<float>(a, plan, stream) : launch_type<__bf16>(a, plan, stream);
 }
 
 }  // namespace fbev
