@@ -31,6 +31,7 @@ namespace fbev {
 namespace {
 
 constexpr int kMostSplits = 512;
+constexpr int kFewSplits = 4;
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -655,7 +656,50 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(SIMD
   }
 }
 
-// Rows split over the pages, a workgroup a row.  A wave takes every waves-th split, eight at a time; the first eight are on
+// Rows split into a few parts: 32 lanes a row, four channels each, all parts' loads in flight.
+template <typename T>
+__global__ __launch_bounds__(256) void cache_attn_join_few(CacheAttnArgs a) {
+  const int64_t n = (int64_t)a.c.B * a.c.Hk * a.R, at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int D = a.c.D, ch = 4 * ((int)threadIdx.x & 31), left = D - ch;
+  if (at >= n || left <= 0) return;
+  const float* p = a.part + at * (D + 2);
+  const int64_t step = n * (D + 2);
+  float2 ml[kFewSplits];
+  float x[kFewSplits][4];
+  float top = kNegInf;
+#pragma unroll
+  for (int s = 0; s < kFewSplits; ++s) {
+    ml[s] = float2{kNegInf, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[s][i] = 0.0f;
+    if (s < a.splits) {
+      ml[s] = float2{p[s * step + D], p[s * step + D + 1]};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left) x[s][i] = p[s * step + ch + i];
+    }
+    top = fmaxf(top, ml[s].x);
+  }
+  float total = 0.0f, y[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int s = 0; s < kFewSplits; ++s) {
+    const float f = share(ml[s].x, ml[s].y, top);
+    if (f == 0.0f) continue;
+    total += f * ml[s].y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] += f * x[s][i];
+  }
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  const int64_t bh = at / a.R;
+  const int row = (int)(at - bh * a.R), t = row / a.G, h = row - t * a.G;
+  const int64_t b = bh / a.c.Hk, hk = bh - b * a.c.Hk;
+  T* out = (T*)a.out + ((b * a.c.T + t) * a.Hq + hk * a.G + h) * D + ch;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < left) out[i] = (T)(y[i] * inv);
+}
+
+// Rows split into many, a workgroup a row.  A wave takes every waves-th split, eight at a time; the first eight are on
 // their way before anything of the shares is known, so a call of few splits waits for memory once.
 template <typename T>
 __global__ __launch_bounds__(1024) void cache_attn_join(CacheAttnArgs a) {
@@ -779,6 +823,10 @@ hipError_t launch_type(const CacheAttnArgs& a, const Plan& plan, hipStream_t str
     launch_width<T, FBEV_CODES_INT8>(a, plan, blocks, stream);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
+  if (a.splits <= kFewSplits) {
+    cache_attn_join_few<T><<<(unsigned)(((int64_t)a.c.B * a.c.Hk * a.R + 7) / 8), 256, 0, stream>>>(a);
+    return hipGetLastError();
+  }
   // a wave for every eight splits; two at least, which have a thread for each channel
   const int waves = a.splits >= 128 ? 16 : a.splits > 16 ? (a.splits + 7) / 8 : 2;
   cache_attn_join<T><<<(unsigned)((int64_t)a.c.B * a.c.Hk * a.R), 64 * waves, 0, stream>>>(a);
