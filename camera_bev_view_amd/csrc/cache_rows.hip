@@ -55,7 +55,7 @@ __device__ __forceinline__ Run find_run(const CacheArgs& c, uint32_t block, int 
 }
 
 __device__ __forceinline__ int kept_rows(const CacheArgs& c, const Run& r) {
-  return c.count ? max(0, min(r.n, c.count[r.b] - r.row)) : r.n;
+  return c.count ? max(0, min(r.n, max(c.count[r.b], 0) - r.row)) : r.n;
 }
 
 // Four words of four bytes turned: out[i] has byte i of w[0 .. 3].

@@ -105,6 +105,18 @@ def test_what_is_dropped():
             same_state(cache, model)
 
 
+def test_no_rows_by_the_least_counts():
+    """Negative counts as far as they go, where a call's rows lie on several pages: no row, and zeros back."""
+    for T in (1, 70, 200):
+        cache, model = both(8, 2, 32, "int8")
+        table, start, count = [[0, 1, 2, 3], [4, 5, 6, 7]], [0, 30], [-2 ** 31, -2 ** 31 + 1]
+        k, v = draw(1, 2, T, 2, 32), draw(2, 2, T, 2, 32)
+        ops.cache_write(cache, k, v, i32(table), i32(start), count=i32(count))
+        same_state(cache, model)
+        for x in ops.cache_read(cache, i32(table), i32(start), T, count=i32(count), dtype=F32):
+            assert not x.any()
+
+
 def test_borders_between_codes():
     """Quotients on a border go to the even code, one step of the type beside it to the nearer one; scales of every size."""
     for kind in ("int8", "e4m3"):
