@@ -166,10 +166,10 @@ fbev_status check_cache_attention(const fbev_cache_desc* cd, const fbev_cache_ro
   if (!aligned(ad->ancestors, 8)) return fail(FBEV_ERR_INVALID_ARGUMENT, "ancestors must be 8-byte aligned");
   const int64_t G = ad->Hq / cd->Hk, rows = (int64_t)cr->T * G, limit = (int64_t)1 << 30;
   if (rows >= limit) return fail(FBEV_ERR_UNSUPPORTED, "T Hq / Hk = %lld rows (limit 2^30 - 1)", (long long)rows);
-  // workgroups of 256 threads stay within a launch's 2^32
-  const int64_t heads = (int64_t)cr->B * cd->Hk, tiles = (rows + 15) / 16, most = (int64_t)1 << 23;
+  // workgroups of up to 512 threads stay below a launch's 2^32
+  const int64_t heads = (int64_t)cr->B * cd->Hk, tiles = (rows + 15) / 16, most = ((int64_t)1 << 23) - 1;
   if (heads > most || (tiles > 0 && heads > most / tiles))
-    return fail(FBEV_ERR_UNSUPPORTED, "B Hk = %lld heads of %lld tiles of 16 rows: above 2^23", (long long)heads,
+    return fail(FBEV_ERR_UNSUPPORTED, "B Hk = %lld heads of %lld tiles of 16 rows: above 2^23 - 1", (long long)heads,
                 (long long)tiles);
   a.Hq = ad->Hq;
   a.G = (int)G;

@@ -560,6 +560,8 @@ typedef enum { FBEV_CODES_INT8 = 0, FBEV_CODES_E4M3 = 1 } fbev_codes;
  *               calls that overlap; NULL is fine without grad_weight.
  *
  * C up to FBEV_MAX_RMS_CHANNELS; 0 rows are allowed (grad_weight is zero then).
+ * Without codes the sum of h^2 is fp32: past 2^128 it is infinite and y zero, and
+ * squares below 2^-126 lose digits (which eps hides unless it is as small).
  */
 #define FBEV_MAX_RMS_CHANNELS 16384
 
@@ -642,8 +644,9 @@ fbev_status fbev_cache_read(const fbev_cache_desc* cd, const fbev_cache_rows* cr
  *   FBEV_DRAFT_TREE  : row j where bit j % 64 of ancestors[b, i, j / 64] is set
  *                      (its own bit is up to the caller): several drafted continuations at once.
  * With `count`, rows t >= count[b] are padding: nobody sees them and they get
- * zeros, as does a query that sees no token.  What unseen tokens hold, NaN
- * among it, reaches no query.
+ * zeros, as does a query that sees no token.  What unseen tokens hold reaches no
+ * query: NaN in the scales of any of them, and any bytes at all behind the
+ * call's last row (the tokens before it hold codes as fbev_cache_write makes them).
  *
  *   q   : [B, T, Hq, D] by element strides, channels contiguous, any alignment.
  *   ancestors : [B, T, words] uint64, words >= ceil(T / 64); NULL without a tree.

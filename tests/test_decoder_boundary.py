@@ -132,6 +132,8 @@ def attn(lib, **kw):
     (attn, dict(dtype=2), UNSUPPORTED, "dtype"),
     (attn, dict(T=1 << 29), UNSUPPORTED, "rows"),
     (attn, dict(B=1 << 20, T=1 << 10), UNSUPPORTED, "tiles"),
+    (attn, dict(B=1 << 22, T=1), UNSUPPORTED, "tiles"),
+    (attn, dict(B=1 << 16, T=1 << 10, Hq=2, Hk=2, D=40), UNSUPPORTED, "tiles"),
     (attn, dict(W=1000, ws=None), INVALID, "workspace"),
     (attn, dict(W=1000, have=16), INVALID, "workspace"),
     (attn, dict(W=1000, ws=FAKE + 8), INVALID, "16-byte"),
@@ -159,6 +161,8 @@ def test_null_descriptors_and_empty_calls(lib):
     assert write(lib, T=0, table=None, start=None) == 0 and write(lib, W=0, table=None) == 0
     assert read(lib, T=0) == 0 and attn(lib, B=0, q=None, out=None, ws=None, have=0) == 0
     assert lib.fbev_cache_read(cache(), rows(), 0, None, None, None) == 0
+    # the most workgroups of one launch
+    assert lib.fbev_cache_attention_workspace(cache(), rows(B=(1 << 22) - 1, T=1), ad, 0, ctypes.byref(n)) == 0
     # few rows over many tokens need a workspace, many rows none
     assert lib.fbev_cache_attention_workspace(cache(), rows(T=1, W=1000), ad, 0, ctypes.byref(n)) == 0 and n.value > 0
     assert lib.fbev_cache_attention_workspace(cache(), rows(B=300, T=640, W=9), ad, 0, ctypes.byref(n)) == 0
