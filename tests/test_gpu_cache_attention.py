@@ -241,6 +241,22 @@ def test_views_and_addresses():
     check(draw(4, 40, 4, 7, 3).permute(3, 2, 1, 0), cache, model, table, [83, 33, 70], "chain", label="channels apart")
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,T,Hq,Hk,D,n,drafts", [
+    (50, 1, 8, 4, 32, 70, "chain"), (64, 3, 6, 3, 64, 200, "tree"), (200, 2, 8, 1, 128, 130, "chain"),
+    (70, 40, 4, 4, 40, 64, "chain"), (32, 90, 6, 2, 128, 300, "chain"), (33, 130, 4, 2, 96, 290, "tree"),
+    (75, 130, 4, 2, 128, 5, "chain"), (112, 260, 2, 2, 64, 0, "tree"), (100, 70, 2, 2, 32, 63, "none")])
+def test_many_sequences(B, T, Hq, Hk, D, n, drafts, dtype):
+    """Enough sequences and heads for workgroups of more waves, calls that need no split and those split in two."""
+    say(f"[case] {B} sequences of {n} + {T}")
+    rng = np.random.default_rng(B)
+    start = [int(x) for x in rng.integers(max(0, n - 40), n + 1, B)]
+    cache, model, table = filled(B, [s + (0 if drafts == "none" else T) for s in start], Hk, D, "e4m3" if B % 2 else "int8")
+    count = [int(x) for x in rng.integers(0, T + 1, B)] if B > 70 else None
+    bits = random_trees(B, B, T) if drafts == "tree" else None
+    check(draw(B, B, T, Hq, D, dtype=dtype), cache, model, table, start, drafts, count, bits)
+
+
 def test_long_caches():
     """Splits over workgroups and their join, more than 64 of them."""
     n, D = 40003, 32
@@ -367,3 +383,34 @@ def test_results_do_not_change_from_run_to_run():
     q = draw(5, 2, 15, 8, 64, dtype=BF16)
     runs = [ops.cache_attention(q, cache, i32(table.tolist()), i32([2985, 85])) for _ in range(3)]
     assert torch.equal(runs[0], runs[1]) and torch.equal(runs[0], runs[2])
+
+
+def test_two_calls_at_once():
+    """Calls that split their tokens, on two streams at the same time, and two captured ones replayed in turn."""
+    cases = []
+    for i, (n, T, dtype) in enumerate(((6000, 1, BF16), (5000, 40, F32))):
+        cache, model, table = filled(20 + i, [n + T], 2, 64, "int8")
+        q = draw(i, 1, T, 8, 64, dtype=dtype)
+        cases.append((q, cache, i32(table.tolist()), i32([n])))
+    want = [ops.cache_attention(*c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    held = [[], []]
+    for _ in range(20):
+        for s, c, h in zip(streams, cases, held):
+            with torch.cuda.stream(s):
+                h.append(ops.cache_attention(*c))
+    torch.cuda.synchronize()
+    for h, w in zip(held, want):
+        assert all(torch.equal(x, w) for x in h)
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in cases], []
+    for g, c in zip(graphs, cases):
+        with torch.cuda.graph(g):
+            outs.append(ops.cache_attention(*c))
+    for k in range(3):
+        for (q, *_), g in zip(cases, graphs):
+            q.mul_(-1 if k else 1)
+            g.replay()
+        torch.cuda.synchronize()
+        for o, c in zip(outs, cases):
+            assert torch.equal(o, ops.cache_attention(*c)), k
