@@ -307,16 +307,25 @@ __device__ __forceinline__ void keep_codes(uint32_t (&w)[4], int left) {
   }
 }
 
+// What a row's scores are taken against: its running maximum, once there is one.
+__device__ __forceinline__ float base_of(float m) { return m == kNegInf ? 0.0f : m; }
+
+// A score from a product and its token's scale: against the base in base-2 units, or, with a cap, divided by the cap (the base
+// comes off behind the tanh).
+__device__ __forceinline__ float score(float acc, float scale, bool capped, float base) {
+  return fmaf(acc, scale, capped ? 0.0f : -base);
+}
+
 // Scores to weights, in parts, for one row tile and page; m, l, o: the row's running maximum, this lane's share of the sum of
-// weights, and the sums.  `s` in base-2 units with the scale in it (or, with a cap, divided by the cap); vs(kk, x): scales of
-// the lane's tokens 8 kk .. 8 kk + 7.
+// weights, and the sums.  `s`: of score(); vs(kk, x): scales of the lane's tokens 8 kk .. 8 kk + 7.
 template <int KP, int TILES, typename F>
 __device__ __forceinline__ void weigh(float (&s)[16], F vs, bool masked, uint32_t bits, float cap, float& m, float& l,
                                       f32x4 (&o)[TILES], bf16x8 (&pf)[2][KP]) {
+  const float base = base_of(m);
   if (cap > 0) {
     const float top = cap * kLog2e;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] = top * tanh_fast<true>(s[i]);
+    for (int i = 0; i < 16; ++i) s[i] = fmaf(top, tanh_fast<true>(s[i]), -base);
   }
   if (masked) {
     const uint32_t seen = opaque(bits);
@@ -331,22 +340,24 @@ __device__ __forceinline__ void weigh(float (&s)[16], F vs, bool masked, uint32_
   for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
   top = query_max(top);
   // the maximum moves where it grows by 2^8 or more: weights stay below that, and sums in fp32 do not mind
-  if (__any(top > m + 8.0f)) {
-    const float to = top > m + 8.0f ? top : m;
-    const float less = to == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+  const bool moves = top > (m == kNegInf ? kNegInf : 8.0f);
+  if (__any(moves)) {
+    const float to = moves ? base + top : m, by = moves ? to - base : 0.0f;
+    const float less = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(-by);
     m = to;
     l *= less;
 #pragma unroll
     for (int i = 0; i < TILES; ++i) o[i] *= less;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] -= by;
   }
-  const float base = m == kNegInf ? 0.0f : m;
 #pragma unroll
   for (int kk = 0; kk < 2; ++kk) {
     if (kk == 0) vs(1, x[1]);                           // under the first half's work
     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float p = __builtin_amdgcn_exp2f(s[8 * kk + i] - base);
+      const float p = __builtin_amdgcn_exp2f(s[8 * kk + i]);
       sum[i & 1] += p;
       x[kk][i] *= p;
     }
@@ -458,6 +469,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attn_few(CacheAttnArgs a)
   load_keys(page);
   load_values(page);
   while (walk.there()) {
+    const float base = base_of(m);
     float s[16];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -469,7 +481,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attn_few(CacheAttnArgs a)
         for (int q = Sh::kQ - 1; q >= 0; --q) acc = mfma(kf, ((const bf16x8*)lds)[(i * Sh::kQ + q) * 64 + lane], acc);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[4 * u + i] = acc[i] * (unit * ks[4 * u + i]);
+      for (int i = 0; i < 4; ++i) s[4 * u + i] = score(acc[i], unit * ks[4 * u + i], a.cap > 0, base);
     }
     const int pos = walk.at * kPage;
     walk.next();
@@ -608,6 +620,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(SIMD
       const int t = (int)(opaque(row0 + r16) / (uint32_t)a.G);
       if (t < p.rows) bits = seen_bits(a, p.b, t, p.start, p.rows, pos + 16 * g);
     }
+    const float base = base_of(m);
     float s[16];
     {
       float ks[16];
@@ -622,7 +635,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(SIMD
           for (int q = Sh::kQ - 1; q >= 0; --q) acc = mfma(kf, qf[i][q], acc);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[4 * u + i] = acc[i] * ks[4 * u + i];
+        for (int i = 0; i < 4; ++i) s[4 * u + i] = score(acc[i], ks[4 * u + i], a.cap > 0, base);
       }
     }
     bf16x8 pf[2][Sh::kP];
