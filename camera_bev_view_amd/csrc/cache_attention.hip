@@ -163,12 +163,21 @@ struct Part {
   int p0, p1;             // its pages
 };
 
+// APART: what follows on an XCD lies eight apart.  Sequences differ in length, and all heads of a long one on one XCD would
+// outlast the others (8 x 4000 rows behind 3000 to 1500 tokens: 316 us against 360).  Not where every workgroup has a CU
+// and pages of its own (32 sequences of 8192 to 4096 tokens: 89 us against 87).
+template <bool APART>
 __device__ __forceinline__ Part find_part(const CacheAttnArgs& a, int rows_held) {
   const CacheArgs& c = a.c;
   Part p;
   int id = xcd_block(blockIdx.x, gridDim.x);
   const int rb = id % a.row_blocks;
   id /= a.row_blocks;
+  if constexpr (APART) {
+    const int n = c.B * c.Hk * a.splits, q = n / 8, r = n % 8, more = r * (q + 1);
+    const int x = id < more ? id / (q + 1) : r + (id - more) / max(q, 1);
+    id = 8 * (id < more ? id - x * (q + 1) : id - more - (x - r) * q) + x;
+  }
   p.split = id % a.splits;
   p.bh = id / a.splits;
   p.b = p.bh / c.Hk;
@@ -179,8 +188,9 @@ __device__ __forceinline__ Part find_part(const CacheAttnArgs& a, int rows_held)
   const int last_t = (min(p.row0 + rows_held, a.R) - 1) / a.G;
   p.end = p.rows > 0 ? (int)visible_end(a, p.start, p.rows, last_t) : 0;
   const int pages = (p.end + kPage - 1) / kPage;
-  p.p0 = (int)((int64_t)pages * p.split / a.splits);
-  p.p1 = (int)((int64_t)pages * (p.split + 1) / a.splits);
+  const int each = pages / a.splits, rest = pages % a.splits;
+  p.p0 = each * p.split + rest * p.split / a.splits;
+  p.p1 = each * (p.split + 1) + rest * (p.split + 1) / a.splits;
   return p;
 }
 
@@ -434,7 +444,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attn_few(CacheAttnArgs a)
   const CacheArgs& c = a.c;
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
-  const Part p = find_part(a, 16);
+  const Part p = find_part<WAVES == 4>(a, 16);
   if (wave < Sh::kSteps) {
     bf16x8 parts[Sh::kQ];
     load_queries<T, DC>(a, p, p.row0 + r16, wave, g, parts);
@@ -544,7 +554,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(SIMD
   const CacheArgs& c = a.c;
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
-  const Part p = find_part(a, 16 * WAVES);
+  const Part p = find_part<true>(a, 16 * WAVES);
   const int row0 = p.row0 + wave * 16;
   const bool idle = row0 >= a.R;                        // it moves pages for the others
   bf16x8 qf[Sh::kSteps][Sh::kQ];
