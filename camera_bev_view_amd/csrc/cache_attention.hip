@@ -792,8 +792,10 @@ struct Plan {
 
 // Few rows: eight waves where that alone gives most CUs a workgroup (no split, no join: 32 sequences of 4000 tokens, 8 key
 // heads of 128, 46 us against 52 with four waves and two splits), else four and splits (one sequence of 4000 tokens, 8 heads of
-// 64: 11 us against 21).  More rows: four waves up to 64 rows; beyond, eight share the widening of a page (64 rows of
-// 16 scenes x 4 heads of 128: 96 us against 116).  Splits make up eight waves a CU, where every four waves of few rows, or
+// 64: 10 us against 21).  More rows: four waves up to 64 rows; beyond, eight share the widening of a page (64 rows of
+// 16 scenes x 4 heads of 128: 73 us against 116).  Splits make up 512 workgroups of four waves, 256 of eight (fp32, 900 rows of
+// 8 heads of 32 over 3600 tokens: 32 us against 41 with 512), or 512 where a wave's work on a page is long and its registers
+// let two in (bf16, heads of 128: 1000 rows of 16 heads behind 9000 tokens 153 us against 164); every four waves of few rows, or
 // every workgroup of more, still have four pages.
 Plan plan_of(const CacheAttnArgs& a) {
   Plan p;
@@ -802,14 +804,10 @@ Plan plan_of(const CacheAttnArgs& a) {
   p.waves = (p.few ? heads >= 192 : a.R > 64) ? 8 : 4;
   const int held = p.few ? 16 : 16 * p.waves;
   p.row_blocks = (a.R + held - 1) / held;
-  const int64_t blocks = heads * p.row_blocks, full = p.waves == 4 ? 512 : 256;
+  const bool two = p.waves == 4 || (a.elem_bytes == 2 && a.c.D > 64);
+  const int64_t blocks = heads * p.row_blocks, full = two ? 512 : 256, most = (a.c.W + 3) / 4;
   int64_t want = 1;
-  const int64_t most = (a.c.W + 3) / 4;
-  if (p.few ? p.waves == 4 : blocks < (p.waves == 4 ? 256 : 192)) {
-    want = (full + blocks - 1) / blocks;
-  } else if (!p.few && p.waves == 8 && blocks < 384 && a.elem_bytes == 2 && a.c.D > 64) {
-    want = 2;             // two workgroups a CU (2 x 4000 rows, 4 heads of 128, 6000 tokens: 208 us against 219)
-  }
+  if (p.few ? p.waves == 4 : blocks < (p.waves == 4 ? 256 : two ? 384 : 192)) want = (full + blocks - 1) / blocks;
   if (want > most) want = most;
   p.splits = (int)(want < 1 ? 1 : want > kMostSplits ? kMostSplits : want);
   return p;
@@ -824,12 +822,10 @@ void launch_rows(const CacheAttnArgs& a, const Plan& plan, unsigned blocks, hipS
       cache_attn_few<T, KIND, DC, 4><<<blocks, 256, 0, stream>>>(a);
   } else if (plan.waves == 4) {
     cache_attn_many<T, KIND, DC, 4, sizeof(T) == 2 && DC < 128 ? 4 : 2><<<blocks, 256, 0, stream>>>(a);
-  } else if (sizeof(T) == 2 && (DC < 128 || blocks >= 448)) {
-    // four waves a SIMD: with heads of 128 it takes tighter code, which pays where two workgroups a CU are there to
-    // use it (8 x 4000 rows: 371 us against 450; 2 x 4000 rows: 245 against 218)
-    if constexpr (sizeof(T) == 2) cache_attn_many<T, KIND, DC, 8, 4><<<blocks, 512, 0, stream>>>(a);
-  } else if constexpr (sizeof(T) == 4 || DC == 128) {
-    cache_attn_many<T, KIND, DC, 8, 2><<<blocks, 512, 0, stream>>>(a);
+  } else {
+    // bf16 takes tighter code that leaves four waves a SIMD (8 x 4000 rows of 128 channels: 371 us against 450; 25 x 256 rows:
+    // 89 against 102; 2 x 1200 rows, a workgroup on every third CU: 25.0 against 24.3); fp32's parts of queries do not fit
+    cache_attn_many<T, KIND, DC, 8, sizeof(T) == 2 ? 4 : 2><<<blocks, 512, 0, stream>>>(a);
   }
 }
 
