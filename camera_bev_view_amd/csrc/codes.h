@@ -38,8 +38,8 @@ struct Codes {
   // A number on the same side of every border as the exact x / scale: the quotient rounded to fp32, moved off itself by one
   // step towards the exact one where it is even (borders are even in fp32, so an odd one lies on none).  Where
   // x is of fp32 its quotient is on a border or at least 2^-33 of itself away: fp64 tells.
-  static __device__ __forceinline__ float side_of(double x, float scale) {
-    const double exact = x / (double)scale;
+  static __device__ __forceinline__ float side_of(double x, double scale) {
+    const double exact = x / scale;
     const float q = (float)exact;
     const double rest = exact - (double)q;
     uint32_t b = __builtin_bit_cast(uint32_t, q);
@@ -51,9 +51,11 @@ struct Codes {
   static __device__ __forceinline__ uint32_t pack(const float (&x)[4], float scale, float inverse) {
     return pack(x, scale, inverse, [&](int i) { return x[i]; });
   }
-  // The same where x[i] are rounded: exact(i) is the i-th value in fp64.
-  template <typename F>
-  static __device__ __forceinline__ uint32_t pack(const float (&x)[4], float scale, float inverse, F exact) {
+  // The same where x[i], the scale and its inverse are rounded (quotients then are within 2^-21 of themselves): exact(i) and
+  // scale are the i-th value and the scale in fp64.
+  template <typename F, typename S>
+  static __device__ __forceinline__ uint32_t pack(const float (&x)[4], S scale, float inverse, F exact) {
+    constexpr bool kWide = sizeof(S) == 8;
     float q[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) q[i] = x[i] * inverse;
@@ -83,10 +85,10 @@ struct Codes {
         off = fmaxf(off, fabsf(q[i] - (n - kTurn)));
         t[i] = __builtin_bit_cast(uint32_t, n);
       }
-      if (off > 0.49996f) {
+      if (off > (kWide ? 0.4999f : 0.49996f)) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if constexpr (sizeof(exact(0)) == 8) {
+          if constexpr (kWide) {
             t[i] = __builtin_bit_cast(uint32_t, side_of(exact(i), scale) + kTurn);
           } else {
             // the rest that the nearest integer n leaves of x is exact in fp32, and n off by one at most

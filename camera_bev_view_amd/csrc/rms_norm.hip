@@ -86,21 +86,27 @@ __device__ __forceinline__ void load_weight(const float* w, int c, int left, flo
   }
 }
 
-__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
 
-// The largest over aligned groups of N lanes (a power of two up to 64).
-__device__ __forceinline__ uint32_t lanes_max(uint32_t x, int n) {
-  if (n >= 2) x = umax(x, dpp<kQuadSwap1>(x));
-  if (n >= 4) x = umax(x, dpp<kQuadSwap2>(x));
-  if (n >= 8) x = umax(x, dpp<kHalfMirror>(x));
-  if (n >= 16) x = umax(x, dpp<kRowMirror>(x));
+// The largest over aligned groups of n lanes (a power of two up to 64).
+template <typename X>
+__device__ __forceinline__ X lanes_max(X x, int n) {
+  if (n >= 2) x = larger(x, dpp<kQuadSwap1>(x));
+  if (n >= 4) x = larger(x, dpp<kQuadSwap2>(x));
+  if (n >= 8) x = larger(x, dpp<kHalfMirror>(x));
+  if (n >= 16) x = larger(x, dpp<kRowMirror>(x));
   if (n >= 32) {
-    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
-    x = umax(r[0], r[1]);
+    const uint32_t b = __builtin_bit_cast(uint32_t, x);
+    const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+    const uint32_t p = r[0], q = r[1];
+    x = larger(__builtin_bit_cast(X, p), __builtin_bit_cast(X, q));
   }
   if (n >= 64) {
-    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-    x = umax(r[0], r[1]);
+    const uint32_t b = __builtin_bit_cast(uint32_t, x);
+    const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    const uint32_t p = r[0], q = r[1];
+    x = larger(__builtin_bit_cast(X, p), __builtin_bit_cast(X, q));
   }
   return x;
 }
@@ -161,17 +167,17 @@ __device__ __forceinline__ X team_sum(X x, double* slots) {
   return x;
 }
 
-template <int L>
-__device__ __forceinline__ uint32_t team_max(uint32_t x, double* slots) {
+template <int L, typename X>
+__device__ __forceinline__ X team_max(X x, double* slots) {
   if constexpr (L <= 64) return lanes_max(x, L);
   x = lanes_max(x, 64);
   __syncthreads();
-  uint32_t* mine = (uint32_t*)slots;
+  X* mine = (X*)slots;
   if ((threadIdx.x & 63) == 0) mine[threadIdx.x >> 6] = x;
   __syncthreads();
-  x = 0;
+  x = mine[0];
 #pragma unroll
-  for (int i = 0; i < L / 64; ++i) x = umax(x, mine[i]);
+  for (int i = 1; i < L / 64; ++i) x = larger(x, mine[i]);
   return x;
 }
 
@@ -183,73 +189,92 @@ __device__ __forceinline__ int64_t row_offset(int64_t row, int64_t inner, const 
   return o * s[0] + (row - (int64_t)o * inner) * s[1];
 }
 
-// y of a row in 8 bits (y = h w r, rounded once): a scale for each `block` channels.  Blocks are narrower than the row only where a lane's pieces lie
-// L apart and a block's 4 to 32 lanes side by side.
+// y = h w r of a row in 8 bits, a scale for each `block` channels.  The codes are those of the exact y over its exact scale,
+// where r cancels but for the least one:  r = 2^e m,  p = (2^e h) w,  code = nearest(p m / max(max |p| m / most, 2^-126)).
+// p is taken in fp32 and a code near a border again in fp64, where the product is exact; the scale takes what rounding dropped
+// of the largest p, and is rounded once.
+// Blocks are narrower than the row only where a lane's pieces lie L apart and a block's 4 to 32 lanes side by side.
 template <int KIND, int L, int K, int V>
-__device__ __forceinline__ void store_codes(const RmsArgs& a, int64_t row, int lane, bool mine, const float (&y)[K][V],
-                                            const float (&h)[K][V], double r, double* slots) {
+__device__ __forceinline__ void store_codes(const RmsArgs& a, int64_t row, int lane, bool mine, const float (&h)[K][V], double r,
+                                            double* slots) {
+#pragma clang fp contract(off)
   using Cd = Codes<KIND>;
   const int nb = a.block < a.C ? a.block / V : 0;       // lanes of a block (0: the row)
   const int blocks = nb ? (a.C + a.block - 1) / a.block : 1;
   uint8_t* out = (uint8_t*)a.y + row * a.C;
+  const int e = __builtin_amdgcn_frexp_exp(r);
+  const double m = __builtin_amdgcn_frexp_mant(r);
+  float x[K][V], w[K][V], p[K][V], rest[K];
   uint32_t top[K];
+  // the row's largest where a row is a block, else each block's
+  const auto widest = [&](auto& t) {
+    if (nb == 0) {
+      auto all = t[0];
+#pragma unroll
+      for (int k = 1; k < K; ++k) all = larger(all, t[k]);
+      all = team_max<L>(all, slots);
+#pragma unroll
+      for (int k = 0; k < K; ++k) t[k] = all;
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k) t[k] = lanes_max(t[k], nb);
+    }
+  };
 #pragma unroll
   for (int k = 0; k < K; ++k) {
+    const int c = (lane + L * k) * V;
+    load_weight(a.weight, c, a.C - c, w[k], V);
     top[k] = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) top[k] = umax(top[k], abs_bits(y[k][i]));
+    for (int i = 0; i < V; ++i) {
+      x[k][i] = __builtin_amdgcn_ldexpf(h[k][i], e);
+      p[k][i] = x[k][i] * w[k][i];
+      top[k] = larger(top[k], abs_bits(p[k][i]));
+    }
   }
-  if (nb == 0) {
-    uint32_t t = top[0];
+  widest(top);
 #pragma unroll
-    for (int k = 1; k < K; ++k) t = umax(t, top[k]);
-    t = team_max<L>(t, slots);
+  for (int k = 0; k < K; ++k) {
+    rest[k] = -__builtin_huge_valf();
 #pragma unroll
-    for (int k = 0; k < K; ++k) top[k] = t;
-  } else {
-#pragma unroll
-    for (int k = 0; k < K; ++k) top[k] = lanes_max(top[k], nb);
+    for (int i = 0; i < V; ++i) {
+      const uint32_t sign = __builtin_bit_cast(uint32_t, p[k][i]) & 0x80000000u;
+      const float dropped = fmaf(x[k][i], w[k][i], -p[k][i]);
+      const float along = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, dropped) ^ sign);
+      rest[k] = abs_bits(p[k][i]) == top[k] ? fmaxf(rest[k], along) : rest[k];
+    }
   }
+  widest(rest);
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int c = (lane + L * k) * V, left = a.C - c;
     if (left <= 0 || !mine) continue;
-    const float scale = Cd::scale_of(top[k]);
-    const bool odd = top[k] >= 0x7f800000u;
-    const float inverse = Cd::inverse_of(scale);
-    uint32_t w[V / 4];
+    const double wide = ((double)__builtin_bit_cast(float, top[k]) + (double)rest[k]) * m * (1.0 / Cd::kMost);
+    const bool odd = top[k] >= 0x7f800000u || wide != wide;
+    const float scale = odd ? __builtin_nanf("") : fmaxf((float)wide, kLeastScale);
+    const float inverse = (float)m * Cd::inverse_of(scale);
+    uint32_t codes[V / 4];
 #pragma unroll
     for (int j = 0; j < V / 4; ++j) {
-      float x[4];
+      float y[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = y[k][4 * j + i];
-      w[j] = Cd::pack(x, scale, inverse, [&](int i) {
-        const int at = c + 4 * j + i;       // (read again: few come here, and it would hold registers)
-        return (double)h[k][4 * j + i] * (double)(a.weight && at < a.C ? a.weight[at] : 1.0f) * r;
-      });
-      if (odd) w[j] = 0;
+      for (int i = 0; i < 4; ++i) y[i] = p[k][4 * j + i];
+      codes[j] = Cd::pack(y, fmax(wide, (double)kLeastScale), inverse,
+                          [&](int i) { return (double)x[k][4 * j + i] * (double)w[k][4 * j + i] * m; });
+      if (odd) codes[j] = 0;
     }
     if (left >= V) {
-      __builtin_memcpy(out + c, w, V);
+      __builtin_memcpy(out + c, codes, V);
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (i < left) out[c + i] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
+        if (i < left) out[c + i] = (uint8_t)(codes[i / 4] >> (8 * (i % 4)));
     }
     if (nb ? (lane & (nb - 1)) == 0 : c == 0) a.scales[row * blocks + (nb ? c / a.block : 0)] = scale;
   }
 }
 
-// h (head + tail) w, rounded once: both products with what their rounding drops.
-__device__ __forceinline__ float product(float h, float head, float tail, float w) {
-#pragma clang fp contract(off)
-  const float p = h * head, dp = fmaf(h, tail, fmaf(h, head, -p));
-  const float z = p * w;
-  return z + fmaf(dp, w, fmaf(p, w, -z));
-}
-
-// CODES: the codes have no other rounding than their own.  The sum of squares and 1 / sqrt are fp64, and y is rounded once;
-// where a code's border is near, it is taken in fp64.
+// CODES: the codes have no other rounding than their own.  The sum of squares and 1 / sqrt are fp64.
 template <typename T, int L, int K, bool CODES>
 __global__ __launch_bounds__(team_threads(L)) void rms_fwd(RmsArgs a) {
   constexpr int V = kVec<T>, kThreads = team_threads(L), kTeams = kThreads / L;
@@ -294,20 +319,10 @@ __global__ __launch_bounds__(team_threads(L)) void rms_fwd(RmsArgs a) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) r = fma(r, fma(-0.5 * mean * r, r, 0.5), r);
     r = mean > 0.0 && mean < __builtin_huge_val() ? r : 1.0 / sqrt(mean);
-    const float head = (float)r, tail = (float)(r - (double)head);
-    float y[K][V];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (lane + L * k) * V;
-      float w[V];
-      load_weight(a.weight, c, a.C - c, w, V);
-#pragma unroll
-      for (int i = 0; i < V; ++i) y[k][i] = product(v[k][i], head, tail, w[i]);
-    }
     if (a.codes == FBEV_CODES_E4M3)
-      store_codes<FBEV_CODES_E4M3, L, K, V>(a, row, lane, mine, y, v, r, slots);
+      store_codes<FBEV_CODES_E4M3, L, K, V>(a, row, lane, mine, v, r, slots);
     else
-      store_codes<FBEV_CODES_INT8, L, K, V>(a, row, lane, mine, y, v, r, slots);
+      store_codes<FBEV_CODES_INT8, L, K, V>(a, row, lane, mine, v, r, slots);
   } else {
     float sum = 0.0f;
 #pragma unroll

@@ -547,7 +547,8 @@ typedef enum { FBEV_CODES_INT8 = 0, FBEV_CODES_E4M3 = 1 } fbev_codes;
  *                 one is contiguous; no other output may share memory with the call's tensors.
  *   rstd        : [rows] fp32, 1 / sqrt(mean h^2 + eps), what the backward needs; may be NULL.
  *
- * fbev_rms_norm_codes gives y in 8 bits instead (before any rounding to dtype):
+ * fbev_rms_norm_codes gives y in 8 bits instead.  Nothing is rounded in front: the
+ * codes are nearest to the exact y over its exact scale, which is rounded once.
  *   out    : [rows, C] codes;  scales : [rows, ceil(C / block)] fp32, one for each
  *            `block` channels (32, 64 or 128), or [rows, 1] with block 0 or >= C.
  *

@@ -149,12 +149,12 @@ def check_codes(x, residual, weight, kind, block, eps=1e-6):
     for i in range(blocks):
         part, c = y[:, i * size:(i + 1) * size], got[:, i * size:(i + 1) * size]
         want = np.maximum(np.abs(part).max(axis=1) / dec.MOST[kind], 2.0 ** -126)
-        # y rounded once to fp32 and the quotient once
-        assert (np.abs(s[:, i] - want) <= 2.01 * U * want).all(), f"scales of block {i}"
-        q = np.abs(part / s[:, i, None])
+        # rounded once
+        assert (np.abs(s[:, i] - want) <= 1.001 * U * want).all(), f"scales of block {i}"
+        q = np.abs(part / want[:, None])
         hi = np.clip(np.searchsorted(ladder, q), 1, len(ladder) - 1)
         least = np.minimum(np.abs(q - ladder[hi - 1]), np.abs(ladder[hi] - q))
-        # the nearest number, unless two are equally near to the fp64 value's last digits
+        # the number nearest to the exact quotient, unless two are equally near to the fp64 value's last digits
         off = np.abs(np.abs(c) - q)
         assert (off <= least + 2.0 ** -40 * q).all(), f"block {i}: {float((off - least).max())}"
         assert (c * part >= 0).all()
