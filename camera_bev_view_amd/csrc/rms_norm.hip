@@ -5,13 +5,18 @@
 //   y = h r w,  r = 1 / sqrt(mean_c h^2 + eps)
 //   backward, with u = gy w:   gx = r (u - h r^2 mean_c(u h)) + gh,   gw = sum_rows gy h r
 //
-// Memory bounds it: each tensor once.  A row belongs to a team of 4 to 1024 lanes that keeps it in registers as fp32 between
-// the reduction and the output (at most four 16-byte pieces a lane), so nothing is read twice; teams of up to 64 lanes
-// reduce by lane exchanges alone, wider ones once through LDS.  The team is the narrowest that holds the row in one piece a
-// lane up to 64 lanes: short rows (heads of 32) then fill the wave with rows instead of idle lanes.  Pieces are moved at
+// Memory bounds it: each tensor once.  A row belongs to a team of 4 to 1024 lanes that keeps it in registers between the
+// reduction and the output, so nothing is read twice.  The team is the narrowest that holds the row in one 16-byte piece a
+// lane, up to 1024 pieces (two or four pieces a lane beyond): short rows (heads of 32) fill the wave with rows instead of idle
+// lanes, long ones spread over many waves (2000 rows of 8192 channels both directions: 67 us, with four pieces a lane
+// 100).  Teams of up to 64 lanes reduce by lane exchanges alone, wider ones once through LDS.  Pieces are moved at
 // any alignment (the card's global loads and stores take any address), the piece across a row's end element by element.
-// The backward's workgroups walk many rows and keep their share of gw in registers; partial sums go to the workspace once
-// per workgroup and a second launch adds them in a fixed order.
+// The backward's workgroups walk many rows, the next one on its way, and keep their share of gw in registers; partial sums go
+// to the workspace once per workgroup and a second launch adds them in a fixed order.
+//
+// 8192 rows of 4096 bf16 channels with a residual into e4m3, 128 channels to a scale: 54 us, 4.4 of the copy's 5.1 TB/s; 39
+// of them issue vector instructions.  67584 rows of 256 both directions: 27 + 29 + 4 us, 4.7 TB/s in the two large launches.
+// 40000 x 8 heads of 32 out of a packed projection: 10 us, the launch and 4.1 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -286,25 +291,49 @@ __global__ __launch_bounds__(team_threads(L)) void rms_fwd(RmsArgs a) {
   const bool mine = first < a.rows;
   const T* x = (const T*)a.x + row_offset(row, a.inner, a.xs);
   const T* res = a.residual ? (const T*)a.residual + row_offset(row, a.inner, a.rs) : nullptr;
-  float v[K][V];
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int c = (lane + L * k) * V;
-    load_piece(x + c, a.C - c, v[k]);
-  }
-  if (res) {
-    float r[K][V];
+  // (weights in front of the rows: 67584 rows of 256 channels both directions 61 us against 63.5, 10007 of 1001 in fp32 65.5 against
+  // 67; not where a row is a wave's smaller part or 1024 threads', whose registers they cost: 10.7 against 9.9, 72 against 67)
+  constexpr bool kEarly = !CODES && L >= 32 && L <= 512;
+  float w[K][V];
+  const auto load_weights = [&] {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = (lane + L * k) * V;
-      load_piece(res + c, a.C - c, r[k]);
+      load_weight(a.weight, c, a.C - c, w[k], V);
+    }
+  };
+  if (kEarly) load_weights();
+  float v[K][V];
+  if constexpr (L < 32) {
+    float more[K][V];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (lane + L * k) * V;
+      load_piece(x + c, a.C - c, v[k]);
+      if (res) load_piece(res + c, a.C - c, more[k]);
     }
 #pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[k][i] = res ? to_f32((T)(v[k][i] + more[k][i])) : v[k][i];
+  } else {
+    T xr[K][V], rr[K][V];
+#pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = (lane + L * k) * V;
+      load_raw(x + c, a.C - c, xr[k]);
+      if (res) load_raw(res + c, a.C - c, rr[k]);
+    }
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[k][i] = to_f32((T)(v[k][i] + r[k][i]));
-      if (mine) store_piece((T*)a.h + row * a.C + c, a.C - c, v[k]);
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[k][i] = res ? to_f32((T)(to_f32(xr[k][i]) + to_f32(rr[k][i]))) : to_f32(xr[k][i]);
+  }
+  if (res && mine) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (lane + L * k) * V;
+      store_piece((T*)a.h + row * a.C + c, a.C - c, v[k]);
     }
   }
   if constexpr (CODES) {
@@ -332,13 +361,12 @@ __global__ __launch_bounds__(team_threads(L)) void rms_fwd(RmsArgs a) {
     sum = team_sum<L>(sum, slots);
     const float r = 1.0f / sqrtf(sum / (float)a.C + a.eps);
     if (a.rstd && lane == 0 && mine) a.rstd[row] = r;
+    if (!kEarly) load_weights();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = (lane + L * k) * V, left = a.C - c;
-      float w[V];
-      load_weight(a.weight, c, left, w, V);
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[k][i] = v[k][i] * r * w[i];
+      for (int i = 0; i < V; ++i) v[k][i] = v[k][i] * r * w[k][i];
       if (mine) store_piece((T*)a.y + row * a.C + c, left, v[k]);
     }
   }
