@@ -14,8 +14,8 @@
 // The backward's workgroups walk many rows, the next one on its way, and keep their share of gw in registers; partial sums go
 // to the workspace once per workgroup and a second launch adds them in a fixed order.
 //
-// 8192 rows of 4096 bf16 channels with a residual into e4m3, 128 channels to a scale: 54 us, 4.4 of the copy's 5.1 TB/s; 39
-// of them issue vector instructions.  67584 rows of 256 both directions: 27 + 29 + 4 us, 4.7 TB/s in the two large launches.
+// 8192 rows of 4096 bf16 channels with a residual into e4m3, 128 channels to a scale: 56 us, 4.2 of the copy's 5.1 TB/s; 45
+// of them issue vector instructions (52 a channel, 7 of them for what the largest product's rounding dropped).  67584 rows of 256 both directions: 27 + 29 + 4 us, 4.7 TB/s in the two large launches.
 // 40000 x 8 heads of 32 out of a packed projection: 10 us, the launch and 4.1 TB/s.
 #include <hip/hip_runtime.h>
 
