@@ -4,7 +4,8 @@
 // format that is nearest to x / scale, ties to the even one.  That is the exact quotient's nearest, not a rounded
 // quotient's: codes are the same wherever they are computed from the same values.  The quotient is first taken by the
 // scale's reciprocal (at most three fp32 roundings, within 2^-22 of itself), and where that leaves the border between two
-// codes within reach, which is one value in some 10^4, in fp64.
+// codes within reach, which is one value in some 10^4, by fp32's exact remainder or in fp64 (in fp64 throughout: 69 us against
+// 63 for 8192 rows of 4096 channels behind the norm).
 // A row that holds an infinity or a NaN has codes 0 and a NaN for scale: it reads back as NaN.
 #pragma once
 

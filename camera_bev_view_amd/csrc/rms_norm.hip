@@ -15,8 +15,9 @@
 // to the workspace once per workgroup and a second launch adds them in a fixed order.
 //
 // 8192 rows of 4096 bf16 channels with a residual into e4m3, 128 channels to a scale: 56 us, 4.2 of the copy's 5.1 TB/s; 45
-// of them issue vector instructions (52 a channel, 7 of them for what the largest product's rounding dropped).  67584 rows of 256 both directions: 27 + 29 + 4 us, 4.7 TB/s in the two large launches.
-// 40000 x 8 heads of 32 out of a packed projection: 10 us, the launch and 4.1 TB/s.
+// of them issue vector instructions (52 a channel, 7 of them for what the largest product's rounding dropped).  67584 rows
+// of 256 both directions: 27 + 29 + 4 us, 4.7 TB/s in the two large launches.  40000 x 8 heads of 32 out of a packed
+// projection: 10 us, the launch and 4.1 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -207,8 +208,8 @@ __device__ __forceinline__ void store_codes(const RmsArgs& a, int64_t row, int l
   const int nb = a.block < a.C ? a.block / V : 0;       // lanes of a block (0: the row)
   const int blocks = nb ? (a.C + a.block - 1) / a.block : 1;
   uint8_t* out = (uint8_t*)a.y + row * a.C;
-  const int e = __builtin_amdgcn_frexp_exp(r);
-  const double m = __builtin_amdgcn_frexp_mant(r);
+  const int e = __builtin_amdgcn_frexp_exp(r) - 1;      // 1 <= m < 2: p is finite where y is
+  const double m = 2.0 * __builtin_amdgcn_frexp_mant(r);
   float x[K][V], w[K][V], p[K][V], rest[K];
   uint32_t top[K];
   // the row's largest where a row is a block, else each block's
@@ -291,8 +292,9 @@ __global__ __launch_bounds__(team_threads(L)) void rms_fwd(RmsArgs a) {
   const bool mine = first < a.rows;
   const T* x = (const T*)a.x + row_offset(row, a.inner, a.xs);
   const T* res = a.residual ? (const T*)a.residual + row_offset(row, a.inner, a.rs) : nullptr;
-  // (weights in front of the rows: 67584 rows of 256 channels both directions 61 us against 63.5, 10007 of 1001 in fp32 65.5 against
-  // 67; not where a row is a wave's smaller part or 1024 threads', whose registers they cost: 10.7 against 9.9, 72 against 67)
+  // (weights in front of the rows: 67584 rows of 256 channels both directions 60 us against 63.5, 10007 of 1001 in fp32 66
+  // against 67; not where a row is a wave's smaller part or 1024 threads', whose registers they cost: 40000 x 8 heads of 32
+  // 10.7 against 9.9, 2000 rows of 8192 channels 72 against 67)
   constexpr bool kEarly = !CODES && L >= 32 && L <= 512;
   float w[K][V];
   const auto load_weights = [&] {

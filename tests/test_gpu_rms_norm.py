@@ -173,6 +173,17 @@ def test_codes(C, block, kind, dtype):
     check_codes(x * 1e-3, None, None, kind, block)
 
 
+def test_codes_of_sizes_far_from_one():
+    """Rows and weights near the ends of fp32's range: what the norm takes out or leaves in, scales at their least."""
+    for kind in ("int8", "e4m3"):
+        for size, weight, eps in ((1e30, 1.0, 1e-6), (1e-30, 1.0, 0.0), (1e-18, 1.0, 1e-6), (1.0, 5e37, 1e-6), (1.0, 1e-35, 1e-6),
+                                  (1.0, 1e-37, 0.0), (3e37, 1e-30, 0.0)):
+            say(f"[case] {kind} rows of {size}, weights of {weight}")
+            x, w = draw(21, 20, 200) * size, (draw(22, 200) * 0.2 + 1).clamp(0.5, 1.5) * weight
+            check_codes(x, None, w, kind, 64, eps)
+            check_codes(x[:, :130], None, w[:130].clone(), kind, 0, eps)
+
+
 def test_codes_of_views():
     packed = draw(1, 6, 7, 3, 4, 40, dtype=BF16)
     check_codes(packed[:, :, 1], None, draw(2, 40), "e4m3", 32)
@@ -312,3 +323,49 @@ def test_more_workgroups_than_a_launch_dimension_holds():
     # equal terms: the sum of n of them by chains of at most n / (1024 * 64) rounds, then 64 + 32 + 32 + 6 shares
     bound = (rows / 65536 + 256) * U * rows * w1.abs().double()
     assert ((gw.double() - rows * w1.double()).abs() <= bound).all()
+
+
+def test_gradients_of_shared_and_broadcast_inputs():
+    w = (draw(3, 96) * 0.3 + 1).requires_grad_()
+    x = draw(1, 1, 96).requires_grad_()
+    gy, gh = draw(4, 40, 96), draw(5, 40, 96)
+    wide = x.expand(40, 96)
+    torch.autograd.backward(ops.rms_norm_add(wide, wide, w), [gy, gh])
+    _, h, s = ops.rms_norm_forward(wide.detach(), w.detach(), residual=wide.detach())
+    gx, gw = ops.rms_norm_backward(gy, h, s, w.detach(), grad_h=gh)
+    # both addends: twice the rows' sum, of 80 terms in another order
+    want = 2 * gx.double().sum(0)
+    assert ((x.grad[0].double() - want).abs() <= 80 * U * 2 * gx.double().abs().sum(0)).all()
+    assert torch.equal(w.grad, gw)
+    # two leaves of one sum have gradients of their own memory
+    a, b = draw(6, 40, 96).requires_grad_(), draw(7, 40, 96).requires_grad_()
+    torch.autograd.backward(ops.rms_norm_add(a, b, w), [gy, gh])
+    before = b.grad.clone()
+    a.grad.mul_(3)
+    assert torch.equal(b.grad, before)
+
+
+def test_captured_training_step():
+    """Both directions through autograd in a graph, replayed between eager steps on the same memory."""
+    x, r, w = draw(1, 500, 256, dtype=BF16), draw(2, 500, 256, dtype=BF16), draw(3, 256) * 0.2 + 1
+    gy, gh = draw(4, 500, 256, dtype=BF16), draw(5, 500, 256, dtype=BF16)
+
+    def step():
+        leaves = [t.detach().requires_grad_() for t in (x, r, w)]
+        y, h = ops.rms_norm_add(*leaves)
+        return [y.detach(), h.detach(), *torch.autograd.grad([y, h], leaves, [gy, gh])]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for k in range(4):
+        x.copy_(draw(60 + k, 500, 256, dtype=BF16))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(held, step()):
+            assert torch.equal(a, b), k
