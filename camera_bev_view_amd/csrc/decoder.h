@@ -31,6 +31,7 @@ struct RmsArgs {
   int codes;               // -1: none, else fbev_codes
   int block;               // channels to a scale; C: the whole row
   float eps;
+  double part_of_row;      // 1 / C
 };
 size_t rms_norm_workspace_bytes(const RmsArgs& a);
 hipError_t launch_rms_norm_forward(const RmsArgs& a, hipStream_t stream);

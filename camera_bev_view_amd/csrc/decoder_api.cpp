@@ -53,6 +53,7 @@ fbev_status check_rms(const fbev_rms_desc* rd, fbev_dtype dtype, fbev::RmsArgs& 
   a.rows = rd->outer * rd->inner;
   a.C = rd->C;
   a.eps = rd->eps;
+  a.part_of_row = 1.0 / rd->C;
   a.elem_bytes = elem_bytes(dtype);
   a.codes = -1;
   for (int i = 0; i < 2; ++i) {

@@ -344,12 +344,12 @@ __global__ __launch_bounds__(team_threads(L)) void rms_fwd(RmsArgs a) {
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int i = 0; i < V; ++i) squares = fma((double)v[k][i], (double)v[k][i], squares);
-    // 1 / sqrt from the hardware's, two steps of Newton's method behind it
-    const double mean = team_sum<L>(squares, slots) / (double)a.C + (double)a.eps;
-    double r = __builtin_amdgcn_rsq(mean);
+    // 1 / sqrt from the hardware's, two steps of Newton's method behind it (0, infinity and NaN as they come)
+    const double mean = team_sum<L>(squares, slots) * a.part_of_row + (double)a.eps, near = __builtin_amdgcn_rsq(mean);
+    double r = near;
 #pragma unroll
     for (int i = 0; i < 2; ++i) r = fma(r, fma(-0.5 * mean * r, r, 0.5), r);
-    r = mean > 0.0 && mean < __builtin_huge_val() ? r : 1.0 / sqrt(mean);
+    r = mean > 0.0 && mean < __builtin_huge_val() ? r : near;
     if (a.codes == FBEV_CODES_E4M3)
       store_codes<FBEV_CODES_E4M3, L, K, V>(a, row, lane, mine, v, r, slots);
     else
