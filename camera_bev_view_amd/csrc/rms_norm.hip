@@ -158,13 +158,13 @@ __device__ __forceinline__ X lanes_sum(X x) {
   return x;
 }
 
-// The team's sum in each of its lanes.  `slots`: LDS for one number of each wave, used by teams of several waves.
+// The team's sum in each of its lanes.  `slots`: LDS for one number of each wave, used by teams of several waves and not
+// again before another barrier.
 template <int L, typename X>
 __device__ __forceinline__ X team_sum(X x, double* slots) {
   if constexpr (L <= 64) return lanes_sum<L>(x);
   x = lanes_sum<64>(x);
   X* mine = (X*)slots;
-  __syncthreads();          // the last use of the slots is over
   if ((threadIdx.x & 63) == 0) mine[threadIdx.x >> 6] = x;
   __syncthreads();
   x = 0;
@@ -177,7 +177,6 @@ template <int L, typename X>
 __device__ __forceinline__ X team_max(X x, double* slots) {
   if constexpr (L <= 64) return lanes_max(x, L);
   x = lanes_max(x, 64);
-  __syncthreads();
   X* mine = (X*)slots;
   if ((threadIdx.x & 63) == 0) mine[threadIdx.x >> 6] = x;
   __syncthreads();
@@ -200,6 +199,8 @@ __device__ __forceinline__ int64_t row_offset(int64_t row, int64_t inner, const 
 // p is taken in fp32 and a code near a border again in fp64, where the product is exact; the scale takes what rounding dropped
 // of the largest p, and is rounded once.
 // Blocks are narrower than the row only where a lane's pieces lie L apart and a block's 4 to 32 lanes side by side.
+template <int L>
+constexpr int kWaves = team_threads(L) / 64;
 template <int KIND, int L, int K, int V>
 __device__ __forceinline__ void store_codes(const RmsArgs& a, int64_t row, int lane, bool mine, const float (&h)[K][V], double r,
                                             double* slots) {
@@ -213,7 +214,7 @@ __device__ __forceinline__ void store_codes(const RmsArgs& a, int64_t row, int l
   float x[K][V], w[K][V], p[K][V], rest[K];
   uint32_t top[K];
   // the row's largest where a row is a block, else each block's
-  const auto widest = [&](auto& t) {
+  const auto widest = [&](auto& t, double* slots) {
     if (nb == 0) {
       auto all = t[0];
 #pragma unroll
@@ -238,7 +239,7 @@ __device__ __forceinline__ void store_codes(const RmsArgs& a, int64_t row, int l
       top[k] = larger(top[k], abs_bits(p[k][i]));
     }
   }
-  widest(top);
+  widest(top, slots);
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     rest[k] = -__builtin_huge_valf();
@@ -250,7 +251,7 @@ __device__ __forceinline__ void store_codes(const RmsArgs& a, int64_t row, int l
       rest[k] = abs_bits(p[k][i]) == top[k] ? fmaxf(rest[k], along) : rest[k];
     }
   }
-  widest(rest);
+  widest(rest, slots + kWaves<L>);
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int c = (lane + L * k) * V, left = a.C - c;
@@ -284,7 +285,7 @@ __device__ __forceinline__ void store_codes(const RmsArgs& a, int64_t row, int l
 template <typename T, int L, int K, bool CODES>
 __global__ __launch_bounds__(team_threads(L)) void rms_fwd(RmsArgs a) {
   constexpr int V = kVec<T>, kThreads = team_threads(L), kTeams = kThreads / L;
-  __shared__ double slots[kThreads / 64];
+  __shared__ double slots[3 * kWaves<L>];               // one reduction each
   const int lane = threadIdx.x % L;
   const int64_t first = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kTeams + threadIdx.x / L;
   if (L > 64 && first >= a.rows) return;                // the whole workgroup; narrower teams stay for the lane exchanges
@@ -351,9 +352,9 @@ __global__ __launch_bounds__(team_threads(L)) void rms_fwd(RmsArgs a) {
     for (int i = 0; i < 2; ++i) r = fma(r, fma(-0.5 * mean * r, r, 0.5), r);
     r = mean > 0.0 && mean < __builtin_huge_val() ? r : near;
     if (a.codes == FBEV_CODES_E4M3)
-      store_codes<FBEV_CODES_E4M3, L, K, V>(a, row, lane, mine, v, r, slots);
+      store_codes<FBEV_CODES_E4M3, L, K, V>(a, row, lane, mine, v, r, slots + kWaves<L>);
     else
-      store_codes<FBEV_CODES_INT8, L, K, V>(a, row, lane, mine, v, r, slots);
+      store_codes<FBEV_CODES_INT8, L, K, V>(a, row, lane, mine, v, r, slots + kWaves<L>);
   } else {
     float sum = 0.0f;
 #pragma unroll
@@ -378,7 +379,7 @@ __global__ __launch_bounds__(team_threads(L)) void rms_fwd(RmsArgs a) {
 template <typename T, int L, int K>
 __global__ __launch_bounds__(team_threads(L)) void rms_bwd(RmsArgs a) {
   constexpr int V = kVec<T>, kThreads = team_threads(L), kTeams = kThreads / L;
-  __shared__ double slots[kThreads / 64];
+  __shared__ double slots[2][kWaves<L>];                // of odd and even rounds: the other round's barrier lies between
   const int lane = threadIdx.x % L;
   float w[K][V], gw[K][V];
 #pragma unroll
@@ -409,7 +410,8 @@ __global__ __launch_bounds__(team_threads(L)) void rms_bwd(RmsArgs a) {
   };
   int64_t at = (int64_t)blockIdx.x * kTeams + threadIdx.x / L;
   if (kAhead) load_row(at);
-  for (int64_t base = (int64_t)blockIdx.x * kTeams; base < a.rows; base += step, at += step) {
+  int odd = 0;
+  for (int64_t base = (int64_t)blockIdx.x * kTeams; base < a.rows; base += step, at += step, odd ^= 1) {
     const bool mine = at < a.rows;
     if (!kAhead) load_row(at);
     float h[K][V], g[K][V], more[K][V], dot = 0.0f;
@@ -427,7 +429,7 @@ __global__ __launch_bounds__(team_threads(L)) void rms_bwd(RmsArgs a) {
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int i = 0; i < V; ++i) dot = fmaf(g[k][i] * w[k][i], h[k][i], dot);
-    dot = team_sum<L>(dot, slots);
+    dot = team_sum<L>(dot, slots[odd]);
     const float along = dot / (float)a.C * r * r;
     if (!mine) continue;
 #pragma unroll
