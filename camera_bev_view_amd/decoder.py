@@ -72,6 +72,8 @@ def _rows(x: torch.Tensor, other: Optional[torch.Tensor]):
     for t in (x, other):
         if t is not None and t.shape[-1] > 1 and t.stride(-1) != 1:
             return None
+    if lead == 2:                       # two strides as they are (the library joins them where it can)
+        return (*x.shape[:2], *x.stride()[:2], *((0, 0) if other is None else other.stride()[:2]))
     for cut in range(lead, -1, -1):
         strides = []
         for t in (x, other):
