@@ -549,20 +549,26 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attn_few(CacheAttnArgs a)
   finish_row<T>(a, p, row, ml, of, r16);
 }
 
-// More rows: every wave has a row tile of its own, the pages are shared.  SIMD_WAVES: waves a SIMD that the registers are meant
-// for.
-template <typename T, int KIND, int DC, int WAVES, int SIMD_WAVES>
+// More rows: every wave has a row tile of its own, the pages are shared.  GROUPS of waves have the same row tiles and take turns
+// at the pages.  SIMD_WAVES: waves a SIMD that the registers are meant for.
+template <typename T, int KIND, int DC, int WAVES, int GROUPS, int SIMD_WAVES>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(SIMD_WAVES, SIMD_WAVES))) void cache_attn_many(CacheAttnArgs a) {
   using Sh = Shape<T, DC>;
   constexpr int kKeys = 4 * Sh::kSteps, kFrags = kKeys + 2 * Sh::kTiles;          // of a widened page
   constexpr int kPageBytes = kFrags * 64 * 16, kSumBytes = WAVES * 16 * Sh::kRow * 4;
-  __shared__ alignas(16) char lds[2 * kPageBytes > kSumBytes ? 2 * kPageBytes : kSumBytes];
-  __shared__ alignas(16) float scales[2][2][kPage];
+  constexpr int kHeldBytes = GROUPS * 2 * kPageBytes;
+  __shared__ alignas(16) char lds[kHeldBytes > kSumBytes ? kHeldBytes : kSumBytes];
+  __shared__ alignas(16) float all_scales[GROUPS][2][2][kPage];
+  __shared__ float2 joined[GROUPS == 1 ? 1 : WAVES][16];
   const CacheArgs& c = a.c;
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
-  const Part p = find_part<true>(a, 16 * WAVES);
-  const int row0 = p.row0 + wave * 16;
+  constexpr int kTileWaves = WAVES / GROUPS;
+  const int group = GROUPS == 1 ? 0 : wave / kTileWaves, tile = wave - group * kTileWaves;
+  const Part p = find_part<true>(a, 16 * kTileWaves);
+  const int row0 = p.row0 + tile * 16;
+  char* const pages = lds + group * 2 * kPageBytes;
+  float(&scales)[2][2][kPage] = all_scales[group];
   const bool idle = row0 >= a.R;                        // it moves pages for the others
   bf16x8 qf[Sh::kSteps][Sh::kQ];
   f32x4 o[Sh::kTiles];
@@ -573,29 +579,29 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(SIMD
   for (int i = 0; i < Sh::kTiles; ++i) o[i] = f32x4{0, 0, 0, 0};
 
   // a wave's part of a page: pieces of 16 codes a lane, keys (u and chunk) from the first wave on, value tiles from the last
-  constexpr int kKeyPieces = 4 * Sh::kChunks, kKeyMine = (kKeyPieces + WAVES - 1) / WAVES;
-  constexpr int kValueMine = (Sh::kTiles + WAVES - 1) / WAVES;
+  constexpr int kKeyPieces = 4 * Sh::kChunks, kKeyMine = (kKeyPieces + kTileWaves - 1) / kTileWaves;
+  constexpr int kValueMine = (Sh::kTiles + kTileWaves - 1) / kTileWaves;
   uint32_t kw[kKeyMine][4], vw[kValueMine][4];
   float scale = 0.0f;
-  const int back = WAVES - 1 - wave;
+  const int back = kTileWaves - 1 - tile;
   const auto load_page = [&](int number, bool there) {
     const Page page = find_page(c, p.hk, number, there);
 #pragma unroll
     for (int j = 0; j < kKeyMine; ++j) {
-      const int piece = wave + WAVES * j;               // (one behind the last is outside the page)
+      const int piece = tile + kTileWaves * j;          // (one behind the last is outside the page)
       load_key<Sh>(c, page, r16, g, piece / Sh::kChunks, piece % Sh::kChunks, kw[j]);
     }
 #pragma unroll
-    for (int j = 0; j < kValueMine; ++j) load_value(page, r16, g, back + WAVES * j, vw[j]);
-    scale = __builtin_bit_cast(float, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(wave & 1 ? page.vs : page.ks, 4 * lane, 0, 0));
+    for (int j = 0; j < kValueMine; ++j) load_value(page, r16, g, back + kTileWaves * j, vw[j]);
+    scale = __builtin_bit_cast(float, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(tile & 1 ? page.vs : page.ks, 4 * lane, 0, 0));
   };
   const float unit = a.cap > 0 ? a.scale / a.cap : a.scale * kLog2e;
   const auto put_page = [&](int buf, int pos) {
-    bf16x8* to = (bf16x8*)(lds + buf * kPageBytes) + lane;
+    bf16x8* to = (bf16x8*)(pages + buf * kPageBytes) + lane;
 #pragma unroll
     for (int j = 0; j < kKeyMine; ++j) {
-      const int piece = wave + WAVES * j;
-      if (kKeyPieces % WAVES == 0 || piece < kKeyPieces) {
+      const int piece = tile + kTileWaves * j;
+      if (kKeyPieces % kTileWaves == 0 || piece < kKeyPieces) {
         const int u = piece / Sh::kChunks, i = piece % Sh::kChunks;
         to[(u * Sh::kSteps + 2 * i) * 64] = widen<KIND>(kw[j][0], kw[j][1]);
         if constexpr (Sh::kChunk == 16) to[(u * Sh::kSteps + 2 * i + 1) * 64] = widen<KIND>(kw[j][2], kw[j][3]);
@@ -603,34 +609,37 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(SIMD
     }
 #pragma unroll
     for (int j = 0; j < kValueMine; ++j) {
-      const int tile = back + WAVES * j;
-      if (Sh::kTiles % WAVES == 0 || tile < Sh::kTiles) {
+      const int rows = back + kTileWaves * j;
+      if (Sh::kTiles % kTileWaves == 0 || rows < Sh::kTiles) {
         if (pos + kPage > p.end) keep_codes<KIND>(vw[j], p.end - pos - 16 * g);
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) to[(kKeys + 2 * tile + kk) * 64] = widen<KIND>(vw[j][2 * kk], vw[j][2 * kk + 1]);
+        for (int kk = 0; kk < 2; ++kk) to[(kKeys + 2 * rows + kk) * 64] = widen<KIND>(vw[j][2 * kk], vw[j][2 * kk + 1]);
       }
     }
-    if (wave < 2) scales[buf][wave][lane] = wave ? scale : scale * unit;
+    if (tile < 2) scales[buf][tile][lane] = tile ? scale : scale * unit;
   };
 
   const int whole = a.mode == FBEV_DRAFT_NONE ? p.end : min(p.start, p.end);      // tokens below are seen by all
-  Walk<1> walk(c, p, p.p0);                             // the page ahead of the one at work
+  Walk<GROUPS> walk(c, p, p.p0 + group);                // the page ahead of the one at work
   int at = walk.at, buf = 0;
   load_page(walk.page, walk.there());
   put_page(0, at * kPage);
   walk.next();
   load_page(walk.page, walk.there());
-  while (at < p.p1) {
+  // (groups may find different numbers of pages that exist: all go round as often as one could have to)
+  const int rounds = (p.p1 - p.p0 + GROUPS - 1) / GROUPS;
+  for (int round = 0; GROUPS == 1 ? at < p.p1 : round < rounds; ++round) {
     const int pos = at * kPage;
+    const bool here = GROUPS == 1 || at < p.p1;
     __syncthreads();                                    // this page is in; the other buffer has been read
-    const bf16x8* from = (const bf16x8*)(lds + buf * kPageBytes) + lane;
+    const bf16x8* from = (const bf16x8*)(pages + buf * kPageBytes) + lane;
     const float(&sc)[2][kPage] = scales[buf];
     at = walk.at;
     buf ^= 1;
     put_page(buf, at * kPage);                          // (behind the last one: zeros that nobody reads)
     walk.next();
     load_page(walk.page, walk.there());
-    if (idle) continue;
+    if (idle || !here) continue;
     const bool masked = pos + kPage > whole;
     uint32_t bits = 0;
     if (masked) {
@@ -672,16 +681,33 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(SIMD
   // a row's channels side by side again, by way of the pages' LDS
   float* sums = (float*)lds + wave * 16 * Sh::kRow;
   l = query_sum(l);
+  if (GROUPS > 1 && g == 0) joined[wave][r16] = float2{m, l};
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < Sh::kTiles; ++i) *(f32x4*)(sums + r16 * Sh::kRow + 16 * i + 4 * g) = o[i];
-  wave_lds_sync();
+  if constexpr (GROUPS == 1) {
+    wave_lds_sync();
 #pragma unroll
-  for (int i = 0; i < 16; i += 4) {
-    const float2 ml[1] = {float2{__shfl(m, i + g), __shfl(l, i + g)}};
-    const float* const of[1] = {sums + (i + g) * Sh::kRow};
-    const int row = row0 + i + g;
-    if (row < a.R) finish_row<T>(a, p, row, ml, of, r16);
+    for (int i = 0; i < 16; i += 4) {
+      const float2 ml[1] = {float2{__shfl(m, i + g), __shfl(l, i + g)}};
+      const float* const of[1] = {sums + (i + g) * Sh::kRow};
+      const int row = row0 + i + g;
+      if (row < a.R) finish_row<T>(a, p, row, ml, of, r16);
+    }
+  } else {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 16 / GROUPS; i += 4) {
+      const int mine = wave * (16 / GROUPS) + i + g, from = mine / 16, r = mine % 16, row = p.row0 + mine;
+      float2 ml[GROUPS];
+      const float* of[GROUPS];
+#pragma unroll
+      for (int n = 0; n < GROUPS; ++n) {
+        ml[n] = joined[from + n * kTileWaves][r];
+        of[n] = (const float*)lds + ((from + n * kTileWaves) * 16 + r) * Sh::kRow;
+      }
+      if (row < a.R) finish_row<T>(a, p, row, ml, of, r16);
+    }
   }
 }
 
@@ -793,17 +819,20 @@ __global__ __launch_bounds__(1024) void cache_attn_join(CacheAttnArgs a) {
 // How a call's rows lie on workgroups.
 struct Plan {
   bool few;               // up to one row tile: waves with pages of their own
-  int waves;              // of a workgroup
+  int waves;              // that hold different rows (few: all)
+  int groups;             // of waves with the same rows
   int row_blocks, splits;
 };
 
 // Few rows: eight waves where that alone gives most CUs a workgroup (no split, no join: 32 sequences of 4000 tokens, 8 key
 // heads of 128, 46 us against 52 with four waves and two splits), else four and splits (one sequence of 4000 tokens, 8 heads of
-// 64: 10 us against 21).  More rows: four waves up to 64 rows; beyond, eight share the widening of a page (64 rows of
-// 16 scenes x 4 heads of 128: 73 us against 116).  Splits make up 512 workgroups of four waves, 256 of eight (fp32, 900 rows of
-// 8 heads of 32 over 3600 tokens: 32 us against 41 with 512), or 512 where a wave's work on a page is long and its registers
-// let two in (bf16, heads of 128: 1000 rows of 16 heads behind 9000 tokens 153 us against 164); every four waves of few rows, or
-// every workgroup of more, still have four pages.
+// 64: 10 us against 21).  More rows: up to 64 in four waves' tiles, two groups of those to a workgroup, which halves what a join
+// reads (15 drafted tokens over 200000: 34 us against 38 with a group and twice the splits), four in long caches where their
+// registers and LDS let 16 waves in (32 us; 40 sequences of 32 rows over 1000 tokens 28 against 23).  Beyond, eight tiles share
+// the widening of a page (64 rows of 16 scenes x 4 heads of 128: 73 us against 116).  Splits make up 512 workgroups of few rows, 256
+// of more (fp32, 900 rows of 8 heads of 32 over 3600 tokens: 32 us against 41 with 512), or 512 where a wave's work on a page is
+// long and its registers let two in (bf16, heads of 128: 1000 rows of 16 heads behind 9000 tokens 153 us against 164); every
+// workgroup still has four pages.
 Plan plan_of(const CacheAttnArgs& a) {
   Plan p;
   const int64_t heads = (int64_t)a.c.B * a.c.Hk;
@@ -811,12 +840,13 @@ Plan plan_of(const CacheAttnArgs& a) {
   p.waves = (p.few ? heads >= 192 : a.R > 64) ? 8 : 4;
   const int held = p.few ? 16 : 16 * p.waves;
   p.row_blocks = (a.R + held - 1) / held;
-  const bool two = p.waves == 4 || (a.elem_bytes == 2 && a.c.D > 64);
+  const bool half = a.elem_bytes == 2, two = p.few || (p.waves == 8 && half && a.c.D > 64);
   const int64_t blocks = heads * p.row_blocks, full = two ? 512 : 256, most = (a.c.W + 3) / 4;
   int64_t want = 1;
   if (p.few ? p.waves == 4 : blocks < (p.waves == 4 ? 256 : two ? 384 : 192)) want = (full + blocks - 1) / blocks;
   if (want > most) want = most;
   p.splits = (int)(want < 1 ? 1 : want > kMostSplits ? kMostSplits : want);
+  p.groups = p.few || p.waves == 8 ? 1 : half && a.c.D <= 64 && blocks <= 64 && a.c.W >= 20 * p.splits ? 4 : 2;
   return p;
 }
 
@@ -827,12 +857,14 @@ void launch_rows(const CacheAttnArgs& a, const Plan& plan, unsigned blocks, hipS
       cache_attn_few<T, KIND, DC, 8><<<blocks, 512, 0, stream>>>(a);
     else
       cache_attn_few<T, KIND, DC, 4><<<blocks, 256, 0, stream>>>(a);
-  } else if (plan.waves == 4) {
-    cache_attn_many<T, KIND, DC, 4, sizeof(T) == 2 && DC < 128 ? 4 : 2><<<blocks, 256, 0, stream>>>(a);
+  } else if (plan.groups == 4) {
+    if constexpr (sizeof(T) == 2 && DC < 128) cache_attn_many<T, KIND, DC, 16, 4, 4><<<blocks, 1024, 0, stream>>>(a);
+  } else if (plan.groups == 2) {
+    cache_attn_many<T, KIND, DC, 8, 2, sizeof(T) == 2 ? 4 : 2><<<blocks, 512, 0, stream>>>(a);
   } else {
     // bf16 takes tighter code that leaves four waves a SIMD (8 x 4000 rows of 128 channels: 371 us against 450; 25 x 256 rows:
     // 89 against 102; 2 x 1200 rows, a workgroup on every third CU: 25.0 against 24.3); fp32's parts of queries do not fit
-    cache_attn_many<T, KIND, DC, 8, sizeof(T) == 2 ? 4 : 2><<<blocks, 512, 0, stream>>>(a);
+    cache_attn_many<T, KIND, DC, 8, 1, sizeof(T) == 2 ? 4 : 2><<<blocks, 512, 0, stream>>>(a);
   }
 }
 

@@ -288,6 +288,46 @@ def test_long_caches():
                 assert (err <= bound).all()
 
 
+@pytest.mark.parametrize("Hk,n,B,D", [(8, 7000, 8, 64), (2, 30000, 3, 24), (3, 2500, 4, 128)])
+def test_long_ragged_caches(Hk, n, B, D):
+    """Groups of waves that take turns at the pages, of which some are lost, with few rows to a head and several splits."""
+    say(f"[case] {B} sequences of up to {n} tokens")
+    W, G = -(-n // 64) + 1, 2
+    lengths = [n, n // 2 + 3, 0, 1, n - 700, 64, 63, n // 3][:B]
+    g = torch.Generator(device="cuda").manual_seed(n)
+    k, v = (torch.randn((B, n, Hk, D), generator=g, device="cuda") for _ in range(2))
+    for kind in ("int8", "e4m3"):
+        cache = ops.token_cache(B * W, Hk, D, codes=KINDS[kind])
+        table = torch.randperm(B * W, generator=torch.Generator().manual_seed(2)).view(B, W).int()
+        table[:, 5::7] = -1
+        table = table.cuda()
+        ops.cache_write(cache, k, v, table, i32([0] * B), count=i32(lengths))
+        kd, vd = (x.double() for x in ops.cache_read(cache, table, i32([0] * B), n, dtype=F32))
+        there = (table >= 0).repeat_interleave(64, 1)[:, :n]
+        for dtype in (F32, BF16):
+            for T in (9, 30):
+                q = draw(T, B, T, Hk * G, D, dtype=dtype)
+                out = ops.cache_attention(q, cache, table, i32(lengths), drafted=False)
+                for b in range(B):
+                    seen = there[b] & (torch.arange(n, device="cuda") < lengths[b])
+                    if not seen.any():
+                        assert not out[b].any()
+                        continue
+                    kb, vb = kd[b][seen].transpose(0, 1), vd[b][seen].transpose(0, 1)
+                    qb = q[b].double().view(T, Hk, G, D).permute(1, 0, 2, 3).reshape(Hk, T * G, D)
+                    s = torch.matmul(qb, kb.transpose(1, 2)) * D ** -0.5
+                    p = torch.softmax(s, -1)
+                    back = lambda x: x.view(Hk, T, G, -1).permute(1, 0, 2, 3).reshape(T, Hk * G, -1)
+                    want, size = back(torch.matmul(p, vb)), back(torch.matmul(p, vb.abs()))
+                    mag = back((D ** -0.5 * torch.matmul(qb.abs(), kb.abs().transpose(1, 2))).amax(-1, keepdim=True))
+                    U = 2.0 ** -24
+                    # as in test_long_caches
+                    rel = 2 * (3 * D + 36) * U * mag + 2 * (n + 64) * U + (2 * U if dtype == F32 else 2.0 ** -17)
+                    bound = rel * size * 1.01
+                    bound = bound + (U if dtype == F32 else 2.0 ** -8) * (want.abs() + bound)
+                    assert ((out[b].double() - want).abs() <= bound).all(), (kind, dtype, T, b)
+
+
 def test_pages_beyond_31_bits():
     pages, Hk, D = 33000, 8, 128
     say(f"[case] cache of {pages} pages")
