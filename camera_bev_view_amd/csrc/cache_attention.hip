@@ -21,9 +21,9 @@
 // are split over workgroups as well, and a second launch joins them.
 //
 // One token of each of 32 sequences (8192 to 4096 tokens, 32 heads over 8 of 128, e4m3): 83 us, 420 MB at 5.1 TB/s, the copy's
-// rate.  60 rows over 200000 tokens of 2 heads of 64 (int8, 51 MB): 29 us and 8 for the join of 256 splits; fetching one hot
-// page instead changes nothing, and more workgroups only lengthen the join.  2 x 4000 rows behind 6000 and 4500 tokens, 4 heads of
-// 128: 175 us, of which the matrix units are busy 57 and vector instructions issue 84 (a quarter more with the exponentials); LDS
+// rate.  60 rows over 200000 tokens of 2 heads of 64 (int8, 51 MB): 27 us and 5 for the join of 128 splits; fetching one hot
+// page instead changes nothing.  2 x 4000 rows behind 6000 and 4500 tokens, 4 heads of
+// 128: 177 us, of which the matrix units are busy 57 and vector instructions issue 84 (a quarter more with the exponentials); LDS
 // reads take 58.  They hide each other little: all of a workgroup's waves come to the same stage together.  fp32 (three parts for
 // queries and weights) does the 64 tokens of 16 scenes at 128 us against 73 in bf16.
 #include <hip/hip_runtime.h>
