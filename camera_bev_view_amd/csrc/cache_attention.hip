@@ -830,9 +830,10 @@ struct Plan {
 // reads (15 drafted tokens over 200000: 34 us against 38 with a group and twice the splits), four in long caches where their
 // registers and LDS let 16 waves in (32 us; 40 sequences of 32 rows over 1000 tokens 28 against 23).  Beyond, eight tiles share
 // the widening of a page (64 rows of 16 scenes x 4 heads of 128: 73 us against 116).  Splits make up 512 workgroups of few rows, 256
-// of more (fp32, 900 rows of 8 heads of 32 over 3600 tokens: 32 us against 41 with 512), or 512 where a wave's work on a page is
-// long and its registers let two in (bf16, heads of 128: 1000 rows of 16 heads behind 9000 tokens 153 us against 164); every
-// workgroup still has four pages.
+// of more (900 rows of 8 heads of 32 over 3600 tokens: 28 us against 37 with 512, in fp32 32 against 41), or 512 where a CU holds
+// two (bf16) and either a wave's work on a page is long (heads of 128: 1000 rows of 16 heads behind 9000 tokens 153 us against
+// 164) or each has a dozen pages and the batch is no single small one (4 x 900 rows of 8 heads of 32 over 3600 tokens 59 us against
+// 72, 16 x 32 rows of 8 heads of 64 over 4000 28 against 33; 32 over 1000 28 against 23).  Every workgroup still has four pages.
 Plan plan_of(const CacheAttnArgs& a) {
   Plan p;
   const int64_t heads = (int64_t)a.c.B * a.c.Hk;
@@ -840,10 +841,11 @@ Plan plan_of(const CacheAttnArgs& a) {
   p.waves = (p.few ? heads >= 192 : a.R > 64) ? 8 : 4;
   const int held = p.few ? 16 : 16 * p.waves;
   p.row_blocks = (a.R + held - 1) / held;
-  const bool half = a.elem_bytes == 2, two = p.few || (p.waves == 8 && half && a.c.D > 64);
-  const int64_t blocks = heads * p.row_blocks, full = two ? 512 : 256, most = (a.c.W + 3) / 4;
+  const bool half = a.elem_bytes == 2, wide = a.c.D > 64;
+  const int64_t blocks = heads * p.row_blocks, most = (a.c.W + 3) / 4, twice = (512 + blocks - 1) / (blocks > 0 ? blocks : 1);
+  const bool two = p.few || (half && (wide ? p.waves == 8 : blocks >= 128 && a.c.W >= 12 * twice));
   int64_t want = 1;
-  if (p.few ? p.waves == 4 : blocks < (p.waves == 4 ? 256 : two ? 384 : 192)) want = (full + blocks - 1) / blocks;
+  if (p.few ? p.waves == 4 : blocks < (two ? 384 : p.waves == 4 ? 256 : 192)) want = two ? twice : (256 + blocks - 1) / blocks;
   if (want > most) want = most;
   p.splits = (int)(want < 1 ? 1 : want > kMostSplits ? kMostSplits : want);
   p.groups = p.few || p.waves == 8 ? 1 : half && a.c.D <= 64 && blocks <= 64 && a.c.W >= 20 * p.splits ? 4 : 2;
