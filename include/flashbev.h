@@ -609,8 +609,8 @@ fbev_status fbev_rms_norm_backward(const void* grad_y, const void* grad_h, const
  * (sequences may share pages that none of them writes).
  *
  * fbev_cache_read gives the values that the codes of the rows' tokens stand
- * for, rounded once to dtype: k_out, v_out [B, T, Hk, D], contiguous, zeros for
- * rows that are padding or have no page.  Either may be NULL.
+ * for (code * scale in fp32, then in dtype): k_out, v_out [B, T, Hk, D],
+ * contiguous, zeros for rows that are padding or have no page.  Either may be NULL.
  */
 #define FBEV_CACHE_PAGE 64
 

@@ -288,7 +288,7 @@ def test_long_caches():
                 assert (err <= bound).all()
 
 
-@pytest.mark.parametrize("Hk,n,B,D", [(8, 7000, 8, 64), (2, 30000, 3, 24), (3, 2500, 4, 128)])
+@pytest.mark.parametrize("Hk,n,B,D", [(8, 7000, 8, 64), (2, 30000, 3, 24), (3, 2500, 4, 128), (16, 3200, 8, 32)])
 def test_long_ragged_caches(Hk, n, B, D):
     """Groups of waves that take turns at the pages, of which some are lost, with few rows to a head and several splits."""
     say(f"[case] {B} sequences of up to {n} tokens")
@@ -305,7 +305,7 @@ def test_long_ragged_caches(Hk, n, B, D):
         kd, vd = (x.double() for x in ops.cache_read(cache, table, i32([0] * B), n, dtype=F32))
         there = (table >= 0).repeat_interleave(64, 1)[:, :n]
         for dtype in (F32, BF16):
-            for T in (9, 30):
+            for T in (9, 30, 70):
                 q = draw(T, B, T, Hk * G, D, dtype=dtype)
                 out = ops.cache_attention(q, cache, table, i32(lengths), drafted=False)
                 for b in range(B):
