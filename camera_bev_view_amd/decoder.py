@@ -239,9 +239,12 @@ def rms_norm_add(x: torch.Tensor, residual: torch.Tensor, weight: Optional[torch
 class TokenCache:
     """Keys and values of many sequences in 8 bits, in pages of 64 tokens: codes k [pages, Hk, 64, Dp] and v [pages, Hk,
     Dp, 64] (torch.int8 or torch.float8_e4m3fn; Dp: D rounded up to a multiple of 16, zeros behind D) and k_scale, v_scale
-    [pages, Hk, 64] fp32, contiguous tensors of one device.  Which page belongs to which sequence is the caller's table."""
+    [pages, Hk, 64] fp32, contiguous tensors of one device.  Which page belongs to which sequence is the caller's table.
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "D", "Hk", "pages", "device", "desc")
+    The tensors are its own from then on: they can be written in place but not replaced, and a call on a cache whose tensors
+    have been resized or given other memory is refused.  A larger cache is a new one; deep and pickled copies have tensors of their own."""
+
+    __slots__ = ("_held",)
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor, D: int):
         shape, dtype, dev = k.shape, k.dtype, k.device
@@ -260,10 +263,34 @@ class TokenCache:
             for name, t, want, kind in (("k", k, (pages, Hk, _PAGE, Dp), dtype), ("v", v, (pages, Hk, Dp, _PAGE), dtype),
                                         ("k_scale", k_scale, side, _F32), ("v_scale", v_scale, side, _F32)):
                 _check_plain(name, t, want, kind, dev)
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.D, self.Hk, self.pages, self.device = D, Hk, pages, dev
-        self.desc = _pack_cache(pages, Hk, D, _CODES[dtype], k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
-                                v_scale.data_ptr())
+        where = k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()
+        sizes = k.numel(), v.numel(), k_scale.numel(), v_scale.numel()
+        object.__setattr__(self, "_held", (k, v, k_scale, v_scale, D, Hk, pages, dev, where + sizes,
+                                           _pack_cache(pages, Hk, D, _CODES[dtype], *where)))
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"a TokenCache is fixed once made: {name} cannot be set (make a new one)")
+
+    def __reduce__(self):
+        return TokenCache, self._held[:5]
+
+    k = property(lambda self: self._held[0])
+    v = property(lambda self: self._held[1])
+    k_scale = property(lambda self: self._held[2])
+    v_scale = property(lambda self: self._held[3])
+    D = property(lambda self: self._held[4])
+    Hk = property(lambda self: self._held[5])
+    pages = property(lambda self: self._held[6])
+    device = property(lambda self: self._held[7])
+
+    @property
+    def desc(self) -> bytes:
+        """The packed descriptor, for a call at once: its addresses have been looked at again."""
+        k, v, ks, vs, _, _, _, _, where, desc = self._held
+        if where != (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), k.numel(), v.numel(), ks.numel(),
+                     vs.numel()):
+            raise ValueError("the cache's tensors have been resized or moved: make a new TokenCache of them")
+        return desc
 
 
 def token_cache(pages: int, Hk: int, D: int, *, codes: torch.dtype = torch.float8_e4m3fn, device="cuda") -> TokenCache:
