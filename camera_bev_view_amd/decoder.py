@@ -286,11 +286,15 @@ class TokenCache:
     @property
     def desc(self) -> bytes:
         """The packed descriptor, for a call at once: its addresses have been looked at again."""
-        k, v, ks, vs, _, _, _, _, where, desc = self._held
-        if where != (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), k.numel(), v.numel(), ks.numel(),
-                     vs.numel()):
-            raise ValueError("the cache's tensors have been resized or moved: make a new TokenCache of them")
-        return desc
+        return _cache_desc(self._held)
+
+
+def _cache_desc(held) -> bytes:
+    k, v, ks, vs, _, _, _, _, where, desc = held
+    if where != (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), k.numel(), v.numel(), ks.numel(),
+                 vs.numel()):
+        raise ValueError("the cache's tensors have been resized or moved: make a new TokenCache of them")
+    return desc
 
 
 def token_cache(pages: int, Hk: int, D: int, *, codes: torch.dtype = torch.float8_e4m3fn, device="cuda") -> TokenCache:
@@ -304,8 +308,8 @@ def token_cache(pages: int, Hk: int, D: int, *, codes: torch.dtype = torch.float
                       torch.zeros((pages, Hk, _PAGE), dtype=torch.float32, device=device), D)
 
 
-def _cache_rows(cache: TokenCache, table, start, count, B: int, T: int) -> bytes:
-    dev, shape = cache.device, table.shape
+def _cache_rows(dev, table, start, count, B: int, T: int) -> bytes:
+    shape = table.shape
     if len(shape) != 2 or shape[0] != B:
         raise ValueError(f"table must be [B={B}, pages of a sequence], got {tuple(shape)}")
     _check_sizes(B, T, shape[1])
@@ -324,18 +328,21 @@ def cache_write(cache: TokenCache, k: torch.Tensor, v: torch.Tensor, table: torc
     """fbev_cache_write: rows k, v [B,T,Hk,D] (fp32 or bf16) become the tokens start[b] .. start[b] + count[b] (T without
     ``count``) of their sequences, whose pages ``table`` [B,W] names (all int32).  Padding and rows without a page are
     dropped.  No token may be written twice in a call."""
-    dev = cache.device
-    _check_values("k", k, 4, dev)
-    _check_values("v", v, 4, dev, k.dtype)
-    B, T = k.shape[:2]
-    if v.shape != k.shape or k.shape[2] != cache.Hk or k.shape[3] != cache.D:
-        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must be [B, T, Hk={cache.Hk}, D={cache.D}]")
-    if cache.D > 1:
-        k = k if k.stride(3) == 1 else k.contiguous()
-        v = v if v.stride(3) == 1 else v.contiguous()
-    cr = _cache_rows(cache, table, start, count, B, T)
-    _call("fbev_cache_write", dev, cache.desc, cr, _data(k), _data(v), _DTYPES[k.dtype], _pack_strides(*k.stride()[:3]),
-          _pack_strides(*v.stride()[:3]))
+    held = cache._held
+    _, _, _, _, D, Hk, _, dev, _, _ = held
+    shape, dtype = k.shape, k.dtype
+    if not (len(shape) == 4 and dtype in _DTYPES and k.device == dev and v.dtype == dtype and v.device == dev):
+        _check_values("k", k, 4, dev)
+        _check_values("v", v, 4, dev, dtype)
+    if v.shape != shape or shape[2] != Hk or shape[3] != D:
+        raise ValueError(f"k {tuple(shape)} and v {tuple(v.shape)} must be [B, T, Hk={Hk}, D={D}]")
+    ks, vs = k.stride(), v.stride()
+    if D > 1 and (ks[3] != 1 or vs[3] != 1):
+        k, v = k.contiguous(), v.contiguous()
+        ks, vs = k.stride(), v.stride()
+    cr = _cache_rows(dev, table, start, count, shape[0], shape[1])
+    _call("fbev_cache_write", dev, _cache_desc(held), cr, k.data_ptr(), v.data_ptr(), _DTYPES[dtype],
+          _pack_strides(*ks[:3]), _pack_strides(*vs[:3]))
 
 
 def cache_read(cache: TokenCache, table: torch.Tensor, start: torch.Tensor, T: int, *,
@@ -345,11 +352,14 @@ def cache_read(cache: TokenCache, table: torch.Tensor, start: torch.Tensor, T: i
     from count[b] on and where there is no page."""
     if dtype not in _DTYPES:
         raise ValueError(f"dtype must be float32 or bfloat16, got {dtype}")
-    dev, B = cache.device, table.shape[0]
-    cr = _cache_rows(cache, table, start, count, B, T)
-    k = torch.empty(B, T, cache.Hk, cache.D, dtype=dtype, device=dev)
+    held = cache._held
+    _, _, _, _, D, Hk, _, dev, _, _ = held
+    shape = table.shape
+    B = shape[0] if shape else 0
+    cr = _cache_rows(dev, table, start, count, B, T)
+    k = torch.empty(B, T, Hk, D, dtype=dtype, device=dev)
     v = torch.empty_like(k)
-    _call("fbev_cache_read", dev, cache.desc, cr, _DTYPES[dtype], _data(k), _data(v))
+    _call("fbev_cache_read", dev, _cache_desc(held), cr, _DTYPES[dtype], k.data_ptr(), v.data_ptr())
     return k, v
 
 
@@ -399,15 +409,20 @@ def cache_attention(q: torch.Tensor, cache: TokenCache, table: torch.Tensor, sta
     (queries that are not tokens of the cache).  Tokens and queries from count[b] on are padding; they, and queries that
     see nothing, get zeros.  ``scale``: 1 / sqrt(D) unless given; ``cap``: scores become cap tanh(score / cap) (0 or None:
     no cap).  Forward only: the cache holds no gradients."""
-    dev = cache.device
-    _check_values("q", q, 4, dev)
-    B, T, Hq, D = q.shape
-    if D != cache.D:
-        raise ValueError(f"q {tuple(q.shape)} must have the cache's D={cache.D} channels")
+    held = cache._held
+    _, _, _, _, held_D, Hk, _, dev, _, _ = held
+    shape, dtype = q.shape, q.dtype
+    if not (len(shape) == 4 and dtype in _DTYPES and q.device == dev):
+        _check_values("q", q, 4, dev)
+    B, T, Hq, D = shape
+    if D != held_D:
+        raise ValueError(f"q {tuple(q.shape)} must have the cache's D={held_D} channels")
     _check_sizes(Hq)
-    if D > 1 and q.stride(3) != 1:
+    qs = q.stride()
+    if D > 1 and qs[3] != 1:
         q = q.contiguous()
-    cr = _cache_rows(cache, table, start, count, B, T)
+        qs = q.stride()
+    cr = _cache_rows(dev, table, start, count, B, T)
     mode, words = (_lib.FBEV_DRAFT_CHAIN if drafted else _lib.FBEV_DRAFT_NONE), 0
     if ancestors is not None:
         if not drafted:
@@ -423,12 +438,11 @@ def cache_attention(q: torch.Tensor, cache: TokenCache, table: torch.Tensor, sta
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _check_plain("out", out, q.shape, q.dtype, dev)
-        _check_apart("out", out, q, cache.k, cache.v, cache.k_scale, cache.v_scale, table, start, count, ancestors,
-                     workspace)
+        _check_apart("out", out, q, *held[:4], table, start, count, ancestors, workspace)
     if scale is None:
         scale = D ** -0.5 if D else 1.0
-    dt = _DTYPES[q.dtype]
-    ad = _pack_attention(Hq, mode, words, *q.stride()[:3], _data(ancestors) or 0, scale, cap or 0.0)
-    workspace, have = _scratch(_cache_attention_scratch(B, T, table.shape[1], Hq, cache.Hk, D, dt), workspace, dev)
-    _call("fbev_cache_attention", dev, cache.desc, cr, ad, _data(q), dt, _data(out), _data(workspace), have)
+    dt = _DTYPES[dtype]
+    ad = _pack_attention(Hq, mode, words, *qs[:3], _data(ancestors) or 0, scale, cap or 0.0)
+    workspace, have = _scratch(_cache_attention_scratch(B, T, table.shape[1], Hq, Hk, D, dt), workspace, dev)
+    _call("fbev_cache_attention", dev, _cache_desc(held), cr, ad, q.data_ptr(), dt, out.data_ptr(), _data(workspace), have)
     return out
