@@ -356,7 +356,7 @@ __device__ __forceinline__ void weigh(float (&s)[16], F vs, bool masked, uint32_
 #pragma unroll
   for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
   top = query_max(top);
-  // the maximum moves where it grows by 2^8 or more: weights stay below that, and sums in fp32 do not mind
+  // the maximum moves where it grows by 2^8 or more: weights stay below that, for which room_for() leaves room
   const bool moves = top > (m == kNegInf ? kNegInf : 8.0f);
   if (__any(moves)) {
     const float to = moves ? base + top : m, by = moves ? to - base : 0.0f;
@@ -413,7 +413,7 @@ __device__ __forceinline__ void finish_row(const CacheAttnArgs& a, const Part& p
     for (int i = 0; i < 8; ++i) x[i] += f * (i < 4 ? lo[i] : hi[i - 4]);
   }
   if (a.splits == 1) {
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    const float inv = total == 0.0f ? 0.0f : 1.0f / (total * a.down);
     T* out = (T*)a.out + (((int64_t)p.b * c.T + t) * a.Hq + p.hk * a.G + h) * c.D + ch;
     T y[8];
 #pragma unroll
@@ -439,6 +439,14 @@ __device__ __forceinline__ void finish_row(const CacheAttnArgs& a, const Part& p
       keep[c.D + 1] = total;
     }
   }
+}
+
+// What values are scaled by until a row is finished, a power of two: sums of the table's tokens at weights of up to 2^8 (what
+// weigh() lets them grow to) stay below 2^127 for values of any size.
+float room_for(int W) {
+  int tokens = 6;                                       // log2 of them, rounded up
+  while (((int64_t)1 << tokens) < (int64_t)W * kPage) ++tokens;
+  return ldexpf(1.0f, -(9 + tokens));
 }
 
 // Up to 16 rows: every wave has pages of its own.
@@ -516,7 +524,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attn_few(CacheAttnArgs a)
         s,
         [&](int kk, float(&x)[8]) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = vs[8 * kk + i];
+          for (int i = 0; i < 8; ++i) x[i] = vs[8 * kk + i] * a.down;
         },
         masked, bits, a.cap, m, l, o, pf);
 #pragma unroll
@@ -616,7 +624,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(SIMD
         for (int kk = 0; kk < 2; ++kk) to[(kKeys + 2 * rows + kk) * 64] = widen<KIND>(vw[j][2 * kk], vw[j][2 * kk + 1]);
       }
     }
-    if (tile < 2) scales[buf][tile][lane] = tile ? scale : scale * unit;
+    if (tile < 2) scales[buf][tile][lane] = scale * (tile ? a.down : unit);
   };
 
   const int whole = a.mode == FBEV_DRAFT_NONE ? p.end : min(p.start, p.end);      // tokens below are seen by all
@@ -748,7 +756,7 @@ __global__ __launch_bounds__(256) void cache_attn_join_few(CacheAttnArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] += f * x[s][i];
   }
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  const float inv = total == 0.0f ? 0.0f : 1.0f / (total * a.down);
   const int64_t bh = at / a.R;
   const int row = (int)(at - bh * a.R), t = row / a.G, h = row - t * a.G;
   const int64_t b = bh / a.c.Hk, hk = bh - b * a.c.Hk;
@@ -813,7 +821,7 @@ __global__ __launch_bounds__(1024) void cache_attn_join(CacheAttnArgs a) {
   const int64_t bh = at / a.R;
   const int row = (int)(at - bh * a.R), t = row / a.G, h = row - t * a.G;
   const int64_t b = bh / a.c.Hk, hk = bh - b * a.c.Hk;
-  ((T*)a.out)[((b * a.c.T + t) * a.Hq + hk * a.G + h) * D + ch] = (T)(total == 0.0f ? 0.0f : y / total);
+  ((T*)a.out)[((b * a.c.T + t) * a.Hq + hk * a.G + h) * D + ch] = (T)(total == 0.0f ? 0.0f : y / (total * a.down));
 }
 
 // How a call's rows lie on workgroups.
@@ -916,6 +924,7 @@ size_t cache_attention_workspace_bytes(const CacheAttnArgs& a) {
 hipError_t launch_cache_attention(CacheAttnArgs a, hipStream_t stream) {
   const Plan plan = plan_of(a);
   a.row_blocks = plan.row_blocks;
+  a.down = room_for(a.c.W);
   a.splits = plan.splits;
   return a.elem_bytes == 4 ? launch_type<float>(a, plan, stream) : launch_type<__bf16>(a, plan, stream);
 }

@@ -74,6 +74,7 @@ struct CacheAttnArgs {
   int elem_bytes;
   // set by the launcher
   int row_blocks, splits;
+  float down;              // of the values' scales
   float* part;             // [splits][B Hk][R][D + 2]
 };
 size_t cache_attention_workspace_bytes(const CacheAttnArgs& a);

@@ -652,7 +652,10 @@ fbev_status fbev_cache_read(const fbev_cache_desc* cd, const fbev_cache_rows* cr
  *   q   : [B, T, Hq, D] by element strides, channels contiguous, any alignment.
  *   ancestors : [B, T, words] uint64, words >= ceil(T / 64); NULL without a tree.
  *   scale, cap : as for fbev_attention_forward.
- *   out : [B, T, Hq, D] of dtype, contiguous, on memory of its own.
+ *   out : [B, T, Hq, D] of dtype, contiguous, on memory of its own: finite for
+ *         values of up to 2^127, with all digits in sequences whose largest
+ *         value is 2^-80 W or more.  Scores are fp32: past 2^128, the
+ *         product of a query with a key's codes among them, they are infinite.
  *   workspace : as above; few queries over many tokens are split along the
  *               tokens and joined from there.
  */
