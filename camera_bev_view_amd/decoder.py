@@ -57,6 +57,26 @@ def _call(name: str, dev: torch.device, *args) -> None:
         _lib.check(status)
 
 
+class _NoBackward(torch.autograd.Function):
+    """The result of a call without a backward, as a part of its inputs' graph: a gradient that arrives there is an error
+    and not lost."""
+
+    @staticmethod
+    def forward(ctx, name, result, *inputs):
+        ctx.name = name
+        return result.view_as(result)
+
+    @staticmethod
+    def backward(ctx, grad):
+        raise RuntimeError(f"{ctx.name} has no backward: call it under torch.no_grad() or on detached tensors")
+
+
+def _without_backward(name: str, result: torch.Tensor, *inputs: Optional[torch.Tensor]) -> torch.Tensor:
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
+        return _NoBackward.apply(name, result, *inputs)
+    return result
+
+
 # ---- root-mean-square norm
 
 @functools.lru_cache(maxsize=1024)
@@ -125,7 +145,8 @@ def rms_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
     """fbev_rms_norm_forward on rows of channels x [..., C] (fp32 or bf16): h = x + residual (like x; rounded once), y = h
     weight / sqrt(mean h^2 + eps).  ``weight`` [C] is contiguous fp32.  Rows may lie at two strides (heads of a packed
     projection); other layouts are copied first.  ``h_out`` may be x or residual themselves, where contiguous.
-    Returns (y, h, rstd [...] fp32); h is x without a residual.  The backward takes h and rstd."""
+    Returns (y, h, rstd [...] fp32); h is x without a residual.  The backward takes h and rstd.  Results are no part of a
+    graph: rms_norm and rms_norm_add are the differentiable calls."""
     dev = x.device
     x, residual, _, _, rd = _rms_desc(x, residual, weight, eps)
     if out is None:
@@ -162,7 +183,7 @@ def rms_norm_codes(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
                    ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """fbev_rms_norm_codes: rms_norm_forward with y in 8 bits (``codes``: torch.int8 or torch.float8_e4m3fn) and a scale for each ``block``
     channels (32, 64 or 128; 0: one for the row).  Returns (codes like x, scales [..., blocks] fp32, h): a code stands for
-    code * scale."""
+    code * scale.  Forward only: a gradient that reaches scales or h is an error."""
     if codes not in _CODES:
         raise ValueError(f"codes must be torch.int8 or torch.float8_e4m3fn, got {codes}")
     dev = x.device
@@ -174,6 +195,10 @@ def rms_norm_codes(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
     h = _sum_out(h_out, x, residual, weight)
     _call("fbev_rms_norm_codes", dev, _data(x), _data(residual), _DTYPES[x.dtype], rd, _data(weight), _CODES[codes],
           block, _data(out), _data(scales), None if residual is None else _data(h))
+    if x.requires_grad or (residual is not None and residual.requires_grad) or (weight is not None and weight.requires_grad):
+        scales = _without_backward("rms_norm_codes", scales, x, residual, weight)
+        if residual is not None:
+            h = _without_backward("rms_norm_codes", h, x, residual, weight)
     return out, scales, h
 
 
@@ -327,7 +352,7 @@ def cache_write(cache: TokenCache, k: torch.Tensor, v: torch.Tensor, table: torc
                 count: Optional[torch.Tensor] = None) -> None:
     """fbev_cache_write: rows k, v [B,T,Hk,D] (fp32 or bf16) become the tokens start[b] .. start[b] + count[b] (T without
     ``count``) of their sequences, whose pages ``table`` [B,W] names (all int32).  Padding and rows without a page are
-    dropped.  No token may be written twice in a call."""
+    dropped.  No token may be written twice in a call.  The cache holds no gradients: what k and v were made from gets none."""
     held = cache._held
     _, _, _, _, D, Hk, _, dev, _, _ = held
     shape, dtype = k.shape, k.dtype
@@ -408,7 +433,8 @@ def cache_attention(q: torch.Tensor, cache: TokenCache, table: torch.Tensor, sta
     of word j / 64 for token j (a tree of drafted tokens; see tree_ancestors), or not at all when not ``drafted``
     (queries that are not tokens of the cache).  Tokens and queries from count[b] on are padding; they, and queries that
     see nothing, get zeros.  ``scale``: 1 / sqrt(D) unless given; ``cap``: scores become cap tanh(score / cap) (0 or None:
-    no cap).  Forward only: the cache holds no gradients."""
+    no cap).  Forward only: the cache holds no gradients, and one that reaches the result of a q that requires them is an
+    error."""
     held = cache._held
     _, _, _, _, held_D, Hk, _, dev, _, _ = held
     shape, dtype = q.shape, q.dtype
@@ -445,4 +471,4 @@ def cache_attention(q: torch.Tensor, cache: TokenCache, table: torch.Tensor, sta
     ad = _pack_attention(Hq, mode, words, *qs[:3], _data(ancestors) or 0, scale, cap or 0.0)
     workspace, have = _scratch(_cache_attention_scratch(B, T, table.shape[1], Hq, Hk, D, dt), workspace, dev)
     _call("fbev_cache_attention", dev, _cache_desc(held), cr, ad, q.data_ptr(), dt, out.data_ptr(), _data(workspace), have)
-    return out
+    return _without_backward("cache_attention", out, q) if q.requires_grad else out

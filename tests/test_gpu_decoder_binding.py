@@ -93,3 +93,39 @@ def test_copies_have_memory_of_their_own():
     ops.cache_write(shallow, rows * 3, rows * 5, table, start)          # the same tensors
     for got, want in zip(ops.cache_read(cache, table, start, 70), ops.cache_read(one, table, start, 70)):
         assert torch.equal(got, want)
+
+
+def test_gradients_are_not_lost_without_a_word():
+    """Calls without a backward, on tensors that require gradients: the values are the same, and a gradient is an error."""
+    x, r, w = draw(1, 6, 96), draw(2, 6, 96), draw(3, 96)
+    want = ops.rms_norm_codes(x, w, residual=r)
+    for which in range(3):
+        args = [x.clone(), r.clone(), w.clone()]
+        args[which].requires_grad_()
+        codes, scales, h = ops.rms_norm_codes(args[0], args[2], residual=args[1])
+        assert torch.equal(codes.view(torch.uint8), want[0].view(torch.uint8))
+        assert torch.equal(scales, want[1]) and torch.equal(h, want[2])
+        for out in (scales, h):
+            with pytest.raises(RuntimeError, match="rms_norm_codes has no backward"):
+                out.sum().backward()
+        # the residual stream of a layer behind it too
+        with pytest.raises(RuntimeError, match="rms_norm_codes has no backward"):
+            ops.rms_norm(h, w).sum().backward()
+        with torch.no_grad():
+            assert not any(t.requires_grad for t in ops.rms_norm_codes(args[0], args[2], residual=args[1]))
+    leaf = x.clone().requires_grad_()
+    codes, scales, h = ops.rms_norm_codes(leaf, w)
+    assert h is leaf and scales.requires_grad           # h is x itself: its graph is x's
+    cache, _, rows, table, start = held_cache()
+    q = draw(4, 1, 5, 4, 32)
+    want = ops.cache_attention(q, cache, table, i32([65]))
+    out = ops.cache_attention(q.requires_grad_(), cache, table, i32([65]))
+    assert torch.equal(out, want)
+    with pytest.raises(RuntimeError, match="cache_attention has no backward"):
+        out.sum().backward()
+    with torch.no_grad():
+        assert not ops.cache_attention(q, cache, table, i32([65])).requires_grad
+    given = torch.empty_like(want)
+    out = ops.cache_attention(q, cache, table, i32([65]), out=given)
+    assert torch.equal(given, want) and out.data_ptr() == given.data_ptr() and out.requires_grad
+    assert ops.cache_attention(q.detach(), cache, table, i32([65]), out=given) is given
