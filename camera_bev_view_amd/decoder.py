@@ -402,11 +402,13 @@ def _cache_attention_scratch(B: int, T: int, W: int, Hq: int, Hk: int, D: int, d
 
 def tree_ancestors(parents: Sequence, *, device="cuda") -> torch.Tensor:
     """The ``ancestors`` of cache_attention from each drafted token's parent among them (-1: none, it follows the cache):
-    [T] parents give [1, T, words], [B, T] give [B, T, words] (int64 bits).  A token sees its ancestors and itself."""
+    [T] parents give [1, T, words], [B, T] give [B, T, words] (int64 bits).  A token sees its ancestors and itself.  Made on
+    the host: parents on the device are waited for, so a captured step takes ancestors made before it."""
     rows = parents.tolist() if torch.is_tensor(parents) else [list(p) if hasattr(p, "__len__") else p for p in parents]
-    if not rows or not isinstance(rows[0], list):
+    shape = tuple(getattr(parents, "shape", ()))        # of a tensor or an array: a batch of none still has its T
+    if len(shape) != 2 and (not rows or not isinstance(rows[0], list)):
         rows = [rows]
-    T = len(rows[0])
+    T = shape[1] if len(shape) == 2 else len(rows[0])
     if any(len(r) != T for r in rows):
         raise ValueError("every tree must have the same number of tokens")
     words, out = max(1, -(-T // 64)), []
