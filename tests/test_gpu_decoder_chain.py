@@ -145,3 +145,42 @@ def test_norm_codes_as_the_left_side_of_a_product():
     got, want = values.double() @ weight.double(), y.double() @ weight.double()
     bound = ((values - y).abs().double() @ weight.double().abs())
     assert ((got - want).abs() <= bound + 1e-9).all()
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+def test_branches_of_a_tree_get_what_they_would_get_alone(kind):
+    """Attention of a tree's tokens against that of each branch as a chain, on the same rows of keys and values (so the same
+    codes) behind a short cache, where a wrong mask shows: a chain over the whole tree, a tree without its siblings hidden."""
+    say(f"[case] branches, {kind}")
+    layer = Layer()
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    table, B, n = i32([[3, 0], [1, 2]]), 2, [5, 62]
+    past, draft = draw(20, B, 62, 128), draw(21, B, 5, 128)
+    parents, depth = [-1, 0, 0, 1, 2], [0, 1, 1, 2, 2]
+    branches = [[0, 1, 3], [0, 2, 4]]
+    with torch.no_grad():
+        _, pk, pv = layer.heads(past, torch.arange(62., device="cuda").expand(B, 62).contiguous())
+        q, k, v = layer.heads(draft, torch.tensor([[m + d for d in depth] for m in n], dtype=F32, device="cuda"))
+
+    def attend(pick, **how):
+        cache = ops.token_cache(4, 2, 32, codes=KINDS[kind])
+        ops.cache_write(cache, pk, pv, table, i32([0, 0]), count=i32(n))
+        ops.cache_write(cache, k[:, pick], v[:, pick], table, i32(n))
+        return ops.cache_attention(q[:, pick], cache, table, i32(n), **how)
+
+    every = list(range(5))
+    tree = attend(every, ancestors=ops.tree_ancestors(parents))
+    # two sums of at most 67 tokens in fp32, scores of 32 products in three parts, all within a few steps of 2^-24 of their
+    # sizes: 2 (3 D + 36) 2^-24 of the largest score and 2 (n + 64) 2^-24 of the largest value, twice
+    size = float(max(v.abs().max(), pv.abs().max())) * 1.1
+    score = float(q.norm(dim=-1).max() * max(k.norm(dim=-1).max(), pk.norm(dim=-1).max())) * 1.1 * 32 ** -0.5
+    bound = 2 * (2 * (3 * 32 + 36) * score + 2 * (67 + 64)) * 2.0 ** -24 * size
+    for branch in branches:
+        alone = attend(branch)
+        assert (alone - tree[:, branch]).abs().max() <= bound, branch
+    # masks that are wrong: far outside
+    chain, all_seen = attend(every), attend(every, ancestors=torch.full((1, 5, 1), 31, dtype=torch.int64, device="cuda"))
+    none = attend(every, drafted=False)
+    for b in range(B):
+        for wrong in (chain, all_seen, none):
+            assert (wrong[b, 3:] - tree[b, 3:]).abs().max() > 20 * bound, b
