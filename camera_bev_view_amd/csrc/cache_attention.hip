@@ -870,7 +870,7 @@ void launch_rows(const CacheAttnArgs& a, const Plan& plan, unsigned blocks, hipS
   } else if (plan.groups == 4) {
     if constexpr (sizeof(T) == 2 && DC < 128) cache_attn_many<T, KIND, DC, 16, 4, 4><<<blocks, 1024, 0, stream>>>(a);
   } else if (plan.groups == 2) {
-    cache_attn_many<T, KIND, DC, 8, 2, sizeof(T) == 2 ? 4 : 2><<<blocks, 512, 0, stream>>>(a);
+    cache_attn_many<T, KIND, DC, 8, 2, sizeof(T) == 2 && DC < 128 ? 4 : 2><<<blocks, 512, 0, stream>>>(a);
   } else {
     // bf16 takes tighter code that leaves four waves a SIMD (8 x 4000 rows of 128 channels: 371 us against 450; 25 x 256 rows:
     // 89 against 102; 2 x 1200 rows, a workgroup on every third CU: 25.0 against 24.3); fp32's parts of queries do not fit

@@ -497,7 +497,7 @@ __global__ __launch_bounds__(1024) void rms_join(const float* part, float* gw, i
 
 // The team of a row of `pieces` pieces: f(lanes, pieces a lane).
 template <typename F>
-hipError_t with_team(int pieces, F f) {
+auto with_team(int pieces, F f) {
   if (pieces <= 4) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
   if (pieces <= 8) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
   if (pieces <= 16) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
@@ -526,12 +526,9 @@ int backward_blocks(const RmsArgs& a, int teams, int threads) {
 
 size_t rms_norm_workspace_bytes(const RmsArgs& a) {
   if (a.rows == 0) return 0;
-  size_t need = 0;
-  with_team(pieces_of(a), [&](auto L, auto) {
-    need = (size_t)backward_blocks(a, team_threads(L) / L, team_threads(L)) * a.C * sizeof(float);
-    return hipSuccess;
+  return with_team(pieces_of(a), [&](auto L, auto) {
+    return (size_t)backward_blocks(a, team_threads(L) / L, team_threads(L)) * a.C * sizeof(float);
   });
-  return need;
 }
 
 hipError_t launch_rms_norm_forward(const RmsArgs& a, hipStream_t stream) {
