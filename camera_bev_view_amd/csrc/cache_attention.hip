@@ -832,16 +832,29 @@ struct Plan {
   int row_blocks, splits;
 };
 
-// Few rows: eight waves where that alone gives most CUs a workgroup (no split, no join: 32 sequences of 4000 tokens, 8 key
-// heads of 128, 46 us against 52 with four waves and two splits), else four and splits (one sequence of 4000 tokens, 8 heads of
-// 64: 10 us against 21).  More rows: up to 64 in four waves' tiles, two groups of those to a workgroup, which halves what a join
-// reads (15 drafted tokens over 200000: 34 us against 38 with a group and twice the splits), four in long caches where their
-// registers and LDS let 16 waves in (32 us; 40 sequences of 32 rows over 1000 tokens 28 against 23).  Beyond, eight tiles share
-// the widening of a page (64 rows of 16 scenes x 4 heads of 128: 73 us against 116).  Splits make up 512 workgroups of few rows, 256
-// of more (900 rows of 8 heads of 32 over 3600 tokens: 28 us against 37 with 512, in fp32 32 against 41), or 512 where a CU holds
-// two (bf16) and either a wave's work on a page is long (heads of 128: 1000 rows of 16 heads behind 9000 tokens 153 us against
-// 164) or each has a dozen pages and the batch is no single small one (4 x 900 rows of 8 heads of 32 over 3600 tokens 59 us against
-// 72, 16 x 32 rows of 8 heads of 64 over 4000 28 against 33; 32 over 1000 28 against 23).  Every workgroup still has four pages.
+// Few rows: eight waves where that alone gives most CUs a workgroup (192 of 256; no split, no join: 32 sequences of 4000 tokens, 8
+// key heads of 128, 46 us against 52 with four waves and two splits; 28 x 8 heads 42 against 47, 20 x 8 heads 37 either way), else
+// four and splits (one sequence of 4000 tokens, 8 heads of 64: 10 us against 21).  More rows: up to 64 in four waves' tiles, two
+// groups of those to a workgroup, which halves what a join reads (15 drafted tokens over 200000: 34 us against 38 with a
+// group and twice the splits), four in long caches where their registers and LDS let 16 waves in (32 us; 40 sequences of 32
+// rows over 1000 tokens 28 against 23).  Heads of 128 in two groups hold 134 KB of LDS: a workgroup a CU, two waves a SIMD (16
+// scenes of 16 drafted tokens x 16 over 4 heads behind 4096 to 2176 tokens 33 us, where bytes would take 11).  Beyond, eight tiles
+// share the widening of a page (64 rows of 16 scenes x 4 heads of 128: 73 us against 116).
+//
+// Splits make up 512 workgroups of few rows, 256 of more (900 rows of 8 heads of 32 over 3600 tokens: 28 us against 37 with
+// 512, in fp32 32 against 41), or 512 where a CU holds two (bf16) and either a wave's work on a page is long (heads of 128: 1000
+// rows of 16 heads behind 9000 tokens 153 us against 164) or each has a dozen pages and there are half a workgroup a CU
+// without a split (4 x 900 rows of 8 heads of 32 over 3600 tokens 59 us against 72, 16 x 32 rows of 8 heads of 64 over 4000 28 against
+// 33, 20 x 32 rows over 6000 45 against 51; 12 x 32 would win too, 36 against 39; 32 rows of 8 heads over 1000 28 against 23).  Calls that come near those numbers unsplit
+// are not split in two, where that would leave CUs with one and two parts: from 384 workgroups of 512 on (448 of 128 rows over 2000
+// tokens 106 us against 122 split, over 8000 330 against 324; 320 of them 102 against 100 unsplit and 248 against 287), from 192 of
+// 256 where waves share pages (fp32: 224 over 2000 tokens 100 against 103, over 6000 251 against 214; 160 of them 95 against 103
+// unsplit and 187 against 250), always below 256 where groups take turns (240 over 2000 tokens 46 against 40 unsplit, over
+// 6000 97 against 104).  Every workgroup still has four pages.
+//
+// All of that goes by the table's width, which the host knows, and not by what the sequences hold: a table far wider than
+// they need costs splits without a page and a join of them (8 tokens over 500 tokens each, 4 heads: 9.5 us behind a table of 8
+// pages, 11.5 behind one of 1024).
 Plan plan_of(const CacheAttnArgs& a) {
   Plan p;
   const int64_t heads = (int64_t)a.c.B * a.c.Hk;

@@ -657,7 +657,8 @@ fbev_status fbev_cache_read(const fbev_cache_desc* cd, const fbev_cache_rows* cr
  *         value is 2^-80 W or more.  Scores are fp32: past 2^128, the
  *         product of a query with a key's codes among them, they are infinite.
  *   workspace : as above; few queries over many tokens are split along the
- *               tokens and joined from there.
+ *               tokens and joined from there (many: 64 W, all that the host
+ *               knows of them; a table far wider than the sequences need costs time).
  */
 typedef enum { FBEV_DRAFT_NONE = 0, FBEV_DRAFT_CHAIN = 1, FBEV_DRAFT_TREE = 2 } fbev_drafts;
 
