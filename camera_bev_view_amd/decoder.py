@@ -21,6 +21,7 @@ from .encoder import (_DTYPES, _check_apart, _check_plain, _check_sizes, _check_
 _CODES = {torch.int8: _lib.FBEV_CODES_INT8, torch.float8_e4m3fn: _lib.FBEV_CODES_E4M3}
 _PAGE = _lib.FBEV_CACHE_PAGE
 _F32, _I32 = torch.float32, torch.int32
+_set = object.__setattr__
 
 # A call's own time counts where a step of serving is a few small ones: descriptors are packed as bytes (a tenth of a
 # ctypes structure's time; the layouts are the structures' of _lib) and go as plain pointers.
@@ -288,10 +289,11 @@ class TokenCache:
             for name, t, want, kind in (("k", k, (pages, Hk, _PAGE, Dp), dtype), ("v", v, (pages, Hk, Dp, _PAGE), dtype),
                                         ("k_scale", k_scale, side, _F32), ("v_scale", v_scale, side, _F32)):
                 _check_plain(name, t, want, kind, dev)
-        where = k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()
-        sizes = k.numel(), v.numel(), k_scale.numel(), v_scale.numel()
-        object.__setattr__(self, "_held", (k, v, k_scale, v_scale, D, Hk, pages, dev, where + sizes,
-                                           _pack_cache(pages, Hk, D, _CODES[dtype], *where)))
+        # addresses and sizes as they are now, and where to ask for them again
+        a, b, c, d = look = k.data_ptr, v.data_ptr, k_scale.data_ptr, v_scale.data_ptr
+        where, n = (a(), b(), c(), d()), pages * Hk * _PAGE
+        _set(self, "_held", (k, v, k_scale, v_scale, D, Hk, pages, dev, _pack_cache(pages, Hk, D, _CODES[dtype], *where),
+                             (*where, n * Dp, n * Dp, n, n), (*look, k.numel, v.numel, k_scale.numel, v_scale.numel)))
 
     def __setattr__(self, name, value):
         raise AttributeError(f"a TokenCache is fixed once made: {name} cannot be set (make a new one)")
@@ -315,9 +317,8 @@ class TokenCache:
 
 
 def _cache_desc(held) -> bytes:
-    k, v, ks, vs, _, _, _, _, where, desc = held
-    if where != (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), k.numel(), v.numel(), ks.numel(),
-                 vs.numel()):
+    _, _, _, _, _, _, _, _, desc, where, (a, b, c, d, e, f, g, h) = held
+    if where != (a(), b(), c(), d(), e(), f(), g(), h()):
         raise ValueError("the cache's tensors have been resized or moved: make a new TokenCache of them")
     return desc
 
@@ -354,7 +355,7 @@ def cache_write(cache: TokenCache, k: torch.Tensor, v: torch.Tensor, table: torc
     ``count``) of their sequences, whose pages ``table`` [B,W] names (all int32).  Padding and rows without a page are
     dropped.  No token may be written twice in a call.  The cache holds no gradients: what k and v were made from gets none."""
     held = cache._held
-    _, _, _, _, D, Hk, _, dev, _, _ = held
+    _, _, _, _, D, Hk, _, dev, _, _, _ = held
     shape, dtype = k.shape, k.dtype
     if not (len(shape) == 4 and dtype in _DTYPES and k.device == dev and v.dtype == dtype and v.device == dev):
         _check_values("k", k, 4, dev)
@@ -378,7 +379,7 @@ def cache_read(cache: TokenCache, table: torch.Tensor, start: torch.Tensor, T: i
     if dtype not in _DTYPES:
         raise ValueError(f"dtype must be float32 or bfloat16, got {dtype}")
     held = cache._held
-    _, _, _, _, D, Hk, _, dev, _, _ = held
+    _, _, _, _, D, Hk, _, dev, _, _, _ = held
     shape = table.shape
     B = shape[0] if shape else 0
     cr = _cache_rows(dev, table, start, count, B, T)
@@ -438,14 +439,15 @@ def cache_attention(q: torch.Tensor, cache: TokenCache, table: torch.Tensor, sta
     no cap).  Forward only: the cache holds no gradients, and one that reaches the result of a q that requires them is an
     error."""
     held = cache._held
-    _, _, _, _, held_D, Hk, _, dev, _, _ = held
+    _, _, _, _, held_D, Hk, _, dev, _, _, _ = held
     shape, dtype = q.shape, q.dtype
     if not (len(shape) == 4 and dtype in _DTYPES and q.device == dev):
         _check_values("q", q, 4, dev)
     B, T, Hq, D = shape
     if D != held_D:
         raise ValueError(f"q {tuple(q.shape)} must have the cache's D={held_D} channels")
-    _check_sizes(Hq)
+    if Hq >= 1 << 31:
+        _check_sizes(Hq)
     qs = q.stride()
     if D > 1 and qs[3] != 1:
         q = q.contiguous()
