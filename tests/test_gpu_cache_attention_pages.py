@@ -137,3 +137,39 @@ def test_every_page_in_its_place(form, dtype, kind):
         err = np.abs(out - want)
         assert (bound < 0.01).all() and (err <= bound).all(), \
             f"call {call}: {int((err > bound).sum())} of {err.size} outside, first at {np.argwhere(err > bound)[:1].tolist()}"
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,Hq,Hk", [(1, 2, 2), (3, 8, 1), (40, 2, 1), (90, 2, 1)])
+def test_the_widest_table(T, Hq, Hk, dtype):
+    """2^24 pages, the most that a table may have, of which a handful exist: the first, the last (which the call's own
+    tokens fill up to the table's end) and some between."""
+    W, D = 1 << 24, 32
+    say(f"[case] table of {W} pages, T={T} {dtype}")
+    cache, keys, values = signed_cache(8, Hk, D, "int8", T)
+    # the last page's own tokens: the same signs, written by the call
+    table = torch.full((1, W), -1, dtype=torch.int32, device="cuda")
+    places = [0, 1, 65, 4097, (1 << 23) + 5, W - 66, W - 2, W - 1]
+    table[0, places] = torch.arange(8, dtype=torch.int32, device="cuda")
+    start = torch.tensor([64 * W - T], dtype=torch.int32, device="cuda")
+    old = [cache.k[7].clone(), cache.v[7].clone()]
+    rows = lambda a, p: torch.from_numpy(a[p].astype(np.float32)).cuda().expand(1, 1, Hk, D)
+    k = torch.cat([rows(keys, 6 + (64 * W - T + t >= 64 * W - 64)) for t in range(T)], 1) * 0.5 * 127
+    v = torch.cat([rows(values, 6 + (64 * W - T + t >= 64 * W - 64)) for t in range(T)], 1) * 0.25 * 127
+    ops.cache_write(cache, k, v, table, start)
+    # rows of one size have the code 127: as values, 1 / 127 of what was written
+    own = slice(64 - min(T, 64), 64)
+    assert torch.equal(cache.k[7][:, own, :D], old[0][:, own, :D] * 127)
+    q = torch.zeros((1, T, Hq, D), dtype=dtype, device="cuda")
+    out = ops.cache_attention(q, cache, table, start)[0].double().cpu().numpy()
+    for t in range(T):
+        tokens = np.array([64] * 6 + [min(64, 128 - T + t + 1), max(0, 64 - T + t + 1)])
+        # values: 0.25 a sign from the pages, 0.25 x 127 from the call's rows, exact in codes of 1 / 127 of their scale
+        mine = np.array([0] * 6 + [max(0, min(64, 128 - T + t + 1) - min(64, 128 - T)), max(0, min(T, 64) - (T - 1 - t))])
+        sums = np.einsum("p,phd->hd", (tokens - mine) + 127.0 * mine, values.astype(np.float64)) * 0.25
+        want = np.repeat(sums / tokens.sum(), Hq // Hk, axis=0)
+        size = 0.25 * (tokens - mine + 127.0 * mine).sum() / tokens.sum()
+        # a scale of 0.25 is one rounding off at most; weights in parts (bf16: 2^-17); 512 sums; the output's rounding
+        bound = size * (520 * 2.0 ** -24 + (0 if dtype == F32 else 2.0 ** -17)) + HALF[dtype] * np.abs(want)
+        err = np.abs(out[t] - want)
+        assert (err <= bound * 1.01).all(), (t, float((err / bound).max()))
